@@ -300,8 +300,8 @@ def prepare(case, seed):
         elif c["ckpt"]:
             s["ckpt"] = torch.zeros(m["R"], 2 * F, dtype=torch.uint8, device="cuda")
             s["ckpt_scale"] = torch.zeros(m["R"], 2 * F // 32, dtype=torch.uint8, device="cuda")
-        s["scratch"] = torch.zeros(_scratch_bytes(c, m["R"]), dtype=torch.uint8, device="cuda")
-    s["status"] = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    if "map" in s:
+        s["scratch"] = torch.zeros(_scratch_bytes(c, s["map"]["R"]), dtype=torch.uint8, device="cuda")
     return s
 
 
@@ -312,10 +312,13 @@ def _empty_fp4(fmt, groups, rows, K):
 
 
 def _scratch_bytes(c, R):
-    """What a caller sets aside for an FFN call, generously: the rows in 4 bits, and for
-    the backward the weights and two row tensors in bf16."""
+    """What a caller sets aside for a call, generously: room for sums in parts, and for an
+    FFN the rows in 4 bits or (backward) the weights and two row tensors in bf16."""
+    n = 20 << 20
+    if c["op"] not in ("ffn", "ffn_bwd"):
+        return n
     H, F, E = c["H"], c["F"], c["E"]
-    n = _up(R, 128) * (_up(H, 256) + _up(F, 256)) + (1 << 16)
+    n += _up(R, 128) * (_up(H, 256) + _up(F, 256))
     if c["op"] == "ffn_bwd":
         n += 6 * E * H * F + 8 * R * F + (1 << 16)
     return n
@@ -429,9 +432,9 @@ def _run_own(s):
     if c["op"] == "product":
         xq = fp4(s["xq"], c["K"])
         B.moe_fp4_quantize(s["x"][None], xq, counts=m["counts"], offsets=m["offsets"],
-                           scratch=s["status"])
+                           scratch=s["scratch"])
         B.moe_fp4_grouped_gemm(xq, fp4(s["W"], c["K"]), m["counts"], m["offsets"], s["alpha"],
-                               s["y"], s["status"])
+                               s["y"], s["scratch"])
         return s["y"]
     cfg = B.MoEConfig(T=c["T"], H=c["H"], E=c["E"], k=c["k"], F=c["F"], n_groups=1, topk_groups=1,
                       route_scale=1.0, row_align=128)
