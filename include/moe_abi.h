@@ -539,6 +539,129 @@ MOE_API moe_status moe_layer_bwd(const moe_config* cfg, const moe_params* params
  * itself. Returns MOE_ERR_INVALID_ARG without a pool or for NULL pointers. */
 MOE_API moe_status moe_stash_release(const moe_config* cfg, const moe_fwd_state* st, void* stream);
 
+/* ------------------------------------------------------------ 4-bit experts
+ * Microscaled 4-bit floating point (the NVFP4 recipe the es summary §2.4 names
+ * for Blackwell, and the MX form of it): E2M1 codes (0, .5, 1, 1.5, 2, 3, 4, 6
+ * and their negatives) with one scale per block of consecutive elements along
+ * the reduced dimension K.
+ *   MOE_FP4_NV: blocks of 16, E4M3 scales, times the tensor's 2^scale_log2;
+ *   MOE_FP4_MX: blocks of 32, power-of-two (UE8M0) scales; scale_log2 is 0.
+ * Codes: [groups, rows, K / 2] bytes, the even element in the low four bits.
+ * Scales: per group ceil(rows / 128) slabs of ceil(K / 256) * (NV 4, MX 2)
+ * atoms of 512 bytes; an atom covers 128 rows and 4 consecutive blocks, the
+ * scale of row r's j-th block at byte (r % 32) * 16 + (r % 128) / 32 * 4 + j.
+ * Bytes of blocks past K must be zero (moe_fp4_quantize writes them so).
+ * An expert's own fp32 scale (a checkpoint's per-tensor scale) is the `alpha`
+ * of the products. */
+enum { MOE_FP4_NV = 0, MOE_FP4_MX = 1 };
+
+typedef struct moe_fp4_tensor {
+    int32_t format;          /* MOE_FP4_NV | MOE_FP4_MX                         */
+    int32_t scale_log2;      /* values are code x scale x 2^scale_log2 (NV:
+                              * -64..64; MX: 0)                                 */
+    int64_t groups;          /* experts, or 1                                   */
+    int64_t rows;            /* rows per group                                  */
+    int64_t K;               /* a multiple of 32                                */
+    void* codes;             /* device, 16-byte aligned                         */
+    void* scales;            /* device, 16-byte aligned                         */
+} moe_fp4_tensor;
+
+/* The experts of a layer in 4 bits: W13 [G, 2F, H] (rows 0..F-1 gate, F..2F-1
+ * up), W2 [G, H, F]; one format for both. */
+typedef struct moe_fp4_experts {
+    moe_fp4_tensor W13;
+    moe_fp4_tensor W2;
+    const float* alpha13;    /* [G] fp32 (device) or NULL (1)                   */
+    const float* alpha2;     /* [G] fp32 (device) or NULL (1)                   */
+    int32_t x_scale_log2;    /* tensor scales (NV) that x and h are quantised   */
+    int32_t h_scale_log2;    /* with: their rows' amax / (6 2^n) should lie in
+                              * E4M3's normal range, 2^-6 .. 448                */
+} moe_fp4_experts;
+
+typedef struct moe_fp4_sizes {
+    int64_t gemm_scratch_bytes;   /* moe_fp4_grouped_gemm (any shape)           */
+    int64_t fwd_scratch_bytes;    /* moe_fp4_ffn_fwd                            */
+    int64_t bwd_scratch_bytes;    /* moe_fp4_ffn_bwd                            */
+} moe_fp4_sizes;
+
+/* Scratch of the 4-bit calls, zero-filled once by the caller and then left to
+ * the calls (its first word is the device status word). cfg may be NULL: only
+ * gemm_scratch_bytes is then set. Calls that may overlap need scratch each.
+ * Host only. */
+MOE_API moe_status moe_fp4_query_sizes(const moe_config* cfg, int32_t format, moe_fp4_sizes* out);
+
+/* Bytes of the scales of one group of rows x K (above). Host only. */
+MOE_API moe_status moe_fp4_scale_bytes(int32_t format, int64_t rows, int64_t K, int64_t* bytes);
+
+/* x (bf16, ldx elements from row to row, a multiple of 8, at least K) into q's
+ * codes and scales. Per block: NV scale = amax / (6 2^scale_log2) rounded to
+ * E4M3 (to nearest, at most 448), MX scale = 2^ceil(log2(amax / 6)) (1 for a
+ * zero block); codes = the values over the scale rounded to the nearest of the
+ * grid, ties to even, at most 6 in magnitude (zero where the scale is zero). A
+ * block that holds an infinity or a NaN gets the scale NaN, and every value it
+ * stands for is then NaN.
+ * counts, offsets NULL: x is [groups, rows, K]. Else x is [rows, K] (groups 1)
+ * and only the rows offsets[i] .. offsets[i] + counts[i] - 1 of the `segments`
+ * segments (as moe_permute lays them out: ascending, at multiples of 128) are
+ * read and written; a segment outside the rows or off that grid records
+ * MOE_ERR_DEVICE_CHECK in `scratch`'s status word and is left out.
+ * values: NULL, or [.., K] bf16 (contiguous): what the codes stand for, exact
+ * except past bf16's range (straight-through training). scratch may be NULL (nothing is recorded). */
+MOE_API moe_status moe_fp4_quantize(const moe_fp4_tensor* q, const void* x, int64_t ldx,
+                                    const int32_t* counts, const int32_t* offsets,
+                                    int32_t segments, void* values, void* scratch, void* stream);
+
+/* The bf16 values q's codes stand for, exact except past bf16's range: out [groups, rows, K] with ldo
+ * elements from row to row (a multiple of 8, at least K). */
+MOE_API moe_status moe_fp4_dequantize(const moe_fp4_tensor* q, void* out, int64_t ldo,
+                                      void* stream);
+
+/* Grouped product on the FP4 tensor cores: for every group g of b [G, N, K] and
+ * the rows r = offsets[g] .. offsets[g] + counts[g] - 1 of a [rows, K],
+ *   out[r, n] = bf16(alpha[g] sum_k a[r, k] b[g, n, k]),
+ * fp32 accumulation; out [rows, N] bf16, N a multiple of 8; other rows of out
+ * are not written. counts, offsets NULL: G = 1 and every row. offsets at
+ * multiples of 128 (else MOE_ERR_DEVICE_CHECK, the group left out). alpha [G]
+ * fp32 or NULL. The result does not depend on timing (fixed summation order),
+ * and few rows do not cost the full machine: the reduction is then cut over
+ * the SMs through `scratch`. */
+MOE_API moe_status moe_fp4_grouped_gemm(const moe_fp4_tensor* a, const moe_fp4_tensor* b,
+                                        const int32_t* counts, const int32_t* offsets,
+                                        const float* alpha, void* out, void* scratch,
+                                        void* stream);
+
+/* Stage 3 with 4-bit experts (moe_grouped_ffn_fwd's counterpart): on every
+ * group's rows of x_perm, x4 = quantised x,
+ *   [G|U] = bf16(alpha13 x4 W13^T), h = bf16(silu(G) U), h4 = quantised h,
+ *   y_perm = bf16(alpha2 h4 W2^T).
+ * ckpt, ckpt_scale: NULL, or the 8-bit checkpoint for moe_fp4_ffn_bwd ([R, 2F]
+ * E4M3 codes and [R, 2F / 32] UE8M0 bytes: [G|U] over 2^ceil(log2(amax / 448))
+ * of each 32 values; a block with an infinity or a NaN gets the byte 255): 1.03
+ * bytes a value where GU and h keep 3. Rows past a group's counts are not
+ * written. R = moe_sizes.rows_max; cfg->dtype is MOE_DTYPE_BF16 (the router and
+ * the activations stay as they are); no paged stash, no weights_in_expert
+ * (MOE_ERR_UNSUPPORTED). scratch: fwd_scratch_bytes. */
+MOE_API moe_status moe_fp4_ffn_fwd(const moe_config* cfg, const moe_fp4_experts* experts,
+                                   const void* x_perm, const int32_t* counts,
+                                   const int32_t* offsets, void* ckpt, void* ckpt_scale,
+                                   void* y_perm, void* scratch, void* stream);
+
+/* Backward of moe_fp4_ffn_fwd at its input, both activation quantisers passed
+ * straight through and the experts' 4-bit weights held fixed (W^: the values
+ * their codes stand for, times alpha): with g, u the checkpoint's values,
+ * s = 1 / (1 + e^-g),
+ *   dh = dO W2^, dU = dh g s, dG = dh u s (1 + g (1 - s)), dX_perm = [dG|dU] W13^
+ * (+ dlogits[token_of[r], e] W_r[e] for the rows of a routed expert e, as in
+ * moe_grouped_ffn_bwd, unless dlogits is NULL). [dG|dU] is rounded to bf16
+ * between the products. Padding rows of dO_perm are zero (as moe_unpermute_bwd
+ * leaves them); those of dX_perm in a segment's last 128-row block are then
+ * zero too. scratch: bwd_scratch_bytes. */
+MOE_API moe_status moe_fp4_ffn_bwd(const moe_config* cfg, const moe_fp4_experts* experts,
+                                   const void* dO_perm, const void* ckpt, const void* ckpt_scale,
+                                   const int32_t* counts, const int32_t* offsets,
+                                   const int32_t* token_of, const float* dlogits,
+                                   const float* W_r, void* dX_perm, void* scratch, void* stream);
+
 /* Synchronises `stream`, then copies the device status word from scratch to
  * *code (0 = no problem recorded). */
 MOE_API moe_status moe_last_device_status(const void* scratch, int32_t* code, void* stream);

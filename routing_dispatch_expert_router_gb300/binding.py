@@ -28,6 +28,8 @@ ENTRY_POINTS = (
     "moe_grouped_ffn_fwd_reordered", "moe_unpermute_bwd_reordered",
     "moe_grouped_ffn_dgrad_reordered", "moe_route_bwd", "moe_permute_bwd",
     "moe_router_wgrad", "moe_layer_fwd", "moe_layer_bwd", "moe_stash_release",
+    "moe_fp4_query_sizes", "moe_fp4_scale_bytes", "moe_fp4_quantize", "moe_fp4_dequantize",
+    "moe_fp4_grouped_gemm", "moe_fp4_ffn_fwd", "moe_fp4_ffn_bwd",
     "moe_last_device_status",
     "moe_clear_device_status", "moe_check_bounded_wait", "moe_status_string",
 )
@@ -303,6 +305,150 @@ def moe_layer_bwd(cfg, params: MoEParams, x, dY, fwd: MoEFwdState, bwd: MoEBwdSt
 
 def moe_stash_release(cfg, fwd: MoEFwdState, stream=None):
     _call("moe_stash_release", _cfg(cfg), fwd, _stream(stream))
+
+
+# ------------------------------------------------------------------ 4-bit experts
+MOE_FP4_NV, MOE_FP4_MX = 0, 1
+_FP4_BLOCK = (16, 32)
+
+
+class MoEFp4Tensor(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("scale_log2", ctypes.c_int32),
+                ("groups", ctypes.c_int64), ("rows", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("codes", _P), ("scales", _P)]
+
+
+class MoEFp4Experts(ctypes.Structure):
+    _fields_ = [("W13", MoEFp4Tensor), ("W2", MoEFp4Tensor), ("alpha13", _P), ("alpha2", _P),
+                ("x_scale_log2", ctypes.c_int32), ("h_scale_log2", ctypes.c_int32)]
+
+
+class MoEFp4Sizes(ctypes.Structure):
+    _fields_ = [("gemm_scratch_bytes", ctypes.c_int64), ("fwd_scratch_bytes", ctypes.c_int64),
+                ("bwd_scratch_bytes", ctypes.c_int64)]
+
+
+@dataclass
+class Fp4Tensor:
+    """A tensor [groups, rows, K] in 4 bits: packed codes [groups, rows, K / 2] and
+    scale atoms [groups, slabs, atoms, 512] (include/moe_abi.h has the layout)."""
+    format: int
+    K: int
+    codes: torch.Tensor
+    scales: torch.Tensor
+    scale_log2: int = 0
+
+    def struct(self) -> MoEFp4Tensor:
+        g, rows, kb = self.codes.shape
+        if kb * 2 != self.K:
+            raise ValueError(f"codes hold {2 * kb} elements a row, K is {self.K}")
+        if self.scales.numel() != g * fp4_scale_bytes(self.format, rows, self.K):
+            raise ValueError("scales do not have the atoms of the codes' shape")
+        if not (self.codes.is_contiguous() and self.scales.is_contiguous()):
+            raise ValueError("codes and scales are contiguous")
+        return MoEFp4Tensor(self.format, self.scale_log2, g, rows, self.K, self.codes.data_ptr(),
+                            self.scales.data_ptr())
+
+
+def fp4_scale_bytes(fmt: int, rows: int, K: int) -> int:
+    """moe_fp4_scale_bytes: bytes of the scale atoms of one group of rows x K."""
+    n = ctypes.c_int64(0)
+    _check("moe_fp4_scale_bytes",
+           lib().moe_fp4_scale_bytes(ctypes.c_int32(fmt), ctypes.c_int64(rows),
+                                     ctypes.c_int64(K), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_fp4(fmt: int, groups: int, rows: int, K: int, device="cuda",
+              scale_log2: int = 0) -> Fp4Tensor:
+    """Uninitialised room for [groups, rows, K] in 4 bits."""
+    atoms = fp4_scale_bytes(fmt, rows, K) // 512
+    slabs = -(-rows // 128)
+    u8 = torch.uint8
+    return Fp4Tensor(fmt, K, torch.empty(groups, rows, K // 2, dtype=u8, device=device),
+                     torch.empty(groups, slabs, atoms // max(slabs, 1), 512, dtype=u8,
+                                 device=device), scale_log2)
+
+
+def fp4_experts(W13: Fp4Tensor, W2: Fp4Tensor, alpha13=None, alpha2=None, x_scale_log2: int = 0,
+                h_scale_log2: int = 0) -> MoEFp4Experts:
+    """The experts' 4-bit weights for the FFN calls; the tensors must outlive them."""
+    return MoEFp4Experts(W13.struct(), W2.struct(), _ptr(alpha13), _ptr(alpha2), x_scale_log2,
+                         h_scale_log2)
+
+
+def moe_fp4_query_sizes(cfg, fmt: int) -> MoEFp4Sizes:
+    out = MoEFp4Sizes()
+    c = None if cfg is None else ctypes.byref(_cfg(cfg))
+    _check("moe_fp4_query_sizes",
+           lib().moe_fp4_query_sizes(c, ctypes.c_int32(fmt), ctypes.byref(out)))
+    return out
+
+
+def alloc_fp4_scratch(nbytes: int, device="cuda") -> torch.Tensor:
+    """Scratch of the 4-bit calls: zero-filled once (status word, arrival counters)."""
+    return torch.zeros(int(nbytes), dtype=torch.uint8, device=device)
+
+
+def _bf16_rows(t, K: int, what: str) -> int:
+    """Elements from row to row of a bf16 [.., rows, K] tensor whose rows are evenly spaced."""
+    if t.dtype != torch.bfloat16 or t.shape[-1] != K or t.stride(-1) != 1:
+        raise ValueError(f"{what} is bf16 [.., {K}] with contiguous rows")
+    ld = t.stride(-2)
+    if t.dim() == 3 and t.shape[0] > 1 and t.stride(0) != ld * t.shape[1]:
+        raise ValueError(f"{what}'s groups follow each other row by row")
+    return ld if t.shape[-2] > 1 or t.dim() == 3 and t.shape[0] > 1 else max(ld, K)
+
+
+def moe_fp4_quantize(x, q: Fp4Tensor, scale_log2: int | None = None, counts=None, offsets=None,
+                     values=None, scratch=None, stream=None):
+    """x [groups, rows, K] bf16 into q; with counts and offsets only those rows of
+    x [1, rows, K]. values: the bf16 values that the codes stand for."""
+    if scale_log2 is not None:
+        q.scale_log2 = scale_log2
+    if tuple(x.shape) != (*q.codes.shape[:2], q.K):
+        raise ValueError("x has the shape of q")
+    if values is not None and not (values.is_contiguous() and values.shape == x.shape
+                                   and values.dtype == torch.bfloat16):
+        raise ValueError("values is contiguous bf16 of x's shape")
+    _call("moe_fp4_quantize", q.struct(), x, _bf16_rows(x, q.K, "x"), counts, offsets,
+          0 if counts is None else counts.numel(), values, scratch, _stream(stream))
+
+
+def moe_fp4_dequantize(q: Fp4Tensor, out, scale_log2: int | None = None, stream=None):
+    """out [groups, rows, K] bf16 = the values that q's codes stand for."""
+    s = q.struct()
+    if scale_log2 is not None:
+        s.scale_log2 = scale_log2
+    if tuple(out.shape) != (*q.codes.shape[:2], q.K):
+        raise ValueError("out has the shape of q")
+    _call("moe_fp4_dequantize", s, out, _bf16_rows(out, q.K, "out"), _stream(stream))
+
+
+def moe_fp4_grouped_gemm(a: Fp4Tensor, b: Fp4Tensor, counts, offsets, alpha, out, scratch,
+                         stream=None):
+    """out [rows, N] bf16: every group's rows of a [1, rows, K] by b [G, N, K]."""
+    if out.dtype != torch.bfloat16 or not out.is_contiguous() or \
+            tuple(out.shape) != (a.codes.shape[1], b.codes.shape[1]):
+        raise ValueError("out is contiguous bf16 [rows of a, rows of b]")
+    if counts is not None and counts.numel() != b.codes.shape[0]:
+        raise ValueError("one count per group of b")
+    _call("moe_fp4_grouped_gemm", a.struct(), b.struct(), counts, offsets, alpha, out, scratch,
+          _stream(stream))
+
+
+def moe_fp4_ffn_fwd(cfg, experts: MoEFp4Experts, x_perm, counts, offsets, ckpt, ckpt_scale,
+                    y_perm, scratch, stream=None):
+    """The experts' FFN in 4 bits; ckpt, ckpt_scale: None, or the 8-bit checkpoint."""
+    _call("moe_fp4_ffn_fwd", _cfg(cfg), experts, x_perm, counts, offsets, ckpt, ckpt_scale,
+          y_perm, scratch, _stream(stream))
+
+
+def moe_fp4_ffn_bwd(cfg, experts: MoEFp4Experts, dO_perm, ckpt, ckpt_scale, counts, offsets,
+                    token_of, dlogits, W_r, dX_perm, scratch, stream=None):
+    """The gradient at the FFN's input; token_of, dlogits, W_r: None, or the router's term."""
+    _call("moe_fp4_ffn_bwd", _cfg(cfg), experts, dO_perm, ckpt, ckpt_scale, counts, offsets,
+          token_of, dlogits, W_r, dX_perm, scratch, _stream(stream))
 
 
 def moe_last_device_status(scratch, stream=None) -> int:

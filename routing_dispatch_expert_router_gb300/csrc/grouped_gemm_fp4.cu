@@ -1,0 +1,636 @@
+// The expert products of 4-bit operands on the block-scaled FP4 tensor cores:
+// tcgen05.mma.kind::mxf4nvf4 (E2M1 with an E4M3 scale per 16 elements) and
+// kind::mxf4 (a UE8M0 scale per 32), fp32 accumulation in tensor memory.
+//
+// "Scalable Training of Mixture-of-Experts Models with Megatron Core" (es
+// summary, Resumen técnico §2.4) names NVFP4 and MXFP8 as Blackwell's recipes
+// for the expert GEMMs and §2.3.C the grouped GEMM that reads token counts on
+// the device. y[r] = alpha[g] * sum_k x4[r, k] W4[g, n, k] for the rows r of
+// group g: the scales travel with the operands (fp4_layout.cuh) and the tensor
+// core applies them, so the kernel only moves bytes, 0.5625 (NV) or 0.53 (MX)
+// of them per element.
+//
+// One persistent kernel, one CTA per SM, 320 threads:
+//   warp 0     TMA producer (one lane): per 256-deep k-block (128 bytes of codes
+//              a row) A's rows, 256 rows of B and their scale atoms;
+//   warp 1     MMA issuer (one lane) and tensor-memory owner: copies the atoms
+//              into tensor memory (tcgen05.cp), then four M=128 N=256 K=64 MMAs;
+//   warps 2-9  epilogue, two warps per tensor-memory lane quarter, 128 of the
+//              256 accumulator columns each, held in registers while the next
+//              tile's MMAs run.
+//
+// A decode step has a few rows per expert: then the weights' bytes are all the
+// work, and what counts is that every SM streams its share of them. Only the
+// rows a tile has are fetched (boxes of 32), and when the tiles do not fill the
+// SMs their K range is cut into `split` parts (chosen on the device from the
+// counts): every part's fp32 accumulator goes to scratch, and the warp that
+// arrives last at a slice of a tile adds the parts in order, so the result does
+// not depend on the order of arrival. No part waits for another.
+#include "fp4_layout.cuh"
+#include "fp8_layout.cuh"
+#include "gemm_common.cuh"
+
+namespace moe {
+namespace gg {
+
+constexpr int kF4Threads = 320;
+constexpr int kF4BN = 256;
+constexpr int kF4RowBytes = f4::kStep / 2;             // codes of a k-block's row: 128 bytes
+constexpr int kF4ABytes = BM * kF4RowBytes;            // 16 KB
+constexpr int kF4BBytes = kF4BN * kF4RowBytes;         // 32 KB
+constexpr int kF4EpiWarps = 8;
+constexpr uint32_t kF4TmemCols = 512;
+constexpr uint32_t kF4SfCol = kF4BN;                   // first scale-factor column
+
+enum F4Epi : int { kF4Store = 0, kF4Swiglu = 1 };
+
+struct Fp4Params {
+  int G, N, K;                 // groups, output columns (swiglu: 2F), reduction length
+  int64_t rows;                // rows of A and of the outputs
+  const int32_t* counts;       // null: one group of `rows` rows
+  const int32_t* offsets;
+  const float* alpha;          // [G], or null: 1
+  float unit;                  // times alpha: the operands' tensor scales
+  const uint8_t* sfa;          // A's atoms, [slabs][ka][512]
+  const uint8_t* sfb;          // B's, [G][slabs of N][ka][512]
+  int ka;                      // atoms of a slab
+  __nv_bfloat16* out;          // store: [rows, N]
+  // swiglu: h in 4 bits for the next product (codes [rows, F / 2], atoms), and
+  // the checkpoint of gate and up ([rows, 2F] E4M3, [rows, 2F / 32] UE8M0) or null
+  uint8_t* hq;
+  uint8_t* hsf;
+  int hka;
+  float hdown;                 // 2^-(h's scale_log2)
+  uint8_t* ckpt;
+  uint8_t* ckpt_sf;
+  // split K: fp32 parts and their arrival counters (zero before and after a launch)
+  float* part;
+  int64_t part_floats;
+  int32_t* arrived;
+  int arrived_n;
+  int32_t* status;
+};
+
+template <int FMT>
+struct F4Cfg {
+  static constexpr int ATOMS = f4::step_atoms(FMT);              // per slab and k-block
+  static constexpr int SF_A = ATOMS * f4::kAtomBytes;
+  static constexpr int SF_STAGE = 3 * SF_A;                      // A's, then B's two slabs
+  static constexpr int STAGE = kF4ABytes + kF4BBytes;
+  static constexpr int STAGES = 3;
+  static constexpr int SF_OFF = STAGES * STAGE;
+  static constexpr int CTRL_OFF = SF_OFF + STAGES * SF_STAGE;
+  static constexpr int EPI_OFF = (CTRL_OFF + kCtrlBytes + 1023) / 1024 * 1024;
+  static constexpr int SMEM = EPI_OFF + kF4EpiWarps * kBoxBytes + 1024;
+  // scale columns of a k-block: A's 4 per atom, then B's 8 per atom
+  static constexpr int SLOT_COLS = 12 * ATOMS;
+  static constexpr int SLOTS = 2;
+  static_assert(SMEM <= 232448, "FP4 grouped GEMM shared memory");
+  static_assert(kF4SfCol + SLOTS * SLOT_COLS <= kF4TmemCols, "FP4 tensor-memory columns");
+};
+
+// How many parts a tile's nk k-blocks are cut into: the number that makes the
+// busiest SM's k-blocks fewest, a tile's start and end counting as two.
+// More than one part only
+// where they fit scratch.
+__device__ __forceinline__ int choose_split(int tiles, int nk, int grid, int slot_rows,
+                                            int64_t part_floats, int counters) {
+  int best = 1;
+  long long cost = (long long)((tiles + grid - 1) / grid) * (nk + 2);
+  const int most = min(16, nk / 2);
+  for (int s = 2; s <= most; ++s) {
+    if ((int64_t)tiles * s * slot_rows * kF4BN > part_floats || tiles * kF4EpiWarps > counters)
+      break;
+    const long long c = (long long)((tiles * s + grid - 1) / grid) * ((nk + s - 1) / s + 2);
+    if (c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return best;
+}
+
+// h of 32 columns (bf16 pairs) in 4 bits: codes to `dst` (16 bytes); returns the
+// blocks' scale bytes.
+template <int FMT>
+__device__ __forceinline__ uint32_t quantize_h32(const uint4 (&h)[4], float down, uint8_t* dst) {
+  constexpr int BLK = f4::block_of(FMT), V = BLK / 8;
+  uint32_t c[4];
+  uint32_t bytes = 0;
+#pragma unroll
+  for (int b = 0; b < 32 / BLK; ++b) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = max(m, amax_bits8(h[b * V + i]));
+    const Fp4Scale s = fp4_scale<FMT>(__uint_as_float(m << 16), m < 0x7F80u, down);
+    bytes |= s.byte << (8 * b);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float f[8];
+      unpack8(h[b * V + i], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = fp4_quotient<FMT>(f[j], s.inv);
+      c[b * V + i] = s.inv > 0.f ? e2m1x8(f) : 0u;
+    }
+  }
+  *reinterpret_cast<uint4*>(dst) = make_uint4(c[0], c[1], c[2], c[3]);
+  return bytes;
+}
+
+// 32 bf16 values as the checkpoint keeps them: E4M3 codes of the values over
+// 2^ceil(log2(amax / 448)), the scale's byte returned. Half the bytes of bf16;
+// the backward's SwiGLU derivative is the only reader.
+__device__ __forceinline__ uint32_t checkpoint32(const uint4 (&v)[4], uint8_t* dst) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, amax_bits8(v[i]));
+  // an infinity or a NaN: the scale NaN marks the whole block
+  const bool finite = m < 0x7F80u;
+  const uint32_t code = finite ? ue8m0_code(__uint_as_float(m << 16)) : 255u;
+  const float inv = finite ? ue8m0_inv(code) : 0.f;
+  uint2 b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float f[8];
+    unpack8(v[i], f);
+    b[i] = e4m3x8(f, inv);
+  }
+  *reinterpret_cast<uint4*>(dst) = make_uint4(b[0].x, b[0].y, b[1].x, b[1].y);
+  *reinterpret_cast<uint4*>(dst + 16) = make_uint4(b[2].x, b[2].y, b[3].x, b[3].y);
+  return code;
+}
+
+// 32 accumulator columns times alpha, as bf16.
+__device__ __forceinline__ void scale_pack(const uint32_t (&r)[32], float alpha, uint4 (&o)[4]) {
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r[8 * v + i]) * alpha;
+    o[v] = pack8(f);
+  }
+}
+
+// First accumulator column of this warp's c-th 32-column slice: its 128 columns,
+// or (swiglu) gate columns 64 half .. +63, then the matching up columns.
+template <int EPI>
+__device__ __forceinline__ int slice_col(int half, int c) {
+  return EPI == kF4Swiglu ? (c >> 1) * 128 + 64 * half + 32 * (c & 1) : 128 * half + 32 * c;
+}
+
+// Stores a warp's 32 rows x 128 columns (o: bf16, the slices of slice_col): rv of
+// the 32 rows hold data, the others are not written.
+template <int FMT, int EPI>
+__device__ __forceinline__ void f4_epilogue(const Fp4Params& p, const CUtensorMap* tmC,
+                                            uint8_t* stage, uint32_t stage_u32, int nt, int row0,
+                                            int rv, int half, int lane, const uint4 (&o)[4][4]) {
+  if (EPI == kF4Swiglu) {
+    if (lane >= rv) return;
+    const int F = p.N / 2;
+    const int f0 = nt * (kF4BN / 2) + 64 * half;
+    const int64_t row = row0 + lane;
+    uint32_t hs = 0, gs = 0, us = 0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint4 h[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) h[v] = swiglu_h8<false>(o[c][v], o[2 + c][v], 1.f);
+      if (p.ckpt) {
+        gs |= checkpoint32(o[c], p.ckpt + row * 2 * F + f0 + 32 * c) << (8 * c);
+        us |= checkpoint32(o[2 + c], p.ckpt + row * 2 * F + F + f0 + 32 * c) << (8 * c);
+      }
+      hs |= quantize_h32<FMT>(h, p.hdown, p.hq + row * (F / 2) + (f0 + 32 * c) / 2)
+            << (c * 8 * (32 / f4::block_of(FMT)));
+    }
+    uint8_t* sf = p.hsf + (row >> 7) * p.hka * (int64_t)f4::kAtomBytes +
+                  f4::sf_byte((int)(row & 127), f0 / f4::block_of(FMT));
+    if (FMT == MOE_FP4_NV) *reinterpret_cast<uint32_t*>(sf) = hs;
+    else *reinterpret_cast<uint16_t*>(sf) = (uint16_t)hs;
+    if (p.ckpt) {
+      uint8_t* cs = p.ckpt_sf + row * (2 * F / 32) + f0 / 32;
+      *reinterpret_cast<uint16_t*>(cs) = (uint16_t)gs;
+      *reinterpret_cast<uint16_t*>(cs + F / 32) = (uint16_t)us;
+    }
+    return;
+  }
+  const int c0 = nt * kF4BN + 128 * half;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int col = c0 + 32 * c;
+    if (col >= p.N) {
+    } else if (rv >= 32) {
+      // a full 32 x 32 box by TMA, which also clips the columns past N
+      if (lane == 0) ptx::tma_store_wait_read();       // the slot's previous box has been read
+      __syncwarp();
+      stage_row(stage, 0, lane, o[c]);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::tma_store_2d(tmC, stage_u32, col, row0);
+        ptx::tma_store_commit();
+      }
+    } else if (lane < rv) {
+      __nv_bfloat16* dst = p.out + (int64_t)(row0 + lane) * p.N + col;
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (col + 8 * v < p.N) stg_v4(dst + 8 * v, o[c][v]);
+    }
+  }
+}
+
+template <int FMT, int EPI>
+__global__ void __launch_bounds__(kF4Threads, 1)
+grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
+                        const __grid_constant__ CUtensorMap tmA32,
+                        const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmC, const Fp4Params p) {
+  using C = F4Cfg<FMT>;
+  constexpr bool NV = FMT == MOE_FP4_NV;
+  constexpr int kStages = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* sbase = smem_raw + (base - raw);
+  const uint32_t sf_u = base + C::SF_OFF;
+  const uint32_t ctrl_u = base + C::CTRL_OFF;
+  uint8_t* ctrl = sbase + C::CTRL_OFF;
+  uint8_t* epi = sbase + C::EPI_OFF;
+  const uint32_t epi_u = base + C::EPI_OFF;
+  const uint32_t bar_full = ctrl_u;                       // [kStages]
+  const uint32_t bar_empty = ctrl_u + 32;                 // [kStages]
+  const uint32_t bar_tfull = ctrl_u + 64;
+  const uint32_t bar_tempty = bar_tfull + 8;
+  const uint32_t bar_drain = bar_tfull + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 192);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 196);
+  int* s_most = reinterpret_cast<int*>(ctrl + 200);
+  int* prefix = reinterpret_cast<int*>(ctrl + 256);
+  int* mtiles = reinterpret_cast<int*>(ctrl + 1344);
+  int* s_off = reinterpret_cast<int*>(ctrl + 2432);
+  int* s_cnt = reinterpret_cast<int*>(ctrl + 3520);
+  int* tmp = reinterpret_cast<int*>(ctrl + 4608);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.G;
+  const int F = p.N / 2;
+  const int NT = EPI == kF4Swiglu ? F / (kF4BN / 2) : (p.N + kF4BN - 1) / kF4BN;
+  const int nk_all = (p.K + f4::kStep - 1) / f4::kStep;
+  if (tid == 0) {
+    *abort_flag = 0;
+    *s_most = 0;
+  }
+  __syncthreads();
+  for (int g = tid; g < G; g += kF4Threads) {
+    int64_t c = p.counts ? p.counts[g] : p.rows, o = p.counts ? p.offsets[g] : 0;
+    // rows outside the tensor, or off the 128-row grid of the scale atoms: the
+    // group is left out and reported
+    if (c < 0 || o < 0 || o % 128 || o + c > p.rows) {
+      record_status(p.status, MOE_ERR_DEVICE_CHECK);
+      c = o = 0;
+    }
+    s_cnt[g] = (int)c;
+    s_off[g] = (int)o;
+    mtiles[g] = (int)((c + BM - 1) / BM);
+    prefix[g] = mtiles[g] * NT;
+    atomicMax(s_most, (int)c);
+  }
+  __syncthreads();
+  const int tiles = block_exclusive_scan(prefix, G, tmp);
+  if (tid == 0) prefix[G] = tiles;
+  const int slot_rows = min(BM, (*s_most + 31) / 32 * 32);
+  const int split = choose_split(tiles, nk_all, gridDim.x, slot_rows, p.part_floats, p.arrived_n);
+  const int total = tiles * split;
+  __syncthreads();
+  if ((int)blockIdx.x >= total) return;
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(bar_full + 8 * s, 1);
+      ptx::mbar_init(bar_empty + 8 * s, 1);
+    }
+    ptx::mbar_init(bar_tfull, 1);
+    ptx::mbar_init(bar_tempty, kF4EpiWarps);
+    ptx::mbar_init(bar_drain, 1);
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kF4TmemCols);
+    ptx::tmem_relinquish();
+  }
+  if (tid == 0) {
+    ptx::tma_prefetch_desc(&tmA);
+    ptx::tma_prefetch_desc(&tmA32);
+    ptx::tma_prefetch_desc(&tmB);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      uint32_t issued_mask = 0, issued_phase = 0;
+      bool ok = true;
+      const int64_t nslabs = f4::slabs(p.N);
+      for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+        const int tile = item / split, part = item - tile * split;
+        const Tile t = decode(tile, prefix, mtiles, s_cnt, G, 0, p.K, NT, 0);
+        const int kb0 = (int)((int64_t)nk_all * part / split);
+        const int kb1 = (int)((int64_t)nk_all * (part + 1) / split);
+        const int row0 = s_off[t.g] + t.mt * BM;
+        const int valid = min(BM, s_cnt[t.g] - t.mt * BM);
+        const int boxes = (valid + 31) / 32;             // 4: one 128-row box
+        int b0, b1;
+        if (EPI == kF4Swiglu) {
+          b0 = t.nt * (kF4BN / 2);                       // gate rows b0.., up rows F + b0..
+          b1 = F + b0;
+        } else {
+          b0 = t.nt * kF4BN;
+          b1 = b0 + 128;
+        }
+        const int64_t nb0 = b0 / 128, nb1 = min((int64_t)(b1 / 128), nslabs - 1);
+        const int64_t slab_bytes = (int64_t)p.ka * f4::kAtomBytes;
+        const uint8_t* sfa = p.sfa + (int64_t)(row0 / 128) * slab_bytes;
+        const uint8_t* sfb0 = p.sfb + (t.g * nslabs + nb0) * slab_bytes;
+        const uint8_t* sfb1 = p.sfb + (t.g * nslabs + nb1) * slab_bytes;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!ptx::mbar_wait(bar_empty + 8 * stage, phase ^ 1u, kWaitBudget, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = bar_full + 8 * stage;
+          ptx::mbar_arrive_expect_tx(fb, boxes * 4096 + kF4BBytes + C::SF_STAGE);
+          const uint32_t sA = base + stage * C::STAGE;
+          const uint32_t sB = sA + kF4ABytes;
+          const int k0 = kb * kF4RowBytes;
+          const int brow = t.g * p.N;
+          ptx::tma_load_2d(sB, &tmB, fb, k0, brow + b0);
+          ptx::tma_load_2d(sB + 16384, &tmB, fb, k0, brow + b1);
+          if (boxes == 4) {
+            ptx::tma_load_2d(sA, &tmA, fb, k0, row0);
+          } else {
+            for (int i = 0; i < boxes; ++i)
+              ptx::tma_load_2d(sA + 4096 * i, &tmA32, fb, k0, row0 + 32 * i);
+          }
+          const uint32_t sfs = sf_u + stage * C::SF_STAGE;
+          const int64_t ao = (int64_t)kb * C::SF_A;
+          ptx::bulk_load(sfs, sfa + ao, C::SF_A, fb);
+          ptx::bulk_load(sfs + C::SF_A, sfb0 + ao, C::SF_A, fb);
+          ptx::bulk_load(sfs + 2 * C::SF_A, sfb1 + ao, C::SF_A, fb);
+          issued_mask |= 1u << stage;
+          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        record_status(p.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // every load issued must land before the CTA may exit
+      for (int s = 0; s < kStages; ++s)
+        if (issued_mask & (1u << s))
+          ptx::mbar_wait(bar_full + 8 * s, (issued_phase >> s) & 1u, kWaitBudget, nullptr);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t IDESC = ptx::idesc_fp4(BM, kF4BN, NV ? 0 : 1);
+      uint32_t stage = 0, phase = 0, acc_phase = 0, slot = 0;
+      bool ok = true, issued = false;
+      for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+        const int part = item % split;
+        const int kb0 = (int)((int64_t)nk_all * part / split);
+        const int kb1 = (int)((int64_t)nk_all * (part + 1) / split);
+        if (!ptx::mbar_wait(bar_tempty, acc_phase ^ 1u, kWaitBudget, abort_flag)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget, abort_flag)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t sfs = sf_u + stage * C::SF_STAGE;
+          // the copies and the MMAs of this thread run in issue order, so two
+          // slots are enough: one is rewritten after the MMAs that read it
+          const uint32_t sfa_t = tmem_base + kF4SfCol + C::SLOT_COLS * slot;
+          const uint32_t sfb_t = sfa_t + 4 * C::ATOMS;
+          slot ^= 1u;
+#pragma unroll
+          for (int a = 0; a < C::ATOMS; ++a) {
+            ptx::tmem_cp_32x128b_warpx4(sfa_t + 4 * a, ptx::smem_desc_sf(sfs + 512 * a));
+            ptx::tmem_cp_32x128b_warpx4(sfb_t + 8 * a,
+                                        ptx::smem_desc_sf(sfs + C::SF_A + 512 * a));
+            ptx::tmem_cp_32x128b_warpx4(sfb_t + 8 * a + 4,
+                                        ptx::smem_desc_sf(sfs + 2 * C::SF_A + 512 * a));
+          }
+          const uint32_t sA = base + stage * C::STAGE;
+          const uint32_t sB = sA + kF4ABytes;
+          // 64-wide slices of the k-block that K reaches into
+          const int slices = min(4, (p.K - kb * f4::kStep + 63) / 64);
+          for (int kk = 0; kk < slices; ++kk) {
+            const uint64_t ad = ptx::smem_desc_sw128(sA + kk * 32, 16, 1024);
+            const uint64_t bd = ptx::smem_desc_sw128(sB + kk * 32, 16, 1024);
+            const int a = NV ? kk : kk >> 1;
+            const uint32_t id = NV ? IDESC : ptx::idesc_with_sf_id(IDESC, (uint32_t)(kk & 1) * 2);
+            ptx::mma_fp4<NV>(tmem_base, ad, bd, id, sfa_t + 4 * a, sfb_t + 8 * a,
+                             (kb > kb0 || kk) ? 1u : 0u);
+          }
+          issued = true;
+          ptx::mma_commit(bar_empty + 8 * stage);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        ptx::mma_commit(bar_tfull);
+        acc_phase ^= 1u;
+      }
+      if (!ok) {
+        record_status(p.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // wait for every MMA issued by this thread before tensor memory is freed
+      if (issued) {
+        ptx::mma_commit(bar_drain);
+        ptx::mbar_wait(bar_drain, 0, kWaitBudget, nullptr);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;                       // tensor-memory lane quarter
+    const int half = (warp - 2) >> 2;             // which 128 accumulator columns
+    uint8_t* stage = epi + (warp - 2) * kBoxBytes;
+    const uint32_t stage_u32 = epi_u + (warp - 2) * kBoxBytes;
+    const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16);
+    uint32_t acc_phase = 0;
+    for (int item = blockIdx.x; item < total; item += gridDim.x) {
+      const int tile = item / split, part = item - tile * split;
+      const Tile t = decode(tile, prefix, mtiles, s_cnt, G, 0, p.K, NT, 0);
+      const int row0 = s_off[t.g] + t.mt * BM + q * 32;
+      const int rv = s_cnt[t.g] - t.mt * BM - q * 32;    // rows of this warp that hold data
+      const float alpha = (p.alpha ? p.alpha[t.g] : 1.f) * p.unit;
+      const bool ok = __all_sync(
+          0xffffffffu, ptx::mbar_wait(bar_tfull, acc_phase, kWaitBudget, abort_flag));
+      if (!ok) {
+        if (lane == 0) {
+          record_status(p.status, MOE_ERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+        break;
+      }
+      ptx::tc_fence_after();
+      uint4 o[4][4];
+      // a cut tile: this warp's slice of the part, [128 columns][slot_rows] fp32
+      const int64_t slice = (int64_t)slot_rows * 128;
+      float* parts = p.part + ((int64_t)tile * split * 2 + half) * slice + q * 32 + lane;
+      if (rv > 0) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          ptx::tmem_ld32(tq + slice_col<EPI>(half, c), r);
+          ptx::tmem_ld_wait();
+          if (split == 1) {
+            scale_pack(r, alpha, o[c]);
+          } else if (lane < rv) {
+            float* dst = parts + 2 * slice * part + 32 * c * slot_rows;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) __stcg(dst + i * slot_rows, __uint_as_float(r[i]));
+          }
+          __syncwarp();
+        }
+      }
+      // the accumulator is free for the next item's MMAs
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar_tempty);
+      acc_phase ^= 1u;
+      if (rv <= 0) continue;
+      if (split > 1) {
+        __threadfence();
+        __syncwarp();
+        int last = 0;
+        if (lane == 0) {
+          int32_t* a = p.arrived + tile * kF4EpiWarps + (warp - 2);
+          last = atomicAdd(a, 1) == split - 1;
+          if (last) *a = 0;                       // as the next launch expects it
+        }
+        last = __shfl_sync(0xffffffffu, last, 0);
+        if (!last) continue;
+        __threadfence();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = 0u;
+          if (lane < rv) {
+            const float* src = parts + 32 * c * slot_rows;
+            for (int s = 0; s < split; ++s, src += 2 * slice) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                r[i] = __float_as_uint(__uint_as_float(r[i]) + __ldcg(src + i * slot_rows));
+            }
+          }
+          scale_pack(r, alpha, o[c]);
+        }
+      }
+      f4_epilogue<FMT, EPI>(p, &tmC, stage, stage_u32, t.nt, row0, rv, half, lane, o);
+    }
+    if (lane == 0) ptx::tma_store_wait_all();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, kF4TmemCols);
+  }
+}
+
+template <int FMT, int EPI>
+static cudaError_t run_fp4(const CUtensorMap& a, const CUtensorMap& a32, const CUtensorMap& b,
+                           const CUtensorMap& c, const Fp4Params& p, cudaStream_t s) {
+  auto kern = grouped_gemm_fp4_kernel<FMT, EPI>;
+  constexpr int smem = F4Cfg<FMT>::SMEM;
+  static bool attr_set = false;
+  if (!attr_set) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    attr_set = true;
+  }
+  kern<<<num_sms(), kF4Threads, smem, s>>>(a, a32, b, c, p);
+  return cudaGetLastError();
+}
+
+// 4-bit operand: [rows, K / 2] bytes, box of 128 bytes x box_rows.
+static bool make_map_fp4(CUtensorMap* m, const void* ptr, int64_t K, int64_t rows,
+                         uint32_t box_rows) {
+  return make_map_u8(m, ptr, (uint64_t)K / 2, (uint64_t)rows, box_rows);
+}
+
+static Fp4Params fp4_params(const Fp4Problem& q, const Fp4Split& sp, int32_t* status) {
+  Fp4Params p{};
+  p.G = q.G;
+  p.N = (int)q.N;
+  p.K = (int)q.K;
+  p.rows = q.rows;
+  p.counts = q.counts;
+  p.offsets = q.offsets;
+  p.alpha = q.alpha;
+  p.unit = ldexpf(1.f, q.unit_log2);
+  p.sfa = q.sfa;
+  p.sfb = q.sfb;
+  p.ka = (int)f4::atoms_k(q.fmt, q.K);
+  p.part = sp.part;
+  p.part_floats = sp.part_floats;
+  p.arrived = sp.arrived;
+  p.arrived_n = sp.arrived_n;
+  p.status = status;
+  return p;
+}
+
+}  // namespace gg
+
+using namespace gg;
+
+cudaError_t launch_fp4_gemm(const Fp4Problem& q, void* out, const Fp4Split& sp, int32_t* status,
+                            cudaStream_t s) {
+  if (q.rows == 0 || q.N == 0) return cudaSuccess;
+  CUtensorMap a, a32, b, c;
+  if (!make_map_fp4(&a, q.a, q.K, q.rows, 128) || !make_map_fp4(&a32, q.a, q.K, q.rows, 32) ||
+      !make_map_fp4(&b, q.b, q.K, (int64_t)q.G * q.N, 128) ||
+      !make_out_map(&c, out, (uint64_t)q.N, (uint64_t)q.rows))
+    return cudaErrorInvalidValue;
+  Fp4Params p = fp4_params(q, sp, status);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  return q.fmt == MOE_FP4_NV ? run_fp4<MOE_FP4_NV, kF4Store>(a, a32, b, c, p, s)
+                             : run_fp4<MOE_FP4_MX, kF4Store>(a, a32, b, c, p, s);
+}
+
+cudaError_t launch_fp4_swiglu(const Fp4Problem& q, uint8_t* hq, uint8_t* hsf, int h_scale_log2,
+                              uint8_t* ckpt, uint8_t* ckpt_sf, const Fp4Split& sp, int32_t* status,
+                              cudaStream_t s) {
+  if (q.rows == 0) return cudaSuccess;
+  CUtensorMap a, a32, b;
+  if (!make_map_fp4(&a, q.a, q.K, q.rows, 128) || !make_map_fp4(&a32, q.a, q.K, q.rows, 32) ||
+      !make_map_fp4(&b, q.b, q.K, (int64_t)q.G * q.N, 128))
+    return cudaErrorInvalidValue;
+  Fp4Params p = fp4_params(q, sp, status);
+  p.hq = hq;
+  p.hsf = hsf;
+  p.hka = (int)f4::atoms_k(q.fmt, q.N / 2);
+  p.hdown = ldexpf(1.f, -h_scale_log2);
+  p.ckpt = ckpt;
+  p.ckpt_sf = ckpt_sf;
+  return q.fmt == MOE_FP4_NV ? run_fp4<MOE_FP4_NV, kF4Swiglu>(a, a32, b, b, p, s)
+                             : run_fp4<MOE_FP4_MX, kF4Swiglu>(a, a32, b, b, p, s);
+}
+
+}  // namespace moe

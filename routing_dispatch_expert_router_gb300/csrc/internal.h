@@ -166,6 +166,58 @@ struct Fp8Scratch {
 };
 Fp8Scratch fp8_scratch(const moe_config& c, void* scratch);
 
+// The 4-bit experts (fp4_layout.cuh, grouped_gemm_fp4.cu).
+// bf16 rows to codes and scale atoms: groups x rows dense, or (counts != null,
+// groups = 1) the rows [offsets[i], offsets[i] + counts[i]) of `segments`
+// segments that start at multiples of 128. values (optional): what they stand for.
+cudaError_t launch_fp4_quantize(int fmt, const void* x, int64_t ldx, int64_t groups, int64_t rows,
+                                int64_t K, int scale_log2, const int32_t* counts,
+                                const int32_t* offsets, int segments, uint8_t* codes,
+                                uint8_t* scales, void* values, int32_t* status, cudaStream_t s);
+cudaError_t launch_fp4_dequantize(int fmt, const uint8_t* codes, const uint8_t* scales,
+                                  int64_t groups, int64_t rows, int64_t K, int scale_log2,
+                                  void* out, int64_t ldo, cudaStream_t s);
+// One grouped product: A [rows, K] by B [G, N, K], codes and scale atoms.
+struct Fp4Problem {
+  int fmt;
+  int G;
+  int64_t rows, N, K;
+  const uint8_t* a;
+  const uint8_t* sfa;
+  const uint8_t* b;
+  const uint8_t* sfb;
+  const int32_t* counts;      // null: one group of all rows
+  const int32_t* offsets;
+  const float* alpha;         // [G] or null
+  int unit_log2;              // the operands' tensor scales, as a power of two
+};
+// Scratch of the products that cut K: fp32 parts and arrival counters (zero).
+struct Fp4Split {
+  float* part;
+  int64_t part_floats;
+  int32_t* arrived;
+  int arrived_n;
+};
+cudaError_t launch_fp4_gemm(const Fp4Problem& q, void* out, const Fp4Split& sp, int32_t* status,
+                            cudaStream_t s);
+// The gate-up product with SwiGLU: h in 4 bits (hq, hsf), and the checkpoint of
+// gate and up (E4M3 codes and UE8M0 bytes) where ckpt is given.
+cudaError_t launch_fp4_swiglu(const Fp4Problem& q, uint8_t* hq, uint8_t* hsf, int h_scale_log2,
+                              uint8_t* ckpt, uint8_t* ckpt_sf, const Fp4Split& sp, int32_t* status,
+                              cudaStream_t s);
+
+// The 8-bit checkpoint back as bf16 (rows past a segment's counts, up to its
+// 128-row block, become zero).
+cudaError_t launch_fp4_ckpt_expand(const uint8_t* ckpt, const uint8_t* ckpt_sf, int64_t rows,
+                                   int64_t cols, const int32_t* counts, const int32_t* offsets,
+                                   int segments, void* out, int32_t* status, cudaStream_t s);
+cudaError_t launch_ffn_fc1_dgrad_alpha(const moe_config& c, const void* dGU, const int32_t* counts,
+                                       const int32_t* offsets, const void* W13,
+                                       const float* alpha_a, const float* alpha_b, int unit_log2,
+                                       const int32_t* token_of, const float* dlogits,
+                                       const float* W_r, void* dX_perm, int32_t* status,
+                                       cudaStream_t s);
+
 // Router logits for E % 128 == 0 on the tensor cores (W3 = W_r split in three bf16 parts).
 cudaError_t launch_router_logits_tc(const moe_config& c, const void* x, const void* W3,
                                     float* logits, int32_t* status, cudaStream_t s);

@@ -225,6 +225,45 @@ __device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t adesc, uint64
          "r"(sfb_tmem) : "memory");
 }
 
+// ------------------------------------------------- FP4 block-scaled tcgen05 MMA
+// Instruction descriptor of kind::mxf4 / kind::mxf4nvf4 (E2M1 A and B, both
+// K-major, fp32 accumulation), from the same table's 4-bit kinds:
+//   [4,6)   scale-factor id of B (0 or 2: which byte pair, scale_vec::2X)
+//   [7,10)  A format (E2M1 = 1)          [10,12) B format (E2M1 = 1)
+//   [17,23) N >> 3                       [23]    scale type (UE4M3 = 0, UE8M0 = 1)
+//   [27,29) M >> 7                       [29,31) scale-factor id of A
+__host__ __device__ constexpr uint32_t idesc_fp4(int M, int N, int ue8m0) {
+  return (1u << 7) | (1u << 10)
+       | ((uint32_t)(N >> 3) << 17)
+       | ((uint32_t)ue8m0 << 23)
+       | ((uint32_t)(M >> 7) << 27);
+}
+
+// D[tmem] (+)= (A * scale_A) * (B * scale_B)^T over a 64-deep K slice of E2M1
+// operands. NV: an E4M3 scale per 16 elements (scale_vec::4X); else a UE8M0
+// scale per 32 (scale_vec::2X).
+template <bool NV>
+__device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                        uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                        uint32_t accumulate) {
+  if (NV)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X "
+        "[%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+        :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem),
+           "r"(sfb_tmem) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X "
+        "[%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+        :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem),
+           "r"(sfb_tmem) : "memory");
+}
+
 // Shared-memory descriptor of one scale-factor atom for tcgen05.cp: 32 rows of
 // 16 bytes, no swizzle, 8-row core matrices 128 bytes apart (SBO); the atom is
 // one core matrix wide along K, so LBO is unused (0).
