@@ -11,6 +11,7 @@
 // without staging. A block's maximum and its codes need no other lane.
 #include "fp4_layout.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
@@ -60,6 +61,7 @@ fp4_quantize_kernel(const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ c
                     float down, const Rows p) {
   constexpr int BLK = f4::block_of(FMT);
   constexpr int V = BLK / 8;                     // 16-byte vectors of a block
+  ptx::grid_launch_dependents();                 // a product may start fetching its weights
   const int64_t sl = blockIdx.x >> 2;
   int64_t row0;
   const int n = slab_rows(p, sl, row0);

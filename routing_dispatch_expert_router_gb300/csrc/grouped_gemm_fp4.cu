@@ -21,11 +21,12 @@
 //
 // A decode step has a few rows per expert: then the weights' bytes are all the
 // work, and what counts is that every SM streams its share of them. Only the
-// rows a tile has are fetched (boxes of 32), and when the tiles do not fill the
-// SMs their K range is cut into `split` parts (chosen on the device from the
-// counts): every part's fp32 accumulator goes to scratch, and the warp that
-// arrives last at a slice of a tile adds the parts in order, so the result does
-// not depend on the order of arrival. No part waits for another.
+// rows a tile has are fetched (boxes of 32), and where whole tiles would leave
+// SMs idle (few tiles, or a last wave of few) the k-blocks of all tiles are laid
+// end to end and every CTA takes the same length of them. A tile cut that way
+// leaves its parts' fp32 sums in scratch, and the warp that arrives last at a
+// slice of the tile adds them in order, so the result does not depend on the
+// order of arrival. No part waits for another.
 #include "fp4_layout.cuh"
 #include "fp8_layout.cuh"
 #include "gemm_common.cuh"
@@ -39,6 +40,7 @@ constexpr int kF4RowBytes = f4::kStep / 2;             // codes of a k-block's r
 constexpr int kF4ABytes = BM * kF4RowBytes;            // 16 KB
 constexpr int kF4BBytes = kF4BN * kF4RowBytes;         // 32 KB
 constexpr int kF4EpiWarps = 8;
+constexpr int kF4Ahead = 12;                           // k-blocks prefetched by an early start
 constexpr uint32_t kF4TmemCols = 512;
 constexpr uint32_t kF4SfCol = kF4BN;                   // first scale-factor column
 
@@ -68,6 +70,7 @@ struct Fp4Params {
   int64_t part_floats;
   int32_t* arrived;
   int arrived_n;
+  bool early;                  // started before the kernel before it is done
   int32_t* status;
 };
 
@@ -89,25 +92,51 @@ struct F4Cfg {
   static_assert(kF4SfCol + SLOTS * SLOT_COLS <= kF4TmemCols, "FP4 tensor-memory columns");
 };
 
-// How many parts a tile's nk k-blocks are cut into: the number that makes the
-// busiest SM's k-blocks fewest, a tile's start and end counting as two.
-// More than one part only
-// where they fit scratch.
-__device__ __forceinline__ int choose_split(int tiles, int nk, int grid, int slot_rows,
-                                            int64_t part_floats, int counters) {
-  int best = 1;
-  long long cost = (long long)((tiles + grid - 1) / grid) * (nk + 2);
-  const int most = min(16, nk / 2);
-  for (int s = 2; s <= most; ++s) {
-    if ((int64_t)tiles * s * slot_rows * kF4BN > part_floats || tiles * kF4EpiWarps > counters)
-      break;
-    const long long c = (long long)((tiles * s + grid - 1) / grid) * ((nk + s - 1) / s + 2);
-    if (c < cost) {
-      cost = c;
-      best = s;
-    }
+// The work of one CTA: whole tiles blockIdx.x, + gridDim.x, .. (even = 0), or its
+// share of the k-blocks of all tiles laid end to end (even = 1): the positions
+// [pos, end), tile p / nk, k-block p % nk.
+struct Work {
+  int nk, tiles, even, ctas;      // ctas: how many share evenly, two k-blocks each at least
+  int64_t pos, end;
+  int tile, kb0, kb1;             // the current piece
+
+  __device__ __forceinline__ Work(int tiles_, int nk_, int even_)
+      : nk(nk_), tiles(tiles_), even(even_) {
+    const int64_t all = (int64_t)tiles * nk;
+    ctas = (int)min((int64_t)gridDim.x, max((int64_t)1, all / 2));
+    const int64_t b = blockIdx.x;
+    pos = !even ? b * nk : b < ctas ? b * all / ctas : all;
+    end = even && b < ctas ? (b + 1) * all / ctas : all;
   }
-  return best;
+  __device__ __forceinline__ bool next() {
+    if (pos >= end) return false;
+    tile = (int)(pos / nk);
+    kb0 = (int)(pos - (int64_t)tile * nk);
+    kb1 = (int)min((int64_t)nk, end - (int64_t)tile * nk);
+    pos += even ? kb1 - kb0 : (int64_t)gridDim.x * nk;
+    return true;
+  }
+  // The CTAs that hold parts of the current tile: the one that has position p is
+  // the largest b with floor(b all / ctas) <= p.
+  __device__ __forceinline__ int owner(int64_t p) const {
+    return (int)(((p + 1) * ctas - 1) / ((int64_t)tiles * nk));
+  }
+  __device__ __forceinline__ int first() const { return owner((int64_t)tile * nk); }
+  __device__ __forceinline__ int last() const { return owner((int64_t)tile * nk + nk - 1); }
+  __device__ __forceinline__ bool whole() const { return kb1 - kb0 == nk; }
+};
+
+// Whether to share the k-blocks evenly: where whole tiles keep the busiest SM
+// longer than an even share and the joining of parts, which costs about as much
+// as 2 k-blocks and one more per 16 rows, and where the parts (two per
+// CTA at most) fit scratch.
+__device__ __forceinline__ int share_evenly(int tiles, int nk, int grid, int slot_rows,
+                                            int64_t part_floats, int counters) {
+  if ((int64_t)2 * grid * slot_rows * kF4BN > part_floats || tiles * kF4EpiWarps > counters)
+    return 0;
+  const int whole = (tiles + grid - 1) / grid * nk;
+  const int share = (int)(((int64_t)tiles * nk + grid - 1) / grid);
+  return whole > share + 2 + slot_rows / 16;
 }
 
 // h of 32 columns (bf16 pairs) in 4 bits: codes to `dst` (16 bytes); returns the
@@ -238,6 +267,58 @@ __device__ __forceinline__ void f4_epilogue(const Fp4Params& p, const CUtensorMa
   }
 }
 
+// Four columns of one row of a joined tile per lane (v, times alpha already):
+// columns 4 lane .. of the warp's 128 (the slices of slice_col end to end, so in
+// the swiglu form lanes 0-15 hold gate and lanes 16-31 the matching up columns).
+template <int FMT, int EPI>
+__device__ __forceinline__ void f4_epilogue_row(const Fp4Params& p, int nt, int64_t row, int half,
+                                                int lane, const float4& v) {
+  uint2 b = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  if (EPI == kF4Store) {
+    const int col = nt * kF4BN + 128 * half + 4 * lane;
+    if (col < p.N) *reinterpret_cast<uint2*>(p.out + row * p.N + col) = b;
+    return;
+  }
+  const int F = p.N / 2;
+  const int f = nt * (kF4BN / 2) + 64 * half + 4 * (lane & 15);
+  if (p.ckpt) {
+    // 32 values: the 8 lanes 8i .. 8i + 7
+    uint32_t m = max(max(b.x & 0x7FFFu, b.x >> 16 & 0x7FFFu), max(b.y & 0x7FFFu, b.y >> 16 & 0x7FFFu));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const bool finite = m < 0x7F80u;
+    const uint32_t code = finite ? ue8m0_code(__uint_as_float(m << 16)) : 255u;
+    const float inv = finite ? ue8m0_inv(code) : 0.f;
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(lo) : "f"(bf16_hi(b.x) * inv), "f"(bf16_lo(b.x) * inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(hi) : "f"(bf16_hi(b.y) * inv), "f"(bf16_lo(b.y) * inv));
+    const int c = (lane >> 4) * F + f;
+    *reinterpret_cast<uint32_t*>(p.ckpt + row * 2 * F + c) = lo | (uint32_t)hi << 16;
+    if ((lane & 7) == 0) p.ckpt_sf[row * (2 * F / 32) + c / 32] = (uint8_t)code;
+  }
+  const uint32_t ux = __shfl_down_sync(0xffffffffu, b.x, 16);
+  const uint32_t uy = __shfl_down_sync(0xffffffffu, b.y, 16);
+  const uint32_t hx = pack_bf16x2(silu_f(bf16_lo(b.x)) * bf16_lo(ux), silu_f(bf16_hi(b.x)) * bf16_hi(ux));
+  const uint32_t hy = pack_bf16x2(silu_f(bf16_lo(b.y)) * bf16_lo(uy), silu_f(bf16_hi(b.y)) * bf16_hi(uy));
+  constexpr int BLK = f4::block_of(FMT);
+  uint32_t m = max(max(hx & 0x7FFFu, hx >> 16 & 0x7FFFu), max(hy & 0x7FFFu, hy >> 16 & 0x7FFFu));
+#pragma unroll
+  for (int o = 1; o < BLK / 4; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const Fp4Scale s = fp4_scale<FMT>(__uint_as_float(m << 16), m < 0x7F80u, p.hdown);
+  const float q[8] = {fp4_quotient<FMT>(bf16_lo(hx), s.inv), fp4_quotient<FMT>(bf16_hi(hx), s.inv),
+                      fp4_quotient<FMT>(bf16_lo(hy), s.inv), fp4_quotient<FMT>(bf16_hi(hy), s.inv),
+                      0.f, 0.f, 0.f, 0.f};
+  if (lane < 16) {
+    *reinterpret_cast<uint16_t*>(p.hq + row * (F / 2) + f / 2) =
+        s.inv > 0.f ? (uint16_t)e2m1x8(q) : (uint16_t)0;
+    if (lane % (BLK / 4) == 0)
+      p.hsf[(row >> 7) * p.hka * (int64_t)f4::kAtomBytes +
+            f4::sf_byte((int)(row & 127), f / BLK)] = (uint8_t)s.byte;
+  }
+}
+
 template <int FMT, int EPI>
 __global__ void __launch_bounds__(kF4Threads, 1)
 grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -298,10 +379,13 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
   const int tiles = block_exclusive_scan(prefix, G, tmp);
   if (tid == 0) prefix[G] = tiles;
   const int slot_rows = min(BM, (*s_most + 31) / 32 * 32);
-  const int split = choose_split(tiles, nk_all, gridDim.x, slot_rows, p.part_floats, p.arrived_n);
-  const int total = tiles * split;
+  const int even = share_evenly(tiles, nk_all, gridDim.x, slot_rows, p.part_floats, p.arrived_n);
   __syncthreads();
-  if ((int)blockIdx.x >= total) return;
+  Work w(tiles, nk_all, even);
+  if (w.pos >= w.end) {
+    ptx::grid_dependency_wait();                 // this kernel ends after the one before it
+    return;
+  }
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -334,11 +418,25 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
       uint32_t issued_mask = 0, issued_phase = 0;
       bool ok = true;
       const int64_t nslabs = f4::slabs(p.N);
-      for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-        const int tile = item / split, part = item - tile * split;
-        const Tile t = decode(tile, prefix, mtiles, s_cnt, G, 0, p.K, NT, 0);
-        const int kb0 = (int)((int64_t)nk_all * part / split);
-        const int kb1 = (int)((int64_t)nk_all * (part + 1) / split);
+      // weights may be fetched before the kernel before this one is done; A's
+      // rows (what that kernel wrote) only after it
+      bool waited = !p.early;
+      if (p.early) {
+        // into L2 meanwhile: the weights of this CTA's first k-blocks
+        Work f = w;
+        int left = kF4Ahead;
+        while (left > 0 && f.next()) {
+          const Tile t = decode(f.tile, prefix, mtiles, s_cnt, G, 0, p.K, NT, 0);
+          const int b0 = t.nt * (EPI == kF4Swiglu ? kF4BN / 2 : kF4BN);
+          const int b1 = EPI == kF4Swiglu ? F + b0 : b0 + 128;
+          for (int kb = f.kb0; kb < f.kb1 && left > 0; ++kb, --left) {
+            ptx::tma_prefetch_2d(&tmB, kb * kF4RowBytes, t.g * p.N + b0);
+            ptx::tma_prefetch_2d(&tmB, kb * kF4RowBytes, t.g * p.N + b1);
+          }
+        }
+      }
+      while (ok && w.next()) {
+        const Tile t = decode(w.tile, prefix, mtiles, s_cnt, G, 0, p.K, NT, 0);
         const int row0 = s_off[t.g] + t.mt * BM;
         const int valid = min(BM, s_cnt[t.g] - t.mt * BM);
         const int boxes = (valid + 31) / 32;             // 4: one 128-row box
@@ -355,7 +453,7 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
         const uint8_t* sfa = p.sfa + (int64_t)(row0 / 128) * slab_bytes;
         const uint8_t* sfb0 = p.sfb + (t.g * nslabs + nb0) * slab_bytes;
         const uint8_t* sfb1 = p.sfb + (t.g * nslabs + nb1) * slab_bytes;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (!ptx::mbar_wait(bar_empty + 8 * stage, phase ^ 1u, kWaitBudget, abort_flag)) {
             ok = false;
             break;
@@ -368,17 +466,21 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
           const int brow = t.g * p.N;
           ptx::tma_load_2d(sB, &tmB, fb, k0, brow + b0);
           ptx::tma_load_2d(sB + 16384, &tmB, fb, k0, brow + b1);
+          const uint32_t sfs = sf_u + stage * C::SF_STAGE;
+          const int64_t ao = (int64_t)kb * C::SF_A;
+          ptx::bulk_load(sfs + C::SF_A, sfb0 + ao, C::SF_A, fb);
+          ptx::bulk_load(sfs + 2 * C::SF_A, sfb1 + ao, C::SF_A, fb);
+          if (!waited) {
+            ptx::grid_dependency_wait();
+            waited = true;
+          }
+          ptx::bulk_load(sfs, sfa + ao, C::SF_A, fb);
           if (boxes == 4) {
             ptx::tma_load_2d(sA, &tmA, fb, k0, row0);
           } else {
             for (int i = 0; i < boxes; ++i)
               ptx::tma_load_2d(sA + 4096 * i, &tmA32, fb, k0, row0 + 32 * i);
           }
-          const uint32_t sfs = sf_u + stage * C::SF_STAGE;
-          const int64_t ao = (int64_t)kb * C::SF_A;
-          ptx::bulk_load(sfs, sfa + ao, C::SF_A, fb);
-          ptx::bulk_load(sfs + C::SF_A, sfb0 + ao, C::SF_A, fb);
-          ptx::bulk_load(sfs + 2 * C::SF_A, sfb1 + ao, C::SF_A, fb);
           issued_mask |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
           if (++stage == kStages) {
@@ -402,16 +504,13 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
       constexpr uint32_t IDESC = ptx::idesc_fp4(BM, kF4BN, NV ? 0 : 1);
       uint32_t stage = 0, phase = 0, acc_phase = 0, slot = 0;
       bool ok = true, issued = false;
-      for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-        const int part = item % split;
-        const int kb0 = (int)((int64_t)nk_all * part / split);
-        const int kb1 = (int)((int64_t)nk_all * (part + 1) / split);
+      while (ok && w.next()) {
         if (!ptx::mbar_wait(bar_tempty, acc_phase ^ 1u, kWaitBudget, abort_flag)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (!ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget, abort_flag)) {
             ok = false;
             break;
@@ -441,7 +540,7 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
             const int a = NV ? kk : kk >> 1;
             const uint32_t id = NV ? IDESC : ptx::idesc_with_sf_id(IDESC, (uint32_t)(kk & 1) * 2);
             ptx::mma_fp4<NV>(tmem_base, ad, bd, id, sfa_t + 4 * a, sfb_t + 8 * a,
-                             (kb > kb0 || kk) ? 1u : 0u);
+                             (kb > w.kb0 || kk) ? 1u : 0u);
           }
           issued = true;
           ptx::mma_commit(bar_empty + 8 * stage);
@@ -472,9 +571,10 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
     const uint32_t stage_u32 = epi_u + (warp - 2) * kBoxBytes;
     const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16);
     uint32_t acc_phase = 0;
-    for (int item = blockIdx.x; item < total; item += gridDim.x) {
-      const int tile = item / split, part = item - tile * split;
-      const Tile t = decode(tile, prefix, mtiles, s_cnt, G, 0, p.K, NT, 0);
+    // nothing is written before the kernel before this one is done
+    ptx::grid_dependency_wait();
+    while (w.next()) {
+      const Tile t = decode(w.tile, prefix, mtiles, s_cnt, G, 0, p.K, NT, 0);
       const int row0 = s_off[t.g] + t.mt * BM + q * 32;
       const int rv = s_cnt[t.g] - t.mt * BM - q * 32;    // rows of this warp that hold data
       const float alpha = (p.alpha ? p.alpha[t.g] : 1.f) * p.unit;
@@ -489,58 +589,71 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
       }
       ptx::tc_fence_after();
       uint4 o[4][4];
-      // a cut tile: this warp's slice of the part, [128 columns][slot_rows] fp32
+      // a cut tile: this warp's slice of a part, [slot_rows][128 columns] fp32;
+      // CTA b's slots are 2b (a tile that began before its share) and 2b + 1
       const int64_t slice = (int64_t)slot_rows * 128;
-      float* parts = p.part + ((int64_t)tile * split * 2 + half) * slice + q * 32 + lane;
+      float* parts = p.part + half * slice + (int64_t)q * 32 * 128;
       if (rv > 0) {
+        float* mine = parts + (2 * (int64_t)blockIdx.x + (w.kb0 == 0)) * 2 * slice + lane * 128;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t r[32];
           ptx::tmem_ld32(tq + slice_col<EPI>(half, c), r);
           ptx::tmem_ld_wait();
-          if (split == 1) {
+          if (w.whole()) {
             scale_pack(r, alpha, o[c]);
           } else if (lane < rv) {
-            float* dst = parts + 2 * slice * part + 32 * c * slot_rows;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) __stcg(dst + i * slot_rows, __uint_as_float(r[i]));
+            for (int i = 0; i < 32; i += 4)
+              __stcg(reinterpret_cast<uint4*>(mine + 32 * c + i),
+                     make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]));
           }
           __syncwarp();
         }
       }
-      // the accumulator is free for the next item's MMAs
+      // the accumulator is free for the next piece's MMAs
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar_tempty);
       acc_phase ^= 1u;
       if (rv <= 0) continue;
-      if (split > 1) {
+      if (!w.whole()) {
         __threadfence();
         __syncwarp();
+        const int b0 = w.first(), b1 = w.last();
         int last = 0;
         if (lane == 0) {
-          int32_t* a = p.arrived + tile * kF4EpiWarps + (warp - 2);
-          last = atomicAdd(a, 1) == split - 1;
+          int32_t* a = p.arrived + w.tile * kF4EpiWarps + (warp - 2);
+          last = atomicAdd(a, 1) == b1 - b0;
           if (last) *a = 0;                       // as the next launch expects it
         }
         last = __shfl_sync(0xffffffffu, last, 0);
         if (!last) continue;
         __threadfence();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) r[i] = 0u;
-          if (lane < rv) {
-            const float* src = parts + 32 * c * slot_rows;
-            for (int s = 0; s < split; ++s, src += 2 * slice) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                r[i] = __float_as_uint(__uint_as_float(r[i]) + __ldcg(src + i * slot_rows));
-            }
+        const int rows = min(rv, 32);
+        // the first part ends at its CTA's share (slot 2 b0 + 1), the others begin theirs
+        const float* src = parts + 4 * lane;
+        const int64_t step = 4 * slice;           // from a CTA's slots to the next one's
+#pragma unroll 2
+        for (int r = 0; r < rows; ++r) {
+          const float* at = src + (4 * (int64_t)b0 + 2) * slice + r * 128;
+          float4 v = __ldcg(reinterpret_cast<const float4*>(at));
+          at += step - 2 * slice;
+#pragma unroll 4
+          for (int b = b0 + 1; b <= b1; ++b, at += step) {
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(at));
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
           }
-          scale_pack(r, alpha, o[c]);
+          v.x *= alpha;
+          v.y *= alpha;
+          v.z *= alpha;
+          v.w *= alpha;
+          f4_epilogue_row<FMT, EPI>(p, t.nt, row0 + r, half, lane, v);
         }
+        continue;
       }
       f4_epilogue<FMT, EPI>(p, &tmC, stage, stage_u32, t.nt, row0, rv, half, lane, o);
     }
@@ -556,7 +669,8 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
 
 template <int FMT, int EPI>
 static cudaError_t run_fp4(const CUtensorMap& a, const CUtensorMap& a32, const CUtensorMap& b,
-                           const CUtensorMap& c, const Fp4Params& p, cudaStream_t s) {
+                           const CUtensorMap& c, const Fp4Params& p, bool early,
+                           cudaStream_t s) {
   auto kern = grouped_gemm_fp4_kernel<FMT, EPI>;
   constexpr int smem = F4Cfg<FMT>::SMEM;
   static bool attr_set = false;
@@ -565,8 +679,17 @@ static cudaError_t run_fp4(const CUtensorMap& a, const CUtensorMap& a32, const C
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
-  kern<<<num_sms(), kF4Threads, smem, s>>>(a, a32, b, c, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(num_sms(), 1, 1);
+  lc.blockDim = dim3(kF4Threads, 1, 1);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = at;
+  lc.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&lc, kern, a, a32, b, c, p);
 }
 
 // 4-bit operand: [rows, K / 2] bytes, box of 128 bytes x box_rows.
@@ -592,6 +715,7 @@ static Fp4Params fp4_params(const Fp4Problem& q, const Fp4Split& sp, int32_t* st
   p.part_floats = sp.part_floats;
   p.arrived = sp.arrived;
   p.arrived_n = sp.arrived_n;
+  p.early = q.early;
   p.status = status;
   return p;
 }
@@ -610,8 +734,8 @@ cudaError_t launch_fp4_gemm(const Fp4Problem& q, void* out, const Fp4Split& sp, 
     return cudaErrorInvalidValue;
   Fp4Params p = fp4_params(q, sp, status);
   p.out = static_cast<__nv_bfloat16*>(out);
-  return q.fmt == MOE_FP4_NV ? run_fp4<MOE_FP4_NV, kF4Store>(a, a32, b, c, p, s)
-                             : run_fp4<MOE_FP4_MX, kF4Store>(a, a32, b, c, p, s);
+  return q.fmt == MOE_FP4_NV ? run_fp4<MOE_FP4_NV, kF4Store>(a, a32, b, c, p, q.early, s)
+                             : run_fp4<MOE_FP4_MX, kF4Store>(a, a32, b, c, p, q.early, s);
 }
 
 cudaError_t launch_fp4_swiglu(const Fp4Problem& q, uint8_t* hq, uint8_t* hsf, int h_scale_log2,
@@ -629,8 +753,8 @@ cudaError_t launch_fp4_swiglu(const Fp4Problem& q, uint8_t* hq, uint8_t* hsf, in
   p.hdown = ldexpf(1.f, -h_scale_log2);
   p.ckpt = ckpt;
   p.ckpt_sf = ckpt_sf;
-  return q.fmt == MOE_FP4_NV ? run_fp4<MOE_FP4_NV, kF4Swiglu>(a, a32, b, b, p, s)
-                             : run_fp4<MOE_FP4_MX, kF4Swiglu>(a, a32, b, b, p, s);
+  return q.fmt == MOE_FP4_NV ? run_fp4<MOE_FP4_NV, kF4Swiglu>(a, a32, b, b, p, q.early, s)
+                             : run_fp4<MOE_FP4_MX, kF4Swiglu>(a, a32, b, b, p, q.early, s);
 }
 
 }  // namespace moe

@@ -190,6 +190,10 @@ struct Fp4Problem {
   const int32_t* offsets;
   const float* alpha;         // [G] or null
   int unit_log2;              // the operands' tensor scales, as a power of two
+  // The kernel before this one on the stream is one of this library's that
+  // writes only A, and counts, offsets and alpha were complete before that one
+  // began: this one may start while it runs (programmatic dependent launch).
+  bool early;
 };
 // Scratch of the products that cut K: fp32 parts and arrival counters (zero).
 struct Fp4Split {

@@ -302,7 +302,9 @@ def h_interval(fmt, x, W13):
     return gu, lo, hi, h4, slack
 
 
-FFNS = [([1], 128, 128), ([0, 3, 130, 0, 64], 128, 384), ([40, 129], 256, 640)]
+FFNS = [([1], 128, 128), ([0, 3, 130, 0, 64], 128, 384), ([40, 129], 256, 640),
+        # sums cut over the SMs: up to 64 rows, several parts of a tile
+        ([1], 512, 2048), ([40, 0, 1, 64], 1024, 384), ([2, 33], 256, 4096)]
 
 
 def run_ffn(fmt, counts, H, F, ckpt=True, seed=0, T=None):
