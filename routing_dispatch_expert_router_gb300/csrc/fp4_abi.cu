@@ -180,7 +180,8 @@ moe_status moe_fp4_grouped_gemm(const moe_fp4_tensor* a, const moe_fp4_tensor* b
   const Fp4Problem p{a->format, (int)b->groups, a->rows, b->rows, a->K,
                      static_cast<const uint8_t*>(a->codes), static_cast<const uint8_t*>(a->scales),
                      static_cast<const uint8_t*>(b->codes), static_cast<const uint8_t*>(b->scales),
-                     counts, offsets, alpha, a->scale_log2 + b->scale_log2, false};
+                     counts, offsets, alpha, a->scale_log2 + b->scale_log2, false,
+                     a->rows};
   FP4_CUDA(launch_fp4_gemm(p, out, split_of(scratch), status_of(scratch), (cudaStream_t)stream));
   return MOE_OK;
 }
@@ -203,12 +204,12 @@ moe_status moe_fp4_ffn_fwd(const moe_config* cfg, const moe_fp4_experts* ex, con
   const Fp4Problem up{fmt, G, R, 2 * F, H, w.xq, w.xsf,
                       static_cast<const uint8_t*>(ex->W13.codes),
                       static_cast<const uint8_t*>(ex->W13.scales), counts, offsets, ex->alpha13,
-                      ex->x_scale_log2 + ex->W13.scale_log2, true};
+                      ex->x_scale_log2 + ex->W13.scale_log2, true, cfg->T};
   FP4_CUDA(launch_fp4_swiglu(up, w.hq, w.hsf, ex->h_scale_log2, static_cast<uint8_t*>(ckpt),
                              static_cast<uint8_t*>(ckpt_scale), sp, st, s));
   const Fp4Problem down{fmt, G, R, H, F, w.hq, w.hsf, static_cast<const uint8_t*>(ex->W2.codes),
                         static_cast<const uint8_t*>(ex->W2.scales), counts, offsets, ex->alpha2,
-                        ex->h_scale_log2 + ex->W2.scale_log2, true};
+                        ex->h_scale_log2 + ex->W2.scale_log2, true, cfg->T};
   FP4_CUDA(launch_fp4_gemm(down, y_perm, sp, st, s));
   return MOE_OK;
 }

@@ -37,10 +37,10 @@ namespace gg {
 constexpr int kF4Threads = 320;
 constexpr int kF4BN = 256;
 constexpr int kF4RowBytes = f4::kStep / 2;             // codes of a k-block's row: 128 bytes
-constexpr int kF4ABytes = BM * kF4RowBytes;            // 16 KB
 constexpr int kF4BBytes = kF4BN * kF4RowBytes;         // 32 KB
 constexpr int kF4EpiWarps = 8;
-constexpr int kF4Ahead = 12;                           // k-blocks prefetched by an early start
+constexpr int kF4Ahead = 8;                            // k-blocks that an early start prefetches
+constexpr int kF4QueueOff = 4864;                      // stages without A yet, in the control block
 constexpr uint32_t kF4TmemCols = 512;
 constexpr uint32_t kF4SfCol = kF4BN;                   // first scale-factor column
 
@@ -74,20 +74,29 @@ struct Fp4Params {
   int32_t* status;
 };
 
-template <int FMT>
+// AROWS: rows of A that a stage has room for. Where the caller knows that no group
+// has more than 32 (64) rows, the room of the others holds more stages. The MMA
+// still reads 128 rows; the ones past the room are the stage's own B bytes, finite
+// codes whose results no one reads.
+template <int FMT, int AROWS>
 struct F4Cfg {
   static constexpr int ATOMS = f4::step_atoms(FMT);              // per slab and k-block
   static constexpr int SF_A = ATOMS * f4::kAtomBytes;
   static constexpr int SF_STAGE = 3 * SF_A;                      // A's, then B's two slabs
-  static constexpr int STAGE = kF4ABytes + kF4BBytes;
-  static constexpr int STAGES = 3;
+  static constexpr int A_BYTES = AROWS * kF4RowBytes;
+  static constexpr int STAGE = A_BYTES + kF4BBytes;
+  static constexpr int STAGES = AROWS == 32 ? 5 : AROWS == 64 ? 4 : 3;
+  static constexpr bool BOXES = AROWS > 32;                      // whole 32-row boxes by TMA
   static constexpr int SF_OFF = STAGES * STAGE;
   static constexpr int CTRL_OFF = SF_OFF + STAGES * SF_STAGE;
   static constexpr int EPI_OFF = (CTRL_OFF + kCtrlBytes + 1023) / 1024 * 1024;
-  static constexpr int SMEM = EPI_OFF + kF4EpiWarps * kBoxBytes + 1024;
+  static constexpr int SMEM = EPI_OFF + (BOXES ? kF4EpiWarps * kBoxBytes : 0) + 1024;
   // scale columns of a k-block: A's 4 per atom, then B's 8 per atom
   static constexpr int SLOT_COLS = 12 * ATOMS;
   static constexpr int SLOTS = 2;
+  static_assert(STAGES <= 8, "barrier arrays");
+  static_assert(kF4QueueOff >= 4608 + 33 * 4 && kF4QueueOff + STAGES * 12 <= kCtrlBytes,
+                "queue inside the control block, after the scan scratch");
   static_assert(SMEM <= 232448, "FP4 grouped GEMM shared memory");
   static_assert(kF4SfCol + SLOTS * SLOT_COLS <= kF4TmemCols, "FP4 tensor-memory columns");
 };
@@ -209,7 +218,7 @@ __device__ __forceinline__ int slice_col(int half, int c) {
 
 // Stores a warp's 32 rows x 128 columns (o: bf16, the slices of slice_col): rv of
 // the 32 rows hold data, the others are not written.
-template <int FMT, int EPI>
+template <int FMT, int EPI, bool BOXES>
 __device__ __forceinline__ void f4_epilogue(const Fp4Params& p, const CUtensorMap* tmC,
                                             uint8_t* stage, uint32_t stage_u32, int nt, int row0,
                                             int rv, int half, int lane, const uint4 (&o)[4][4]) {
@@ -247,7 +256,7 @@ __device__ __forceinline__ void f4_epilogue(const Fp4Params& p, const CUtensorMa
   for (int c = 0; c < 4; ++c) {
     const int col = c0 + 32 * c;
     if (col >= p.N) {
-    } else if (rv >= 32) {
+    } else if (BOXES && rv >= 32) {
       // a full 32 x 32 box by TMA, which also clips the columns past N
       if (lane == 0) ptx::tma_store_wait_read();       // the slot's previous box has been read
       __syncwarp();
@@ -319,13 +328,13 @@ __device__ __forceinline__ void f4_epilogue_row(const Fp4Params& p, int nt, int6
   }
 }
 
-template <int FMT, int EPI>
+template <int FMT, int EPI, int AROWS>
 __global__ void __launch_bounds__(kF4Threads, 1)
 grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmA32,
                         const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmC, const Fp4Params p) {
-  using C = F4Cfg<FMT>;
+  using C = F4Cfg<FMT, AROWS>;
   constexpr bool NV = FMT == MOE_FP4_NV;
   constexpr int kStages = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -338,8 +347,8 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
   uint8_t* epi = sbase + C::EPI_OFF;
   const uint32_t epi_u = base + C::EPI_OFF;
   const uint32_t bar_full = ctrl_u;                       // [kStages]
-  const uint32_t bar_empty = ctrl_u + 32;                 // [kStages]
-  const uint32_t bar_tfull = ctrl_u + 64;
+  const uint32_t bar_empty = ctrl_u + 64;                 // [kStages]
+  const uint32_t bar_tfull = ctrl_u + 128;
   const uint32_t bar_tempty = bar_tfull + 8;
   const uint32_t bar_drain = bar_tfull + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 192);
@@ -363,9 +372,9 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
   __syncthreads();
   for (int g = tid; g < G; g += kF4Threads) {
     int64_t c = p.counts ? p.counts[g] : p.rows, o = p.counts ? p.offsets[g] : 0;
-    // rows outside the tensor, or off the 128-row grid of the scale atoms: the
-    // group is left out and reported
-    if (c < 0 || o < 0 || o % 128 || o + c > p.rows) {
+    // rows outside the tensor, off the 128-row grid of the scale atoms, or more
+    // than the caller said: the group is left out and reported
+    if (c < 0 || o < 0 || o % 128 || o + c > p.rows || (AROWS < BM && c > AROWS)) {
       record_status(p.status, MOE_ERR_DEVICE_CHECK);
       c = o = 0;
     }
@@ -410,6 +419,7 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  ptx::grid_launch_dependents();     // the next kernel's CTAs may start as these leave
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -418,23 +428,32 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
       uint32_t issued_mask = 0, issued_phase = 0;
       bool ok = true;
       const int64_t nslabs = f4::slabs(p.N);
-      // weights may be fetched before the kernel before this one is done; A's
-      // rows (what that kernel wrote) only after it
-      bool waited = !p.early;
-      if (p.early) {
-        // into L2 meanwhile: the weights of this CTA's first k-blocks
-        Work f = w;
-        int left = kF4Ahead;
-        while (left > 0 && f.next()) {
-          const Tile t = decode(f.tile, prefix, mtiles, s_cnt, G, 0, p.K, NT, 0);
-          const int b0 = t.nt * (EPI == kF4Swiglu ? kF4BN / 2 : kF4BN);
-          const int b1 = EPI == kF4Swiglu ? F + b0 : b0 + 128;
-          for (int kb = f.kb0; kb < f.kb1 && left > 0; ++kb, --left) {
-            ptx::tma_prefetch_2d(&tmB, kb * kF4RowBytes, t.g * p.N + b0);
-            ptx::tma_prefetch_2d(&tmB, kb * kF4RowBytes, t.g * p.N + b1);
+      const int64_t slab_bytes = (int64_t)p.ka * f4::kAtomBytes;
+      // Started early, this kernel fetches the weights of its first stages at once
+      // and their A rows when the kernel before it (which writes them) is done:
+      // `queue` of the last `queued` stages still lack them.
+      struct Todo { int kb, row0, boxes; };
+      Todo* queue = reinterpret_cast<Todo*>(ctrl + kF4QueueOff);
+      int queued = 0, hold = p.early ? kStages : 1;
+      auto load_a = [&]() {
+        if (hold > 1) ptx::grid_dependency_wait();
+        hold = 1;
+        uint32_t s = stage + kStages - queued;           // the first queued stage
+        for (int i = 0; i < queued; ++i, ++s) {
+          if (s >= kStages) s -= kStages;
+          const Todo d = queue[i];
+          const uint32_t fb = bar_full + 8 * s, sA = base + s * C::STAGE;
+          ptx::bulk_load(sf_u + s * C::SF_STAGE,
+                         p.sfa + d.row0 / 128 * slab_bytes + (int64_t)d.kb * C::SF_A, C::SF_A, fb);
+          if (AROWS == BM && d.boxes == 4) {
+            ptx::tma_load_2d(sA, &tmA, fb, d.kb * kF4RowBytes, d.row0);
+          } else {
+            for (int j = 0; j < d.boxes; ++j)
+              ptx::tma_load_2d(sA + 4096 * j, &tmA32, fb, d.kb * kF4RowBytes, d.row0 + 32 * j);
           }
         }
-      }
+        queued = 0;
+      };
       while (ok && w.next()) {
         const Tile t = decode(w.tile, prefix, mtiles, s_cnt, G, 0, p.K, NT, 0);
         const int row0 = s_off[t.g] + t.mt * BM;
@@ -449,8 +468,6 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
           b1 = b0 + 128;
         }
         const int64_t nb0 = b0 / 128, nb1 = min((int64_t)(b1 / 128), nslabs - 1);
-        const int64_t slab_bytes = (int64_t)p.ka * f4::kAtomBytes;
-        const uint8_t* sfa = p.sfa + (int64_t)(row0 / 128) * slab_bytes;
         const uint8_t* sfb0 = p.sfb + (t.g * nslabs + nb0) * slab_bytes;
         const uint8_t* sfb1 = p.sfb + (t.g * nslabs + nb1) * slab_bytes;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
@@ -460,8 +477,7 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
           }
           const uint32_t fb = bar_full + 8 * stage;
           ptx::mbar_arrive_expect_tx(fb, boxes * 4096 + kF4BBytes + C::SF_STAGE);
-          const uint32_t sA = base + stage * C::STAGE;
-          const uint32_t sB = sA + kF4ABytes;
+          const uint32_t sB = base + stage * C::STAGE + C::A_BYTES;
           const int k0 = kb * kF4RowBytes;
           const int brow = t.g * p.N;
           ptx::tma_load_2d(sB, &tmB, fb, k0, brow + b0);
@@ -470,25 +486,26 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
           const int64_t ao = (int64_t)kb * C::SF_A;
           ptx::bulk_load(sfs + C::SF_A, sfb0 + ao, C::SF_A, fb);
           ptx::bulk_load(sfs + 2 * C::SF_A, sfb1 + ao, C::SF_A, fb);
-          if (!waited) {
-            ptx::grid_dependency_wait();
-            waited = true;
-          }
-          ptx::bulk_load(sfs, sfa + ao, C::SF_A, fb);
-          if (boxes == 4) {
-            ptx::tma_load_2d(sA, &tmA, fb, k0, row0);
-          } else {
-            for (int i = 0; i < boxes; ++i)
-              ptx::tma_load_2d(sA + 4096 * i, &tmA32, fb, k0, row0 + 32 * i);
-          }
+          queue[queued++] = Todo{kb, row0, boxes};
           issued_mask |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
+          if (queued < hold) continue;
+          if (hold > 1) {
+            // all stages hold weights: the piece's next ones into L2 meanwhile
+            const int ahead = min(w.kb1, kb + 1 + kF4Ahead);
+            for (int k = kb + 1; k < ahead; ++k) {
+              ptx::tma_prefetch_2d(&tmB, k * kF4RowBytes, brow + b0);
+              ptx::tma_prefetch_2d(&tmB, k * kF4RowBytes, brow + b1);
+            }
+          }
+          load_a();
         }
       }
+      load_a();
       if (!ok) {
         record_status(p.status, MOE_ERR_TIMEOUT);
         *abort_flag = 1;
@@ -531,7 +548,7 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
                                         ptx::smem_desc_sf(sfs + 2 * C::SF_A + 512 * a));
           }
           const uint32_t sA = base + stage * C::STAGE;
-          const uint32_t sB = sA + kF4ABytes;
+          const uint32_t sB = sA + C::A_BYTES;
           // 64-wide slices of the k-block that K reaches into
           const int slices = min(4, (p.K - kb * f4::kStep + 63) / 64);
           for (int kk = 0; kk < slices; ++kk) {
@@ -618,23 +635,21 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
       acc_phase ^= 1u;
       if (rv <= 0) continue;
       if (!w.whole()) {
-        __threadfence();
         __syncwarp();
         const int b0 = w.first(), b1 = w.last();
         int last = 0;
         if (lane == 0) {
           int32_t* a = p.arrived + w.tile * kF4EpiWarps + (warp - 2);
-          last = atomicAdd(a, 1) == b1 - b0;
+          last = ptx::atom_add_acq_rel(a, 1) == b1 - b0;
           if (last) *a = 0;                       // as the next launch expects it
         }
         last = __shfl_sync(0xffffffffu, last, 0);
         if (!last) continue;
-        __threadfence();
         const int rows = min(rv, 32);
         // the first part ends at its CTA's share (slot 2 b0 + 1), the others begin theirs
         const float* src = parts + 4 * lane;
         const int64_t step = 4 * slice;           // from a CTA's slots to the next one's
-#pragma unroll 2
+#pragma unroll 1
         for (int r = 0; r < rows; ++r) {
           const float* at = src + (4 * (int64_t)b0 + 2) * slice + r * 128;
           float4 v = __ldcg(reinterpret_cast<const float4*>(at));
@@ -655,7 +670,7 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
         }
         continue;
       }
-      f4_epilogue<FMT, EPI>(p, &tmC, stage, stage_u32, t.nt, row0, rv, half, lane, o);
+      f4_epilogue<FMT, EPI, C::BOXES>(p, &tmC, stage, stage_u32, t.nt, row0, rv, half, lane, o);
     }
     if (lane == 0) ptx::tma_store_wait_all();
   }
@@ -667,12 +682,12 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
   }
 }
 
-template <int FMT, int EPI>
-static cudaError_t run_fp4(const CUtensorMap& a, const CUtensorMap& a32, const CUtensorMap& b,
+template <int FMT, int EPI, int AROWS>
+static cudaError_t run_fp4_rows(const CUtensorMap& a, const CUtensorMap& a32, const CUtensorMap& b,
                            const CUtensorMap& c, const Fp4Params& p, bool early,
                            cudaStream_t s) {
-  auto kern = grouped_gemm_fp4_kernel<FMT, EPI>;
-  constexpr int smem = F4Cfg<FMT>::SMEM;
+  auto kern = grouped_gemm_fp4_kernel<FMT, EPI, AROWS>;
+  constexpr int smem = F4Cfg<FMT, AROWS>::SMEM;
   static bool attr_set = false;
   if (!attr_set) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -690,6 +705,21 @@ static cudaError_t run_fp4(const CUtensorMap& a, const CUtensorMap& a32, const C
   lc.attrs = at;
   lc.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&lc, kern, a, a32, b, c, p);
+}
+
+template <int EPI>
+static cudaError_t run_fp4(const Fp4Problem& q, const CUtensorMap& a, const CUtensorMap& a32,
+                           const CUtensorMap& b, const CUtensorMap& c, const Fp4Params& p,
+                           cudaStream_t s) {
+  const bool nv = q.fmt == MOE_FP4_NV;
+  if (q.most_rows <= 32)
+    return nv ? run_fp4_rows<MOE_FP4_NV, EPI, 32>(a, a32, b, c, p, q.early, s)
+              : run_fp4_rows<MOE_FP4_MX, EPI, 32>(a, a32, b, c, p, q.early, s);
+  if (q.most_rows <= 64)
+    return nv ? run_fp4_rows<MOE_FP4_NV, EPI, 64>(a, a32, b, c, p, q.early, s)
+              : run_fp4_rows<MOE_FP4_MX, EPI, 64>(a, a32, b, c, p, q.early, s);
+  return nv ? run_fp4_rows<MOE_FP4_NV, EPI, 128>(a, a32, b, c, p, q.early, s)
+            : run_fp4_rows<MOE_FP4_MX, EPI, 128>(a, a32, b, c, p, q.early, s);
 }
 
 // 4-bit operand: [rows, K / 2] bytes, box of 128 bytes x box_rows.
@@ -734,8 +764,7 @@ cudaError_t launch_fp4_gemm(const Fp4Problem& q, void* out, const Fp4Split& sp, 
     return cudaErrorInvalidValue;
   Fp4Params p = fp4_params(q, sp, status);
   p.out = static_cast<__nv_bfloat16*>(out);
-  return q.fmt == MOE_FP4_NV ? run_fp4<MOE_FP4_NV, kF4Store>(a, a32, b, c, p, q.early, s)
-                             : run_fp4<MOE_FP4_MX, kF4Store>(a, a32, b, c, p, q.early, s);
+  return run_fp4<kF4Store>(q, a, a32, b, c, p, s);
 }
 
 cudaError_t launch_fp4_swiglu(const Fp4Problem& q, uint8_t* hq, uint8_t* hsf, int h_scale_log2,
@@ -753,8 +782,7 @@ cudaError_t launch_fp4_swiglu(const Fp4Problem& q, uint8_t* hq, uint8_t* hsf, in
   p.hdown = ldexpf(1.f, -h_scale_log2);
   p.ckpt = ckpt;
   p.ckpt_sf = ckpt_sf;
-  return q.fmt == MOE_FP4_NV ? run_fp4<MOE_FP4_NV, kF4Swiglu>(a, a32, b, b, p, q.early, s)
-                             : run_fp4<MOE_FP4_MX, kF4Swiglu>(a, a32, b, b, p, q.early, s);
+  return run_fp4<kF4Swiglu>(q, a, a32, b, b, p, s);
 }
 
 }  // namespace moe

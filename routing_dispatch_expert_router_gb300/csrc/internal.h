@@ -194,6 +194,7 @@ struct Fp4Problem {
   // writes only A, and counts, offsets and alpha were complete before that one
   // began: this one may start while it runs (programmatic dependent launch).
   bool early;
+  int64_t most_rows;          // no group has more rows than this
 };
 // Scratch of the products that cut K: fp32 parts and arrival counters (zero).
 struct Fp4Split {

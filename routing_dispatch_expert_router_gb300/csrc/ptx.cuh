@@ -85,6 +85,15 @@ __device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int32_t c0, in
                :: "l"(tmap), "r"(c0), "r"(c1) : "memory");
 }
 
+// Adds at device scope and returns the old value, ordering this thread's earlier
+// accesses (and those it has synchronised with) before it and its later ones after.
+__device__ __forceinline__ int atom_add_acq_rel(int* p, int v) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;"
+               : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
+
 // Programmatic dependent launch: waits until the kernel before this one on the
 // stream is complete and its writes are visible (returns at once in a launch
 // without that attribute); and lets the kernel after this one start early.

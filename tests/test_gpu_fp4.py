@@ -213,13 +213,14 @@ def test_product_matches_oracle(fmt, counts, N, K):
     assert torch.equal(out, again)                         # the counters were left at zero
 
 
-def test_product_dense_form_and_no_alpha():
+@pytest.mark.parametrize("rows", [1, 20, 32, 50, 64, 200])
+def test_product_dense_form_and_no_alpha(rows):
     rng = np.random.default_rng(5)
-    x = rows_of(rng, 1, 200, 320)
-    xq = B.alloc_fp4(B.MOE_FP4_NV, 1, 200, 320)
+    x = rows_of(rng, 1, rows, 320)
+    xq = B.alloc_fp4(B.MOE_FP4_NV, 1, rows, 320)
     B.moe_fp4_quantize(x, xq, scale_log2=1)
     wq, wv = weights(B.MOE_FP4_NV, rng, 1, 72, 320)
-    out = torch.empty(200, 72, device=DEV, dtype=torch.bfloat16)
+    out = torch.empty(rows, 72, device=DEV, dtype=torch.bfloat16)
     sc = B.alloc_fp4_scratch(B.moe_fp4_query_sizes(None, 0).gemm_scratch_bytes)
     B.moe_fp4_grouped_gemm(xq, wq, None, None, None, out, sc)
     xv = O.real(B.MOE_FP4_NV, f64(x)[0], 1)
