@@ -10,14 +10,19 @@
 // core applies them, so the kernel only moves bytes, 0.5625 (NV) or 0.53 (MX)
 // of them per element.
 //
-// One persistent kernel, one CTA per SM, 320 threads:
-//   warp 0     TMA producer (one lane): per 256-deep k-block (128 bytes of codes
-//              a row) A's rows, 256 rows of B and their scale atoms;
-//   warp 1     MMA issuer (one lane) and tensor-memory owner: copies the atoms
-//              into tensor memory (tcgen05.cp), then four M=128 N=256 K=64 MMAs;
-//   warps 2-9  epilogue, two warps per tensor-memory lane quarter, 128 of the
-//              256 accumulator columns each, held in registers while the next
-//              tile's MMAs run.
+// One persistent kernel, one CTA per SM, 448 threads:
+//   warp 0       TMA producer (one lane): per 256-deep k-block (128 bytes of codes
+//                a row) A's rows, 256 rows of B and their scale atoms;
+//   warp 1       MMA issuer (one lane) and tensor-memory owner: four M=128 N=256
+//                K=64 MMAs a k-block;
+//   warps 2-9    epilogue, two warps per tensor-memory lane quarter, 128 of the
+//                256 accumulator columns each, held in registers while the next
+//                tile's MMAs run;
+//   warps 10-13  scales: each writes a k-block's atoms into its lane quarter of
+//                tensor memory (tcgen05.st). tcgen05.cp would do it in one thread,
+//                but runs in the tensor core's own queue: the 12 copies of an NV
+//                k-block take as long as its MMAs (8192 x 8192 x 8192: 340 us with
+//                the copies, 254 us so).
 //
 // A decode step has a few rows per expert: then the weights' bytes are all the
 // work, and what counts is that every SM streams its share of them. Only the
@@ -34,7 +39,8 @@
 namespace moe {
 namespace gg {
 
-constexpr int kF4Threads = 320;
+constexpr int kF4Threads = 448;
+constexpr int kF4ScaleWarp = 10;                       // the first of the four
 constexpr int kF4BN = 256;
 constexpr int kF4RowBytes = f4::kStep / 2;             // codes of a k-block's row: 128 bytes
 constexpr int kF4BBytes = kF4BN * kF4RowBytes;         // 32 KB
@@ -93,12 +99,11 @@ struct F4Cfg {
   static constexpr int SMEM = EPI_OFF + (BOXES ? kF4EpiWarps * kBoxBytes : 0) + 1024;
   // scale columns of a k-block: A's 4 per atom, then B's 8 per atom
   static constexpr int SLOT_COLS = 12 * ATOMS;
-  static constexpr int SLOTS = 2;
   static_assert(STAGES <= 8, "barrier arrays");
   static_assert(kF4QueueOff >= 4608 + 33 * 4 && kF4QueueOff + STAGES * 12 <= kCtrlBytes,
                 "queue inside the control block, after the scan scratch");
   static_assert(SMEM <= 232448, "FP4 grouped GEMM shared memory");
-  static_assert(kF4SfCol + SLOTS * SLOT_COLS <= kF4TmemCols, "FP4 tensor-memory columns");
+  static_assert(kF4SfCol + STAGES * SLOT_COLS <= kF4TmemCols, "FP4 tensor-memory columns");
 };
 
 // The work of one CTA: whole tiles blockIdx.x, + gridDim.x, .. (even = 0), or its
@@ -348,6 +353,7 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
   const uint32_t epi_u = base + C::EPI_OFF;
   const uint32_t bar_full = ctrl_u;                       // [kStages]
   const uint32_t bar_empty = ctrl_u + 64;                 // [kStages]
+  const uint32_t bar_scales = ctrl_u + 208;               // [kStages]
   const uint32_t bar_tfull = ctrl_u + 128;
   const uint32_t bar_tempty = bar_tfull + 8;
   const uint32_t bar_drain = bar_tfull + 16;
@@ -400,6 +406,7 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(bar_full + 8 * s, 1);
       ptx::mbar_init(bar_empty + 8 * s, 1);
+      ptx::mbar_init(bar_scales + 8 * s, 4);
     }
     ptx::mbar_init(bar_tfull, 1);
     ptx::mbar_init(bar_tempty, kF4EpiWarps);
@@ -519,7 +526,7 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t IDESC = ptx::idesc_fp4(BM, kF4BN, NV ? 0 : 1);
-      uint32_t stage = 0, phase = 0, acc_phase = 0, slot = 0;
+      uint32_t stage = 0, phase = 0, acc_phase = 0;
       bool ok = true, issued = false;
       while (ok && w.next()) {
         if (!ptx::mbar_wait(bar_tempty, acc_phase ^ 1u, kWaitBudget, abort_flag)) {
@@ -528,25 +535,14 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
         }
         ptx::tc_fence_after();
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (!ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget, abort_flag)) {
+          if (!ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget, abort_flag) ||
+              !ptx::mbar_wait(bar_scales + 8 * stage, phase, kWaitBudget, abort_flag)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t sfs = sf_u + stage * C::SF_STAGE;
-          // the copies and the MMAs of this thread run in issue order, so two
-          // slots are enough: one is rewritten after the MMAs that read it
-          const uint32_t sfa_t = tmem_base + kF4SfCol + C::SLOT_COLS * slot;
+          const uint32_t sfa_t = tmem_base + kF4SfCol + C::SLOT_COLS * stage;
           const uint32_t sfb_t = sfa_t + 4 * C::ATOMS;
-          slot ^= 1u;
-#pragma unroll
-          for (int a = 0; a < C::ATOMS; ++a) {
-            ptx::tmem_cp_32x128b_warpx4(sfa_t + 4 * a, ptx::smem_desc_sf(sfs + 512 * a));
-            ptx::tmem_cp_32x128b_warpx4(sfb_t + 8 * a,
-                                        ptx::smem_desc_sf(sfs + C::SF_A + 512 * a));
-            ptx::tmem_cp_32x128b_warpx4(sfb_t + 8 * a + 4,
-                                        ptx::smem_desc_sf(sfs + 2 * C::SF_A + 512 * a));
-          }
           const uint32_t sA = base + stage * C::STAGE;
           const uint32_t sB = sA + C::A_BYTES;
           // 64-wide slices of the k-block that K reaches into
@@ -579,6 +575,51 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
         ptx::mma_commit(bar_drain);
         ptx::mbar_wait(bar_drain, 0, kWaitBudget, nullptr);
       }
+    }
+  } else if (warp >= kF4ScaleWarp) {
+    // -------------------------------------------------------------- scales
+    // The stage's columns are free when its loads have landed again: the
+    // producer waited for the MMAs that read them.
+    const uint32_t tq = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + kF4SfCol;
+    const uint8_t* sfl = sbase + C::SF_OFF + lane * 16;
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    while (ok && w.next()) {
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget,
+                                                    abort_flag));
+        if (!ok) break;
+        uint32_t a[4 * C::ATOMS], b[8 * C::ATOMS];
+        const uint8_t* src = sfl + stage * C::SF_STAGE;
+#pragma unroll
+        for (int i = 0; i < C::ATOMS; ++i) {
+          *reinterpret_cast<uint4*>(a + 4 * i) = *reinterpret_cast<const uint4*>(src + 512 * i);
+          *reinterpret_cast<uint4*>(b + 8 * i) =
+              *reinterpret_cast<const uint4*>(src + C::SF_A + 512 * i);
+          *reinterpret_cast<uint4*>(b + 8 * i + 4) =
+              *reinterpret_cast<const uint4*>(src + 2 * C::SF_A + 512 * i);
+        }
+        const uint32_t col = tq + C::SLOT_COLS * stage;
+        if (NV) {
+          ptx::tmem_st16(col, a);
+          ptx::tmem_st32(col + 16, b);
+        } else {
+          ptx::tmem_st8(col, a);
+          ptx::tmem_st16(col + 8, b);
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar_scales + 8 * stage);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      record_status(p.status, MOE_ERR_TIMEOUT);
+      *abort_flag = 1;
     }
   } else {
     // ------------------------------------------------------------ epilogue
