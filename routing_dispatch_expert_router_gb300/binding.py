@@ -96,6 +96,8 @@ def lib():
         for name in ENTRY_POINTS:
             f = getattr(L, name)
             f.restype = ctypes.c_int
+        for name, args in _FP4_ARGS.items():
+            getattr(L, name).argtypes = args
         L.moe_status_string.restype = ctypes.c_char_p
         L.moe_status_string.argtypes = [ctypes.c_int]
         _lib = L
@@ -142,7 +144,8 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # (with the device given, torch does not look for one: 1 us instead of 6)
+        return torch.cuda.current_stream(torch.cuda.current_device()).cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -328,21 +331,36 @@ class MoEFp4Sizes(ctypes.Structure):
                 ("bwd_scratch_bytes", ctypes.c_int64)]
 
 
-@dataclass
+# with the argument types declared, a call converts its integers (addresses, sizes)
+# without wrapping each: these calls can be shorter than that
+_T = ctypes.POINTER(MoEFp4Tensor)
+_I32, _I64 = ctypes.c_int32, ctypes.c_int64
+_FP4_ARGS = {
+    "moe_fp4_quantize": [_T, _P, _I64, _P, _P, _I32, _P, _P, _P],
+    "moe_fp4_dequantize": [_T, _P, _I64, _P],
+    "moe_fp4_grouped_gemm": [_T, _T, _P, _P, _P, _P, _P, _P],
+    "moe_fp4_ffn_fwd": [ctypes.POINTER(MoEConfig), ctypes.POINTER(MoEFp4Experts)] + [_P] * 8,
+    "moe_fp4_ffn_bwd": [ctypes.POINTER(MoEConfig), ctypes.POINTER(MoEFp4Experts)] + [_P] * 11,
+}
+
+
 class Fp4Tensor:
     """A tensor [groups, rows, K] in 4 bits: packed codes [groups, rows, K / 2] and
     scale atoms [groups, slabs, atoms, 512] (include/moe_abi.h has the layout)."""
-    format: int
-    K: int
-    codes: torch.Tensor
-    scales: torch.Tensor
-    scale_log2: int = 0
+    __slots__ = ("format", "K", "codes", "scales", "scale_log2")
+
+    def __init__(self, format: int, K: int, codes: torch.Tensor, scales: torch.Tensor,
+                 scale_log2: int = 0):
+        self.format, self.K, self.codes, self.scales = format, K, codes, scales
+        self.scale_log2 = scale_log2
 
     def struct(self) -> MoEFp4Tensor:
         g, rows, kb = self.codes.shape
         if kb * 2 != self.K:
             raise ValueError(f"codes hold {2 * kb} elements a row, K is {self.K}")
-        if self.scales.numel() != g * fp4_scale_bytes(self.format, rows, self.K):
+        # ceil(K / 256) steps of 4 (NV) or 2 (MX) atoms per 128 rows
+        if self.format not in (0, 1) or self.scales.numel() != \
+                g * -(-rows // 128) * -(-self.K // 256) * (2048 >> self.format):
             raise ValueError("scales do not have the atoms of the codes' shape")
         if not (self.codes.is_contiguous() and self.scales.is_contiguous()):
             raise ValueError("codes and scales are contiguous")
@@ -390,14 +408,20 @@ def alloc_fp4_scratch(nbytes: int, device="cuda") -> torch.Tensor:
     return torch.zeros(int(nbytes), dtype=torch.uint8, device=device)
 
 
-def _bf16_rows(t, K: int, what: str) -> int:
-    """Elements from row to row of a bf16 [.., rows, K] tensor whose rows are evenly spaced."""
-    if t.dtype != torch.bfloat16 or t.shape[-1] != K or t.stride(-1) != 1:
-        raise ValueError(f"{what} is bf16 [.., {K}] with contiguous rows")
-    ld = t.stride(-2)
-    if t.dim() == 3 and t.shape[0] > 1 and t.stride(0) != ld * t.shape[1]:
-        raise ValueError(f"{what}'s groups follow each other row by row")
-    return ld if t.shape[-2] > 1 or t.dim() == 3 and t.shape[0] > 1 else max(ld, K)
+def _bf16_rows(t, shape, what: str) -> int:
+    """Elements from row to row of a bf16 tensor of this shape whose rows are evenly spaced."""
+    if t.shape != shape or t.dtype != torch.bfloat16:
+        raise ValueError(f"{what} is bf16 {tuple(shape)}")
+    if t.is_contiguous():
+        return shape[2]
+    sg, ld, one = t.stride()
+    if one != 1 or (shape[0] > 1 and sg != ld * shape[1]):
+        raise ValueError(f"{what} has contiguous rows, its groups following each other row by row")
+    return ld if shape[0] > 1 or shape[1] > 1 else shape[2]
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def moe_fp4_quantize(x, q: Fp4Tensor, scale_log2: int | None = None, counts=None, offsets=None,
@@ -406,13 +430,15 @@ def moe_fp4_quantize(x, q: Fp4Tensor, scale_log2: int | None = None, counts=None
     x [1, rows, K]. values: the bf16 values that the codes stand for."""
     if scale_log2 is not None:
         q.scale_log2 = scale_log2
-    if tuple(x.shape) != (*q.codes.shape[:2], q.K):
-        raise ValueError("x has the shape of q")
+    s = q.struct()
+    ldx = _bf16_rows(x, (s.groups, s.rows, s.K), "x")
     if values is not None and not (values.is_contiguous() and values.shape == x.shape
                                    and values.dtype == torch.bfloat16):
         raise ValueError("values is contiguous bf16 of x's shape")
-    _call("moe_fp4_quantize", q.struct(), x, _bf16_rows(x, q.K, "x"), counts, offsets,
-          0 if counts is None else counts.numel(), values, scratch, _stream(stream))
+    rc = lib().moe_fp4_quantize(s, x.data_ptr(), ldx, _addr(counts), _addr(offsets),
+                                0 if counts is None else counts.numel(), _addr(values),
+                                _addr(scratch), _stream(stream))
+    _check("moe_fp4_quantize", rc)
 
 
 def moe_fp4_dequantize(q: Fp4Tensor, out, scale_log2: int | None = None, stream=None):
@@ -420,35 +446,41 @@ def moe_fp4_dequantize(q: Fp4Tensor, out, scale_log2: int | None = None, stream=
     s = q.struct()
     if scale_log2 is not None:
         s.scale_log2 = scale_log2
-    if tuple(out.shape) != (*q.codes.shape[:2], q.K):
-        raise ValueError("out has the shape of q")
-    _call("moe_fp4_dequantize", s, out, _bf16_rows(out, q.K, "out"), _stream(stream))
+    ldo = _bf16_rows(out, (s.groups, s.rows, s.K), "out")
+    _check("moe_fp4_dequantize",
+           lib().moe_fp4_dequantize(s, out.data_ptr(), ldo, _stream(stream)))
 
 
 def moe_fp4_grouped_gemm(a: Fp4Tensor, b: Fp4Tensor, counts, offsets, alpha, out, scratch,
                          stream=None):
     """out [rows, N] bf16: every group's rows of a [1, rows, K] by b [G, N, K]."""
-    if out.dtype != torch.bfloat16 or not out.is_contiguous() or \
-            tuple(out.shape) != (a.codes.shape[1], b.codes.shape[1]):
+    sa, sb = a.struct(), b.struct()
+    if out.dtype != torch.bfloat16 or not out.is_contiguous() or out.shape != (sa.rows, sb.rows):
         raise ValueError("out is contiguous bf16 [rows of a, rows of b]")
-    if counts is not None and counts.numel() != b.codes.shape[0]:
+    if counts is not None and counts.numel() != sb.groups:
         raise ValueError("one count per group of b")
-    _call("moe_fp4_grouped_gemm", a.struct(), b.struct(), counts, offsets, alpha, out, scratch,
-          _stream(stream))
+    _check("moe_fp4_grouped_gemm",
+           lib().moe_fp4_grouped_gemm(sa, sb, _addr(counts), _addr(offsets), _addr(alpha),
+                                      out.data_ptr(), _addr(scratch), _stream(stream)))
 
 
 def moe_fp4_ffn_fwd(cfg, experts: MoEFp4Experts, x_perm, counts, offsets, ckpt, ckpt_scale,
                     y_perm, scratch, stream=None):
     """The experts' FFN in 4 bits; ckpt, ckpt_scale: None, or the 8-bit checkpoint."""
-    _call("moe_fp4_ffn_fwd", _cfg(cfg), experts, x_perm, counts, offsets, ckpt, ckpt_scale,
-          y_perm, scratch, _stream(stream))
+    _check("moe_fp4_ffn_fwd",
+           lib().moe_fp4_ffn_fwd(_cfg(cfg), experts, _addr(x_perm), _addr(counts), _addr(offsets),
+                                 _addr(ckpt), _addr(ckpt_scale), _addr(y_perm), _addr(scratch),
+                                 _stream(stream)))
 
 
 def moe_fp4_ffn_bwd(cfg, experts: MoEFp4Experts, dO_perm, ckpt, ckpt_scale, counts, offsets,
                     token_of, dlogits, W_r, dX_perm, scratch, stream=None):
     """The gradient at the FFN's input; token_of, dlogits, W_r: None, or the router's term."""
-    _call("moe_fp4_ffn_bwd", _cfg(cfg), experts, dO_perm, ckpt, ckpt_scale, counts, offsets,
-          token_of, dlogits, W_r, dX_perm, scratch, _stream(stream))
+    _check("moe_fp4_ffn_bwd",
+           lib().moe_fp4_ffn_bwd(_cfg(cfg), experts, _addr(dO_perm), _addr(ckpt),
+                                 _addr(ckpt_scale), _addr(counts), _addr(offsets),
+                                 _addr(token_of), _addr(dlogits), _addr(W_r), _addr(dX_perm),
+                                 _addr(scratch), _stream(stream)))
 
 
 def moe_last_device_status(scratch, stream=None) -> int:

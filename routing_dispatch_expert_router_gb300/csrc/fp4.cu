@@ -192,44 +192,6 @@ fp4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restri
   }
 }
 
-// One thread: 16 checkpoint values of a row.
-__global__ void __launch_bounds__(kQThreads)
-ckpt_expand_kernel(const uint8_t* __restrict__ ckpt, const uint8_t* __restrict__ ckpt_sf,
-                   __nv_bfloat16* __restrict__ out, const Rows p) {
-  int64_t row0;
-  const int n = slab_rows(p, blockIdx.x, row0);
-  if (n == 0) return;
-  const int64_t per = p.K / 16;
-  for (int64_t i = (int64_t)blockIdx.y * kQThreads + threadIdx.x; i < 128 * per;
-       i += (int64_t)gridDim.y * kQThreads) {
-    const int r = (int)(i / per);
-    const int64_t c = (i - r * per) * 16, row = row0 + r;
-    if (row >= p.rows) continue;
-    uint4 o[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (r < n) {
-      const uint4 v = ldg_nc_v4(ckpt + row * p.K + c);
-      const float s = fp4_scale_value<MOE_FP4_MX>(ckpt_sf[row * (p.K / 32) + c / 32]);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float f[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t h2;
-          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2)
-              : "h"((uint16_t)(w[2 * j + (k >> 1)] >> (16 * (k & 1)))));
-          const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-          f[2 * k] = t.x * s;
-          f[2 * k + 1] = t.y * s;
-        }
-        o[j] = pack8(f);
-      }
-    }
-    stg_v4(out + row * p.K + c, o[0]);
-    stg_v4(out + row * p.K + c + 8, o[1]);
-  }
-}
-
 float pow2f(int e) { return ldexpf(1.f, e); }
 
 }  // namespace
@@ -252,17 +214,6 @@ cudaError_t launch_fp4_quantize(int fmt, const void* x, int64_t ldx, int64_t gro
     if (values) fp4_quantize_kernel<MOE_FP4_MX, true><<<grid, kQThreads, 0, s>>>(xb, codes, scales, vb, up, down, p);
     else fp4_quantize_kernel<MOE_FP4_MX, false><<<grid, kQThreads, 0, s>>>(xb, codes, scales, vb, up, down, p);
   }
-  return cudaGetLastError();
-}
-
-cudaError_t launch_fp4_ckpt_expand(const uint8_t* ckpt, const uint8_t* ckpt_sf, int64_t rows,
-                                   int64_t cols, const int32_t* counts, const int32_t* offsets,
-                                   int segments, void* out, int32_t* status, cudaStream_t s) {
-  const Rows p{rows, cols, cols, counts, offsets, segments, status};
-  const int64_t sl = f4::slabs(rows);
-  if (sl == 0) return cudaSuccess;
-  ckpt_expand_kernel<<<dim3((unsigned)sl, 16), kQThreads, 0, s>>>(
-      ckpt, ckpt_sf, static_cast<__nv_bfloat16*>(out), p);
   return cudaGetLastError();
 }
 

@@ -81,21 +81,10 @@ int64_t fwd_region(const moe_config& c, int fmt, void* scratch, FwdScratch* f) {
   return off;
 }
 
-// The backward's: the weights, gate-up and its gradient in bf16.
-struct BwdScratch {
-  uint8_t *W13, *W2, *GU, *dGU;
-};
-int64_t bwd_region(const moe_config& c, void* scratch, BwdScratch* b) {
-  const int64_t R = rows_max(c), G = c.E + c.n_shared, H = c.H, F = c.F;
-  const int64_t sizes[4] = {G * 2 * F * H * 2, G * H * F * 2, R * 2 * F * 2, R * 2 * F * 2};
-  int64_t off = 4096;
-  uint8_t* ptr[4];
-  for (int i = 0; i < 4; ++i) {
-    ptr[i] = scratch ? static_cast<uint8_t*>(scratch) + off : nullptr;
-    off += up256(sizes[i]);
-  }
-  if (b) *b = BwdScratch{ptr[0], ptr[1], ptr[2], ptr[3]};
-  return off;
+// The backward's: [dG | dU] between the products, without the weights' scales.
+constexpr int64_t kDguOffset = 4096;
+int64_t bwd_region(const moe_config& c) {
+  return kDguOffset + up256(rows_max(c) * 2 * c.F * 2);
 }
 
 moe_status check_layer(const moe_config* cfg, const moe_fp4_experts* ex) {
@@ -126,7 +115,7 @@ moe_status moe_fp4_query_sizes(const moe_config* cfg, int32_t format, moe_fp4_si
   if (cfg->dtype != MOE_DTYPE_BF16 || cfg->weights_in_expert || cfg->stash_pool_pages)
     return MOE_ERR_UNSUPPORTED;
   out->fwd_scratch_bytes = fwd_region(*cfg, format, nullptr, nullptr);
-  out->bwd_scratch_bytes = bwd_region(*cfg, nullptr, nullptr);
+  out->bwd_scratch_bytes = bwd_region(*cfg);
   return MOE_OK;
 }
 
@@ -225,22 +214,20 @@ moe_status moe_fp4_ffn_bwd(const moe_config* cfg, const moe_fp4_experts* ex, con
   cudaStream_t s = (cudaStream_t)stream;
   const int fmt = ex->W13.format, G = cfg->E + cfg->n_shared;
   const int64_t R = rows_max(*cfg), H = cfg->H, F = cfg->F;
-  BwdScratch w;
-  bwd_region(*cfg, scratch, &w);
+  uint8_t* dGU = static_cast<uint8_t*>(scratch) + kDguOffset;
   int32_t* st = status_of(scratch);
-  FP4_CUDA(launch_fp4_dequantize(fmt, static_cast<const uint8_t*>(ex->W2.codes),
-                                 static_cast<const uint8_t*>(ex->W2.scales), G, H, F, 0, w.W2, F,
-                                 s));
-  FP4_CUDA(launch_fp4_dequantize(fmt, static_cast<const uint8_t*>(ex->W13.codes),
-                                 static_cast<const uint8_t*>(ex->W13.scales), G, 2 * F, H, 0,
-                                 w.W13, H, s));
-  FP4_CUDA(launch_fp4_ckpt_expand(static_cast<const uint8_t*>(ckpt),
-                                  static_cast<const uint8_t*>(ckpt_scale), R, 2 * F, counts,
-                                  offsets, G, w.GU, st, s));
-  FP4_CUDA(launch_ffn_fc2_dgrad(*cfg, dO_perm, counts, offsets, w.W2, w.GU, w.dGU, st, s));
-  FP4_CUDA(launch_ffn_fc1_dgrad_alpha(*cfg, w.dGU, counts, offsets, w.W13, ex->alpha13, ex->alpha2,
-                                      ex->W13.scale_log2 + ex->W2.scale_log2, token_of, dlogits,
-                                      W_r, dX_perm, st, s));
+  const Fp4Problem down{fmt, G, R, F, H, static_cast<const uint8_t*>(dO_perm), nullptr,
+                        static_cast<const uint8_t*>(ex->W2.codes),
+                        static_cast<const uint8_t*>(ex->W2.scales), counts, offsets, nullptr, 0,
+                        false, cfg->T};
+  FP4_CUDA(launch_fp4_dgrad_swiglu(down, static_cast<const uint8_t*>(ckpt),
+                                   static_cast<const uint8_t*>(ckpt_scale), dGU, st, s));
+  const Fp4Problem up{fmt, G, R, H, 2 * F, dGU, nullptr,
+                      static_cast<const uint8_t*>(ex->W13.codes),
+                      static_cast<const uint8_t*>(ex->W13.scales), counts, offsets, ex->alpha13,
+                      ex->W13.scale_log2 + ex->W2.scale_log2, false, cfg->T};
+  FP4_CUDA(launch_fp4_dgrad_out(up, ex->alpha2, dX_perm, token_of, dlogits, W_r, cfg->E, cfg->T,
+                                st, s));
   return MOE_OK;
 }
 

@@ -27,11 +27,7 @@ enum Epi : int { kEpiSwigluFwd = 0, kEpiStore = 1, kEpiSwigluBwd = 2, kEpiWgrad 
                  // the layer with the routing weight inside the expert: FC1 writes
                  // h_s = w_row silu(G) U; the FC2 data gradient scales dh_s by w_row
                  // and writes each row's partial <dh_s, h> for the weight's gradient
-                 kEpiSwigluFwdW = 7, kEpiSwigluBwdW = 8,
-                 // FC1 data gradient of 4-bit experts: the accumulator times the
-                 // group's scales, plus the router term
-                 kEpiDgradAlpha = 9 };
-constexpr bool dgrad_router(int epi) { return epi == kEpiDgradRouter || epi == kEpiDgradAlpha; }
+                 kEpiSwigluFwdW = 7, kEpiSwigluBwdW = 8 };
 constexpr bool swiglu_fwd(int epi) { return epi == kEpiSwigluFwd || epi == kEpiSwigluFwdW; }
 constexpr bool swiglu_bwd(int epi) { return epi == kEpiSwigluBwd || epi == kEpiSwigluBwdW; }
 
@@ -73,11 +69,6 @@ struct Params {
   float* dw_part;
   __nv_bfloat16* h_out;       // SwiGLU-bwd: h rewritten from GU ([rows, F]), or null
   int dw_nt;
-  // kEpiDgradAlpha: the accumulator's factor, alpha_a[g] alpha_b[g] alpha_unit
-  // (a null array counts as ones)
-  const float* alpha_a;
-  const float* alpha_b;
-  float alpha_unit;
   // FP8 block-scaled operands (grouped_gemm_fp8.cu): UE8M0 scale atoms of A
   // ([R/128][sfa_kg]) and of B ([G * sfb_nb][sfb_kg]), fp8_layout.cuh
   const uint8_t* sfa;

@@ -51,12 +51,12 @@ __device__ __forceinline__ void epilogue_tile(const Params& p, const CUtensorMap
   // router term of this warp's row (lane) for the FC1 data gradient
   float rd = 0.f;
   const float* rw = nullptr;
-  if (dgrad_router(EPI) && g < p.router_E) {
+  if (EPI == kEpiDgradRouter && g < p.router_E) {
     const int t = p.token_of[row0 + lane];
     if (t >= 0 && t < p.router_T) rd = p.dlogits[(long long)t * p.router_E + g];
     rw = p.W_r + (long long)g * p.N + f0;
   }
-  if (EPI == kEpiStore || EPI == kEpiWgrad || dgrad_router(EPI) || EPI == kEpiAddBf16) {
+  if (EPI == kEpiStore || EPI == kEpiWgrad || EPI == kEpiDgradRouter || EPI == kEpiAddBf16) {
     // plain bf16 output in 32 x 64 boxes: 128-byte rows (128-byte swizzle), so
     // every store fills whole 128-byte lines; 64 accumulator columns per
     // tensor-memory wait
@@ -71,16 +71,7 @@ __device__ __forceinline__ void epilogue_tile(const Params& p, const CUtensorMap
         ptx::tmem_ld32(tbase + c + 32, r1);
         ptx::tmem_ld_wait();
       }
-      if (EPI == kEpiDgradAlpha) {
-        const float a = (p.alpha_a ? p.alpha_a[g] : 1.f) * (p.alpha_b ? p.alpha_b[g] : 1.f) *
-                        p.alpha_unit;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          r0[i] = __float_as_uint(__uint_as_float(r0[i]) * a);
-          r1[i] = __float_as_uint(__uint_as_float(r1[i]) * a);
-        }
-      }
-      if (dgrad_router(EPI) && rw) {
+      if (EPI == kEpiDgradRouter && rw) {
         // fp32 accumulator + dlogits * W_r, rounded to bf16 once
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
@@ -1073,41 +1064,6 @@ cudaError_t launch_ffn_fc1_dgrad(const moe_config& c, const void* dGU, const int
   if (use_pairs(c, c.H)) return run_pair<kEpiDgradRouter, 0, 1>(a, b, oc, oc2, p, s);
   return bn == 256 ? run<kEpiDgradRouter, 256, 0, 1, 4>(a, b, oc, oc2, p, s)
                    : run<kEpiDgradRouter, 128, 0, 1, 6>(a, b, oc, oc2, p, s);
-}
-
-// The same for 4-bit experts: the product times the experts' scales; the router
-// term only where dlogits is given.
-cudaError_t launch_ffn_fc1_dgrad_alpha(const moe_config& c, const void* dGU, const int32_t* counts,
-                                       const int32_t* offsets, const void* W13,
-                                       const float* alpha_a, const float* alpha_b, int unit_log2,
-                                       const int32_t* token_of, const float* dlogits,
-                                       const float* W_r, void* dX_perm, int32_t* status,
-                                       cudaStream_t s) {
-  const int64_t R = rows_max(c);
-  const int G = c.E + c.n_shared;
-  const int bn = (c.H % 256 == 0) ? 256 : 128;
-  CUtensorMap a, b, oc;
-  if (!make_map(&a, dGU, 2ULL * c.F, R, 128) ||
-      !make_map_chunks(&b, W13, c.H, (uint64_t)G * 2 * c.F, use_pairs(c, c.H) ? 2 : bn / 64) ||
-      !make_out_map_w64(&oc, dX_perm, c.H, R))
-    return cudaErrorInvalidValue;
-  Params p = base_params(c, counts, offsets, status);
-  p.N = c.H;
-  p.K = 2 * c.F;
-  p.b_rows = 2 * c.F;
-  p.out = static_cast<__nv_bfloat16*>(dX_perm);
-  p.ldo = c.H;
-  p.alpha_a = alpha_a;
-  p.alpha_b = alpha_b;
-  p.alpha_unit = ldexpf(1.f, unit_log2);
-  p.token_of = token_of;
-  p.dlogits = dlogits;
-  p.W_r = W_r;
-  p.router_E = dlogits ? c.E : 0;
-  p.router_T = c.T;
-  if (use_pairs(c, c.H)) return run_pair<kEpiDgradAlpha, 0, 1>(a, b, oc, oc, p, s);
-  return bn == 256 ? run<kEpiDgradAlpha, 256, 0, 1, 4>(a, b, oc, oc, p, s)
-                   : run<kEpiDgradAlpha, 128, 0, 1, 6>(a, b, oc, oc, p, s);
 }
 
 cudaError_t launch_ffn_wgrad_fc2(const moe_config& c, const void* dO_perm, const void* h,

@@ -211,17 +211,17 @@ cudaError_t launch_fp4_swiglu(const Fp4Problem& q, uint8_t* hq, uint8_t* hsf, in
                               uint8_t* ckpt, uint8_t* ckpt_sf, const Fp4Split& sp, int32_t* status,
                               cudaStream_t s);
 
-// The 8-bit checkpoint back as bf16 (rows past a segment's counts, up to its
-// 128-row block, become zero).
-cudaError_t launch_fp4_ckpt_expand(const uint8_t* ckpt, const uint8_t* ckpt_sf, int64_t rows,
-                                   int64_t cols, const int32_t* counts, const int32_t* offsets,
-                                   int segments, void* out, int32_t* status, cudaStream_t s);
-cudaError_t launch_ffn_fc1_dgrad_alpha(const moe_config& c, const void* dGU, const int32_t* counts,
-                                       const int32_t* offsets, const void* W13,
-                                       const float* alpha_a, const float* alpha_b, int unit_log2,
-                                       const int32_t* token_of, const float* dlogits,
-                                       const float* W_r, void* dX_perm, int32_t* status,
-                                       cudaStream_t s);
+// Their data gradients: A bf16 [rows, K] by the 4-bit weights [G, K, N] (q.a is A;
+// q.sfa and q.early are not used). FC2's, times SwiGLU's derivative from the 8-bit
+// checkpoint -> dGU [rows, 2N] bf16, without the weights' scales; FC1's, with both
+// products' scales (q.alpha, alpha_b, q.unit_log2) and the router's term where
+// dlogits is given -> dX [rows, N] bf16.
+cudaError_t launch_fp4_dgrad_swiglu(const Fp4Problem& q, const uint8_t* ckpt,
+                                    const uint8_t* ckpt_sf, void* dGU, int32_t* status,
+                                    cudaStream_t s);
+cudaError_t launch_fp4_dgrad_out(const Fp4Problem& q, const float* alpha_b, void* dX,
+                                 const int32_t* token_of, const float* dlogits, const float* W_r,
+                                 int router_E, int router_T, int32_t* status, cudaStream_t s);
 
 // Router logits for E % 128 == 0 on the tensor cores (W3 = W_r split in three bf16 parts).
 cudaError_t launch_router_logits_tc(const moe_config& c, const void* x, const void* W3,

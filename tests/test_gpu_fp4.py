@@ -380,6 +380,26 @@ def test_ffn_rows_do_not_depend_on_the_batch():
 
 
 # ------------------------------------------------------------------- backward
+def test_backward_reports_bad_segments():
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=DEV)  # noqa: E731
+    rng = np.random.default_rng(12)
+    cfg = B.config(MoEShape("b", T=200, H=128, E=2, k=1, F=128))
+    R = B.moe_query_sizes(cfg).rows_max
+    ex = experts_of(0, rng, 2, 128, 128)
+    dO = torch.ones(R, 128, device=DEV, dtype=torch.bfloat16)
+    ck = torch.full((R, 256), 0x38, dtype=torch.uint8, device=DEV)
+    cs = torch.full((R, 8), 127, dtype=torch.uint8, device=DEV)
+    sc = B.alloc_fp4_scratch(B.moe_fp4_query_sizes(cfg, 0).bwd_scratch_bytes)
+    for counts, offsets in (([5, R], [0, 128]), ([5, -2], [0, 128]), ([5, 5], [0, 64]),
+                            ([5, 5], [0, -128])):
+        B.moe_clear_device_status(sc)
+        dX = torch.full((R, 128), 7.0, device=DEV, dtype=torch.bfloat16)
+        B.moe_fp4_ffn_bwd(cfg, ex[0], dO, ck, cs, i32(counts), i32(offsets), None, None, None, dX, sc)
+        assert B.moe_last_device_status(sc) == 6
+        got = f64(dX)
+        assert (got[:5] != 7.0).any() and (got[5:128] == 0).all() and (got[128:] == 7.0).all()
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("counts,H,F,router", [
     ([1], 128, 128, False), ([0, 3, 130, 0, 64], 128, 384, True), ([40, 129], 256, 640, False),
@@ -431,7 +451,7 @@ def test_ffn_backward_matches_oracle(fmt, counts, H, F, router):
         rel = np.linalg.norm(got[r] - ref) / np.linalg.norm(ref)
         assert rel < 2.0 ** -8 * 1.2, rel
         pad = got[off[g] + c:off[g + 1]]
-        assert ((pad == 0) | (pad == 7.0)).all()
+        assert (pad == 0).all()
 
 
 # -------------------------------------------------------------- a layer, a graph
