@@ -351,13 +351,15 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     }
   } else if (warp >= kD4ConvWarp) {  // up to kD4CodeWarp - 1
     // ------------------------------------------------------ codes to values
-    // Thread: rows t / 4 + 16 i of the k-block and, in both 64-column halves, the 16
-    // columns 16 (t % 4) ..: eight threads then store to eight distinct 16-byte
-    // bank groups.
+    // Lane: row lane / 4 of eight rows, the 32 columns 32 (lane % 4) .., so that a warp
+    // reads 512 consecutive bytes of codes. Its four 16-byte pieces of values go out
+    // in the order 0 1 2 3, or 2 3 0 1 in the right 64 columns: eight lanes then store
+    // to eight distinct 16-byte bank groups (piece ^ (row % 8), two rows, four lanes).
     constexpr int kRows = 32 * kD4ConvWarps / kD4Teams / 4;      // rows of a pass
     const int team = (warp - kD4ConvWarp) / (kD4ConvWarps / kD4Teams);
     const int t = (tid - kD4ConvWarp * 32) % (32 * kD4ConvWarps / kD4Teams);
     const int trow = t >> 2, sub = t & 3;
+    const int half = sub >> 1;                                   // which 64 columns
     uint32_t stage = 0, phase = 0, slot = 0, cphase = 0;
     int turn = 0;
     bool ok = true;
@@ -376,18 +378,17 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
           uint8_t* sB = sbase + stage * C::STAGE + kD4ABytes;
           // all loads before the first store (the compiler cannot tell them apart)
           constexpr int kPass = BK / kRows;
-          uint2 c[kPass][2];
-          uint32_t f[kPass][2];
+          uint4 c[kPass];
+          uint32_t f[kPass];                                     // the columns' scale bytes
 #pragma unroll
           for (int i = 0; i < kPass; ++i) {
             const int row = trow + kRows * i;
             const int r = (kb & 1) * 64 + row;                   // row of the 128-row slab
             const uint8_t* sf = rawp + kD4CodeBytes + (r & 31) * 16 + (r >> 5) * 4;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              c[i][h] = *reinterpret_cast<const uint2*>(rawp + row * 64 + h * 32 + sub * 8);
-              f[i][h] = FMT == MOE_FP4_NV ? sf[h * f4::kAtomBytes + sub] : sf[2 * h + (sub >> 1)];
-            }
+            c[i] = *reinterpret_cast<const uint4*>(rawp + row * 64 + sub * 16);
+            f[i] = FMT == MOE_FP4_NV
+                       ? *reinterpret_cast<const uint16_t*>(sf + half * f4::kAtomBytes + (sub & 1) * 2)
+                       : sf[sub];
           }
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bar_code_empty + 8 * slot);
@@ -398,19 +399,22 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 #pragma unroll
           for (int i = 0; i < kPass; ++i) {
             const int row = trow + kRows * i;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t s = scale_pair<FMT>(f[i][h]);
-              uint8_t* dst = sB + row * 128 + h * 8192;
-              *reinterpret_cast<uint4*>(dst + (((2 * sub) ^ (row & 7)) << 4)) =
-                  weight8(c[i][h].x, s);
-              *reinterpret_cast<uint4*>(dst + (((2 * sub + 1) ^ (row & 7)) << 4)) =
-                  weight8(c[i][h].y, s);
-            }
+            const uint32_t s0 = scale_pair<FMT>(f[i] & 255u);
+            const uint32_t s1 = FMT == MOE_FP4_NV ? scale_pair<FMT>(f[i] >> 8) : s0;
+            uint8_t* dst = sB + row * 128 + half * 8192;
+            // pieces 0, 1 (the first 16 columns) and 2, 3, swapped in the right half
+            const uint32_t wa = half ? c[i].z : c[i].x, wb = half ? c[i].w : c[i].y;
+            const uint32_t wc = half ? c[i].x : c[i].z, wd = half ? c[i].y : c[i].w;
+            const uint32_t sa = half ? s1 : s0, sc = half ? s0 : s1;
+            const int first = 4 * (sub & 1) + 2 * half, x = row & 7;
+            *reinterpret_cast<uint4*>(dst + ((first ^ x) << 4)) = weight8(wa, sa);
+            *reinterpret_cast<uint4*>(dst + (((first + 1) ^ x) << 4)) = weight8(wb, sa);
+            *reinterpret_cast<uint4*>(dst + (((first ^ 2) ^ x) << 4)) = weight8(wc, sc);
+            *reinterpret_cast<uint4*>(dst + ((((first ^ 2) + 1) ^ x) << 4)) = weight8(wd, sc);
           }
           ptx::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster(leader_full + 8 * stage);
+          if (lane == 0) ptx::mbar_arrive_cluster_async(leader_full + 8 * stage);
         }
         if (++turn == kD4Teams) turn = 0;
         if (++slot == kD4CodeSlots) {

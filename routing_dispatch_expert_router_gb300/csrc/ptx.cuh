@@ -444,6 +444,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                :: "r"(cluster_addr) : "memory");
 }
 
+// The same for shared-memory data that only the async proxy reads, and that this
+// CTA's threads have made visible to it (fence.proxy.async) before: the arrival then
+// orders nothing at cluster scope, which takes under a hundred cycles where
+// release.cluster takes 1600.
+__device__ __forceinline__ void mbar_arrive_cluster_async(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+}
+
 // 2D tiled load into this CTA's shared memory whose completion is counted on an
 // mbarrier that may live in the peer CTA of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, uint32_t bar_cluster,
