@@ -17,15 +17,21 @@
 // CTA pairs, 256 x 256 tiles, one persistent CTA pair per two SMs, 480 threads:
 //   warp 0      TMA producer of A (one lane): per 64-deep k-block this CTA's 128 rows;
 //   warp 14     TMA producer of the codes and scale atoms of 64 weight rows x 128
-//               columns a k-block (one lane), in a ring of their own that is small
-//               and therefore deeper: a stage of A and B is then not held while
-//               codes are on their way (with one ring: 0.68 us a k-block);
+//               columns a k-block (one lane), in a ring of their own: a stage of A and
+//               B is then not held while codes are on their way;
 //   warp 1      MMA issuer (one lane of the even CTA): M=256 N=256 K=16;
 //   warps 2-5   epilogue, one tensor-memory lane quarter each;
 //   warps 6-13  the codes' values into B's stage (MN-major, 128-byte swizzle), 8192
 //               elements a k-block; teams of two warps take k-blocks in turn, so that
-//               one team's wait, loads and fence pass under the others' work (all
-//               eight on one k-block: 1.12 us a k-block, D4_TEAMS).
+//               one team's waits, loads and stores pass under the others' work.
+// Both products of that layer (32768 rows) take 1334 us: 0.42 us a k-block, of which
+// the MMAs and A's loads alone take 0.34. What is left is shared memory's bandwidth:
+// the MMAs' reads, A's arrival and the codes' way in and values' way out fill about 600
+// of 780 cycles a k-block. On the way: all eight warps on one k-block 3306 us, teams of
+// four warps 2608, of two 1820; without bank conflicts 1772; the arrivals at the even
+// CTA's barrier without release.cluster (1600 cycles each) 1334. Tiles of 512 x 128 (B
+// made once for 512 rows) take 2057: MMAs of N=128 run at half rate. 512 x 256 with one
+// set of accumulators: 1850 before the arrivals changed (1772 then).
 #include "fp4_layout.cuh"
 #include "gemm_common.cuh"
 
@@ -314,7 +320,7 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + acc * kD4BN;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!ptx::mbar_wait_cluster(bar_full + 8 * stage, phase, kWaitBudget, abort_flag)) {
+          if (!ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget, abort_flag)) {
             ok = false;
             break;
           }
