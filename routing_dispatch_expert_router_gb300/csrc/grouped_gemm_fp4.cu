@@ -10,9 +10,10 @@
 // core applies them, so the kernel only moves bytes, 0.5625 (NV) or 0.53 (MX)
 // of them per element.
 //
-// One persistent kernel, one CTA per SM, 448 threads:
-//   warp 0       TMA producer (one lane): per 256-deep k-block (128 bytes of codes
-//                a row) A's rows, 256 rows of B and their scale atoms;
+// One persistent kernel, one CTA per SM, 480 threads:
+//   warp 0       TMA producer of the weights (one lane): per 256-deep k-block (128
+//                bytes of codes a row) 256 rows of B and their scale atoms;
+//   warp 14      TMA producer of the rows (one lane): A's rows and atoms;
 //   warp 1       MMA issuer (one lane) and tensor-memory owner: four M=128 N=256
 //                K=64 MMAs a k-block;
 //   warps 2-9    epilogue, two warps per tensor-memory lane quarter, 128 of the
@@ -39,14 +40,13 @@
 namespace moe {
 namespace gg {
 
-constexpr int kF4Threads = 448;
+constexpr int kF4Threads = 480;
 constexpr int kF4ScaleWarp = 10;                       // the first of the four
+constexpr int kF4RowWarp = 14;
 constexpr int kF4BN = 256;
 constexpr int kF4RowBytes = f4::kStep / 2;             // codes of a k-block's row: 128 bytes
 constexpr int kF4BBytes = kF4BN * kF4RowBytes;         // 32 KB
 constexpr int kF4EpiWarps = 8;
-constexpr int kF4Ahead = 8;                            // k-blocks that an early start prefetches
-constexpr int kF4QueueOff = 4864;                      // stages without A yet, in the control block
 constexpr uint32_t kF4TmemCols = 512;
 constexpr uint32_t kF4SfCol = kF4BN;                   // first scale-factor column
 
@@ -60,7 +60,6 @@ struct Fp4Params {
   const float* alpha;          // [G], or null: 1
   float unit;                  // times alpha: the operands' tensor scales
   const uint8_t* sfa;          // A's atoms, [slabs][ka][512]
-  const uint8_t* sfb;          // B's, [G][slabs of N][ka][512]
   int ka;                      // atoms of a slab
   __nv_bfloat16* out;          // store: [rows, N]
   // swiglu: h in 4 bits for the next product (codes [rows, F / 2], atoms), and
@@ -76,7 +75,6 @@ struct Fp4Params {
   int64_t part_floats;
   int32_t* arrived;
   int arrived_n;
-  bool early;                  // started before the kernel before it is done
   int32_t* status;
 };
 
@@ -100,8 +98,6 @@ struct F4Cfg {
   // scale columns of a k-block: A's 4 per atom, then B's 8 per atom
   static constexpr int SLOT_COLS = 12 * ATOMS;
   static_assert(STAGES <= 8, "barrier arrays");
-  static_assert(kF4QueueOff >= 4608 + 33 * 4 && kF4QueueOff + STAGES * 12 <= kCtrlBytes,
-                "queue inside the control block, after the scan scratch");
   static_assert(SMEM <= 232448, "FP4 grouped GEMM shared memory");
   static_assert(kF4SfCol + STAGES * SLOT_COLS <= kF4TmemCols, "FP4 tensor-memory columns");
 };
@@ -338,6 +334,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
 grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmA32,
                         const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmSB,
                         const __grid_constant__ CUtensorMap tmC, const Fp4Params p) {
   using C = F4Cfg<FMT, AROWS>;
   constexpr bool NV = FMT == MOE_FP4_NV;
@@ -404,7 +401,7 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(bar_full + 8 * s, 1);
+      ptx::mbar_init(bar_full + 8 * s, 2);             // the two producers
       ptx::mbar_init(bar_empty + 8 * s, 1);
       ptx::mbar_init(bar_scales + 8 * s, 4);
     }
@@ -421,6 +418,7 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
     ptx::tma_prefetch_desc(&tmA);
     ptx::tma_prefetch_desc(&tmA32);
     ptx::tma_prefetch_desc(&tmB);
+    ptx::tma_prefetch_desc(&tmSB);
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -429,90 +427,36 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
   ptx::grid_launch_dependents();     // the next kernel's CTAs may start as these leave
 
   if (warp == 0) {
-    // ------------------------------------------------------------ producer
+    // ------------------------------------- producer of the weights' stages
     if (lane == 0) {
       uint32_t stage = 0, phase = 0;
       uint32_t issued_mask = 0, issued_phase = 0;
       bool ok = true;
-      const int64_t nslabs = f4::slabs(p.N);
-      const int64_t slab_bytes = (int64_t)p.ka * f4::kAtomBytes;
-      // Started early, this kernel fetches the weights of its first stages at once
-      // and their A rows when the kernel before it (which writes them) is done:
-      // `queue` of the last `queued` stages still lack them.
-      struct Todo { int kb, row0, boxes; };
-      Todo* queue = reinterpret_cast<Todo*>(ctrl + kF4QueueOff);
-      int queued = 0, hold = p.early ? kStages : 1;
-      auto load_a = [&]() {
-        if (hold > 1) ptx::grid_dependency_wait();
-        hold = 1;
-        uint32_t s = stage + kStages - queued;           // the first queued stage
-        for (int i = 0; i < queued; ++i, ++s) {
-          if (s >= kStages) s -= kStages;
-          const Todo d = queue[i];
-          const uint32_t fb = bar_full + 8 * s, sA = base + s * C::STAGE;
-          ptx::bulk_load(sf_u + s * C::SF_STAGE,
-                         p.sfa + d.row0 / 128 * slab_bytes + (int64_t)d.kb * C::SF_A, C::SF_A, fb);
-          if (AROWS == BM && d.boxes == 4) {
-            ptx::tma_load_2d(sA, &tmA, fb, d.kb * kF4RowBytes, d.row0);
-          } else {
-            for (int j = 0; j < d.boxes; ++j)
-              ptx::tma_load_2d(sA + 4096 * j, &tmA32, fb, d.kb * kF4RowBytes, d.row0 + 32 * j);
-          }
-        }
-        queued = 0;
-      };
       while (ok && w.next()) {
         const Tile t = decode(w.tile, prefix, mtiles, s_cnt, G, 0, p.K, NT, 0);
-        const int row0 = s_off[t.g] + t.mt * BM;
-        const int valid = min(BM, s_cnt[t.g] - t.mt * BM);
-        const int boxes = (valid + 31) / 32;             // 4: one 128-row box
-        int b0, b1;
-        if (EPI == kF4Swiglu) {
-          b0 = t.nt * (kF4BN / 2);                       // gate rows b0.., up rows F + b0..
-          b1 = F + b0;
-        } else {
-          b0 = t.nt * kF4BN;
-          b1 = b0 + 128;
-        }
-        const int64_t nb0 = b0 / 128, nb1 = min((int64_t)(b1 / 128), nslabs - 1);
-        const uint8_t* sfb0 = p.sfb + (t.g * nslabs + nb0) * slab_bytes;
-        const uint8_t* sfb1 = p.sfb + (t.g * nslabs + nb1) * slab_bytes;
+        // rows of B and their slab: of group g, or (swiglu) of the gate and up parts
+        // 2g, 2g + 1, both brought by one box
+        const int b0 = t.nt * (EPI == kF4Swiglu ? kF4BN / 2 : kF4BN);
+        const int part = EPI == kF4Swiglu ? 2 * t.g : t.g;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (!ptx::mbar_wait(bar_empty + 8 * stage, phase ^ 1u, kWaitBudget, abort_flag)) {
             ok = false;
             break;
           }
           const uint32_t fb = bar_full + 8 * stage;
-          ptx::mbar_arrive_expect_tx(fb, boxes * 4096 + kF4BBytes + C::SF_STAGE);
-          const uint32_t sB = base + stage * C::STAGE + C::A_BYTES;
-          const int k0 = kb * kF4RowBytes;
-          const int brow = t.g * p.N;
-          ptx::tma_load_2d(sB, &tmB, fb, k0, brow + b0);
-          ptx::tma_load_2d(sB + 16384, &tmB, fb, k0, brow + b1);
-          const uint32_t sfs = sf_u + stage * C::SF_STAGE;
-          const int64_t ao = (int64_t)kb * C::SF_A;
-          ptx::bulk_load(sfs + C::SF_A, sfb0 + ao, C::SF_A, fb);
-          ptx::bulk_load(sfs + 2 * C::SF_A, sfb1 + ao, C::SF_A, fb);
-          queue[queued++] = Todo{kb, row0, boxes};
+          ptx::mbar_arrive_expect_tx(fb, kF4BBytes + 2 * C::SF_A);
+          ptx::tma_load_3d(base + stage * C::STAGE + C::A_BYTES, &tmB, fb, kb * kF4RowBytes, b0,
+                           part);
+          ptx::tma_load_3d(sf_u + stage * C::SF_STAGE + C::SF_A, &tmSB, fb, kb * (C::SF_A / 8),
+                           b0 / 128, part);
           issued_mask |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
-          if (queued < hold) continue;
-          if (hold > 1) {
-            // all stages hold weights: the piece's next ones into L2 meanwhile
-            const int ahead = min(w.kb1, kb + 1 + kF4Ahead);
-            for (int k = kb + 1; k < ahead; ++k) {
-              ptx::tma_prefetch_2d(&tmB, k * kF4RowBytes, brow + b0);
-              ptx::tma_prefetch_2d(&tmB, k * kF4RowBytes, brow + b1);
-            }
-          }
-          load_a();
         }
       }
-      load_a();
       if (!ok) {
         record_status(p.status, MOE_ERR_TIMEOUT);
         *abort_flag = 1;
@@ -521,6 +465,47 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
       for (int s = 0; s < kStages; ++s)
         if (issued_mask & (1u << s))
           ptx::mbar_wait(bar_full + 8 * s, (issued_phase >> s) & 1u, kWaitBudget, nullptr);
+    }
+  } else if (warp == kF4RowWarp) {
+    // ----------------------------------------- producer of the rows' stages
+    // A thread of its own: one thread issues a load in about 0.15 us, four a k-block;
+    // and an early start holds the rows (which the kernel before this one writes) back
+    // while the weights are already on their way.
+    if (lane == 0) {
+      ptx::grid_dependency_wait();
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      const int64_t slab_bytes = (int64_t)p.ka * f4::kAtomBytes;
+      while (ok && w.next()) {
+        const Tile t = decode(w.tile, prefix, mtiles, s_cnt, G, 0, p.K, NT, 0);
+        const int row0 = s_off[t.g] + t.mt * BM;
+        const int valid = min(BM, s_cnt[t.g] - t.mt * BM);
+        const int boxes = (valid + 31) / 32;             // 4: one 128-row box
+        const uint8_t* sfa = p.sfa + row0 / 128 * slab_bytes;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (!ptx::mbar_wait(bar_empty + 8 * stage, phase ^ 1u, kWaitBudget, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = bar_full + 8 * stage, sA = base + stage * C::STAGE;
+          ptx::mbar_arrive_expect_tx(fb, boxes * 4096 + C::SF_A);
+          if (AROWS == BM && boxes == 4) {
+            ptx::tma_load_2d(sA, &tmA, fb, kb * kF4RowBytes, row0);
+          } else {
+            for (int i = 0; i < boxes; ++i)
+              ptx::tma_load_2d(sA + 4096 * i, &tmA32, fb, kb * kF4RowBytes, row0 + 32 * i);
+          }
+          ptx::bulk_load(sf_u + stage * C::SF_STAGE, sfa + (int64_t)kb * C::SF_A, C::SF_A, fb);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        record_status(p.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -725,8 +710,8 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
 
 template <int FMT, int EPI, int AROWS>
 static cudaError_t run_fp4_rows(const CUtensorMap& a, const CUtensorMap& a32, const CUtensorMap& b,
-                           const CUtensorMap& c, const Fp4Params& p, bool early,
-                           cudaStream_t s) {
+                                const CUtensorMap& sb, const CUtensorMap& c, const Fp4Params& p,
+                                bool early, cudaStream_t s) {
   auto kern = grouped_gemm_fp4_kernel<FMT, EPI, AROWS>;
   constexpr int smem = F4Cfg<FMT, AROWS>::SMEM;
   static bool attr_set = false;
@@ -745,28 +730,55 @@ static cudaError_t run_fp4_rows(const CUtensorMap& a, const CUtensorMap& a32, co
   at[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = at;
   lc.numAttrs = early ? 1 : 0;
-  return cudaLaunchKernelEx(&lc, kern, a, a32, b, c, p);
+  return cudaLaunchKernelEx(&lc, kern, a, a32, b, sb, c, p);
 }
 
 template <int EPI>
 static cudaError_t run_fp4(const Fp4Problem& q, const CUtensorMap& a, const CUtensorMap& a32,
-                           const CUtensorMap& b, const CUtensorMap& c, const Fp4Params& p,
-                           cudaStream_t s) {
+                           const CUtensorMap& b, const CUtensorMap& sb, const CUtensorMap& c,
+                           const Fp4Params& p, cudaStream_t s) {
   const bool nv = q.fmt == MOE_FP4_NV;
   if (q.most_rows <= 32)
-    return nv ? run_fp4_rows<MOE_FP4_NV, EPI, 32>(a, a32, b, c, p, q.early, s)
-              : run_fp4_rows<MOE_FP4_MX, EPI, 32>(a, a32, b, c, p, q.early, s);
+    return nv ? run_fp4_rows<MOE_FP4_NV, EPI, 32>(a, a32, b, sb, c, p, q.early, s)
+              : run_fp4_rows<MOE_FP4_MX, EPI, 32>(a, a32, b, sb, c, p, q.early, s);
   if (q.most_rows <= 64)
-    return nv ? run_fp4_rows<MOE_FP4_NV, EPI, 64>(a, a32, b, c, p, q.early, s)
-              : run_fp4_rows<MOE_FP4_MX, EPI, 64>(a, a32, b, c, p, q.early, s);
-  return nv ? run_fp4_rows<MOE_FP4_NV, EPI, 128>(a, a32, b, c, p, q.early, s)
-            : run_fp4_rows<MOE_FP4_MX, EPI, 128>(a, a32, b, c, p, q.early, s);
+    return nv ? run_fp4_rows<MOE_FP4_NV, EPI, 64>(a, a32, b, sb, c, p, q.early, s)
+              : run_fp4_rows<MOE_FP4_MX, EPI, 64>(a, a32, b, sb, c, p, q.early, s);
+  return nv ? run_fp4_rows<MOE_FP4_NV, EPI, 128>(a, a32, b, sb, c, p, q.early, s)
+            : run_fp4_rows<MOE_FP4_MX, EPI, 128>(a, a32, b, sb, c, p, q.early, s);
 }
 
 // 4-bit operand: [rows, K / 2] bytes, box of 128 bytes x box_rows.
 static bool make_map_fp4(CUtensorMap* m, const void* ptr, int64_t K, int64_t rows,
                          uint32_t box_rows) {
   return make_map_u8(m, ptr, (uint64_t)K / 2, (uint64_t)rows, box_rows);
+}
+
+// Weights in 4 bits as `parts` blocks of `rows` rows, a box of 128 bytes x box_rows x
+// box_parts, and their scale atoms, 8 bytes an element: one k-block's atoms of as many
+// slabs. What lies past a block's rows reads as zero.
+static bool make_map_weights(CUtensorMap* codes, CUtensorMap* scales, const Fp4Problem& q,
+                             int64_t rows, int64_t parts, uint32_t box_rows, uint32_t box_parts) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t kb = (cuuint64_t)q.K / 2, sl = (cuuint64_t)f4::slabs(rows);
+  const cuuint64_t sb = (cuuint64_t)f4::atoms_k(q.fmt, q.K) * f4::kAtomBytes;
+  const cuuint32_t es[3] = {1, 1, 1};
+  const cuuint64_t d[3] = {kb, (cuuint64_t)rows, (cuuint64_t)parts};
+  const cuuint64_t st[2] = {kb, kb * (cuuint64_t)rows};
+  const cuuint32_t box[3] = {kF4RowBytes, box_rows, box_parts};
+  const cuuint64_t ds[3] = {sb / 8, sl, (cuuint64_t)parts};
+  const cuuint64_t sts[2] = {sb, sb * sl};
+  const cuuint32_t boxs[3] = {(cuuint32_t)f4::step_atoms(q.fmt) * f4::kAtomBytes / 8,
+                              box_rows / 128, box_parts};
+  return fn(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(q.b), d, st, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+             CUDA_SUCCESS &&
+         fn(scales, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 3, const_cast<uint8_t*>(q.sfb), ds, sts, boxs,
+            es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+             CUDA_SUCCESS;
 }
 
 static Fp4Params fp4_params(const Fp4Problem& q, const Fp4Split& sp, int32_t* status) {
@@ -780,13 +792,11 @@ static Fp4Params fp4_params(const Fp4Problem& q, const Fp4Split& sp, int32_t* st
   p.alpha = q.alpha;
   p.unit = ldexpf(1.f, q.unit_log2);
   p.sfa = q.sfa;
-  p.sfb = q.sfb;
   p.ka = (int)f4::atoms_k(q.fmt, q.K);
   p.part = sp.part;
   p.part_floats = sp.part_floats;
   p.arrived = sp.arrived;
   p.arrived_n = sp.arrived_n;
-  p.early = q.early;
   p.status = status;
   return p;
 }
@@ -798,23 +808,23 @@ using namespace gg;
 cudaError_t launch_fp4_gemm(const Fp4Problem& q, void* out, const Fp4Split& sp, int32_t* status,
                             cudaStream_t s) {
   if (q.rows == 0 || q.N == 0) return cudaSuccess;
-  CUtensorMap a, a32, b, c;
+  CUtensorMap a, a32, b, sb, c;
   if (!make_map_fp4(&a, q.a, q.K, q.rows, 128) || !make_map_fp4(&a32, q.a, q.K, q.rows, 32) ||
-      !make_map_fp4(&b, q.b, q.K, (int64_t)q.G * q.N, 128) ||
+      !make_map_weights(&b, &sb, q, q.N, q.G, 256, 1) ||
       !make_out_map(&c, out, (uint64_t)q.N, (uint64_t)q.rows))
     return cudaErrorInvalidValue;
   Fp4Params p = fp4_params(q, sp, status);
   p.out = static_cast<__nv_bfloat16*>(out);
-  return run_fp4<kF4Store>(q, a, a32, b, c, p, s);
+  return run_fp4<kF4Store>(q, a, a32, b, sb, c, p, s);
 }
 
 cudaError_t launch_fp4_swiglu(const Fp4Problem& q, uint8_t* hq, uint8_t* hsf, int h_scale_log2,
                               uint8_t* ckpt, uint8_t* ckpt_sf, const Fp4Split& sp, int32_t* status,
                               cudaStream_t s) {
   if (q.rows == 0) return cudaSuccess;
-  CUtensorMap a, a32, b;
+  CUtensorMap a, a32, b, sb;
   if (!make_map_fp4(&a, q.a, q.K, q.rows, 128) || !make_map_fp4(&a32, q.a, q.K, q.rows, 32) ||
-      !make_map_fp4(&b, q.b, q.K, (int64_t)q.G * q.N, 128))
+      !make_map_weights(&b, &sb, q, q.N / 2, 2 * (int64_t)q.G, 128, 2))
     return cudaErrorInvalidValue;
   Fp4Params p = fp4_params(q, sp, status);
   p.hq = hq;
@@ -823,7 +833,7 @@ cudaError_t launch_fp4_swiglu(const Fp4Problem& q, uint8_t* hq, uint8_t* hsf, in
   p.hdown = ldexpf(1.f, -h_scale_log2);
   p.ckpt = ckpt;
   p.ckpt_sf = ckpt_sf;
-  return run_fp4<kF4Swiglu>(q, a, a32, b, b, p, s);
+  return run_fp4<kF4Swiglu>(q, a, a32, b, sb, b, p, s);
 }
 
 }  // namespace moe

@@ -79,12 +79,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint
       :: "r"(dst), "l"(tmap), "r"(bar), "r"(c0), "r"(c1), "r"(c2) : "memory");
 }
 
-// 2D tiled prefetch global -> L2.
-__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int32_t c0, int32_t c1) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];"
-               :: "l"(tmap), "r"(c0), "r"(c1) : "memory");
-}
-
 // Adds at device scope and returns the old value, ordering this thread's earlier
 // accesses (and those it has synchronised with) before it and its later ones after.
 __device__ __forceinline__ int atom_add_acq_rel(int* p, int v) {
