@@ -30,28 +30,29 @@ struct Rows {
   int32_t* status;
 };
 
-// First row (in the tensor) and row count of slab `sl`; 0 rows when it is empty.
+// First row (in the tensor) and row count of slab `sl`; 0 rows when it is empty. All
+// threads of the block call it (ragged form: each looks at some of the segments, one
+// load deep where a search would be as deep as their number's logarithm).
 __device__ __forceinline__ int slab_rows(const Rows& p, int64_t sl, int64_t& row0) {
   if (!p.counts) {
     const int64_t per = f4::slabs(p.rows), g = sl / per, r = (sl - g * per) * 128;
     row0 = g * p.rows + r;
     return (int)min((int64_t)128, p.rows - r);
   }
+  __shared__ int found;
   row0 = sl * 128;
-  int lo = 0, hi = p.segments - 1;               // the last segment that starts at or before row0
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.offsets[mid] <= row0) lo = mid;
-    else hi = mid - 1;
+  if (threadIdx.x == 0) found = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.segments; i += blockDim.x) {
+    const int64_t off = p.offsets[i], cnt = p.counts[i];
+    if (off < 0 || off % 128 || cnt < 0 || off + cnt > p.rows) {
+      record_status(p.status, MOE_ERR_DEVICE_CHECK);
+    } else if (off <= row0 && row0 < off + cnt) {
+      found = (int)min((int64_t)128, off + cnt - row0);
+    }
   }
-  // (empty segments share their start with the next one; the search takes the last)
-  const int64_t off = p.offsets[lo], cnt = p.counts[lo];
-  if (off < 0 || off % 128 || cnt < 0 || off + cnt > p.rows) {
-    if (threadIdx.x == 0) record_status(p.status, MOE_ERR_DEVICE_CHECK);
-    return 0;
-  }
-  const int64_t n = off + cnt - row0;
-  return row0 < off || n <= 0 ? 0 : (int)min((int64_t)128, n);
+  __syncthreads();
+  return found;
 }
 
 template <int FMT, bool VALUES>
