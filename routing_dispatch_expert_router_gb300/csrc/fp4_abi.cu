@@ -225,7 +225,7 @@ moe_status moe_fp4_ffn_bwd(const moe_config* cfg, const moe_fp4_experts* ex, con
   const Fp4Problem up{fmt, G, R, H, 2 * F, dGU, nullptr,
                       static_cast<const uint8_t*>(ex->W13.codes),
                       static_cast<const uint8_t*>(ex->W13.scales), counts, offsets, ex->alpha13,
-                      ex->W13.scale_log2 + ex->W2.scale_log2, false, cfg->T};
+                      ex->W13.scale_log2 + ex->W2.scale_log2, true, cfg->T};
   FP4_CUDA(launch_fp4_dgrad_out(up, ex->alpha2, dX_perm, token_of, dlogits, W_r, cfg->E, cfg->T,
                                 st, s));
   return MOE_OK;

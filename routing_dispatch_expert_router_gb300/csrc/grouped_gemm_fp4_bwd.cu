@@ -14,22 +14,23 @@
 // keeps the weights' traffic at 0.53-0.56 bytes an element; writing them out as bf16
 // first costs 4 more each way (one layer of 64 experts, 4096 x 2048: 0.70 of 1.88 ms).
 //
-// CTA pairs, 256 x 256 tiles, one persistent CTA pair per two SMs, 480 threads:
+// CTA pairs, 256 x 256 tiles, one persistent CTA pair per two SMs, 608 threads:
 //   warp 0      TMA producer of A (one lane): per 64-deep k-block this CTA's 128 rows;
-//   warp 14     TMA producer of the codes and scale atoms of 64 weight rows x 128
+//   warp 18     TMA producer of the codes and scale atoms of 64 weight rows x 128
 //               columns a k-block (one lane), in a ring of their own: a stage of A and
 //               B is then not held while codes are on their way;
 //   warp 1      MMA issuer (one lane of the even CTA): M=256 N=256 K=16;
-//   warps 2-5   epilogue, one tensor-memory lane quarter each;
-//   warps 6-13  the codes' values into B's stage (MN-major, 128-byte swizzle), 8192
+//   warps 2-9   epilogue, two warps per tensor-memory lane quarter, 128 of the 256
+//               columns each;
+//   warps 10-17 the codes' values into B's stage (MN-major, 128-byte swizzle), 8192
 //               elements a k-block; teams of two warps take k-blocks in turn, so that
 //               one team's waits, loads and stores pass under the others' work.
-// Both products of that layer (32768 rows) take 1334 us: 0.42 us a k-block, of which
+// Both products of that layer (32768 rows) take 1345 us: 0.42 us a k-block, of which
 // the MMAs and A's loads alone take 0.34. What is left is shared memory's bandwidth:
 // the MMAs' reads, A's arrival and the codes' way in and values' way out fill about 600
 // of 780 cycles a k-block. On the way: all eight warps on one k-block 3306 us, teams of
 // four warps 2608, of two 1820; without bank conflicts 1772; the arrivals at the even
-// CTA's barrier without release.cluster (1600 cycles each) 1334. Tiles of 512 x 128 (B
+// CTA's barrier without release.cluster (1600 cycles each) 1345. Tiles of 512 x 128 (B
 // made once for 512 rows) take 2057: MMAs of N=128 run at half rate. 512 x 256 with one
 // set of accumulators: 1850 before the arrivals changed (1772 then).
 #include "fp4_layout.cuh"
@@ -38,18 +39,19 @@
 namespace moe {
 namespace gg {
 
-constexpr int kD4Threads = 480;
+constexpr int kD4Threads = 608;
 constexpr int kD4BN = 256;
-constexpr int kD4Stages = 6;
+constexpr int kD4Stages = 5;
 constexpr int kD4ABytes = BM * BK * 2;                 // 16 KB
 constexpr int kD4BBytes = 128 * BK * 2;                // 16 KB: this CTA's 128 columns
 constexpr int kD4CodeBytes = BK * 64;                  // 64 rows x 128 codes
-constexpr int kD4ConvWarp = 6;                         // the first of the eight
+constexpr int kD4EpiWarps = 8;
+constexpr int kD4ConvWarp = 2 + kD4EpiWarps;           // the first of the eight
 constexpr int kD4ConvWarps = 8;
 constexpr int kD4CodeWarp = kD4ConvWarp + kD4ConvWarps;
 constexpr int kD4CodeSlots = 4;
 constexpr int kD4Teams = 4;                            // of two warps, each every fourth k-block
-constexpr int kD4EpiBytes = kBoxBytes;                 // staging per epilogue warp
+constexpr int kD4EpiBytes = 2 * kBoxBytes;             // staging per epilogue warp: dG and dU
 constexpr uint32_t kD4TmemCols = 2 * kD4BN;
 enum D4Epi : int { kD4Swiglu = 0, kD4Out = 1 };
 
@@ -80,7 +82,7 @@ struct D4Cfg {
   static constexpr int RAW_OFF = kD4Stages * STAGE;
   static constexpr int CTRL_OFF = RAW_OFF + kD4CodeSlots * RAW;
   static constexpr int EPI_OFF = (CTRL_OFF + kCtrlBytes + 1023) / 1024 * 1024;
-  static constexpr int SMEM = EPI_OFF + 4 * kD4EpiBytes + 1024;
+  static constexpr int SMEM = EPI_OFF + kD4EpiWarps * kD4EpiBytes + 1024;
   static_assert(SMEM <= 232448, "4-bit data gradient shared memory");
   static_assert(4864 + 16 * kD4CodeSlots <= kCtrlBytes, "code barriers in the control block");
 };
@@ -191,7 +193,10 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
   const int total = block_exclusive_scan(prefix, G, tmp);
   if (tid == 0) prefix[G] = total;
   __syncthreads();
-  if (cluster >= total) return;                          // both CTAs of the pair leave together
+  if (cluster >= total) {                                // both CTAs of the pair leave together
+    ptx::grid_dependency_wait();                         // and after the kernel before this one
+    return;
+  }
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -206,7 +211,7 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(bar_tfull + 8 * a, 1);
-      ptx::mbar_init(bar_tempty + 8 * a, 8);             // 4 epilogue warps x 2 CTAs
+      ptx::mbar_init(bar_tempty + 8 * a, 2 * kD4EpiWarps);
     }
     ptx::mbar_init(bar_drain, 1);
     ptx::fence_mbar_init();
@@ -224,6 +229,7 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  ptx::grid_launch_dependents();     // the next kernel's CTAs may start as these leave
   // pair tile -> group, m-pair, n-tile; m-pairs fastest
   auto decode_pair = [&](int pt, int& g, int& mp, int& nt) {
     g = find_group(prefix, G, pt);
@@ -236,6 +242,7 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
   if (warp == 0) {
     // ------------------------------------------------------- producer of A
     if (lane == 0) {
+      ptx::grid_dependency_wait();     // A is what the kernel before this one wrote
       uint32_t stage = 0, phase = 0;
       bool ok = true;
       for (int pt = cluster; pt < total && ok; pt += nclusters) {
@@ -396,8 +403,6 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                        ? *reinterpret_cast<const uint16_t*>(sf + half * f4::kAtomBytes + (sub & 1) * 2)
                        : sf[sub];
           }
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bar_code_empty + 8 * slot);
           // the MMAs that read this stage's B are done
           ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_empty + 8 * stage, phase ^ 1u,
                                                       kWaitBudget, abort_flag));
@@ -420,7 +425,12 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
           }
           ptx::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster_async(leader_full + 8 * stage);
+          // (the codes' slot too only now: right after its reads the arrival could pass
+          // ones that had not returned, and the next codes landed under them)
+          if (lane == 0) {
+            ptx::mbar_arrive(bar_code_empty + 8 * slot);
+            ptx::mbar_arrive_cluster_async(leader_full + 8 * stage);
+          }
         }
         if (++turn == kD4Teams) turn = 0;
         if (++slot == kD4CodeSlots) {
@@ -439,19 +449,21 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;
+    const int q = warp & 3;                                  // lane quarter
+    const int ch = (warp - 2) >> 2;                          // which 128 of the 256 columns
     uint8_t* box = sbase + C::EPI_OFF + (warp - 2) * kD4EpiBytes;
     const uint32_t box_u32 = base + C::EPI_OFF + (warp - 2) * kD4EpiBytes;
     const uint32_t leader_tempty[2] = {ptx::mapa_shared(bar_tempty, 0),
                                        ptx::mapa_shared(bar_tempty + 8, 0)};
     uint32_t acc = 0, acc_phase = 0;
+    ptx::grid_dependency_wait();       // nothing is written before that kernel is done
     for (int pt = cluster; pt < total; pt += nclusters) {
       int g, mp, nt;
       decode_pair(pt, g, mp, nt);
       const int mt = 2 * mp + (int)rank;
       const int row0 = s_off[g] + mt * BM + q * 32;
       const int rv = s_cnt[g] - mt * BM - q * 32;            // rows of this warp that hold data
-      const int f0 = nt * kD4BN;
+      const int f0 = nt * kD4BN + 128 * ch;
       const int64_t row = row0 + lane;
       // what the row needs besides the accumulator: gate and up of its next 32
       // columns, or the router's term
@@ -489,19 +501,19 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         break;
       }
       ptx::tc_fence_after();
-      const uint32_t tbase = tmem_base + acc * kD4BN + ((uint32_t)(q * 32) << 16);
+      const uint32_t tbase = tmem_base + acc * kD4BN + 128 * ch + ((uint32_t)(q * 32) << 16);
       // swiglu: rows without data need no gradient. out: a group's 128-row blocks are
       // written whole, their rows without data as zeros
       if (EPI == kD4Swiglu ? rv > 0 : mt < mtiles[g]) {
 #pragma unroll 1
-        for (int c = 0; c < kD4BN && f0 + c < p.N; c += 32) {
+        for (int c = 0; c < 128 && f0 + c < p.N; c += 32) {
           uint32_t r[32];
           ptx::tmem_ld32(tbase + c, r);
           ptx::tmem_ld_wait();
           uint4 o[2][4];                                     // dG and dU, or dX
           if (EPI == kD4Swiglu) {
             const Kept n = k;
-            fetch(f0 + c + 32);
+            if (c < 96) fetch(f0 + c + 32);
             const float gs = fp4_scale_value<MOE_FP4_MX>(n.gs);
             const float us = fp4_scale_value<MOE_FP4_MX>(n.us);
             const uint32_t gw[8] = {n.g[0].x, n.g[0].y, n.g[0].z, n.g[0].w,
@@ -540,18 +552,21 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             }
             pack_slice(r, o[0]);
           }
-          // one box at a time (dG then dU, or dX) through the staging
-#pragma unroll
-          for (int i = 0; i < (EPI == kD4Swiglu ? 2 : 1); ++i) {
-            if (lane == 0) ptx::tma_store_wait_read();
-            __syncwarp();
-            stage_row(box, 0, lane, o[i]);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              ptx::tma_store_2d(&tmC, box_u32, i * p.N + f0 + c, row0);
-              ptx::tma_store_commit();
-            }
+          // dG and dU in the staging's two boxes, or dX in one of them in turn
+          if (lane == 0) {
+            if (EPI == kD4Swiglu) ptx::tma_store_wait_read();
+            else ptx::tma_store_wait_read_1();
+          }
+          __syncwarp();
+          const int at = EPI == kD4Swiglu ? 0 : (c >> 5) & 1;
+          stage_row(box, at, lane, o[0]);
+          if (EPI == kD4Swiglu) stage_row(box, 1, lane, o[1]);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            ptx::tma_store_2d(&tmC, box_u32 + at * kBoxBytes, f0 + c, row0);
+            if (EPI == kD4Swiglu) ptx::tma_store_2d(&tmC, box_u32 + kBoxBytes, p.N + f0 + c, row0);
+            ptx::tma_store_commit();
           }
         }
       }
@@ -590,7 +605,7 @@ static bool make_map_codes(CUtensorMap* m, const void* ptr, int64_t cols, int64_
 // As many pairs as can be resident at once (the tile loop strides over them).
 template <int FMT, int EPI>
 static cudaError_t run_dgrad4(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
-                              const Dgrad4Params& p, cudaStream_t s) {
+                              const Dgrad4Params& p, bool early, cudaStream_t s) {
   auto kern = fp4_dgrad_kernel<FMT, EPI>;
   constexpr int smem = D4Cfg<FMT>::SMEM;
   static int grid = 0;
@@ -609,8 +624,17 @@ static cudaError_t run_dgrad4(const CUtensorMap& a, const CUtensorMap& b, const 
     }
     grid = 2 * clusters;
   }
-  kern<<<grid, kD4Threads, smem, s>>>(a, b, c, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(grid, 1, 1);
+  lc.blockDim = dim3(kD4Threads, 1, 1);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = at;
+  lc.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&lc, kern, a, b, c, p);
 }
 
 static Dgrad4Params dgrad4_params(const Fp4Problem& q, int32_t* status) {
@@ -643,8 +667,8 @@ cudaError_t launch_fp4_dgrad_swiglu(const Fp4Problem& q, const uint8_t* ckpt,
   Dgrad4Params p = dgrad4_params(q, status);
   p.ckpt = ckpt;
   p.ckpt_sf = ckpt_sf;
-  return q.fmt == MOE_FP4_NV ? run_dgrad4<MOE_FP4_NV, kD4Swiglu>(a, b, c, p, s)
-                             : run_dgrad4<MOE_FP4_MX, kD4Swiglu>(a, b, c, p, s);
+  return q.fmt == MOE_FP4_NV ? run_dgrad4<MOE_FP4_NV, kD4Swiglu>(a, b, c, p, q.early, s)
+                             : run_dgrad4<MOE_FP4_MX, kD4Swiglu>(a, b, c, p, q.early, s);
 }
 
 cudaError_t launch_fp4_dgrad_out(const Fp4Problem& q, const float* alpha_b, void* dX,
@@ -665,8 +689,8 @@ cudaError_t launch_fp4_dgrad_out(const Fp4Problem& q, const float* alpha_b, void
   p.W_r = W_r;
   p.router_E = router_E;
   p.router_T = router_T;
-  return q.fmt == MOE_FP4_NV ? run_dgrad4<MOE_FP4_NV, kD4Out>(a, b, c, p, s)
-                             : run_dgrad4<MOE_FP4_MX, kD4Out>(a, b, c, p, s);
+  return q.fmt == MOE_FP4_NV ? run_dgrad4<MOE_FP4_NV, kD4Out>(a, b, c, p, q.early, s)
+                             : run_dgrad4<MOE_FP4_MX, kD4Out>(a, b, c, p, q.early, s);
 }
 
 }  // namespace moe

@@ -212,7 +212,7 @@ cudaError_t launch_fp4_swiglu(const Fp4Problem& q, uint8_t* hq, uint8_t* hsf, in
                               cudaStream_t s);
 
 // Their data gradients: A bf16 [rows, K] by the 4-bit weights [G, K, N] (q.a is A;
-// q.sfa and q.early are not used). FC2's, times SwiGLU's derivative from the 8-bit
+// q.sfa is not used). FC2's, times SwiGLU's derivative from the 8-bit
 // checkpoint -> dGU [rows, 2N] bf16, without the weights' scales; FC1's, with both
 // products' scales (q.alpha, alpha_b, q.unit_log2) and the router's term where
 // dlogits is given -> dX [rows, N] bf16.

@@ -454,6 +454,35 @@ def test_ffn_backward_matches_oracle(fmt, counts, H, F, router):
         assert (pad == 0).all()
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_repeated_passes_are_equal_bit_for_bit(fmt):
+    """Thirty passes of every product over the same rows: whatever the order in which loads
+    land and parts arrive, the results are the same numbers."""
+    rng = np.random.default_rng(21)
+    counts, H, F = [520, 0, 600, 40], 512, 1024
+    off, rows, cnt, offs = segments(counts)
+    cfg = B.config(MoEShape("r", T=len(rows), H=H, E=4, k=1, F=F))
+    R = B.moe_query_sizes(cfg).rows_max
+    ex = experts_of(fmt, rng, 4, H, F)
+    x = torch.zeros(R, H, device=DEV, dtype=torch.bfloat16)
+    x[rows] = rows_of(rng, len(rows), H, spread=False)
+    ck = torch.zeros(R, 2 * F, dtype=torch.uint8, device=DEV)
+    cs = torch.zeros(R, 2 * F // 32, dtype=torch.uint8, device=DEV)
+    sz = B.moe_fp4_query_sizes(cfg, fmt)
+    sf, sb = B.alloc_fp4_scratch(sz.fwd_scratch_bytes), B.alloc_fp4_scratch(sz.bwd_scratch_bytes)
+    few = torch.tensor([3, 0, 64, 1], dtype=torch.int32, device=DEV)      # sums cut over the SMs
+    first = None
+    for _ in range(30):
+        y, z, dX = (torch.zeros(R, H, device=DEV, dtype=torch.bfloat16) for _ in range(3))
+        B.moe_fp4_ffn_fwd(cfg, ex[0], x, few, offs, None, None, z, sf)
+        B.moe_fp4_ffn_fwd(cfg, ex[0], x, cnt, offs, ck, cs, y, sf)
+        B.moe_fp4_ffn_bwd(cfg, ex[0], y, ck, cs, cnt, offs, None, None, None, dX, sb)
+        now = (y, z, dX, ck.clone(), cs.clone())
+        first = first or now
+        assert all(torch.equal(a, b) for a, b in zip(first, now))
+    assert B.moe_last_device_status(sf) == 0 and B.moe_last_device_status(sb) == 0
+
+
 # -------------------------------------------------------------- a layer, a graph
 LAYER = MoEShape("fp4_layer", T=300, H=256, E=8, k=2, F=384, bias_kind="none")
 
