@@ -583,3 +583,20 @@ def test_shared_experts_and_sigmoid_router_rows():
     x, y = f64(f["x_perm"])[off:off + 70], f64(f["y_perm"])[off:off + 70]
     _, _, _, ref = O.ffn_fwd(0, x, f64(v13[4]), f64(v2[4]))
     assert np.linalg.norm(y - ref) <= 2.0 ** -7 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_layer_class_serves_and_trains(fmt):
+    """The layer of the command: a serving step against the bf16 layer (4-bit weights and rows
+    are about 0.1 away each; a wrong path would be 1 or more), and its gradients finite."""
+    from routing_dispatch_expert_router_gb300 import fp4_layer as L
+    shape = TINY.with_(T=70)
+    inp = {k: (v.to(DEV) if torch.is_tensor(v) else v) for k, v in make_inputs(shape, seed=3).items()}
+    layer = L.Fp4Layer(shape, inp, fmt, training=True)
+    out = layer.forward(inp["x"])
+    ref = L._bf16_output(shape, inp)
+    dx, dW_r = layer.backward(inp["x"], inp["dY"])
+    layer.check()
+    a, b = f64(out), f64(ref)
+    assert np.linalg.norm(a - b) < 0.4 * np.linalg.norm(b)
+    assert np.isfinite(f64(dx)).all() and f64(dx).any() and np.isfinite(f64(dW_r)).all()
