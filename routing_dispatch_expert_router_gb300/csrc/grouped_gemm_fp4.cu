@@ -136,17 +136,23 @@ struct Work {
   __device__ __forceinline__ bool whole() const { return kb1 - kb0 == nk; }
 };
 
-// Whether to share the k-blocks evenly: where whole tiles keep the busiest SM
-// longer than an even share and the joining of parts, which costs about as much
-// as 2 k-blocks and one more per 16 rows, and where the parts (two per
-// CTA at most) fit scratch.
-__device__ __forceinline__ int share_evenly(int tiles, int nk, int grid, int slot_rows,
+// Whether to share the k-blocks evenly. Unit: a hundredth of a k-block's time while all
+// SMs stream weights (0.98 us). Whole tiles cost their full waves, and a last wave of m
+// tiles as much as the m SMs take on their own, at best kAlone of that time. Even shares
+// cost the share and the joining of the last tile's parts, kJoin and kJoinRow a row.
+// They need scratch for two parts per CTA. Measured whole / even, us, for two experts:
+// K = 14336, N = 4096: 35.8 / 18.5 with 1 row, 36.3 / 22.9 with 8, 36.1 / 31.6 with 16,
+// 36.5 / 41 with 32; K = 4096, N = 28672: 30.3 / 28.6 with 1 row, 31.7 / 40 with 32.
+constexpr int kAlone = 65, kJoin = 200, kJoinRow = 80;
+__device__ __forceinline__ int share_evenly(int tiles, int nk, int grid, int most_rows,
                                             int64_t part_floats, int counters) {
+  const int slot_rows = min(BM, (most_rows + 31) / 32 * 32);
   if ((int64_t)2 * grid * slot_rows * kF4BN > part_floats || tiles * kF4EpiWarps > counters)
     return 0;
-  const int whole = (tiles + grid - 1) / grid * nk;
-  const int share = (int)(((int64_t)tiles * nk + grid - 1) / grid);
-  return whole > share + 2 + slot_rows / 16;
+  const int m = tiles % grid;
+  const int64_t whole = (int64_t)nk * (tiles / grid * 100 + (m ? max(kAlone, 100 * m / grid) : 0));
+  const int64_t share = (int64_t)tiles * nk * 100 / grid;
+  return whole > share + kJoin + most_rows * kJoinRow;
 }
 
 // h of 32 columns (bf16 pairs) in 4 bits: codes to `dst` (16 bytes); returns the
@@ -217,71 +223,63 @@ __device__ __forceinline__ int slice_col(int half, int c) {
   return EPI == kF4Swiglu ? (c >> 1) * 128 + 64 * half + 32 * (c & 1) : 128 * half + 32 * c;
 }
 
-// Stores a warp's 32 rows x 128 columns (o: bf16, the slices of slice_col): rv of
-// the 32 rows hold data, the others are not written.
+// Stores one 32-column piece of a warp's 32 rows, of which rv hold data (the others are
+// not written): c is the piece's number, 0-3 (store: o its bf16 values) or 0-1 (swiglu:
+// o its gate and u its up values).
 template <int FMT, int EPI, bool BOXES>
 __device__ __forceinline__ void f4_epilogue(const Fp4Params& p, const CUtensorMap* tmC,
                                             uint8_t* stage, uint32_t stage_u32, int nt, int row0,
-                                            int rv, int half, int lane, const uint4 (&o)[4][4]) {
+                                            int rv, int half, int lane, int c, const uint4 (&o)[4],
+                                            const uint4 (&u)[4]) {
   if (EPI == kF4Swiglu) {
     if (lane >= rv) return;
     const int F = p.N / 2;
-    const int f0 = nt * (kF4BN / 2) + 64 * half;
+    const int f = nt * (kF4BN / 2) + 64 * half + 32 * c;
     const int64_t row = row0 + lane;
-    uint32_t hs = 0, gs = 0, us = 0;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint4 h[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) h[v] = swiglu_h8<false>(o[c][v], o[2 + c][v], 1.f);
-      if (p.ckpt) {
-        gs |= checkpoint32(o[c], p.ckpt + row * 2 * F + f0 + 32 * c) << (8 * c);
-        us |= checkpoint32(o[2 + c], p.ckpt + row * 2 * F + F + f0 + 32 * c) << (8 * c);
-      }
-      hs |= quantize_h32<FMT>(h, p.hdown, p.hq + row * (F / 2) + (f0 + 32 * c) / 2)
-            << (c * 8 * (32 / f4::block_of(FMT)));
-    }
-    uint8_t* sf = p.hsf + (row >> 7) * p.hka * (int64_t)f4::kAtomBytes +
-                  f4::sf_byte((int)(row & 127), f0 / f4::block_of(FMT));
-    if (FMT == MOE_FP4_NV) *reinterpret_cast<uint32_t*>(sf) = hs;
-    else *reinterpret_cast<uint16_t*>(sf) = (uint16_t)hs;
     if (p.ckpt) {
-      uint8_t* cs = p.ckpt_sf + row * (2 * F / 32) + f0 / 32;
-      *reinterpret_cast<uint16_t*>(cs) = (uint16_t)gs;
-      *reinterpret_cast<uint16_t*>(cs + F / 32) = (uint16_t)us;
+      uint8_t* ck = p.ckpt + row * 2 * F + f;
+      uint8_t* cs = p.ckpt_sf + row * (2 * F / 32) + f / 32;
+      cs[0] = (uint8_t)checkpoint32(o, ck);
+      cs[F / 32] = (uint8_t)checkpoint32(u, ck + F);
     }
+    uint4 h[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) h[v] = swiglu_h8<false>(o[v], u[v], 1.f);
+    const uint32_t s = quantize_h32<FMT>(h, p.hdown, p.hq + row * (F / 2) + f / 2);
+    uint8_t* sf = p.hsf + (row >> 7) * p.hka * (int64_t)f4::kAtomBytes +
+                  f4::sf_byte((int)(row & 127), f / f4::block_of(FMT));
+    if (FMT == MOE_FP4_NV) *reinterpret_cast<uint16_t*>(sf) = (uint16_t)s;
+    else *sf = (uint8_t)s;
     return;
   }
-  const int c0 = nt * kF4BN + 128 * half;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int col = c0 + 32 * c;
-    if (col >= p.N) {
-    } else if (BOXES && rv >= 32) {
-      // a full 32 x 32 box by TMA, which also clips the columns past N
-      if (lane == 0) ptx::tma_store_wait_read();       // the slot's previous box has been read
-      __syncwarp();
-      stage_row(stage, 0, lane, o[c]);
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        ptx::tma_store_2d(tmC, stage_u32, col, row0);
-        ptx::tma_store_commit();
-      }
-    } else if (lane < rv) {
-      __nv_bfloat16* dst = p.out + (int64_t)(row0 + lane) * p.N + col;
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        if (col + 8 * v < p.N) stg_v4(dst + 8 * v, o[c][v]);
+  const int col = nt * kF4BN + 128 * half + 32 * c;
+  if (col >= p.N) return;
+  if (BOXES && rv >= 32) {
+    // a full 32 x 32 box by TMA, which also clips the columns past N
+    if (lane == 0) ptx::tma_store_wait_read();         // the slot's previous box has been read
+    __syncwarp();
+    stage_row(stage, 0, lane, o);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      ptx::tma_store_2d(tmC, stage_u32, col, row0);
+      ptx::tma_store_commit();
     }
+  } else if (lane < rv) {
+    __nv_bfloat16* dst = p.out + (int64_t)(row0 + lane) * p.N + col;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (col + 8 * v < p.N) stg_v4(dst + 8 * v, o[v]);
   }
 }
 
+// (Not inlined: a decode step runs every instruction here once, from HBM -- the weights
+// have swept L2 -- so that code costs by its length.)
 // Four columns of one row of a joined tile per lane (v, times alpha already):
 // columns 4 lane .. of the warp's 128 (the slices of slice_col end to end, so in
 // the swiglu form lanes 0-15 hold gate and lanes 16-31 the matching up columns).
 template <int FMT, int EPI>
-__device__ __forceinline__ void f4_epilogue_row(const Fp4Params& p, int nt, int64_t row, int half,
+__device__ __noinline__ void f4_epilogue_row(const Fp4Params& p, int nt, int64_t row, int half,
                                                 int lane, const float4& v) {
   uint2 b = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
   if (EPI == kF4Store) {
@@ -391,7 +389,7 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
   const int tiles = block_exclusive_scan(prefix, G, tmp);
   if (tid == 0) prefix[G] = tiles;
   const int slot_rows = min(BM, (*s_most + 31) / 32 * 32);
-  const int even = share_evenly(tiles, nk_all, gridDim.x, slot_rows, p.part_floats, p.arrived_n);
+  const int even = share_evenly(tiles, nk_all, gridDim.x, *s_most, p.part_floats, p.arrived_n);
   __syncthreads();
   Work w(tiles, nk_all, even);
   if (w.pos >= w.end) {
@@ -631,21 +629,65 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
         break;
       }
       ptx::tc_fence_after();
-      uint4 o[4][4];
       // a cut tile: this warp's slice of a part, [slot_rows][128 columns] fp32;
       // CTA b's slots are 2b (a tile that began before its share) and 2b + 1
       const int64_t slice = (int64_t)slot_rows * 128;
       float* parts = p.part + half * slice + (int64_t)q * 32 * 128;
-      if (rv > 0) {
-        float* mine = parts + (2 * (int64_t)blockIdx.x + (w.kb0 == 0)) * 2 * slice + lane * 128;
+      auto release = [&]() {                      // the accumulator is free for the next piece
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar_tempty);
+      };
+      acc_phase ^= 1u;
+      if (rv <= 0) {
+        release();
+        continue;
+      }
+      if (w.whole()) {
+        if constexpr (AROWS == BM) {
+          // the tile's columns into registers first, so that the next one's MMAs start
+          uint4 o[4][4];
 #pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[32];
+            ptx::tmem_ld32(tq + slice_col<EPI>(half, c), r);
+            ptx::tmem_ld_wait();
+            scale_pack(r, alpha, o[c]);
+          }
+          release();
+#pragma unroll
+          for (int c = 0; c < (EPI == kF4Swiglu ? 2 : 4); ++c)
+            f4_epilogue<FMT, EPI, C::BOXES>(p, &tmC, stage, stage_u32, t.nt, row0, rv, half, lane,
+                                            c, o[c], o[(c + 2) & 3]);
+        } else {
+          // few rows: the weights' arrival is what the kernel waits for, and short code
+          // what it needs
+#pragma unroll 1
+          for (int c = 0; c < (EPI == kF4Swiglu ? 2 : 4); ++c) {
+            uint32_t r[32];
+            uint4 o[4], u[4];
+            ptx::tmem_ld32(tq + slice_col<EPI>(half, c), r);
+            ptx::tmem_ld_wait();
+            scale_pack(r, alpha, o);
+            if (EPI == kF4Swiglu) {
+              ptx::tmem_ld32(tq + slice_col<EPI>(half, c + 2), r);
+              ptx::tmem_ld_wait();
+              scale_pack(r, alpha, u);
+            }
+            f4_epilogue<FMT, EPI, C::BOXES>(p, &tmC, stage, stage_u32, t.nt, row0, rv, half, lane,
+                                            c, o, u);
+            __syncwarp();
+          }
+          release();
+        }
+      } else {
+        float* mine = parts + (2 * (int64_t)blockIdx.x + (w.kb0 == 0)) * 2 * slice + lane * 128;
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t r[32];
           ptx::tmem_ld32(tq + slice_col<EPI>(half, c), r);
           ptx::tmem_ld_wait();
-          if (w.whole()) {
-            scale_pack(r, alpha, o[c]);
-          } else if (lane < rv) {
+          if (lane < rv) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
               __stcg(reinterpret_cast<uint4*>(mine + 32 * c + i),
@@ -653,14 +695,7 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
           }
           __syncwarp();
         }
-      }
-      // the accumulator is free for the next piece's MMAs
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar_tempty);
-      acc_phase ^= 1u;
-      if (rv <= 0) continue;
-      if (!w.whole()) {
+        release();
         __syncwarp();
         const int b0 = w.first(), b1 = w.last();
         int last = 0;
@@ -673,30 +708,24 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
         if (!last) continue;
         const int rows = min(rv, 32);
         // the first part ends at its CTA's share (slot 2 b0 + 1), the others begin theirs
-        const float* src = parts + 4 * lane;
-        const int64_t step = 4 * slice;           // from a CTA's slots to the next one's
+        const float* first = parts + (4 * (int64_t)b0 + 2) * slice + 4 * lane;
+        const float* others = parts + 4 * (int64_t)(b0 + 1) * slice + 4 * lane;
 #pragma unroll 1
-        for (int r = 0; r < rows; ++r) {
-          const float* at = src + (4 * (int64_t)b0 + 2) * slice + r * 128;
-          float4 v = __ldcg(reinterpret_cast<const float4*>(at));
-          at += step - 2 * slice;
+        for (int r = 0; r < rows; ++r, first += 128, others += 128) {
+          float4 v = __ldcg(reinterpret_cast<const float4*>(first));
+          const float* at = others;
 #pragma unroll 4
-          for (int b = b0 + 1; b <= b1; ++b, at += step) {
+          for (int b = b0; b < b1; ++b, at += 4 * slice) {
             const float4 u = __ldcg(reinterpret_cast<const float4*>(at));
             v.x += u.x;
             v.y += u.y;
             v.z += u.z;
             v.w += u.w;
           }
-          v.x *= alpha;
-          v.y *= alpha;
-          v.z *= alpha;
-          v.w *= alpha;
-          f4_epilogue_row<FMT, EPI>(p, t.nt, row0 + r, half, lane, v);
+          f4_epilogue_row<FMT, EPI>(p, t.nt, row0 + r, half, lane,
+                                    make_float4(v.x * alpha, v.y * alpha, v.z * alpha, v.w * alpha));
         }
-        continue;
       }
-      f4_epilogue<FMT, EPI, C::BOXES>(p, &tmC, stage, stage_u32, t.nt, row0, rv, half, lane, o);
     }
     if (lane == 0) ptx::tma_store_wait_all();
   }
