@@ -17,7 +17,7 @@ namespace moe {
 namespace {
 
 constexpr int kQThreads = 256;
-constexpr int kQCols = 512;                      // columns of one CTA
+constexpr int kQCols = 512;                      // columns of one turn of a CTA
 
 // Rows of a 128-row slab that hold data, and where the slab lies. Dense
 // tensors: groups x rows; ragged: the rows [offsets[g], offsets[g] + counts[g])
@@ -59,7 +59,7 @@ template <int FMT, bool VALUES>
 __global__ void __launch_bounds__(kQThreads)
 fp4_quantize_kernel(const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ codes,
                     uint8_t* __restrict__ scales, __nv_bfloat16* __restrict__ values, float up,
-                    float down, const Rows p) {
+                    float down, int turns, const Rows p) {
   constexpr int BLK = f4::block_of(FMT);
   constexpr int V = BLK / 8;                     // 16-byte vectors of a block
   ptx::grid_launch_dependents();                 // a product may start fetching its weights
@@ -78,59 +78,64 @@ fp4_quantize_kernel(const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ c
   uint8_t* cr = codes + (row0 + r) * (p.K / 2);
   __nv_bfloat16* vr = VALUES ? values + (row0 + r) * p.K : nullptr;
   uint8_t* sf = scales + sl * ka * f4::kAtomBytes;
-  const int64_t b0 = (int64_t)blockIdx.y * (kQCols / BLK) + (lane & 7);
   constexpr int IT = kQCols / (8 * BLK);
-  uint4 v[IT][V];
+#pragma unroll 1
+  for (int turn = 0; turn < turns; ++turn) {
+    const int64_t k0 = ((int64_t)blockIdx.y * turns + turn) * kQCols;
+    if (k0 >= p.K) break;
+    const int64_t b0 = k0 / BLK + (lane & 7);
+    uint4 v[IT][V];
 #pragma unroll
-  for (int it = 0; it < IT; ++it) {
-    const int64_t b = b0 + 8 * it;
+    for (int it = 0; it < IT; ++it) {
+      const int64_t b = b0 + 8 * it;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      v[it][i] = live && b < nblk ? ldg_nc_v4(xr + b * BLK + 8 * i) : make_uint4(0, 0, 0, 0);
-  }
-#pragma unroll
-  for (int it = 0; it < IT; ++it) {
-    const int64_t b = b0 + 8 * it;
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) m = max(m, amax_bits8(v[it][i]));
-    const Fp4Scale s = fp4_scale<FMT>(__uint_as_float(m << 16), m < 0x7F80u, down);
-    uint32_t c[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float f[8];
-      unpack8(v[it][i], f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = fp4_quotient<FMT>(f[j], s.inv);
-      c[i] = s.inv > 0.f ? e2m1x8(f) : 0u;
+      for (int i = 0; i < V; ++i)
+        v[it][i] = live && b < nblk ? ldg_nc_v4(xr + b * BLK + 8 * i) : make_uint4(0, 0, 0, 0);
     }
-    if (live && b < nblk) {
-      if (V == 2) *reinterpret_cast<uint2*>(cr + b * 8) = make_uint2(c[0], c[1]);
-      else *reinterpret_cast<uint4*>(cr + b * 16) = make_uint4(c[0], c[1], c[V - 2], c[V - 1]);
-      if (VALUES) {
-        const float sv = fp4_scale_value<FMT>(s.byte) * up;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          uint32_t h[4];
-          e2m1x8_to_half(c[i], h);
-          float f[8];
+    for (int it = 0; it < IT; ++it) {
+      const int64_t b = b0 + 8 * it;
+      uint32_t m = 0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-            f[2 * j] = t.x * sv;
-            f[2 * j + 1] = t.y * sv;
+      for (int i = 0; i < V; ++i) m = max(m, amax_bits8(v[it][i]));
+      const Fp4Scale s = fp4_scale<FMT>(__uint_as_float(m << 16), m < 0x7F80u, down);
+      uint32_t c[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float f[8];
+        unpack8(v[it][i], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = fp4_quotient<FMT>(f[j], s.inv);
+        c[i] = s.inv > 0.f ? e2m1x8(f) : 0u;
+      }
+      if (live && b < nblk) {
+        if (V == 2) *reinterpret_cast<uint2*>(cr + b * 8) = make_uint2(c[0], c[1]);
+        else *reinterpret_cast<uint4*>(cr + b * 16) = make_uint4(c[0], c[1], c[V - 2], c[V - 1]);
+        if (VALUES) {
+          const float sv = fp4_scale_value<FMT>(s.byte) * up;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            uint32_t h[4];
+            e2m1x8_to_half(c[i], h);
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+              f[2 * j] = t.x * sv;
+              f[2 * j + 1] = t.y * sv;
+            }
+            stg_v4(vr + b * BLK + 8 * i, pack8(f));
           }
-          stg_v4(vr + b * BLK + 8 * i, pack8(f));
         }
       }
+      // four blocks' bytes of a row in one word; the words of the four rows are
+      // one line of the atom
+      uint32_t word = (b < nblk && live ? s.byte : 0u) << (8 * (lane & 3));
+      word |= __shfl_xor_sync(0xffffffffu, word, 1);
+      word |= __shfl_xor_sync(0xffffffffu, word, 2);
+      if ((lane & 3) == 0 && (b >> 2) < ka)
+        *reinterpret_cast<uint32_t*>(sf + f4::sf_byte(r, b)) = word;
     }
-    // four blocks' bytes of a row in one word; the words of the four rows are
-    // one line of the atom
-    uint32_t word = (b < nblk && live ? s.byte : 0u) << (8 * (lane & 3));
-    word |= __shfl_xor_sync(0xffffffffu, word, 1);
-    word |= __shfl_xor_sync(0xffffffffu, word, 2);
-    if ((lane & 3) == 0 && (b >> 2) < ka)
-      *reinterpret_cast<uint32_t*>(sf + f4::sf_byte(r, b)) = word;
   }
 }
 
@@ -196,16 +201,21 @@ cudaError_t launch_fp4_quantize(int fmt, const void* x, int64_t ldx, int64_t gro
   const Rows p{rows, K, ldx, counts, offsets, segments, status};
   const int64_t sl = groups * f4::slabs(rows);
   if (sl == 0) return cudaSuccess;
-  const dim3 grid((unsigned)(4 * sl), (unsigned)((K + kQCols - 1) / kQCols));
+  // Where there are many CTAs, four turns each: a CTA's start and the look for its
+  // segment take longer than a turn's loads (36800 rows of 4096 in 64 segments, 74 us
+  // with one turn, 70 with four); few rows keep a turn to a CTA, side by side.
+  const int64_t chunks = (K + kQCols - 1) / kQCols;
+  const int turns = 4 * sl * chunks > 16 * num_sms() ? 4 : 1;
+  const dim3 grid((unsigned)(4 * sl), (unsigned)((chunks + turns - 1) / turns));
   const float up = pow2f(scale_log2), down = pow2f(-scale_log2);
   auto xb = static_cast<const __nv_bfloat16*>(x);
   auto vb = static_cast<__nv_bfloat16*>(values);
   if (fmt == MOE_FP4_NV) {
-    if (values) fp4_quantize_kernel<MOE_FP4_NV, true><<<grid, kQThreads, 0, s>>>(xb, codes, scales, vb, up, down, p);
-    else fp4_quantize_kernel<MOE_FP4_NV, false><<<grid, kQThreads, 0, s>>>(xb, codes, scales, vb, up, down, p);
+    if (values) fp4_quantize_kernel<MOE_FP4_NV, true><<<grid, kQThreads, 0, s>>>(xb, codes, scales, vb, up, down, turns, p);
+    else fp4_quantize_kernel<MOE_FP4_NV, false><<<grid, kQThreads, 0, s>>>(xb, codes, scales, vb, up, down, turns, p);
   } else {
-    if (values) fp4_quantize_kernel<MOE_FP4_MX, true><<<grid, kQThreads, 0, s>>>(xb, codes, scales, vb, up, down, p);
-    else fp4_quantize_kernel<MOE_FP4_MX, false><<<grid, kQThreads, 0, s>>>(xb, codes, scales, vb, up, down, p);
+    if (values) fp4_quantize_kernel<MOE_FP4_MX, true><<<grid, kQThreads, 0, s>>>(xb, codes, scales, vb, up, down, turns, p);
+    else fp4_quantize_kernel<MOE_FP4_MX, false><<<grid, kQThreads, 0, s>>>(xb, codes, scales, vb, up, down, turns, p);
   }
   return cudaGetLastError();
 }

@@ -170,7 +170,7 @@ moe_status moe_fp4_grouped_gemm(const moe_fp4_tensor* a, const moe_fp4_tensor* b
                      static_cast<const uint8_t*>(a->codes), static_cast<const uint8_t*>(a->scales),
                      static_cast<const uint8_t*>(b->codes), static_cast<const uint8_t*>(b->scales),
                      counts, offsets, alpha, a->scale_log2 + b->scale_log2, false,
-                     a->rows};
+                     a->rows, a->rows / b->groups};
   FP4_CUDA(launch_fp4_gemm(p, out, split_of(scratch), status_of(scratch), (cudaStream_t)stream));
   return MOE_OK;
 }
@@ -183,6 +183,7 @@ moe_status moe_fp4_ffn_fwd(const moe_config* cfg, const moe_fp4_experts* ex, con
   FP4_REQUIRE(!ckpt == !ckpt_scale && al16_or_null(ckpt) && al16_or_null(ckpt_scale));
   cudaStream_t s = (cudaStream_t)stream;
   const int fmt = ex->W13.format, G = cfg->E + cfg->n_shared;
+  const int64_t per_expert = (int64_t)cfg->T * cfg->k / cfg->E;
   const int64_t R = rows_max(*cfg), H = cfg->H, F = cfg->F;
   FwdScratch w;
   fwd_region(*cfg, fmt, scratch, &w);
@@ -193,12 +194,12 @@ moe_status moe_fp4_ffn_fwd(const moe_config* cfg, const moe_fp4_experts* ex, con
   const Fp4Problem up{fmt, G, R, 2 * F, H, w.xq, w.xsf,
                       static_cast<const uint8_t*>(ex->W13.codes),
                       static_cast<const uint8_t*>(ex->W13.scales), counts, offsets, ex->alpha13,
-                      ex->x_scale_log2 + ex->W13.scale_log2, true, cfg->T};
+                      ex->x_scale_log2 + ex->W13.scale_log2, true, cfg->T, per_expert};
   FP4_CUDA(launch_fp4_swiglu(up, w.hq, w.hsf, ex->h_scale_log2, static_cast<uint8_t*>(ckpt),
                              static_cast<uint8_t*>(ckpt_scale), sp, st, s));
   const Fp4Problem down{fmt, G, R, H, F, w.hq, w.hsf, static_cast<const uint8_t*>(ex->W2.codes),
                         static_cast<const uint8_t*>(ex->W2.scales), counts, offsets, ex->alpha2,
-                        ex->h_scale_log2 + ex->W2.scale_log2, true, cfg->T};
+                        ex->h_scale_log2 + ex->W2.scale_log2, true, cfg->T, per_expert};
   FP4_CUDA(launch_fp4_gemm(down, y_perm, sp, st, s));
   return MOE_OK;
 }
@@ -213,19 +214,20 @@ moe_status moe_fp4_ffn_bwd(const moe_config* cfg, const moe_fp4_experts* ex, con
   if (dlogits) FP4_REQUIRE(al4(dlogits) && al4(token_of) && al16(W_r));
   cudaStream_t s = (cudaStream_t)stream;
   const int fmt = ex->W13.format, G = cfg->E + cfg->n_shared;
+  const int64_t per_expert = (int64_t)cfg->T * cfg->k / cfg->E;
   const int64_t R = rows_max(*cfg), H = cfg->H, F = cfg->F;
   uint8_t* dGU = static_cast<uint8_t*>(scratch) + kDguOffset;
   int32_t* st = status_of(scratch);
   const Fp4Problem down{fmt, G, R, F, H, static_cast<const uint8_t*>(dO_perm), nullptr,
                         static_cast<const uint8_t*>(ex->W2.codes),
                         static_cast<const uint8_t*>(ex->W2.scales), counts, offsets, nullptr, 0,
-                        false, cfg->T};
+                        false, cfg->T, per_expert};
   FP4_CUDA(launch_fp4_dgrad_swiglu(down, static_cast<const uint8_t*>(ckpt),
                                    static_cast<const uint8_t*>(ckpt_scale), dGU, st, s));
   const Fp4Problem up{fmt, G, R, H, 2 * F, dGU, nullptr,
                       static_cast<const uint8_t*>(ex->W13.codes),
                       static_cast<const uint8_t*>(ex->W13.scales), counts, offsets, ex->alpha13,
-                      ex->W13.scale_log2 + ex->W2.scale_log2, true, cfg->T};
+                      ex->W13.scale_log2 + ex->W2.scale_log2, true, cfg->T, per_expert};
   FP4_CUDA(launch_fp4_dgrad_out(up, ex->alpha2, dX_perm, token_of, dlogits, W_r, cfg->E, cfg->T,
                                 st, s));
   return MOE_OK;

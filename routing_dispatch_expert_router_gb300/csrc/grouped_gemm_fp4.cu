@@ -327,6 +327,30 @@ __device__ __noinline__ void f4_epilogue_row(const Fp4Params& p, int nt, int64_t
   }
 }
 
+// A scale warp's part of a k-block: its lane's line of every atom into its lane quarter
+// of tensor memory (A's atoms, then B's two slabs' by turns), complete on return.
+template <int FMT>
+__device__ __forceinline__ void write_scales(const uint8_t* src, uint32_t col) {
+  constexpr int ATOMS = f4::step_atoms(FMT), SF_A = ATOMS * f4::kAtomBytes;
+  uint32_t a[4 * ATOMS], b[8 * ATOMS];
+#pragma unroll
+  for (int i = 0; i < ATOMS; ++i) {
+    *reinterpret_cast<uint4*>(a + 4 * i) = *reinterpret_cast<const uint4*>(src + 512 * i);
+    *reinterpret_cast<uint4*>(b + 8 * i) = *reinterpret_cast<const uint4*>(src + SF_A + 512 * i);
+    *reinterpret_cast<uint4*>(b + 8 * i + 4) =
+        *reinterpret_cast<const uint4*>(src + 2 * SF_A + 512 * i);
+  }
+  if (FMT == MOE_FP4_NV) {
+    ptx::tmem_st16(col, a);
+    ptx::tmem_st32(col + 16, b);
+  } else {
+    ptx::tmem_st8(col, a);
+    ptx::tmem_st16(col + 8, b);
+  }
+  ptx::tmem_st_wait();
+  ptx::tc_fence_before();
+}
+
 template <int FMT, int EPI, int AROWS>
 __global__ void __launch_bounds__(kF4Threads, 1)
 grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -572,26 +596,7 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget,
                                                     abort_flag));
         if (!ok) break;
-        uint32_t a[4 * C::ATOMS], b[8 * C::ATOMS];
-        const uint8_t* src = sfl + stage * C::SF_STAGE;
-#pragma unroll
-        for (int i = 0; i < C::ATOMS; ++i) {
-          *reinterpret_cast<uint4*>(a + 4 * i) = *reinterpret_cast<const uint4*>(src + 512 * i);
-          *reinterpret_cast<uint4*>(b + 8 * i) =
-              *reinterpret_cast<const uint4*>(src + C::SF_A + 512 * i);
-          *reinterpret_cast<uint4*>(b + 8 * i + 4) =
-              *reinterpret_cast<const uint4*>(src + 2 * C::SF_A + 512 * i);
-        }
-        const uint32_t col = tq + C::SLOT_COLS * stage;
-        if (NV) {
-          ptx::tmem_st16(col, a);
-          ptx::tmem_st32(col + 16, b);
-        } else {
-          ptx::tmem_st8(col, a);
-          ptx::tmem_st16(col + 8, b);
-        }
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
+        write_scales<FMT>(sfl + stage * C::SF_STAGE, tq + C::SLOT_COLS * stage);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar_scales + 8 * stage);
         if (++stage == kStages) {
@@ -737,6 +742,331 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
   }
 }
 
+// ------------------------------------------------------------ CTA pairs
+// The same product for experts with many rows: tiles of 256 x 256, each CTA of a pair
+// holding 128 rows of A and 128 of B (swiglu: the gate rows in the even CTA, the matching
+// up rows in the odd one), its rows' scales and those of all 256 columns. A k-block is 38 KB
+// a CTA instead of 54, so that five stages fit where three did: the cycle from an MMA's
+// end over the next loads and their scales to the MMA that waits for them is what bounds
+// the single CTA. Whole tiles only.
+template <int FMT>
+struct F4PairCfg {
+  static constexpr int ATOMS = f4::step_atoms(FMT);
+  static constexpr int SF_A = ATOMS * f4::kAtomBytes;
+  static constexpr int SF_STAGE = 3 * SF_A;
+  static constexpr int A_BYTES = BM * kF4RowBytes;               // 16 KB
+  static constexpr int STAGE = 2 * A_BYTES;
+  static constexpr int STAGES = 5;
+  static constexpr int SF_OFF = STAGES * STAGE;
+  static constexpr int CTRL_OFF = SF_OFF + STAGES * SF_STAGE;
+  static constexpr int EPI_OFF = (CTRL_OFF + kCtrlBytes + 1023) / 1024 * 1024;
+  static constexpr int SMEM = EPI_OFF + kF4EpiWarps * kBoxBytes + 1024;
+  static constexpr int SLOT_COLS = 12 * ATOMS;
+  static_assert(SMEM <= 232448, "FP4 pair shared memory");
+  static_assert(kF4SfCol + STAGES * SLOT_COLS <= kF4TmemCols, "FP4 pair tensor-memory columns");
+};
+
+template <int FMT, int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF4Threads, 1)
+grouped_gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA,
+                             const __grid_constant__ CUtensorMap tmB,
+                             const __grid_constant__ CUtensorMap tmSB,
+                             const __grid_constant__ CUtensorMap tmC, const Fp4Params p) {
+  using C = F4PairCfg<FMT>;
+  constexpr bool NV = FMT == MOE_FP4_NV;
+  constexpr int kStages = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* sbase = smem_raw + (base - raw);
+  const uint32_t sf_u = base + C::SF_OFF;
+  const uint32_t ctrl_u = base + C::CTRL_OFF;
+  uint8_t* ctrl = sbase + C::CTRL_OFF;
+  const uint32_t bar_full = ctrl_u;                       // [kStages], the even CTA's
+  const uint32_t bar_empty = ctrl_u + 40;                 // [kStages]
+  const uint32_t bar_sf = ctrl_u + 80;                    // [kStages] this CTA's scale atoms
+  const uint32_t bar_scales = ctrl_u + 120;               // [kStages], the even CTA's
+  const uint32_t bar_tfull = ctrl_u + 160;
+  const uint32_t bar_tempty = ctrl_u + 168;
+  const uint32_t bar_drain = ctrl_u + 176;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 192);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 196);
+  int* prefix = reinterpret_cast<int*>(ctrl + 256);
+  int* mtiles = reinterpret_cast<int*>(ctrl + 1344);
+  int* s_off = reinterpret_cast<int*>(ctrl + 2432);
+  int* s_cnt = reinterpret_cast<int*>(ctrl + 3520);
+  int* tmp = reinterpret_cast<int*>(ctrl + 4608);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  const int G = p.G;
+  const int F = p.N / 2;
+  const int NT = EPI == kF4Swiglu ? F / (kF4BN / 2) : (p.N + kF4BN - 1) / kF4BN;
+  const int nk = (p.K + f4::kStep - 1) / f4::kStep;
+  for (int g = tid; g < G; g += kF4Threads) {
+    int64_t c = p.counts ? p.counts[g] : p.rows, o = p.counts ? p.offsets[g] : 0;
+    if (c < 0 || o < 0 || o % 128 || o + c > p.rows) {    // as in the single-CTA kernel
+      record_status(p.status, MOE_ERR_DEVICE_CHECK);
+      c = o = 0;
+    }
+    s_cnt[g] = (int)c;
+    s_off[g] = (int)o;
+    mtiles[g] = (int)((c + 2 * BM - 1) / (2 * BM));       // 256-row tiles
+    prefix[g] = mtiles[g] * NT;
+  }
+  if (tid == 0) *abort_flag = 0;
+  __syncthreads();
+  const int total = block_exclusive_scan(prefix, G, tmp);
+  if (tid == 0) prefix[G] = total;
+  __syncthreads();
+  if (cluster >= total) {                                 // both CTAs of the pair leave together
+    ptx::grid_dependency_wait();
+    return;
+  }
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(bar_full + 8 * s, 2);                // the even CTA's two producers
+      ptx::mbar_init(bar_empty + 8 * s, 1);
+      ptx::mbar_init(bar_sf + 8 * s, 2);
+      ptx::mbar_init(bar_scales + 8 * s, 8);              // four warps of both CTAs
+    }
+    ptx::mbar_init(bar_tfull, 1);
+    ptx::mbar_init(bar_tempty, 2 * kF4EpiWarps);
+    ptx::mbar_init(bar_drain, 1);
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), kF4TmemCols);
+    ptx::tmem_relinquish_pair();
+  }
+  if (tid == 0) {
+    ptx::tma_prefetch_desc(&tmA);
+    ptx::tma_prefetch_desc(&tmB);
+    ptx::tma_prefetch_desc(&tmSB);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  ptx::grid_launch_dependents();
+
+  if (warp == 0) {
+    // ------------------------------------- producer of the weights' stages
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, issued_mask = 0, issued_phase = 0;
+      bool ok = true;
+      for (int pt = cluster; pt < total && ok; pt += nclusters) {
+        const Tile t = decode(pt, prefix, mtiles, s_cnt, G, 0, p.K, NT, 0);
+        const int b0 = t.nt * (EPI == kF4Swiglu ? kF4BN / 2 : kF4BN);
+        const int part = EPI == kF4Swiglu ? 2 * t.g : t.g;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!ptx::mbar_wait(bar_empty + 8 * stage, phase ^ 1u, kWaitBudget, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t lf = ptx::mapa_shared(bar_full + 8 * stage, 0);
+          if (rank == 0) ptx::mbar_arrive_expect_tx(bar_full + 8 * stage, 2 * C::A_BYTES);
+          ptx::tma_load_3d_pair(base + stage * C::STAGE + C::A_BYTES, &tmB, lf, kb * kF4RowBytes,
+                                EPI == kF4Swiglu ? b0 : b0 + 128 * (int)rank,
+                                EPI == kF4Swiglu ? part + (int)rank : part);
+          const uint32_t sb = bar_sf + 8 * stage;
+          ptx::mbar_arrive_expect_tx(sb, 2 * C::SF_A);
+          ptx::tma_load_3d(sf_u + stage * C::SF_STAGE + C::SF_A, &tmSB, sb, kb * (C::SF_A / 8),
+                           b0 / 128, part);
+          issued_mask |= 1u << stage;
+          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        record_status(p.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+        // loads already issued land within microseconds; give them time
+        const long long t0 = clock64();
+        while (clock64() - t0 < 200000) {
+        }
+      }
+      for (int s = 0; s < kStages; ++s)
+        if (issued_mask & (1u << s))
+          ptx::mbar_wait(bar_sf + 8 * s, (issued_phase >> s) & 1u, kWaitBudget, nullptr);
+    }
+  } else if (warp == kF4RowWarp) {
+    // ----------------------------------------- producer of the rows' stages
+    if (lane == 0) {
+      ptx::grid_dependency_wait();
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      const int64_t slab_bytes = (int64_t)p.ka * f4::kAtomBytes;
+      for (int pt = cluster; pt < total && ok; pt += nclusters) {
+        const Tile t = decode(pt, prefix, mtiles, s_cnt, G, 0, p.K, NT, 0);
+        const int row0 = s_off[t.g] + (2 * t.mt + (int)rank) * BM;
+        // a tile's second half may hold no rows, and then may lie past the last slab
+        const int64_t slab = min((int64_t)(row0 / 128), f4::slabs(p.rows) - 1);
+        const uint8_t* sfa = p.sfa + slab * slab_bytes;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!ptx::mbar_wait(bar_empty + 8 * stage, phase ^ 1u, kWaitBudget, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t lf = ptx::mapa_shared(bar_full + 8 * stage, 0);
+          if (rank == 0) ptx::mbar_arrive_expect_tx(bar_full + 8 * stage, 2 * C::A_BYTES);
+          ptx::tma_load_2d_pair(base + stage * C::STAGE, &tmA, lf, kb * kF4RowBytes, row0);
+          const uint32_t sb = bar_sf + 8 * stage;
+          ptx::mbar_arrive_expect_tx(sb, C::SF_A);
+          ptx::bulk_load(sf_u + stage * C::SF_STAGE, sfa + (int64_t)kb * C::SF_A, C::SF_A, sb);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        record_status(p.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+        const long long t0 = clock64();
+        while (clock64() - t0 < 200000) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t IDESC = ptx::idesc_fp4(2 * BM, kF4BN, NV ? 0 : 1);
+      uint32_t stage = 0, phase = 0, acc_phase = 0;
+      bool ok = true, issued = false;
+      for (int pt = cluster; pt < total && ok; pt += nclusters) {
+        if (!ptx::mbar_wait(bar_tempty, acc_phase ^ 1u, kWaitBudget, abort_flag)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget, abort_flag) ||
+              !ptx::mbar_wait(bar_scales + 8 * stage, phase, kWaitBudget, abort_flag)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t sfa_t = tmem_base + kF4SfCol + C::SLOT_COLS * stage;
+          const uint32_t sfb_t = sfa_t + 4 * C::ATOMS;
+          const uint32_t sA = base + stage * C::STAGE;
+          const uint32_t sB = sA + C::A_BYTES;
+          const int slices = min(4, (p.K - kb * f4::kStep + 63) / 64);
+          for (int kk = 0; kk < slices; ++kk) {
+            const int a = NV ? kk : kk >> 1;
+            const uint32_t id = NV ? IDESC : ptx::idesc_with_sf_id(IDESC, (uint32_t)(kk & 1) * 2);
+            ptx::mma_fp4_pair<NV>(tmem_base, ptx::smem_desc_sw128(sA + kk * 32, 16, 1024),
+                                  ptx::smem_desc_sw128(sB + kk * 32, 16, 1024), id, sfa_t + 4 * a,
+                                  sfb_t + 8 * a, (kb | kk) ? 1u : 0u);
+          }
+          issued = true;
+          ptx::mma_commit_pair(bar_empty + 8 * stage, 3);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        ptx::mma_commit_pair(bar_tfull, 3);
+        acc_phase ^= 1u;
+      }
+      if (!ok) {
+        record_status(p.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      if (issued) {
+        ptx::mma_commit_pair(bar_drain, 1);
+        ptx::mbar_wait(bar_drain, 0, kWaitBudget, nullptr);
+      }
+    }
+  } else if (warp >= kF4ScaleWarp) {
+    // -------------------------------------------------------------- scales
+    const uint32_t tq = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + kF4SfCol;
+    const uint8_t* sfl = sbase + C::SF_OFF + lane * 16;
+    const uint32_t leader_scales = ptx::mapa_shared(bar_scales, 0);
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int pt = cluster; pt < total && ok; pt += nclusters) {
+      for (int kb = 0; kb < nk; ++kb) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_sf + 8 * stage, phase, kWaitBudget,
+                                                    abort_flag));
+        if (!ok) break;
+        write_scales<FMT>(sfl + stage * C::SF_STAGE, tq + C::SLOT_COLS * stage);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster_async(leader_scales + 8 * stage);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      record_status(p.status, MOE_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;
+    const int half = (warp - 2) >> 2;
+    uint8_t* stage = sbase + C::EPI_OFF + (warp - 2) * kBoxBytes;
+    const uint32_t stage_u32 = base + C::EPI_OFF + (warp - 2) * kBoxBytes;
+    const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16);
+    const uint32_t leader_tempty = ptx::mapa_shared(bar_tempty, 0);
+    uint32_t acc_phase = 0;
+    ptx::grid_dependency_wait();
+    for (int pt = cluster; pt < total; pt += nclusters) {
+      const Tile t = decode(pt, prefix, mtiles, s_cnt, G, 0, p.K, NT, 0);
+      const int m0 = (2 * t.mt + (int)rank) * BM + q * 32;
+      const int row0 = s_off[t.g] + m0;
+      const int rv = s_cnt[t.g] - m0;
+      const float alpha = (p.alpha ? p.alpha[t.g] : 1.f) * p.unit;
+      const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_tfull, acc_phase, kWaitBudget,
+                                                             abort_flag));
+      if (!ok) {
+        if (lane == 0) {
+          record_status(p.status, MOE_ERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+        break;
+      }
+      ptx::tc_fence_after();
+      uint4 o[4][4];
+      if (rv > 0) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          ptx::tmem_ld32(tq + slice_col<EPI>(half, c), r);
+          ptx::tmem_ld_wait();
+          scale_pack(r, alpha, o[c]);
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster_async(leader_tempty);
+      acc_phase ^= 1u;
+      if (rv <= 0) continue;
+#pragma unroll
+      for (int c = 0; c < (EPI == kF4Swiglu ? 2 : 4); ++c)
+        f4_epilogue<FMT, EPI, true>(p, &tmC, stage, stage_u32, t.nt, row0, rv, half, lane, c, o[c],
+                                    o[(c + 2) & 3]);
+    }
+    if (lane == 0) ptx::tma_store_wait_all();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem_base, kF4TmemCols);
+  }
+}
+
 template <int FMT, int EPI, int AROWS>
 static cudaError_t run_fp4_rows(const CUtensorMap& a, const CUtensorMap& a32, const CUtensorMap& b,
                                 const CUtensorMap& sb, const CUtensorMap& c, const Fp4Params& p,
@@ -762,11 +1092,53 @@ static cudaError_t run_fp4_rows(const CUtensorMap& a, const CUtensorMap& a32, co
   return cudaLaunchKernelEx(&lc, kern, a, a32, b, sb, c, p);
 }
 
+template <int FMT, int EPI>
+static cudaError_t run_fp4_pair(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& sb,
+                                const CUtensorMap& c, const Fp4Params& p, bool early,
+                                cudaStream_t s) {
+  auto kern = grouped_gemm_fp4_pair_kernel<FMT, EPI>;
+  constexpr int smem = F4PairCfg<FMT>::SMEM;
+  cudaLaunchConfig_t lc = {};
+  lc.blockDim = dim3(kF4Threads, 1, 1);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  static int grid = 0;
+  if (grid == 0) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    lc.gridDim = dim3(2 * (num_sms() / 2), 1, 1);
+    int clusters = 0;
+    e = cudaOccupancyMaxActiveClusters(&clusters, kern, &lc);
+    if (e != cudaSuccess || clusters <= 0) {
+      (void)cudaGetLastError();
+      clusters = num_sms() / 2;
+    }
+    grid = 2 * clusters;
+  }
+  lc.gridDim = dim3(grid, 1, 1);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = at;
+  lc.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&lc, kern, a, b, sb, c, p);
+}
+
+// Pairs where the experts expect at least kPairRows rows each: a 256-row tile whose second
+// half is empty still takes its time. 512 rows each exactly (64 experts, 4096 x 4096): 265 us
+// with single CTAs, 233 with pairs; 512 on average, 200 to 1200 (a whole FFN): 573 and 579;
+// 1024 on average (eight experts, 4096 x 14336, with the quantiser): 299 and 287.
+constexpr int64_t kPairRows = 768;
+static bool fp4_pairs(const Fp4Problem& q) { return q.mean_rows >= kPairRows; }
+
 template <int EPI>
 static cudaError_t run_fp4(const Fp4Problem& q, const CUtensorMap& a, const CUtensorMap& a32,
                            const CUtensorMap& b, const CUtensorMap& sb, const CUtensorMap& c,
                            const Fp4Params& p, cudaStream_t s) {
   const bool nv = q.fmt == MOE_FP4_NV;
+  if (fp4_pairs(q))
+    return nv ? run_fp4_pair<MOE_FP4_NV, EPI>(a, b, sb, c, p, q.early, s)
+              : run_fp4_pair<MOE_FP4_MX, EPI>(a, b, sb, c, p, q.early, s);
   if (q.most_rows <= 32)
     return nv ? run_fp4_rows<MOE_FP4_NV, EPI, 32>(a, a32, b, sb, c, p, q.early, s)
               : run_fp4_rows<MOE_FP4_MX, EPI, 32>(a, a32, b, sb, c, p, q.early, s);
@@ -784,10 +1156,11 @@ static bool make_map_fp4(CUtensorMap* m, const void* ptr, int64_t K, int64_t row
 }
 
 // Weights in 4 bits as `parts` blocks of `rows` rows, a box of 128 bytes x box_rows x
-// box_parts, and their scale atoms, 8 bytes an element: one k-block's atoms of as many
-// slabs. What lies past a block's rows reads as zero.
+// box_parts (pair: one CTA's half of it), and their scale atoms, 8 bytes an element: one
+// k-block's atoms of as many slabs. What lies past a block's rows reads as zero.
 static bool make_map_weights(CUtensorMap* codes, CUtensorMap* scales, const Fp4Problem& q,
-                             int64_t rows, int64_t parts, uint32_t box_rows, uint32_t box_parts) {
+                             int64_t rows, int64_t parts, uint32_t box_rows, uint32_t box_parts,
+                             bool pair) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t kb = (cuuint64_t)q.K / 2, sl = (cuuint64_t)f4::slabs(rows);
@@ -795,7 +1168,7 @@ static bool make_map_weights(CUtensorMap* codes, CUtensorMap* scales, const Fp4P
   const cuuint32_t es[3] = {1, 1, 1};
   const cuuint64_t d[3] = {kb, (cuuint64_t)rows, (cuuint64_t)parts};
   const cuuint64_t st[2] = {kb, kb * (cuuint64_t)rows};
-  const cuuint32_t box[3] = {kF4RowBytes, box_rows, box_parts};
+  const cuuint32_t box[3] = {kF4RowBytes, pair ? 128u : box_rows, pair ? 1u : box_parts};
   const cuuint64_t ds[3] = {sb / 8, sl, (cuuint64_t)parts};
   const cuuint64_t sts[2] = {sb, sb * sl};
   const cuuint32_t boxs[3] = {(cuuint32_t)f4::step_atoms(q.fmt) * f4::kAtomBytes / 8,
@@ -839,7 +1212,7 @@ cudaError_t launch_fp4_gemm(const Fp4Problem& q, void* out, const Fp4Split& sp, 
   if (q.rows == 0 || q.N == 0) return cudaSuccess;
   CUtensorMap a, a32, b, sb, c;
   if (!make_map_fp4(&a, q.a, q.K, q.rows, 128) || !make_map_fp4(&a32, q.a, q.K, q.rows, 32) ||
-      !make_map_weights(&b, &sb, q, q.N, q.G, 256, 1) ||
+      !make_map_weights(&b, &sb, q, q.N, q.G, 256, 1, fp4_pairs(q)) ||
       !make_out_map(&c, out, (uint64_t)q.N, (uint64_t)q.rows))
     return cudaErrorInvalidValue;
   Fp4Params p = fp4_params(q, sp, status);
@@ -853,7 +1226,7 @@ cudaError_t launch_fp4_swiglu(const Fp4Problem& q, uint8_t* hq, uint8_t* hsf, in
   if (q.rows == 0) return cudaSuccess;
   CUtensorMap a, a32, b, sb;
   if (!make_map_fp4(&a, q.a, q.K, q.rows, 128) || !make_map_fp4(&a32, q.a, q.K, q.rows, 32) ||
-      !make_map_weights(&b, &sb, q, q.N / 2, 2 * (int64_t)q.G, 128, 2))
+      !make_map_weights(&b, &sb, q, q.N / 2, 2 * (int64_t)q.G, 128, 2, fp4_pairs(q)))
     return cudaErrorInvalidValue;
   Fp4Params p = fp4_params(q, sp, status);
   p.hq = hq;

@@ -195,6 +195,7 @@ struct Fp4Problem {
   // began: this one may start while it runs (programmatic dependent launch).
   bool early;
   int64_t most_rows;          // no group has more rows than this
+  int64_t mean_rows;          // about how many a group has
 };
 // Scratch of the products that cut K: fp32 parts and arrival counters (zero).
 struct Fp4Split {

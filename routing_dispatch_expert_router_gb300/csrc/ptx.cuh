@@ -313,6 +313,31 @@ __device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_
            "r"(sfb_tmem) : "memory");
 }
 
+// The pair form: A rows and B columns split between the two CTAs' shared memory as in
+// mma_bf16_pair, each CTA's tensor memory holding its own rows' scales of A and the
+// scales of all of B's columns.
+template <bool NV>
+__device__ __forceinline__ void mma_fp4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                             uint32_t accumulate) {
+  if (NV)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X "
+        "[%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+        :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem),
+           "r"(sfb_tmem) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X "
+        "[%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+        :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem),
+           "r"(sfb_tmem) : "memory");
+}
+
 // Shared-memory descriptor of one scale-factor atom for tcgen05.cp: 32 rows of
 // 16 bytes, no swizzle, 8-row core matrices 128 bytes apart (SBO); the atom is
 // one core matrix wide along K, so LBO is unused (0).

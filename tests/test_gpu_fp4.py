@@ -179,6 +179,8 @@ def weights(fmt, rng, G, N, K, log2=0):
 
 PRODUCTS = [
     ([1], 8, 32), ([0], 64, 64), ([1, 0, 1, 3], 1000, 288), ([127, 128, 129, 0, 1], 264, 1504),
+    # many rows an expert (CTA pairs): odd and even numbers of 128-row tiles, an empty one
+    ([1700, 3, 0, 1900], 264, 800), ([812], 136, 96), ([1100, 900], 512, 2080),
     ([300, 2], 128, 4096), ([33], 512, 7168), ([600], 520, 544), ([31, 32, 64, 65, 96, 97], 256, 256),
 ]
 
@@ -305,7 +307,9 @@ def h_interval(fmt, x, W13):
 
 FFNS = [([1], 128, 128), ([0, 3, 130, 0, 64], 128, 384), ([40, 129], 256, 640),
         # sums cut over the SMs: up to 64 rows, several parts of a tile
-        ([1], 512, 2048), ([40, 0, 1, 64], 1024, 384), ([2, 33], 256, 4096)]
+        ([1], 512, 2048), ([40, 0, 1, 64], 1024, 384), ([2, 33], 256, 4096),
+        # CTA pairs
+        ([1000, 612], 256, 384), ([2200, 0, 260], 384, 256)]
 
 
 def run_ffn(fmt, counts, H, F, ckpt=True, seed=0, T=None):
@@ -459,7 +463,7 @@ def test_repeated_passes_are_equal_bit_for_bit(fmt):
     """Thirty passes of every product over the same rows: whatever the order in which loads
     land and parts arrive, the results are the same numbers."""
     rng = np.random.default_rng(21)
-    counts, H, F = [520, 0, 600, 40], 512, 1024
+    counts, H, F = [2520, 0, 600, 40], 512, 1024
     off, rows, cnt, offs = segments(counts)
     cfg = B.config(MoEShape("r", T=len(rows), H=H, E=4, k=1, F=F))
     R = B.moe_query_sizes(cfg).rows_max
