@@ -17,6 +17,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 namespace f4 {
@@ -49,6 +50,11 @@ struct Fp4Scale {
   float inv;
 };
 
+// To 12 significant bits, to nearest.
+__device__ __forceinline__ float fp4_snap(float q) {
+  return __uint_as_float((__float_as_uint(q) + 0x800u) & 0xFFFFF000u);
+}
+
 // amax: the block's largest magnitude, a bf16 number; finite: whether every
 // element of the block is. down = 2^-scale_log2 (NV).
 // NV: the scale is amax / (6 2^scale_log2) rounded to E4M3 (to nearest, at most
@@ -60,16 +66,19 @@ template <int FMT>
 __device__ __forceinline__ Fp4Scale fp4_scale(float amax, bool finite, float down) {
   Fp4Scale s;
   if (FMT == MOE_FP4_NV) {
-    const float a = amax * down;
+    // a sixth as a product: amax has 8 significant bits and a border between two
+    // scales 5, so a quotient that is not on one is 2^-10 away; rounding the product
+    // (within 2^-23) to 12 bits puts those that are exactly there (a tie)
+    const float a = fp4_snap(amax * down * (1.f / 6.f));
     uint16_t h;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(0.f), "f"(__fdiv_rn(a, 6.f)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(0.f), "f"(a));
     uint32_t half2;                              // the scale's value, as an fp16 pair
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"(h));
     float v;
     asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}"
         : "=f"(v) : "r"(half2));
     s.byte = finite ? (h & 0xffu) : 0x7Fu;
-    s.inv = (finite && v > 0.f) ? __fdiv_rn(down, v) : 0.f;
+    s.inv = (finite && v > 0.f) ? down * ptx::rcp_approx(v) : 0.f;
   } else {
     const uint32_t b = __float_as_uint(amax);
     int code = (int)(b >> 23) - 2 + ((b & 0x7FFFFFu) > 0x400000u ? 1 : 0);
@@ -91,7 +100,7 @@ template <int FMT>
 __device__ __forceinline__ float fp4_quotient(float x, float inv) {
   const float q = x * inv;
   if (FMT == MOE_FP4_MX) return q;
-  return __uint_as_float((__float_as_uint(q) + 0x800u) & 0xFFFFF000u);
+  return fp4_snap(q);
 }
 
 // E2M1 codes of eight quotients (to nearest, ties to even, at most 6): 4 bytes
@@ -135,16 +144,12 @@ __device__ __forceinline__ float fp4_scale_value(uint32_t byte) {
   return __uint_as_float(byte ? byte << 23 : 0x00400000u);
 }
 
-// Largest magnitude of eight bf16 values; NaN counts as infinite.
+// Largest magnitude of eight bf16 values, as its bits (magnitudes order as integers; NaN
+// counts as more than infinite).
 __device__ __forceinline__ uint32_t amax_bits8(const uint4& v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    m = max(m, w[i] & 0x7FFFu);                  // magnitudes of bf16 order as integers
-    m = max(m, (w[i] >> 16) & 0x7FFFu);
-  }
-  return m;
+  constexpr uint32_t kMag = 0x7FFF7FFFu;
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & kMag, v.y & kMag), __vmaxu2(v.z & kMag, v.w & kMag));
+  return max(m & 0xFFFFu, m >> 16);
 }
 
 }  // namespace moe
