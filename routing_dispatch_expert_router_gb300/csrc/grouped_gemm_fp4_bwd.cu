@@ -25,8 +25,9 @@
 //   warps 10-17 the codes' values into B's stage (MN-major, 128-byte swizzle), 8192
 //               elements a k-block; teams of two warps take k-blocks in turn, so that
 //               one team's waits, loads and stores pass under the others' work.
-// Both products of that layer (32768 rows) take 1345 us: 0.42 us a k-block, of which
-// the MMAs and A's loads alone take 0.34. What is left is shared memory's bandwidth:
+// Both products of that layer (32768 rows) take 1345 us again and again on the same
+// inputs, 1460 to 1490 with three sets in turn: 0.42 us a k-block, of which the MMAs and
+// A's loads alone take 0.34. What is left is shared memory's bandwidth:
 // the MMAs' reads, A's arrival and the codes' way in and values' way out fill about 600
 // of 780 cycles a k-block. On the way: all eight warps on one k-block 3306 us, teams of
 // four warps 2608, of two 1820; without bank conflicts 1772; the arrivals at the even
