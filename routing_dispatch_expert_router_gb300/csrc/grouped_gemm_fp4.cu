@@ -711,6 +711,9 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
         }
         last = __shfl_sync(0xffffffffu, last, 0);
         if (!last) continue;
+        // a shuffle orders no memory: what lane 0's atomic acquired (the other parts) the
+        // other lanes may read only past this
+        __syncwarp();
         const int rows = min(rv, 32);
         // the first part ends at its CTA's share (slot 2 b0 + 1), the others begin theirs
         const float* first = parts + (4 * (int64_t)b0 + 2) * slice + 4 * lane;
