@@ -831,7 +831,7 @@ grouped_gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA,
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(bar_full + 8 * s, 2);                // the even CTA's two producers
-      ptx::mbar_init(bar_empty + 8 * s, 1);
+      ptx::mbar_init(bar_empty + 8 * s, 1 + 4);           // the MMAs, and this CTA's scale warps
       ptx::mbar_init(bar_sf + 8 * s, 2);
       ptx::mbar_init(bar_scales + 8 * s, 8);              // four warps of both CTAs
     }
@@ -866,7 +866,8 @@ grouped_gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA,
         const int b0 = t.nt * (EPI == kF4Swiglu ? kF4BN / 2 : kF4BN);
         const int part = EPI == kF4Swiglu ? 2 * t.g : t.g;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!ptx::mbar_wait(bar_empty + 8 * stage, phase ^ 1u, kWaitBudget, abort_flag)) {
+          if (!ptx::mbar_wait_cluster(bar_empty + 8 * stage, phase ^ 1u, kWaitBudget,
+                                      abort_flag)) {
             ok = false;
             break;
           }
@@ -913,7 +914,8 @@ grouped_gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA,
         const int64_t slab = min((int64_t)(row0 / 128), f4::slabs(p.rows) - 1);
         const uint8_t* sfa = p.sfa + slab * slab_bytes;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!ptx::mbar_wait(bar_empty + 8 * stage, phase ^ 1u, kWaitBudget, abort_flag)) {
+          if (!ptx::mbar_wait_cluster(bar_empty + 8 * stage, phase ^ 1u, kWaitBudget,
+                                      abort_flag)) {
             ok = false;
             break;
           }
@@ -944,14 +946,14 @@ grouped_gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA,
       uint32_t stage = 0, phase = 0, acc_phase = 0;
       bool ok = true, issued = false;
       for (int pt = cluster; pt < total && ok; pt += nclusters) {
-        if (!ptx::mbar_wait(bar_tempty, acc_phase ^ 1u, kWaitBudget, abort_flag)) {
+        if (!ptx::mbar_wait_cluster(bar_tempty, acc_phase ^ 1u, kWaitBudget, abort_flag)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
         for (int kb = 0; kb < nk; ++kb) {
-          if (!ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget, abort_flag) ||
-              !ptx::mbar_wait(bar_scales + 8 * stage, phase, kWaitBudget, abort_flag)) {
+          if (!ptx::mbar_wait_cluster(bar_full + 8 * stage, phase, kWaitBudget, abort_flag) ||
+              !ptx::mbar_wait_cluster(bar_scales + 8 * stage, phase, kWaitBudget, abort_flag)) {
             ok = false;
             break;
           }
@@ -1002,7 +1004,12 @@ grouped_gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA,
         if (!ok) break;
         write_scales<FMT>(sfl + stage * C::SF_STAGE, tq + C::SLOT_COLS * stage);
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster_async(leader_scales + 8 * stage);
+        if (lane == 0) {
+          // the even CTA's MMAs may read the columns, and the slot's bytes, read here, may
+          // be overwritten once those MMAs are done (an order within this CTA)
+          ptx::mbar_arrive_cluster_tmem(leader_scales + 8 * stage);
+          ptx::mbar_arrive(bar_empty + 8 * stage);
+        }
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1u;
@@ -1029,8 +1036,8 @@ grouped_gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA,
       const int row0 = s_off[t.g] + m0;
       const int rv = s_cnt[t.g] - m0;
       const float alpha = (p.alpha ? p.alpha[t.g] : 1.f) * p.unit;
-      const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_tfull, acc_phase, kWaitBudget,
-                                                             abort_flag));
+      const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(bar_tfull, acc_phase,
+                                                                     kWaitBudget, abort_flag));
       if (!ok) {
         if (lane == 0) {
           record_status(p.status, MOE_ERR_TIMEOUT);
@@ -1051,7 +1058,7 @@ grouped_gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA,
       }
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster_async(leader_tempty);
+      if (lane == 0) ptx::mbar_arrive_cluster_tmem(leader_tempty);
       acc_phase ^= 1u;
       if (rv <= 0) continue;
 #pragma unroll

@@ -25,15 +25,17 @@
 //   warps 10-17 the codes' values into B's stage (MN-major, 128-byte swizzle), 8192
 //               elements a k-block; teams of two warps take k-blocks in turn, so that
 //               one team's waits, loads and stores pass under the others' work.
-// Both products of that layer (32768 rows) take 1345 us again and again on the same
-// inputs, 1460 to 1490 with three sets in turn: 0.42 us a k-block, of which the MMAs and
+// Both products of that layer (32768 rows) take 1373 to 1381 us again and again on the same
+// inputs, 1457 to 1493 with three sets in turn: 0.43 us a k-block, of which the MMAs and
 // A's loads alone take 0.34. What is left is shared memory's bandwidth:
 // the MMAs' reads, A's arrival and the codes' way in and values' way out fill about 600
 // of 780 cycles a k-block. On the way: all eight warps on one k-block 3306 us, teams of
-// four warps 2608, of two 1820; without bank conflicts 1772; the arrivals at the even
-// CTA's barrier without release.cluster (1600 cycles each) 1345. Tiles of 512 x 128 (B
-// made once for 512 rows) take 2057: MMAs of N=128 run at half rate. 512 x 256 with one
-// set of accumulators: 1850 before the arrivals changed (1772 then).
+// four warps 2608, of two 1820; without bank conflicts 1772; the odd CTA's
+// arrivals at the even CTA's barrier with a release of shared memory alone 1375 (one of
+// all memory takes a warp 1600 cycles; made by a thread of its own, one k-block after the
+// other, 2888). Tiles of 512 x 128 (B made once for 512 rows) take 2057: MMAs of N=128 run
+// at half rate. 512 x 256 with one set of accumulators: 1850 before the arrivals changed
+// (1772 then).
 #include "fp4_layout.cuh"
 #include "gemm_common.cuh"
 
@@ -251,7 +253,8 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         decode_pair(pt, g, mp, nt);
         const int row0 = s_off[g] + (2 * mp + (int)rank) * BM;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!ptx::mbar_wait(bar_empty + 8 * stage, phase ^ 1u, kWaitBudget, abort_flag)) {
+          if (!ptx::mbar_wait_cluster(bar_empty + 8 * stage, phase ^ 1u, kWaitBudget,
+                                      abort_flag)) {
             ok = false;
             break;
           }
@@ -321,14 +324,15 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true, issued = false;
       for (int pt = cluster; pt < total && ok; pt += nclusters) {
-        if (!ptx::mbar_wait(bar_tempty + 8 * acc, acc_phase ^ 1u, kWaitBudget, abort_flag)) {
+        if (!ptx::mbar_wait_cluster(bar_tempty + 8 * acc, acc_phase ^ 1u, kWaitBudget,
+                                    abort_flag)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + acc * kD4BN;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget, abort_flag)) {
+          if (!ptx::mbar_wait_cluster(bar_full + 8 * stage, phase, kWaitBudget, abort_flag)) {
             ok = false;
             break;
           }
@@ -405,8 +409,8 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                        : sf[sub];
           }
           // the MMAs that read this stage's B are done
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_empty + 8 * stage, phase ^ 1u,
-                                                      kWaitBudget, abort_flag));
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(bar_empty + 8 * stage, phase ^ 1u,
+                                                              kWaitBudget, abort_flag));
           if (!ok) break;
 #pragma unroll
           for (int i = 0; i < kPass; ++i) {
@@ -430,7 +434,8 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
           // ones that had not returned, and the next codes landed under them)
           if (lane == 0) {
             ptx::mbar_arrive(bar_code_empty + 8 * slot);
-            ptx::mbar_arrive_cluster_async(leader_full + 8 * stage);
+            if (rank == 0) ptx::mbar_arrive(bar_full + 8 * stage);
+            else ptx::mbar_arrive_cluster_smem(leader_full + 8 * stage);
           }
         }
         if (++turn == kD4Teams) turn = 0;
@@ -492,8 +497,8 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
           rw = p.W_r + (int64_t)g * p.N + f0;
         }
       }
-      bool ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_tfull + 8 * acc, acc_phase,
-                                                       kWaitBudget, abort_flag));
+      bool ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(bar_tfull + 8 * acc, acc_phase,
+                                                               kWaitBudget, abort_flag));
       if (!ok) {
         if (lane == 0) {
           record_status(p.status, MOE_ERR_TIMEOUT);

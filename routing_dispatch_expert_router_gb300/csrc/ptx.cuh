@@ -445,12 +445,43 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                :: "r"(cluster_addr) : "memory");
 }
 
-// The same for shared-memory data that only the async proxy reads, and that this
-// CTA's threads have made visible to it (fence.proxy.async) before: the arrival then
-// orders nothing at cluster scope, which takes under a hundred cycles where
-// release.cluster takes 1600.
-__device__ __forceinline__ void mbar_arrive_cluster_async(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+// The same where what the arrival publishes are accesses to tensor memory alone: the
+// PTX ISA's pattern for tcgen05 operations of two threads, tcgen05.wait and
+// tcgen05.fence::before_thread_sync, this arrival, a wait at cluster scope,
+// tcgen05.fence::after_thread_sync. It orders no access to shared or global memory.
+__device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];"
+               :: "r"(cluster_addr) : "memory");
+}
+
+// The same where it publishes writes to this CTA's shared memory alone: a release at
+// cluster scope restricted to that window, and the arrival.
+__device__ __forceinline__ void mbar_arrive_cluster_smem(uint32_t cluster_addr) {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;\n\t"
+               "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];"
+               :: "r"(cluster_addr) : "memory");
+}
+
+// mbar_wait on a barrier of this CTA that the other CTA of the pair arrives at too:
+// acquires at cluster scope what was released there.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, long long budget,
+                                                  volatile int* abort) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (abort && *abort) return false;
+    if (clock64() - t0 > budget) return false;
+  }
 }
 
 // 2D tiled load into this CTA's shared memory whose completion is counted on an
