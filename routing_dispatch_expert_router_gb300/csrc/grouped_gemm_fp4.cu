@@ -340,6 +340,7 @@ __device__ __forceinline__ void write_scales(const uint8_t* src, uint32_t col) {
     *reinterpret_cast<uint4*>(b + 8 * i + 4) =
         *reinterpret_cast<const uint4*>(src + 2 * SF_A + 512 * i);
   }
+  ptx::tc_fence_after();                 // after the MMAs that read these columns before
   if (FMT == MOE_FP4_NV) {
     ptx::tmem_st16(col, a);
     ptx::tmem_st32(col + 16, b);

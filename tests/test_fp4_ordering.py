@@ -47,3 +47,13 @@ def test_values_made_for_the_other_ctas_mma_are_released():
     f = ptx[ptx.index("void mbar_arrive_cluster_smem"):]
     f = f[:f.index("\n}\n")]
     assert f.index("fence.release.sync_restrict::shared::cta.cluster") < f.index("mbarrier.arrive")
+
+
+def test_scale_columns_are_written_behind_a_tensor_memory_fence():
+    """The columns' last readers are MMAs of the stage's turn before: between the barrier
+    that says so and tcgen05.st stands the fence that orders them."""
+    text = source("grouped_gemm_fp4.cu")
+    f = text[text.index("void write_scales("):]
+    f = f[:f.index("\n}\n")]
+    assert "tc_fence_after" in f and f.index("tc_fence_after") < f.index("tmem_st")
+    assert f.rindex("tmem_st_wait") < f.index("tc_fence_before")
