@@ -8,13 +8,15 @@ using namespace moe;
 
 namespace {
 
-// Scratch of a product: the status word, the arrival counters of the parts of
-// cut tiles (8 epilogue warps each), then the fp32 parts.
+// Scratch of a product: the status word, each CTA's count of its launches, the arrival
+// counters of the parts of cut tiles (8 epilogue warps each), then the fp32 parts.
+constexpr int64_t kLaunchesOffset = 1024;
 constexpr int64_t kArrivedOffset = 4096;
 constexpr int kArrived = 8192;
 constexpr int64_t kPartOffset = 65536;
 constexpr int64_t kPartBytes = 39LL << 19;       // 64 rows in two parts per SM
 constexpr int64_t kGemmScratch = kPartOffset + kPartBytes;
+static_assert(kLaunchesOffset + kFp4SplitCtas * 4 <= kArrivedOffset, "launches before the counters");
 static_assert(kArrivedOffset + kArrived * 4 <= kPartOffset, "counters before the parts");
 
 #define FP4_TRY(expr)                  \
@@ -60,7 +62,8 @@ moe_status check_tensor(const moe_fp4_tensor* q) {
 Fp4Split split_of(void* scratch) {
   uint8_t* p = static_cast<uint8_t*>(scratch);
   return Fp4Split{reinterpret_cast<float*>(p + kPartOffset), kPartBytes / 4,
-                  reinterpret_cast<int32_t*>(p + kArrivedOffset), kArrived};
+                  reinterpret_cast<uint32_t*>(p + kArrivedOffset), kArrived,
+                  reinterpret_cast<uint32_t*>(p + kLaunchesOffset)};
 }
 
 // What an FFN call keeps behind a product's scratch.

@@ -70,11 +70,12 @@ struct Fp4Params {
   float hdown;                 // 2^-(h's scale_log2)
   uint8_t* ckpt;
   uint8_t* ckpt_sf;
-  // split K: fp32 parts and their arrival counters (zero before and after a launch)
+  // split K: fp32 parts, their arrival counters, the CTAs' counts of launches
   float* part;
   int64_t part_floats;
-  int32_t* arrived;
+  uint32_t* arrived;
   int arrived_n;
+  uint32_t* launches;
   int32_t* status;
 };
 
@@ -147,12 +148,32 @@ constexpr int kAlone = 65, kJoin = 200, kJoinRow = 80;
 __device__ __forceinline__ int share_evenly(int tiles, int nk, int grid, int most_rows,
                                             int64_t part_floats, int counters) {
   const int slot_rows = min(BM, (most_rows + 31) / 32 * 32);
-  if ((int64_t)2 * grid * slot_rows * kF4BN > part_floats || tiles * kF4EpiWarps > counters)
+  if ((int64_t)2 * grid * slot_rows * kF4BN > part_floats || tiles * kF4EpiWarps > counters ||
+      grid > kFp4SplitCtas)
     return 0;
   const int m = tiles % grid;
   const int64_t whole = (int64_t)nk * (tiles / grid * 100 + (m ? max(kAlone, 100 * m / grid) : 0));
   const int64_t share = (int64_t)tiles * nk * 100 / grid;
   return whole > share + kJoin + most_rows * kJoinRow;
+}
+
+// The launch's number on this scratch, from 1: every CTA of every launch counts itself once,
+// behind the kernel before this one, whatever becomes of its waits.
+__device__ __forceinline__ uint32_t count_launch(const Fp4Params& p) {
+  return gridDim.x <= kFp4SplitCtas ? atomicAdd(p.launches + blockIdx.x, 1u) + 1u : 0u;
+}
+
+// An arrival counter holds the parts that have arrived in its low eight bits and above them
+// the launch they arrived in (`tag`). Each part's warp opens the counter before it waits for
+// its first MMAs: what an earlier launch has left there (one that gave up leaves some
+// arrivals counted and others not) gives way to this launch's zero.
+__device__ __forceinline__ void open_counter(uint32_t* a, uint32_t tag) {
+  uint32_t v = 0;
+  while (true) {
+    const uint32_t old = atomicCAS(a, v, tag);
+    if (old == v || (old ^ tag) <= 255u) return;
+    v = old;
+  }
 }
 
 // h of 32 columns (bf16 pairs) in 4 bits: codes to `dst` (16 bytes); returns the
@@ -380,6 +401,7 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 192);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 196);
   int* s_most = reinterpret_cast<int*>(ctrl + 200);
+  uint32_t* s_launch = reinterpret_cast<uint32_t*>(ctrl + 204);
   int* prefix = reinterpret_cast<int*>(ctrl + 256);
   int* mtiles = reinterpret_cast<int*>(ctrl + 1344);
   int* s_off = reinterpret_cast<int*>(ctrl + 2432);
@@ -419,6 +441,7 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
   Work w(tiles, nk_all, even);
   if (w.pos >= w.end) {
     ptx::grid_dependency_wait();                 // this kernel ends after the one before it
+    if (tid == 0) count_launch(p);
     return;
   }
 
@@ -620,6 +643,14 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
     uint32_t acc_phase = 0;
     // nothing is written before the kernel before this one is done
     ptx::grid_dependency_wait();
+    if (tid == 64) *s_launch = count_launch(p);
+    asm volatile("bar.sync 1, %0;" :: "n"(32 * kF4EpiWarps) : "memory");
+    if (even && lane < 2) {
+      // the counters of the first and the last tile of this CTA's share: no other is cut
+      const int tile = (int)(lane ? w.end - 1 : w.pos) / nk_all;
+      open_counter(p.arrived + tile * kF4EpiWarps + (warp - 2), *s_launch << 8);
+    }
+    __syncwarp();
     while (w.next()) {
       const Tile t = decode(w.tile, prefix, mtiles, s_cnt, G, 0, p.K, NT, 0);
       const int row0 = s_off[t.g] + t.mt * BM + q * 32;
@@ -706,9 +737,9 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
         const int b0 = w.first(), b1 = w.last();
         int last = 0;
         if (lane == 0) {
-          int32_t* a = p.arrived + w.tile * kF4EpiWarps + (warp - 2);
-          last = ptx::atom_add_acq_rel(a, 1) == b1 - b0;
-          if (last) *a = 0;                       // as the next launch expects it
+          uint32_t* counter = p.arrived + w.tile * kF4EpiWarps + (warp - 2);
+          last = (int)(ptx::atom_add_acq_rel(counter, 1u) & 255u) == b1 - b0;
+          if (last) *counter = 0;                 // so that a tag that comes round again meets none
         }
         last = __shfl_sync(0xffffffffu, last, 0);
         if (!last) continue;
@@ -1210,6 +1241,7 @@ static Fp4Params fp4_params(const Fp4Problem& q, const Fp4Split& sp, int32_t* st
   p.part_floats = sp.part_floats;
   p.arrived = sp.arrived;
   p.arrived_n = sp.arrived_n;
+  p.launches = sp.launches;
   p.status = status;
   return p;
 }

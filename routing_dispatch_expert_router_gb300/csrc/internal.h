@@ -197,13 +197,18 @@ struct Fp4Problem {
   int64_t most_rows;          // no group has more rows than this
   int64_t mean_rows;          // about how many a group has
 };
-// Scratch of the products that cut K: fp32 parts and arrival counters (zero).
+// Scratch of the products that cut K: fp32 parts, their arrival counters, and how often
+// each CTA's index has run on this scratch (zero at first; the same number for every CTA
+// of a launch).
 struct Fp4Split {
   float* part;
   int64_t part_floats;
-  int32_t* arrived;
+  uint32_t* arrived;
   int arrived_n;
+  uint32_t* launches;
 };
+// The most CTAs that may share tiles: a counter has eight bits for a tile's parts.
+constexpr int kFp4SplitCtas = 255;
 cudaError_t launch_fp4_gemm(const Fp4Problem& q, void* out, const Fp4Split& sp, int32_t* status,
                             cudaStream_t s);
 // The gate-up product with SwiGLU: h in 4 bits (hq, hsf), and the checkpoint of
