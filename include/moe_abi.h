@@ -586,7 +586,8 @@ typedef struct moe_fp4_sizes {
 
 /* Scratch of the 4-bit calls, zero-filled once by the caller and then left to
  * the calls (its first word is the device status word). cfg may be NULL: only
- * gemm_scratch_bytes is then set. Calls that may overlap need scratch each.
+ * gemm_scratch_bytes is then set. Calls that may overlap need scratch each; calls
+ * that follow each other on a stream may share one of the largest size.
  * After a call that recorded MOE_ERR_TIMEOUT, moe_clear_device_status is enough:
  * no later call reads what that one left in its scratch.
  * Host only. */

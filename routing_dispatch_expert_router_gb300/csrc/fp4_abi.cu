@@ -84,8 +84,9 @@ int64_t fwd_region(const moe_config& c, int fmt, void* scratch, FwdScratch* f) {
   return off;
 }
 
-// The backward's: [dG | dU] between the products, without the weights' scales.
-constexpr int64_t kDguOffset = 4096;
+// The backward's: [dG | dU] between the products, without the weights' scales; behind the
+// counters of a forward that the caller runs on the same scratch.
+constexpr int64_t kDguOffset = kPartOffset;
 int64_t bwd_region(const moe_config& c) {
   return kDguOffset + up256(rows_max(c) * 2 * c.F * 2);
 }

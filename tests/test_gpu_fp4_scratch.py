@@ -76,3 +76,29 @@ def test_product_after_a_call_that_gave_up():
             torch.cuda.synchronize()
             assert torch.equal(out, first)
     assert B.moe_last_device_status(sc) == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_one_scratch_for_forward_product_and_backward(fmt):
+    """Calls that follow each other may share scratch: what the backward keeps there lies
+    behind the counters, and the forward's and the product's numbers are a fresh scratch's."""
+    counts, H, F = [1, 1], 4096, 4096
+    s = T4.run_ffn(fmt, counts, H, F)
+    rows = s["rows"]
+    y = s["y"][rows].clone()
+    sz = B.moe_fp4_query_sizes(s["cfg"], fmt)
+    sc = B.alloc_fp4_scratch(max(sz.gemm_scratch_bytes, sz.fwd_scratch_bytes, sz.bwd_scratch_bytes))
+    dX = [torch.zeros_like(s["y"]) for _ in range(2)]
+    for i in range(2):
+        s["y"].fill_(7.0)
+        B.moe_fp4_ffn_fwd(s["cfg"], s["ex"][0], s["x"], s["cnt"], s["offs"], s["ck"], s["cs"],
+                          s["y"], sc)
+        assert torch.equal(y, s["y"][rows])
+        before = sc[COUNTERS].clone()
+        # dO = the token rows: gradients of ordinary size
+        B.moe_fp4_ffn_bwd(s["cfg"], s["ex"][0], s["x"], s["ck"], s["cs"], s["cnt"], s["offs"],
+                          None, None, None, dX[i], sc)
+        assert dX[i][rows].any()
+        assert torch.equal(before, sc[COUNTERS])
+    assert torch.equal(dX[0], dX[1])
+    assert B.moe_last_device_status(sc) == 0
