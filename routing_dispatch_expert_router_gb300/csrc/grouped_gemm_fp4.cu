@@ -58,7 +58,8 @@ struct Fp4Params {
   const int32_t* counts;       // null: one group of `rows` rows
   const int32_t* offsets;
   const float* alpha;          // [G], or null: 1
-  float unit;                  // times alpha: the operands' tensor scales
+  float unit;                  // times alpha: the operands' tensor scales, 2^unit_log2
+  int unit_log2;
   const uint8_t* sfa;          // A's atoms, [slabs][ka][512]
   int ka;                      // atoms of a slab
   __nv_bfloat16* out;          // store: [rows, N]
@@ -301,8 +302,10 @@ __device__ __forceinline__ void f4_epilogue(const Fp4Params& p, const CUtensorMa
 // the swiglu form lanes 0-15 hold gate and lanes 16-31 the matching up columns).
 template <int FMT, int EPI>
 __device__ __noinline__ void f4_epilogue_row(const Fp4Params& p, int nt, int64_t row, int half,
-                                                int lane, const float4& v) {
+                                                int lane, const float4& v, uint32_t rest) {
   uint2 b = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(b.x) : "r"(rest));
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(b.y) : "r"(rest));
   if (EPI == kF4Store) {
     const int col = nt * kF4BN + 128 * half + 4 * lane;
     if (col < p.N) *reinterpret_cast<uint2*>(p.out + row * p.N + col) = b;
@@ -655,7 +658,9 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
       const Tile t = decode(w.tile, prefix, mtiles, s_cnt, G, 0, p.K, NT, 0);
       const int row0 = s_off[t.g] + t.mt * BM + q * 32;
       const int rv = s_cnt[t.g] - t.mt * BM - q * 32;    // rows of this warp that hold data
-      const float alpha = (p.alpha ? p.alpha[t.g] : 1.f) * p.unit;
+      const Fp4Factor f = fp4_factor(p.alpha ? p.alpha[t.g] : 1.f, 1.f, p.unit, p.unit_log2);
+      const float alpha = f.by;
+      const uint32_t rest = f.rest;
       const bool ok = __all_sync(
           0xffffffffu, ptx::mbar_wait(bar_tfull, acc_phase, kWaitBudget, abort_flag));
       if (!ok) {
@@ -692,6 +697,10 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
             scale_pack(r, alpha, o[c]);
           }
           release();
+          if (rest != kFp4One) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) fp4_times(o[i >> 2][i & 3], rest);
+          }
 #pragma unroll
           for (int c = 0; c < (EPI == kF4Swiglu ? 2 : 4); ++c)
             f4_epilogue<FMT, EPI, C::BOXES>(p, &tmC, stage, stage_u32, t.nt, row0, rv, half, lane,
@@ -710,6 +719,13 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
               ptx::tmem_ld32(tq + slice_col<EPI>(half, c + 2), r);
               ptx::tmem_ld_wait();
               scale_pack(r, alpha, u);
+            }
+            if (rest != kFp4One) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                fp4_times(o[i], rest);
+                if (EPI == kF4Swiglu) fp4_times(u[i], rest);
+              }
             }
             f4_epilogue<FMT, EPI, C::BOXES>(p, &tmC, stage, stage_u32, t.nt, row0, rv, half, lane,
                                             c, o, u);
@@ -762,8 +778,9 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
             v.z += u.z;
             v.w += u.w;
           }
-          f4_epilogue_row<FMT, EPI>(p, t.nt, row0 + r, half, lane,
-                                    make_float4(v.x * alpha, v.y * alpha, v.z * alpha, v.w * alpha));
+          f4_epilogue_row<FMT, EPI>(
+              p, t.nt, row0 + r, half, lane,
+              make_float4(v.x * alpha, v.y * alpha, v.z * alpha, v.w * alpha), rest);
         }
       }
     }
@@ -1067,7 +1084,9 @@ grouped_gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA,
       const int m0 = (2 * t.mt + (int)rank) * BM + q * 32;
       const int row0 = s_off[t.g] + m0;
       const int rv = s_cnt[t.g] - m0;
-      const float alpha = (p.alpha ? p.alpha[t.g] : 1.f) * p.unit;
+      const Fp4Factor f = fp4_factor(p.alpha ? p.alpha[t.g] : 1.f, 1.f, p.unit, p.unit_log2);
+      const float alpha = f.by;
+      const uint32_t rest = f.rest;
       const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(bar_tfull, acc_phase,
                                                                      kWaitBudget, abort_flag));
       if (!ok) {
@@ -1093,6 +1112,10 @@ grouped_gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA,
       if (lane == 0) ptx::mbar_arrive_cluster_tmem(leader_tempty);
       acc_phase ^= 1u;
       if (rv <= 0) continue;
+      if (rest != kFp4One) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) fp4_times(o[i >> 2][i & 3], rest);
+      }
 #pragma unroll
       for (int c = 0; c < (EPI == kF4Swiglu ? 2 : 4); ++c)
         f4_epilogue<FMT, EPI, true>(p, &tmC, stage, stage_u32, t.nt, row0, rv, half, lane, c, o[c],
@@ -1235,6 +1258,7 @@ static Fp4Params fp4_params(const Fp4Problem& q, const Fp4Split& sp, int32_t* st
   p.offsets = q.offsets;
   p.alpha = q.alpha;
   p.unit = ldexpf(1.f, q.unit_log2);
+  p.unit_log2 = q.unit_log2;
   p.sfa = q.sfa;
   p.ka = (int)f4::atoms_k(q.fmt, q.K);
   p.part = sp.part;

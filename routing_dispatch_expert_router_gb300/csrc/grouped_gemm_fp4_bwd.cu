@@ -69,7 +69,8 @@ struct Dgrad4Params {
   const uint8_t* ckpt_sf;
   const float* alpha_a;        // out: the factor, alpha_a[g] alpha_b[g] unit
   const float* alpha_b;
-  float unit;
+  float unit;                  // 2^unit_log2
+  int unit_log2;
   const int32_t* token_of;     // out: the router's term, where dlogits is given
   const float* dlogits;
   const float* W_r;
@@ -474,7 +475,8 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       // what the row needs besides the accumulator: gate and up of its next 32
       // columns, or the router's term
       Kept k = {};
-      float rd = 0.f, alpha = 1.f;
+      float rd = 0.f;
+      Fp4Factor alpha = {1.f, kFp4One};
       const float* rw = nullptr;
       auto fetch = [&](int col) {
         if (lane >= rv || col >= p.N) return;
@@ -490,7 +492,8 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       if (EPI == kD4Swiglu) {
         fetch(f0);
       } else {
-        alpha = (p.alpha_a ? p.alpha_a[g] : 1.f) * (p.alpha_b ? p.alpha_b[g] : 1.f) * p.unit;
+        alpha = fp4_factor(p.alpha_a ? p.alpha_a[g] : 1.f, p.alpha_b ? p.alpha_b[g] : 1.f, p.unit,
+                           p.unit_log2);
         if (p.dlogits && g < p.router_E) {
           const int tk = lane < rv ? p.token_of[row] : -1;
           if (tk >= 0 && tk < p.router_T) rd = p.dlogits[(int64_t)tk * p.router_E + g];
@@ -545,7 +548,12 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              r[i] = __float_as_uint(lane < rv ? __uint_as_float(r[i]) * alpha : 0.f);
+              r[i] = __float_as_uint(lane < rv ? __uint_as_float(r[i]) * alpha.by : 0.f);
+            if (alpha.rest != kFp4One) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                r[i] = __float_as_uint(__uint_as_float(r[i]) * __uint_as_float(alpha.rest << 16));
+            }
             if (rw) {
 #pragma unroll
               for (int v = 0; v < 8; ++v) {
@@ -690,6 +698,7 @@ cudaError_t launch_fp4_dgrad_out(const Fp4Problem& q, const float* alpha_b, void
   p.alpha_a = q.alpha;
   p.alpha_b = alpha_b;
   p.unit = ldexpf(1.f, q.unit_log2);
+  p.unit_log2 = q.unit_log2;
   p.token_of = token_of;
   p.dlogits = dlogits;
   p.W_r = W_r;
