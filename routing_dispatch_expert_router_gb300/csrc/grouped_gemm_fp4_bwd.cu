@@ -496,8 +496,12 @@ fp4_dgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                            p.unit_log2);
         if (p.dlogits && g < p.router_E) {
           const int tk = lane < rv ? p.token_of[row] : -1;
-          if (tk >= 0 && tk < p.router_T) rd = p.dlogits[(int64_t)tk * p.router_E + g];
-          rw = p.W_r + (int64_t)g * p.N + f0;
+          // (a lane without a token has no term: zero times W_r would be NaN where W_r is
+          // not finite)
+          if (tk >= 0 && tk < p.router_T) {
+            rd = p.dlogits[(int64_t)tk * p.router_E + g];
+            rw = p.W_r + (int64_t)g * p.N + f0;
+          }
         }
       }
       bool ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(bar_tfull + 8 * acc, acc_phase,
