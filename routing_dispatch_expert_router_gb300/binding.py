@@ -415,6 +415,8 @@ def _bf16_rows(t, shape, what: str) -> int:
     if t.is_contiguous():
         return shape[2]
     sg, ld, one = t.stride()
+    if shape[1] == 1:
+        ld = sg                                            # the stride of a single row says nothing
     if one != 1 or (shape[0] > 1 and sg != ld * shape[1]):
         raise ValueError(f"{what} has contiguous rows, its groups following each other row by row")
     return ld if shape[0] > 1 or shape[1] > 1 else shape[2]
