@@ -429,10 +429,12 @@ def _addr(t):
 def moe_fp4_quantize(x, q: Fp4Tensor, scale_log2: int | None = None, counts=None, offsets=None,
                      values=None, scratch=None, stream=None):
     """x [groups, rows, K] bf16 into q; with counts and offsets only those rows of
-    x [1, rows, K]. values: the bf16 values that the codes stand for."""
-    if scale_log2 is not None:
-        q.scale_log2 = scale_log2
+    x [1, rows, K]. values: the bf16 values that the codes stand for. scale_log2: the tensor
+    scale to quantise with; it is part of what the codes mean, so q keeps it (a call that is
+    refused leaves q as it was). None: q's own."""
     s = q.struct()
+    if scale_log2 is not None:
+        s.scale_log2 = scale_log2
     ldx = _bf16_rows(x, (s.groups, s.rows, s.K), "x")
     if values is not None and not (values.is_contiguous() and values.shape == x.shape
                                    and values.dtype == torch.bfloat16):
@@ -441,10 +443,12 @@ def moe_fp4_quantize(x, q: Fp4Tensor, scale_log2: int | None = None, counts=None
                                 0 if counts is None else counts.numel(), _addr(values),
                                 _addr(scratch), _stream(stream))
     _check("moe_fp4_quantize", rc)
+    q.scale_log2 = s.scale_log2
 
 
 def moe_fp4_dequantize(q: Fp4Tensor, out, scale_log2: int | None = None, stream=None):
-    """out [groups, rows, K] bf16 = the values that q's codes stand for."""
+    """out [groups, rows, K] bf16 = the values that q's codes stand for, with q's tensor scale
+    or, in this call alone, with scale_log2."""
     s = q.struct()
     if scale_log2 is not None:
         s.scale_log2 = scale_log2

@@ -29,3 +29,12 @@ def test_row_spacing_of_views():
         B._bf16_rows(wide[:, :3, :288], (6, 3, 288), "x")  # groups four rows apart
     with pytest.raises(ValueError):
         B._bf16_rows(wide.transpose(0, 1)[:, :, :288], (4, 6, 288), "x")
+
+
+def test_a_refused_quantisation_leaves_the_tensor_as_it_was():
+    q = B.alloc_fp4(B.MOE_FP4_NV, 1, 4, 64, device="cpu", scale_log2=-3)
+    for x, log2 in ((torch.zeros(1, 4, 32, dtype=BF), 5), (torch.zeros(1, 4, 64), 5),
+                    (torch.zeros(1, 4, 64, dtype=BF), 65)):
+        with pytest.raises((ValueError, B.MoEError)):
+            B.moe_fp4_quantize(x, q, scale_log2=log2, stream=0)
+        assert q.scale_log2 == -3
