@@ -7,6 +7,7 @@ no compute in Python and no fallback: if the library is missing, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -144,8 +145,8 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        # (with the device given, torch does not look for one: 1 us instead of 6)
-        return torch.cuda.current_stream(torch.cuda.current_device()).cuda_stream
+        # (the handle alone: a Stream object takes a microsecond, some calls eight)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -355,17 +356,21 @@ class Fp4Tensor:
         self.scale_log2 = scale_log2
 
     def struct(self) -> MoEFp4Tensor:
-        g, rows, kb = self.codes.shape
+        codes, scales, u8 = self.codes, self.scales, torch.uint8
+        g, rows, kb = codes.shape
         if kb * 2 != self.K:
             raise ValueError(f"codes hold {2 * kb} elements a row, K is {self.K}")
         # ceil(K / 256) steps of 4 (NV) or 2 (MX) atoms per 128 rows
-        if self.format not in (0, 1) or self.scales.numel() != \
+        if self.format not in (0, 1) or scales.numel() != \
                 g * -(-rows // 128) * -(-self.K // 256) * (2048 >> self.format):
             raise ValueError("scales do not have the atoms of the codes' shape")
-        if not (self.codes.is_contiguous() and self.scales.is_contiguous()):
-            raise ValueError("codes and scales are contiguous")
-        return MoEFp4Tensor(self.format, self.scale_log2, g, rows, self.K, self.codes.data_ptr(),
-                            self.scales.data_ptr())
+        if codes.dtype is not u8 or scales.dtype is not u8 or \
+                not (codes.is_contiguous() and scales.is_contiguous()):
+            raise ValueError("codes and scales are contiguous uint8")
+        if not (codes.is_cuda and scales.is_cuda):
+            raise ValueError("codes and scales are on the GPU")
+        return MoEFp4Tensor(self.format, self.scale_log2, g, rows, self.K, codes.data_ptr(),
+                            scales.data_ptr())
 
 
 def fp4_scale_bytes(fmt: int, rows: int, K: int) -> int:
@@ -390,8 +395,12 @@ def alloc_fp4(fmt: int, groups: int, rows: int, K: int, device="cuda",
 
 def fp4_experts(W13: Fp4Tensor, W2: Fp4Tensor, alpha13=None, alpha2=None, x_scale_log2: int = 0,
                 h_scale_log2: int = 0) -> MoEFp4Experts:
-    """The experts' 4-bit weights for the FFN calls; the tensors must outlive them."""
-    return MoEFp4Experts(W13.struct(), W2.struct(), _ptr(alpha13), _ptr(alpha2), x_scale_log2,
+    """The experts' 4-bit weights for the FFN calls; alpha13, alpha2: None, or their own scales
+    (fp32, one per expert). The tensors must outlive them."""
+    a, b = W13.struct(), W2.struct()
+    return MoEFp4Experts(a, b,
+                         _vector(alpha13, a.groups, torch.float32, "alpha13"),
+                         _vector(alpha2, b.groups, torch.float32, "alpha2"), x_scale_log2,
                          h_scale_log2)
 
 
@@ -422,8 +431,43 @@ def _bf16_rows(t, shape, what: str) -> int:
     return ld if shape[0] > 1 or shape[1] > 1 else shape[2]
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+# Addresses of the calls' tensors. A kernel can see neither a tensor's type nor its size: what
+# does not fit is refused here. None passes, to be refused (or taken) by the C entry.
+def _vector(t, n: int, dtype, what: str):
+    """At least n elements in a row."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{what} is contiguous {dtype} of {n} elements, on the GPU")
+    return t.data_ptr()
+
+
+def _rows(t, rows: int, cols: int, dtype, what: str):
+    """[at least rows, cols]; dtype None: any of one byte."""
+    if t is None:
+        return None
+    if t.dim() != 2 or t.shape[1] != cols or t.shape[0] < rows or not t.is_contiguous() or \
+            not t.is_cuda or (t.dtype is not dtype if dtype else t.element_size() != 1):
+        raise ValueError(f"{what} is contiguous {dtype or 'bytes'} [{rows}, {cols}], on the GPU")
+    return t.data_ptr()
+
+
+def _scratch(t, nbytes: int):
+    if t is None:
+        return None
+    if t.numel() * t.element_size() < nbytes or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"scratch has {nbytes} bytes on the GPU")
+    return t.data_ptr()
+
+
+_gemm_scratch_bytes = 0
+
+
+def _gemm_scratch(t):
+    global _gemm_scratch_bytes
+    if not _gemm_scratch_bytes:                            # of any shape and format
+        _gemm_scratch_bytes = moe_fp4_query_sizes(None, MOE_FP4_NV).gemm_scratch_bytes
+    return _scratch(t, _gemm_scratch_bytes)
 
 
 def moe_fp4_quantize(x, q: Fp4Tensor, scale_log2: int | None = None, counts=None, offsets=None,
@@ -439,9 +483,14 @@ def moe_fp4_quantize(x, q: Fp4Tensor, scale_log2: int | None = None, counts=None
     if values is not None and not (values.is_contiguous() and values.shape == x.shape
                                    and values.dtype == torch.bfloat16):
         raise ValueError("values is contiguous bf16 of x's shape")
-    rc = lib().moe_fp4_quantize(s, x.data_ptr(), ldx, _addr(counts), _addr(offsets),
-                                0 if counts is None else counts.numel(), _addr(values),
-                                _addr(scratch), _stream(stream))
+    n = 0 if counts is None else counts.numel()
+    if not x.is_cuda or (values is not None and not values.is_cuda):
+        raise ValueError("x and values are on the GPU")
+    rc = lib().moe_fp4_quantize(s, x.data_ptr(), ldx,
+                                _vector(counts, n, torch.int32, "counts"),
+                                _vector(offsets, n, torch.int32, "offsets"), n,
+                                None if values is None else values.data_ptr(),
+                                _scratch(scratch, 4), _stream(stream))
     _check("moe_fp4_quantize", rc)
     q.scale_log2 = s.scale_log2
 
@@ -453,6 +502,8 @@ def moe_fp4_dequantize(q: Fp4Tensor, out, scale_log2: int | None = None, stream=
     if scale_log2 is not None:
         s.scale_log2 = scale_log2
     ldo = _bf16_rows(out, (s.groups, s.rows, s.K), "out")
+    if not out.is_cuda:
+        raise ValueError("out is on the GPU")
     _check("moe_fp4_dequantize",
            lib().moe_fp4_dequantize(s, out.data_ptr(), ldo, _stream(stream)))
 
@@ -461,32 +512,64 @@ def moe_fp4_grouped_gemm(a: Fp4Tensor, b: Fp4Tensor, counts, offsets, alpha, out
                          stream=None):
     """out [rows, N] bf16: every group's rows of a [1, rows, K] by b [G, N, K]."""
     sa, sb = a.struct(), b.struct()
-    if out.dtype != torch.bfloat16 or not out.is_contiguous() or out.shape != (sa.rows, sb.rows):
-        raise ValueError("out is contiguous bf16 [rows of a, rows of b]")
+    if out.dtype != torch.bfloat16 or not out.is_contiguous() or out.shape != (sa.rows, sb.rows) \
+            or not out.is_cuda:
+        raise ValueError("out is contiguous bf16 [rows of a, rows of b], on the GPU")
     if counts is not None and counts.numel() != sb.groups:
         raise ValueError("one count per group of b")
     _check("moe_fp4_grouped_gemm",
-           lib().moe_fp4_grouped_gemm(sa, sb, _addr(counts), _addr(offsets), _addr(alpha),
-                                      out.data_ptr(), _addr(scratch), _stream(stream)))
+           lib().moe_fp4_grouped_gemm(sa, sb,
+                                      _vector(counts, sb.groups, torch.int32, "counts"),
+                                      _vector(offsets, sb.groups, torch.int32, "offsets"),
+                                      _vector(alpha, sb.groups, torch.float32, "alpha"),
+                                      out.data_ptr(), _gemm_scratch(scratch), _stream(stream)))
+
+
+@functools.lru_cache(maxsize=64)
+def _layer_sizes(config: bytes, fmt: int):
+    """Rows of a layer's buffers and the scratch of its 4-bit calls: rows, forward, backward.
+    By the configuration's bytes: asking the library takes as long as checking every tensor."""
+    c = MoEConfig.from_buffer_copy(config)
+    s = moe_fp4_query_sizes(c, fmt)
+    return moe_query_sizes(c).rows_max, s.fwd_scratch_bytes, s.bwd_scratch_bytes
 
 
 def moe_fp4_ffn_fwd(cfg, experts: MoEFp4Experts, x_perm, counts, offsets, ckpt, ckpt_scale,
                     y_perm, scratch, stream=None):
-    """The experts' FFN in 4 bits; ckpt, ckpt_scale: None, or the 8-bit checkpoint."""
+    """The experts' FFN in 4 bits on x_perm's rows [R, H] (bf16, R = rows_max at least) into
+    y_perm's; counts, offsets: int32, one per group at least. ckpt [R, 2F], ckpt_scale
+    [R, 2F / 32]: None, or the 8-bit checkpoint."""
+    c = _cfg(cfg)
+    R, need, _ = _layer_sizes(bytes(c), experts.W13.format)
+    G, H, F2, bf16 = c.E + c.n_shared, c.H, 2 * c.F, torch.bfloat16
     _check("moe_fp4_ffn_fwd",
-           lib().moe_fp4_ffn_fwd(_cfg(cfg), experts, _addr(x_perm), _addr(counts), _addr(offsets),
-                                 _addr(ckpt), _addr(ckpt_scale), _addr(y_perm), _addr(scratch),
-                                 _stream(stream)))
+           lib().moe_fp4_ffn_fwd(c, experts, _rows(x_perm, R, H, bf16, "x_perm"),
+                                 _vector(counts, G, torch.int32, "counts"),
+                                 _vector(offsets, G, torch.int32, "offsets"),
+                                 _rows(ckpt, R, F2, None, "ckpt"),
+                                 _rows(ckpt_scale, R, F2 // 32, None, "ckpt_scale"),
+                                 _rows(y_perm, R, H, bf16, "y_perm"),
+                                 _scratch(scratch, need), _stream(stream)))
 
 
 def moe_fp4_ffn_bwd(cfg, experts: MoEFp4Experts, dO_perm, ckpt, ckpt_scale, counts, offsets,
                     token_of, dlogits, W_r, dX_perm, scratch, stream=None):
-    """The gradient at the FFN's input; token_of, dlogits, W_r: None, or the router's term."""
+    """The gradient at the FFN's input, the tensors as moe_fp4_ffn_fwd's; token_of (int32, R),
+    dlogits [T, E], W_r [E, H] (fp32): None, or the router's term."""
+    c = _cfg(cfg)
+    R, _, need = _layer_sizes(bytes(c), experts.W13.format)
+    G, H, F2, bf16, f32 = c.E + c.n_shared, c.H, 2 * c.F, torch.bfloat16, torch.float32
     _check("moe_fp4_ffn_bwd",
-           lib().moe_fp4_ffn_bwd(_cfg(cfg), experts, _addr(dO_perm), _addr(ckpt),
-                                 _addr(ckpt_scale), _addr(counts), _addr(offsets),
-                                 _addr(token_of), _addr(dlogits), _addr(W_r), _addr(dX_perm),
-                                 _addr(scratch), _stream(stream)))
+           lib().moe_fp4_ffn_bwd(c, experts, _rows(dO_perm, R, H, bf16, "dO_perm"),
+                                 _rows(ckpt, R, F2, None, "ckpt"),
+                                 _rows(ckpt_scale, R, F2 // 32, None, "ckpt_scale"),
+                                 _vector(counts, G, torch.int32, "counts"),
+                                 _vector(offsets, G, torch.int32, "offsets"),
+                                 _vector(token_of, R, torch.int32, "token_of"),
+                                 _rows(dlogits, c.T, c.E, f32, "dlogits"),
+                                 _rows(W_r, c.E, H, f32, "W_r"),
+                                 _rows(dX_perm, R, H, bf16, "dX_perm"),
+                                 _scratch(scratch, need), _stream(stream)))
 
 
 def moe_last_device_status(scratch, stream=None) -> int:
