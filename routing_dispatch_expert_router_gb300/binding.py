@@ -396,12 +396,13 @@ def alloc_fp4(fmt: int, groups: int, rows: int, K: int, device="cuda",
 def fp4_experts(W13: Fp4Tensor, W2: Fp4Tensor, alpha13=None, alpha2=None, x_scale_log2: int = 0,
                 h_scale_log2: int = 0) -> MoEFp4Experts:
     """The experts' 4-bit weights for the FFN calls; alpha13, alpha2: None, or their own scales
-    (fp32, one per expert). The tensors must outlive them."""
+    (fp32, one per expert). The result keeps the tensors alive."""
     a, b = W13.struct(), W2.struct()
-    return MoEFp4Experts(a, b,
-                         _vector(alpha13, a.groups, torch.float32, "alpha13"),
-                         _vector(alpha2, b.groups, torch.float32, "alpha2"), x_scale_log2,
-                         h_scale_log2)
+    ex = MoEFp4Experts(a, b, _vector(alpha13, a.groups, torch.float32, "alpha13"),
+                       _vector(alpha2, b.groups, torch.float32, "alpha2"), x_scale_log2,
+                       h_scale_log2)
+    ex.tensors = (W13.codes, W13.scales, W2.codes, W2.scales, alpha13, alpha2)
+    return ex
 
 
 def moe_fp4_query_sizes(cfg, fmt: int) -> MoEFp4Sizes:

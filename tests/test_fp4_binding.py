@@ -152,3 +152,19 @@ def test_quantiser_and_product_refuse_tensors_that_do_not_fit():
         for bad in bads:
             with pytest.raises(ValueError, match=name):
                 B.moe_fp4_grouped_gemm(q, b, **{**args, name: bad}, stream=0)
+
+
+def test_experts_keep_their_tensors():
+    """The structure holds addresses; tensors made for it alone live as long as it does."""
+    import gc
+    import weakref
+    one = [gpu(G, dtype=F32), gpu(G, dtype=F32)]
+    W = [fp4(0, G, 2 * F, H), fp4(0, G, H, F)]
+    refs = [weakref.ref(t) for t in (W[0].codes, W[0].scales, W[1].codes, W[1].scales, *one)]
+    ex = B.fp4_experts(*W, *one)
+    one.clear(), W.clear()
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    del ex
+    gc.collect()
+    assert not any(r() is not None for r in refs)
