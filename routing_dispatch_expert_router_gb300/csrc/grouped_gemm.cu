@@ -883,39 +883,22 @@ static cudaError_t run(const CUtensorMap& a, const CUtensorMap& b, const CUtenso
   using L = Layout<BN, STAGES, b_parts<EPI>()>;
   static_assert(L::SMEM <= 232448, "shared memory per block");
   auto kern = grouped_gemm_kernel<EPI, BN, A_MN, B_MN, STAGES>;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static PerDevice set;
+  const cudaError_t e = set_smem_once(set, kern, L::SMEM);
+  if (e != cudaSuccess) return e;
   kern<<<num_sms(), kThreads, L::SMEM, s>>>(a, b, c, c2, p);
   return cudaGetLastError();
 }
 
-// CTA-pair launch: as many clusters as can be resident at once (the tile loop
-// strides statically over clusters, so every launched cluster must run).
+// CTA-pair launch: as many clusters as can be resident at once.
 template <int EPI, int A_MN, int B_MN>
 static cudaError_t run_pair(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
                             const CUtensorMap& c2, const Params& p, cudaStream_t s) {
   auto kern = grouped_gemm_pair_kernel<EPI, A_MN, B_MN>;
-  static int grid = 0;
-  if (grid == 0) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         PairCfg<EPI>::SMEM);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(2 * (num_sms() / 2), 1, 1);
-    lc.blockDim = dim3(kThreads, 1, 1);
-    lc.dynamicSmemBytes = PairCfg<EPI>::SMEM;
-    int clusters = 0;
-    e = cudaOccupancyMaxActiveClusters(&clusters, kern, &lc);
-    if (e != cudaSuccess || clusters <= 0) {
-      (void)cudaGetLastError();
-      clusters = num_sms() / 2;
-    }
-    grid = 2 * clusters;
-  }
+  static PerDevice set;
+  int grid = 0;
+  const cudaError_t e = pair_grid_once(set, kern, kThreads, PairCfg<EPI>::SMEM, &grid);
+  if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, PairCfg<EPI>::SMEM, s>>>(a, b, c, c2, p);
   return cudaGetLastError();
 }

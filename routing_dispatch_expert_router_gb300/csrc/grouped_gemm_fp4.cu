@@ -1138,12 +1138,9 @@ static cudaError_t run_fp4_rows(const CUtensorMap& a, const CUtensorMap& a32, co
                                 bool early, cudaStream_t s) {
   auto kern = grouped_gemm_fp4_kernel<FMT, EPI, AROWS>;
   constexpr int smem = F4Cfg<FMT, AROWS>::SMEM;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static PerDevice set;
+  const cudaError_t e = set_smem_once(set, kern, smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(num_sms(), 1, 1);
   lc.blockDim = dim3(kF4Threads, 1, 1);
@@ -1163,24 +1160,15 @@ static cudaError_t run_fp4_pair(const CUtensorMap& a, const CUtensorMap& b, cons
                                 cudaStream_t s) {
   auto kern = grouped_gemm_fp4_pair_kernel<FMT, EPI>;
   constexpr int smem = F4PairCfg<FMT>::SMEM;
+  static PerDevice set;
+  int grid = 0;
+  const cudaError_t e = pair_grid_once(set, kern, kF4Threads, smem, &grid);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(grid, 1, 1);
   lc.blockDim = dim3(kF4Threads, 1, 1);
   lc.dynamicSmemBytes = smem;
   lc.stream = s;
-  static int grid = 0;
-  if (grid == 0) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    lc.gridDim = dim3(2 * (num_sms() / 2), 1, 1);
-    int clusters = 0;
-    e = cudaOccupancyMaxActiveClusters(&clusters, kern, &lc);
-    if (e != cudaSuccess || clusters <= 0) {
-      (void)cudaGetLastError();
-      clusters = num_sms() / 2;
-    }
-    grid = 2 * clusters;
-  }
-  lc.gridDim = dim3(grid, 1, 1);
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;

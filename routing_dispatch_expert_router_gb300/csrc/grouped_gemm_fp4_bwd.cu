@@ -620,28 +620,16 @@ static bool make_map_codes(CUtensorMap* m, const void* ptr, int64_t cols, int64_
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// As many pairs as can be resident at once (the tile loop strides over them).
+// As many pairs as can be resident at once.
 template <int FMT, int EPI>
 static cudaError_t run_dgrad4(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
                               const Dgrad4Params& p, bool early, cudaStream_t s) {
   auto kern = fp4_dgrad_kernel<FMT, EPI>;
   constexpr int smem = D4Cfg<FMT>::SMEM;
-  static int grid = 0;
-  if (grid == 0) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(2 * (num_sms() / 2), 1, 1);
-    lc.blockDim = dim3(kD4Threads, 1, 1);
-    lc.dynamicSmemBytes = smem;
-    int clusters = 0;
-    e = cudaOccupancyMaxActiveClusters(&clusters, kern, &lc);
-    if (e != cudaSuccess || clusters <= 0) {
-      (void)cudaGetLastError();
-      clusters = num_sms() / 2;
-    }
-    grid = 2 * clusters;
-  }
+  static PerDevice set;
+  int grid = 0;
+  const cudaError_t e = pair_grid_once(set, kern, kD4Threads, smem, &grid);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(grid, 1, 1);
   lc.blockDim = dim3(kD4Threads, 1, 1);

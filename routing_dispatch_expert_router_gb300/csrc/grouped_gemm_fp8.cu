@@ -600,12 +600,9 @@ static cudaError_t run_fp8_t(const CUtensorMap& a, const CUtensorMap& b, const C
                              const CUtensorMap& c2, const Params& p, cudaStream_t s) {
   auto kern = grouped_gemm_fp8_kernel<EPI, B_MN, MX>;
   constexpr int smem = F8Cfg<EPI>::SMEM;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static PerDevice set;
+  const cudaError_t e = set_smem_once(set, kern, smem);
+  if (e != cudaSuccess) return e;
   kern<<<num_sms(), kF8Threads, smem, s>>>(a, b, c, c2, p);
   return cudaGetLastError();
 }

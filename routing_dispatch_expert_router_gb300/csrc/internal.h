@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "../../include/moe_abi.h"
+#include "per_device.h"
 
 namespace moe {
 
@@ -14,6 +15,41 @@ int64_t capacity_rows(const moe_config& c);
 int64_t rows_max(const moe_config& c);
 int n_chunks(const moe_config& c);
 int num_sms();
+// The calling thread's device, -1 without one.
+inline int current_device() {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+// A kernel's dynamic shared memory, set at its first launch on each device.
+template <class Kernel>
+cudaError_t set_smem_once(PerDevice& set, Kernel kern, int bytes) {
+  int done = 0;
+  return set.get(current_device(), &done, [&](int* v) {
+    *v = 1;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
+}
+// The same for a kernel of CTA pairs, and as many CTAs as can be resident at once (its tile
+// loop strides over the pairs, so every launched pair must run).
+template <class Kernel>
+cudaError_t pair_grid_once(PerDevice& set, Kernel kern, int threads, int smem, int* grid) {
+  return set.get(current_device(), grid, [&](int* v) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(2 * (num_sms() / 2), 1, 1);
+    lc.blockDim = dim3(threads, 1, 1);
+    lc.dynamicSmemBytes = smem;
+    int clusters = 0;
+    e = cudaOccupancyMaxActiveClusters(&clusters, kern, &lc);
+    if (e != cudaSuccess || clusters <= 0) {
+      (void)cudaGetLastError();
+      clusters = num_sms() / 2;
+    }
+    *v = 2 * clusters;
+    return cudaSuccess;
+  });
+}
 
 cudaError_t launch_route(const moe_config& c, const void* x, const float* W_r, const float* bias,
                          float* logits, int32_t* idx, float* w, uint8_t* scratch, cudaStream_t s);
