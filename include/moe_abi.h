@@ -641,8 +641,13 @@ MOE_API moe_status moe_fp4_grouped_gemm(const moe_fp4_tensor* a, const moe_fp4_t
  * E4M3 codes and [R, 2F / 32] UE8M0 bytes: [G|U] over 2^ceil(log2(amax / 448))
  * of each 32 values; a block with an infinity or a NaN gets the byte 255): 1.03
  * bytes a value where GU and h keep 3. Rows past a group's counts are not
- * written. R = moe_sizes.rows_max; cfg->dtype is MOE_DTYPE_BF16 (the router and
- * the activations stay as they are); no paged stash, no weights_in_expert
+ * written. offsets at multiples of 128 inside the rows (else the group is left
+ * out and MOE_ERR_DEVICE_CHECK recorded). A group has T rows at most, as
+ * moe_permute lays them out (a token takes an expert once): one of more may be
+ * left out and reported in the same way, and is where the kernel has room for
+ * 32 or 64 rows a group (T <= 64). R = moe_sizes.rows_max; cfg->dtype is
+ * MOE_DTYPE_BF16 (the router and the activations stay as they are); no paged
+ * stash, no weights_in_expert
  * (MOE_ERR_UNSUPPORTED). scratch: fwd_scratch_bytes. */
 MOE_API moe_status moe_fp4_ffn_fwd(const moe_config* cfg, const moe_fp4_experts* experts,
                                    const void* x_perm, const int32_t* counts,
