@@ -798,9 +798,9 @@ grouped_gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA,
 // The same product for experts with many rows: tiles of 256 x 256, each CTA of a pair
 // holding 128 rows of A and 128 of B (swiglu: the gate rows in the even CTA, the matching
 // up rows in the odd one), its rows' scales and those of all 256 columns. A k-block is 38 KB
-// a CTA instead of 54, so that five stages fit where three did: the cycle from an MMA's
-// end over the next loads and their scales to the MMA that waits for them is what bounds
-// the single CTA. Whole tiles only.
+// a CTA instead of 54, so that five stages fit where three did (512 rows each, 64 experts,
+// 4096 x 4096: 265 us with single CTAs, 233 so). What bounds either is not settled: tensor
+// pipe 53 % active (single CTAs 40), L2 to the SMs 31 % (32) of its peak. Whole tiles only.
 template <int FMT>
 struct F4PairCfg {
   static constexpr int ATOMS = f4::step_atoms(FMT);
