@@ -6,10 +6,10 @@
 // Scale bytes lie the way the block-scaled tensor-core MMA reads them, in the
 // 512-byte atoms of fp8_layout.cuh: one atom per 128 rows and 4 consecutive
 // blocks (64 elements of K for NV, 128 for MX), the scale of row r's j-th block
-// at byte (r % 32) * 16 + (r % 128) / 32 * 4 + j. tcgen05.cp .32x128b.warpx4
-// puts an atom into four tensor-memory columns, where the MMA of a 64-wide K
-// slice reads all four bytes of a row (scale_vec::4X, NV) or the two that its
-// scale-factor id names (scale_vec::2X, MX). A 128-row slab's atoms follow each
+// at byte (r % 32) * 16 + (r % 128) / 32 * 4 + j. An atom's 32 lines of 16 bytes
+// go into four tensor-memory columns of each lane quarter, where the MMA of a
+// 64-wide K slice reads all four bytes of a row (scale_vec::4X, NV) or the two
+// that its scale-factor id names (scale_vec::2X, MX). A 128-row slab's atoms follow each
 // other along K and fill whole 256-element steps (one GEMM k-block = 128 bytes
 // of codes); bytes of blocks past K are zero.
 #pragma once
