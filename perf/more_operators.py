@@ -289,18 +289,13 @@ def _plain_dispatch(s, c):
     token_of[row[live]] = (live // k).int()
     xq, xsf = torch.zeros_like(s["xq"]), torch.zeros_like(s["xsf"])
     xq[row[live]] = s["codes"][live // k]
-    # scales: atoms of 128 rows; rows of a segment's last block without a token have the scale 1
+    # scales: atoms of 128 rows (rows without a token are left as they were)
     n = H // c["block"]
     byte = torch.zeros(_up(R, 128), n, dtype=torch.uint8, device="cuda")
-    at = torch.arange(R, device="cuda")
-    seg = torch.searchsorted(start + size, at, right=True).clamp(max=E - 1)
-    local = at - start[seg]
-    byte[:R][(local >= kept[seg]) & (local < (kept[seg] + 127) // 128 * 128)] = 127
     byte[row[live]] = s["scales"][live // k]
     full = byte.new_zeros(byte.shape[0], xsf.shape[1] * 4)
     full[:, :n] = byte
-    live_block = full.view(-1, 128, xsf.shape[1], 4)
-    xsf = live_block.view(-1, 4, 32, xsf.shape[1], 4).permute(0, 3, 2, 1, 4).reshape(xsf.shape)
+    xsf = full.view(-1, 4, 32, xsf.shape[1], 4).permute(0, 3, 2, 1, 4).reshape(xsf.shape)
     out = {"codes": xq, "scales": xsf, "counts": kept.int(), "row_of": row.int(),
            "offsets": torch.cat((start, start[-1:] + size[-1:])).int(), "token_of": token_of}
     return _values8(out)
