@@ -673,6 +673,62 @@ MOE_API moe_status moe_fp4_ffn_bwd(const moe_config* cfg, const moe_fp4_experts*
                                    const int32_t* token_of, const float* dlogits,
                                    const float* W_r, void* dX_perm, void* scratch, void* stream);
 
+/* ------------------------------------------------- the norm before a layer
+ * Root-mean-square norm of bf16 rows, with the residual stream's addition in
+ * front of it and the 8-bit form of its output behind it:
+ *   h = bf16(x + residual)   (x where residual is NULL),
+ *   s = (mean over the row of h^2, + eps)^-1/2,  y = bf16(h s gamma),
+ *   codes = E4M3(y / 2^c), scales = c + 127, c = ceil(log2(amax / 448)) of every
+ *   `block` consecutive values of y (1 for a zero block): what moe_permute makes
+ *   of such rows in the FP8 modes (block 128; MXFP8: 32), and moe_permute_fp8
+ *   takes.
+ * x, residual, sum, out: [T, H] with ld* elements from row to row (a multiple
+ * of 8, at least H; of a NULL tensor not looked at). H a multiple of 8, at most
+ * 32768; the row's sum of squares is taken in fp32. gamma [H] in bf16 or fp32
+ * (gamma_dtype). eps >= 0, finite. sum: h, or NULL; it may be x or residual
+ * itself. out: y, or NULL (then with codes); it may be x itself. codes [T, H]
+ * and scales [T, H / block] (contiguous), or NULL both: H a multiple of block.
+ * rstd [T] fp32: s, or NULL (the backward reads it). */
+enum { MOE_GAMMA_BF16 = 0, MOE_GAMMA_F32 = 1 };
+MOE_API moe_status moe_rmsnorm_fwd(int64_t T, int64_t H, const void* x, int64_t ldx,
+                                   const void* residual, int64_t ldr, const void* gamma,
+                                   int32_t gamma_dtype, float eps, void* sum, int64_t lds,
+                                   void* out, int64_t ldo, void* codes, void* scales,
+                                   int32_t block, float* rstd, void* stream);
+
+/* Its backward from h (`sum`, or x without a residual) and rstd: with
+ * t = dy gamma, n = h rstd,
+ *   dx = bf16(rstd (t - n mean(t n)) + dsum),  dgamma = sum over rows of dy n,
+ * dx the gradient of x and of the residual alike; dsum: the gradient that
+ * reaches h past the norm, or NULL. dx may be dy or dsum itself. dgamma [H]
+ * fp32 (zeros for T = 0), or NULL (gamma is held; scratch is then not used). The
+ * rows are summed in a fixed order: the same bits in every call. scratch:
+ * moe_rmsnorm_scratch_bytes bytes, of any content. */
+MOE_API moe_status moe_rmsnorm_bwd(int64_t T, int64_t H, const void* dy, int64_t lddy,
+                                   const void* h, int64_t ldh, const float* rstd,
+                                   const void* gamma, int32_t gamma_dtype, const void* dsum,
+                                   int64_t ldds, void* dx, int64_t lddx, float* dgamma,
+                                   void* scratch, void* stream);
+
+/* Bytes of moe_rmsnorm_bwd's scratch. Host only. */
+MOE_API moe_status moe_rmsnorm_scratch_bytes(int64_t H, int64_t* bytes);
+
+/* Stage 2 of a forward whose tokens are in 8 bits already (cfg->dtype one of
+ * the FP8 modes): codes [T, H] E4M3 and scales [T, H / block] UE8M0 bytes (block
+ * 128; MXFP8: 32) into the experts' segments, a third of moe_permute's bytes.
+ * The maps are moe_permute's. Rows without a token are left as they were, and no
+ * bf16 rows are written: it serves a forward that no backward follows.
+ * codes_perm, scales_perm: NULL both, the places in `scratch` that
+ * moe_grouped_ffn_fwd reads (its x_perm may then be NULL); or the caller's [R, H]
+ * and ceil(R / 128) rows of atoms (fp8_layout: 512 bytes for 128 rows and 512
+ * columns; MXFP8: 128 columns), where 4352 + 4 E ceil(T / 256) bytes of scratch
+ * are enough. */
+MOE_API moe_status moe_permute_fp8(const moe_config* cfg, const void* codes, const void* scales,
+                                   const int32_t* idx, int32_t* counts, int32_t* offsets,
+                                   int32_t* row_of, int32_t* token_of, int32_t* sel_offsets,
+                                   int32_t* sel_tokens, void* codes_perm, void* scales_perm,
+                                   void* scratch, void* stream);
+
 /* Synchronises `stream`, then copies the device status word from scratch to
  * *code (0 = no problem recorded). */
 MOE_API moe_status moe_last_device_status(const void* scratch, int32_t* code, void* stream);

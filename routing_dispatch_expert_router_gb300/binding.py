@@ -31,6 +31,7 @@ ENTRY_POINTS = (
     "moe_router_wgrad", "moe_layer_fwd", "moe_layer_bwd", "moe_stash_release",
     "moe_fp4_query_sizes", "moe_fp4_scale_bytes", "moe_fp4_quantize", "moe_fp4_dequantize",
     "moe_fp4_grouped_gemm", "moe_fp4_ffn_fwd", "moe_fp4_ffn_bwd",
+    "moe_rmsnorm_fwd", "moe_rmsnorm_bwd", "moe_rmsnorm_scratch_bytes", "moe_permute_fp8",
     "moe_last_device_status",
     "moe_clear_device_status", "moe_check_bounded_wait", "moe_status_string",
 )
@@ -97,7 +98,7 @@ def lib():
         for name in ENTRY_POINTS:
             f = getattr(L, name)
             f.restype = ctypes.c_int
-        for name, args in _FP4_ARGS.items():
+        for name, args in (*_FP4_ARGS.items(), *_PRODUCT_ARGS.items()):
             getattr(L, name).argtypes = args
         L.moe_status_string.restype = ctypes.c_char_p
         L.moe_status_string.argtypes = [ctypes.c_int]
@@ -571,6 +572,143 @@ def moe_fp4_ffn_bwd(cfg, experts: MoEFp4Experts, dO_perm, ckpt, ckpt_scale, coun
                                  _rows(W_r, c.E, H, f32, "W_r"),
                                  _rows(dX_perm, R, H, bf16, "dX_perm"),
                                  _scratch(scratch, need), _stream(stream)))
+
+
+# ---------------------------------- the norm before a layer, the dispatch of rows in 8 bits
+MOE_GAMMA_BF16, MOE_GAMMA_F32 = 0, 1
+
+_PRODUCT_ARGS = {
+    "moe_rmsnorm_fwd": [_I64, _I64, _P, _I64, _P, _I64, _P, _I32, ctypes.c_float, _P, _I64, _P, _I64,
+                        _P, _P, _I32, _P, _P],
+    "moe_rmsnorm_bwd": [_I64, _I64, _P, _I64, _P, _I64, _P, _P, _I32, _P, _I64, _P, _I64, _P, _P, _P],
+    "moe_rmsnorm_scratch_bytes": [_I64, ctypes.POINTER(_I64)],
+    "moe_permute_fp8": [ctypes.POINTER(MoEConfig)] + [_P] * 13,
+}
+
+
+def _strided(t, rows: int, cols: int, what: str):
+    """Address and elements from row to row of bf16 [rows, cols] with contiguous rows."""
+    if t is None:
+        return None, 0
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not torch.bfloat16 or len(shape) != 2 or shape[0] != rows or shape[1] != cols \
+            or (stride[1] != 1 and cols > 1) or not t.is_cuda:
+        raise ValueError(f"{what} is bf16 [{rows}, {cols}] with contiguous rows, on the GPU")
+    ld = stride[0] if rows > 1 else cols + -cols % 8   # (the stride of a single row says nothing)
+    if ld < cols:
+        raise ValueError(f"{what}'s rows lie one after the other")
+    return t.data_ptr(), ld
+
+
+def _gamma(t, H: int):
+    if t.dtype is torch.float32:
+        return _vector(t, H, torch.float32, "gamma"), MOE_GAMMA_F32
+    return _vector(t, H, torch.bfloat16, "gamma"), MOE_GAMMA_BF16
+
+
+def _here(*tensors):
+    """Every tensor lies on the current device, whose stream the call takes."""
+    here = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and here is not None and t.get_device() != here:
+            raise ValueError(f"tensors are on the current device, {here}")
+
+
+def moe_rmsnorm_fwd(x, gamma, out, residual=None, sum=None, rstd=None, codes=None, scales=None,
+                    eps: float = 1e-6, stream=None):
+    """out [T, H] = the RMS norm of x (+ residual, whose sum goes to `sum`) times gamma (bf16 or
+    fp32 [H]); codes [T, H] and scales [T, H / 32 or H / 128]: its E4M3 form, with which out may
+    be None; rstd [T] fp32 for the backward. x, residual, sum, out: bf16, contiguous rows."""
+    T, H = x.shape
+    _here(x, gamma, out, residual, sum, rstd, codes, scales)
+    g, kind = _gamma(gamma, H)
+    block = 0
+    if scales is not None:
+        block = H // scales.shape[1] if scales.dim() == 2 and scales.shape[1] else 0
+        if codes is None or block not in (32, 128) or scales.shape[1] * block != H:
+            raise ValueError("codes [T, H] have scales [T, H / 32] or [T, H / 128]")
+    if codes is not None and scales is None:
+        raise ValueError("codes have scales")
+    px, ldx = _strided(x, T, H, "x")
+    pr, ldr = _strided(residual, T, H, "residual")
+    ps, lds = _strided(sum, T, H, "sum")
+    po, ldo = _strided(out, T, H, "out")
+    _check("moe_rmsnorm_fwd",
+           lib().moe_rmsnorm_fwd(T, H, px, ldx, pr, ldr, g, kind, eps, ps, lds, po, ldo,
+                                 None if codes is None else _exactly(codes, T, H, "codes"),
+                                 None if codes is None else
+                                 _exactly(scales, T, H // block, "scales"), block,
+                                 _vector(rstd, T, torch.float32, "rstd"), _stream(stream)))
+
+
+def _exactly(t, rows: int, cols: int, what: str):
+    """[rows, cols] of one byte each, contiguous."""
+    if t.shape[0] != rows:
+        raise ValueError(f"{what} has {rows} rows")
+    return _rows(t, rows, cols, None, what)
+
+
+def rmsnorm_scratch_bytes(H: int) -> int:
+    n = ctypes.c_int64(0)
+    _check("moe_rmsnorm_scratch_bytes", lib().moe_rmsnorm_scratch_bytes(H, ctypes.byref(n)))
+    return n.value
+
+
+def moe_rmsnorm_bwd(dy, h, rstd, gamma, dx, dgamma=None, dsum=None, scratch=None, stream=None):
+    """dx [T, H] (x's gradient and the residual's) and dgamma [H] fp32 from h (the forward's sum,
+    or its x) and rstd; dsum: the gradient that reaches h past the norm. scratch:
+    rmsnorm_scratch_bytes(H) bytes, with dgamma."""
+    T, H = h.shape
+    _here(dy, h, rstd, gamma, dx, dgamma, dsum, scratch)
+    g, kind = _gamma(gamma, H)
+    pdy, lddy = _strided(dy, T, H, "dy")
+    ph, ldh = _strided(h, T, H, "h")
+    pds, ldds = _strided(dsum, T, H, "dsum")
+    pdx, lddx = _strided(dx, T, H, "dx")
+    if dgamma is not None and scratch is None:
+        raise ValueError("dgamma is summed through scratch")
+    _check("moe_rmsnorm_bwd",
+           lib().moe_rmsnorm_bwd(T, H, pdy, lddy, ph, ldh,
+                                 _vector(rstd, T, torch.float32, "rstd"), g, kind, pds, ldds, pdx,
+                                 lddx, _vector(dgamma, H, torch.float32, "dgamma"),
+                                 _scratch(scratch, 0 if dgamma is None else 2048 * H),
+                                 _stream(stream)))
+
+
+def moe_permute_fp8(cfg, codes, scales, idx, counts, offsets, row_of, token_of, sel_offsets,
+                    sel_tokens, scratch, codes_perm=None, scales_perm=None, stream=None):
+    """The dispatch of tokens in 8 bits (an FP8 configuration): codes [T, H] and scales
+    [T, H / 128] (MXFP8: [T, H / 32]) into the layer's place in scratch, or into codes_perm
+    [R, H] and scales_perm (the atoms of R rows)."""
+    c = _cfg(cfg)
+    _here(codes, scales, idx, counts, offsets, row_of, token_of, sel_offsets, sel_tokens, scratch,
+          codes_perm, scales_perm)
+    R, need = _fp8_sizes(bytes(c))
+    mx, i32, T, E = c.dtype == 2, torch.int32, c.T, c.E
+    if codes_perm is not None:
+        need = 4352 + 4 * E * (-(-T // 256))
+    blocks = c.H // (32 if mx else 128)
+    _check("moe_permute_fp8",
+           lib().moe_permute_fp8(c, _exactly(codes, T, c.H, "codes"),
+                                 _exactly(scales, T, blocks, "scales"),
+                                 _vector(idx, T * c.k, i32, "idx"),
+                                 _vector(counts, E, i32, "counts"),
+                                 _vector(offsets, E + 1, i32, "offsets"),
+                                 _vector(row_of, T * c.k, i32, "row_of"),
+                                 _vector(token_of, R, i32, "token_of"),
+                                 _vector(sel_offsets, E + 1, i32, "sel_offsets"),
+                                 _vector(sel_tokens, T * c.k, i32, "sel_tokens"),
+                                 _rows(codes_perm, R, c.H, None, "codes_perm"),
+                                 _vector(scales_perm, -(-R // 128) * -(-blocks // 4) * 512,
+                                         torch.uint8, "scales_perm"),
+                                 _scratch(scratch, need), _stream(stream)))
+
+
+@functools.lru_cache(maxsize=64)
+def _fp8_sizes(config: bytes):
+    """Rows of an FP8 layer's buffers and its scratch."""
+    s = moe_query_sizes(MoEConfig.from_buffer_copy(config))
+    return s.rows_max, s.scratch_bytes
 
 
 def moe_last_device_status(scratch, stream=None) -> int:

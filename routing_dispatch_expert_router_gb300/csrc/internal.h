@@ -1,6 +1,7 @@
 // Host-side launchers shared between the translation units of the library.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -85,6 +86,13 @@ cudaError_t launch_permute(const moe_config& c, const void* x, const int32_t* id
                            int32_t* sel_offsets, int32_t* sel_tokens, void* x_perm,
                            uint8_t* scratch, cudaStream_t s, const Fp8Scratch* fp8 = nullptr,
                            const StashAlloc* alloc = nullptr);
+
+// The dispatch of rows in 8 bits: the maps, and the rows and scale atoms alone (no bf16 rows).
+cudaError_t launch_permute_fp8(const moe_config& c, const uint8_t* codes, const uint8_t* scales,
+                               const int32_t* idx, int32_t* counts, int32_t* offsets,
+                               int32_t* row_of, int32_t* token_of, int32_t* sel_offsets,
+                               int32_t* sel_tokens, uint8_t* xq, uint8_t* xsf, uint8_t* scratch,
+                               cudaStream_t s);
 
 // pages (optional): y_perm is paged (StashMap).
 cudaError_t launch_unpermute(const moe_config& c, const void* y_perm, const int32_t* row_of,
@@ -264,6 +272,49 @@ cudaError_t launch_fp4_dgrad_swiglu(const Fp4Problem& q, const uint8_t* ckpt,
 cudaError_t launch_fp4_dgrad_out(const Fp4Problem& q, const float* alpha_b, void* dX,
                                  const int32_t* token_of, const float* dlogits, const float* W_r,
                                  int router_E, int router_T, int32_t* status, cudaStream_t s);
+
+// RMS norm with the residual's addition (norm.cu): bf16 rows [T, H], ld* elements from row to
+// row. residual, sum, out, rstd: or null; codes, scales: the output in E4M3 with a UE8M0 byte
+// per `block` (32 or 128) values, contiguous, or null.
+struct RmsNormFwd {
+  int64_t T;
+  int H;
+  const __nv_bfloat16* x;
+  int64_t ldx;
+  const __nv_bfloat16* residual;
+  int64_t ldr;
+  const void* gamma;
+  bool gamma_f32;
+  float eps;
+  __nv_bfloat16* sum;
+  int64_t lds;
+  __nv_bfloat16* out;
+  int64_t ldo;
+  uint8_t* codes;
+  uint8_t* scales;
+  int block;
+  float* rstd;
+};
+cudaError_t launch_rmsnorm_fwd(const RmsNormFwd& p, cudaStream_t s);
+// Its backward; dsum: or null. parts: [kRmsNormParts, H] fp32, null with dgamma.
+struct RmsNormBwd {
+  int64_t T;
+  int H;
+  const __nv_bfloat16* dy;
+  int64_t lddy;
+  const __nv_bfloat16* h;
+  int64_t ldh;
+  const float* rstd;
+  const void* gamma;
+  bool gamma_f32;
+  const __nv_bfloat16* dsum;
+  int64_t ldds;
+  __nv_bfloat16* dx;
+  int64_t lddx;
+  float* parts;
+};
+constexpr int kRmsNormParts = 512;
+cudaError_t launch_rmsnorm_bwd(const RmsNormBwd& p, float* dgamma, cudaStream_t s);
 
 // Router logits for E % 128 == 0 on the tensor cores (W3 = W_r split in three bf16 parts).
 cudaError_t launch_router_logits_tc(const moe_config& c, const void* x, const void* W3,

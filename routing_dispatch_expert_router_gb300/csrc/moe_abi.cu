@@ -282,7 +282,9 @@ static moe_status ffn_fwd_impl(const moe_config* cfg, const void* x_perm, const 
                                void* h, void* y_perm, void* scratch, void* stream,
     const StashMap& sm) {
   MOE_TRY(check_config(cfg));
-  MOE_REQUIRE(al16(x_perm) && al4(counts) && al4(offsets) && weights_ok(cfg, W13, W2));
+  // (the FP8 GEMMs read x_perm's E4M3 form in scratch: after moe_permute_fp8 there is no other)
+  MOE_REQUIRE(is_fp8(*cfg) ? al16_or_null(x_perm) : al16(x_perm));
+  MOE_REQUIRE(al4(counts) && al4(offsets) && weights_ok(cfg, W13, W2));
   MOE_REQUIRE(al16(GU) && al16(h) && al16(y_perm) && al16(scratch));
   cudaStream_t s = (cudaStream_t)stream;
   int32_t* st = status_word(scratch);

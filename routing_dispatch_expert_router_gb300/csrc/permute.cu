@@ -20,6 +20,7 @@
 #include "common.cuh"
 #include "fp8_layout.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace moe {
 
@@ -330,6 +331,76 @@ permute_scatter_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __res
   }
 }
 
+// Rows that are in 8 bits already (E4M3 codes with a scale byte per 32 or 128 values): a warp
+// reads a token's row once and writes it to each of its rows, 16 bytes a lane; its scale bytes
+// go into the atoms four at a time (fp8_layout.cuh: both layouts keep four consecutive blocks
+// of a row in one word). Rows without a token are not written: a product's rows depend on
+// their own row alone, and only the combine's rows are read behind it. HBM bounds it.
+__global__ void __launch_bounds__(256)
+permute_scatter8_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                        const int32_t* __restrict__ row_of, int T, int H, int k, int block,
+                        uint8_t* __restrict__ xq, uint8_t* __restrict__ xsf) {
+  ptx::grid_dependency_wait();
+  const int lane = threadIdx.x & 31;
+  const int nvec = H >> 4, n = H / block;
+  const int words = (n + 3) >> 2;                  // atoms along the row, in either layout
+  const int warps = gridDim.x * (blockDim.x >> 5);
+  for (int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); t < T; t += warps) {
+    const int myrow = lane < k ? row_of[(size_t)t * k + lane] : -1;
+    int rows[kMaxK];
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j) rows[j] = __shfl_sync(0xffffffffu, myrow, j);
+    const uint8_t* src = codes + (size_t)t * H;
+    for (int c0 = lane; c0 < nvec; c0 += 32 * 4) {
+      uint4 q[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (c0 + 32 * u < nvec) q[u] = ldg_nc_v4(src + (size_t)(c0 + 32 * u) * 16);
+#pragma unroll
+      for (int j = 0; j < kMaxK; ++j) {
+        if (rows[j] < 0) continue;
+        uint8_t* dst = xq + (size_t)rows[j] * H;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (c0 + 32 * u < nvec) stg_v4(dst + (size_t)(c0 + 32 * u) * 16, q[u]);
+      }
+    }
+    const uint8_t* ssrc = scales + (size_t)t * n;
+    for (int w = lane; w < words; w += 32) {
+      uint32_t v = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (4 * w + b < n) v |= (uint32_t)__ldg(ssrc + 4 * w + b) << (8 * b);
+#pragma unroll
+      for (int j = 0; j < kMaxK; ++j) {
+        if (rows[j] < 0) continue;
+        *reinterpret_cast<uint32_t*>(xsf + ((size_t)(rows[j] >> 7) * words + w) * f8::kAtomBytes +
+                                     f8::atom_byte(rows[j], 0)) = v;
+      }
+    }
+  }
+}
+
+// The maps: counts, offsets, rows and tokens of every assignment.
+static cudaError_t launch_permute_maps(const moe_config& c, const int32_t* idx, int32_t* counts,
+                                       int32_t* offsets, int32_t* row_of, int32_t* token_of,
+                                       int32_t* sel_offsets, int32_t* sel_tokens,
+                                       uint8_t* scratch, cudaStream_t s) {
+  int32_t* status = reinterpret_cast<int32_t*>(scratch + kScratchStatus);
+  int32_t* pad_prefix = reinterpret_cast<int32_t*>(scratch + kScratchPadPrefix);
+  int32_t* hist = reinterpret_cast<int32_t*>(scratch + kScratchHist);
+  const int nc = n_chunks(c);
+  if (nc > 0) {
+    permute_hist_kernel<<<nc, 256, 0, s>>>(idx, hist, c.T, c.k, c.E, status);
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+  }
+  permute_rank_kernel<<<nc > 0 ? nc : 1, 256, 0, s>>>(idx, hist, nc, c.T, c.k, c.E, c.n_shared, c.row_align,
+                                         (int)capacity_rows(c), counts, offsets, row_of,
+                                         token_of, sel_offsets, sel_tokens, pad_prefix);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_permute(const moe_config& c, const void* x, const int32_t* idx,
                            int32_t* counts, int32_t* offsets, int32_t* row_of, int32_t* token_of,
                            int32_t* sel_offsets, int32_t* sel_tokens, void* x_perm,
@@ -337,18 +408,8 @@ cudaError_t launch_permute(const moe_config& c, const void* x, const int32_t* id
                            const StashAlloc* alloc) {
   int32_t* status = reinterpret_cast<int32_t*>(scratch + kScratchStatus);
   int32_t* pad_prefix = reinterpret_cast<int32_t*>(scratch + kScratchPadPrefix);
-  int32_t* hist = reinterpret_cast<int32_t*>(scratch + kScratchHist);
-  const int nc = n_chunks(c);
-  cudaError_t err;
-  if (nc > 0) {
-    permute_hist_kernel<<<nc, 256, 0, s>>>(idx, hist, c.T, c.k, c.E, status);
-    err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-  }
-  permute_rank_kernel<<<nc > 0 ? nc : 1, 256, 0, s>>>(idx, hist, nc, c.T, c.k, c.E, c.n_shared, c.row_align,
-                                         (int)capacity_rows(c), counts, offsets, row_of,
-                                         token_of, sel_offsets, sel_tokens, pad_prefix);
-  err = cudaGetLastError();
+  cudaError_t err = launch_permute_maps(c, idx, counts, offsets, row_of, token_of, sel_offsets,
+                                        sel_tokens, scratch, s);
   if (err != cudaSuccess) return err;
   const int32_t* pages = nullptr;
   if (alloc) {
@@ -372,6 +433,29 @@ cudaError_t launch_permute(const moe_config& c, const void* x, const int32_t* id
       static_cast<const __nv_bfloat16*>(x), row_of, counts, offsets, pad_prefix,
       static_cast<__nv_bfloat16*>(x_perm), c.T, c.H, c.k, c.E, c.n_shared, xq, xsf, pages);
   return cudaGetLastError();
+}
+
+cudaError_t launch_permute_fp8(const moe_config& c, const uint8_t* codes, const uint8_t* scales,
+                               const int32_t* idx, int32_t* counts, int32_t* offsets,
+                               int32_t* row_of, int32_t* token_of, int32_t* sel_offsets,
+                               int32_t* sel_tokens, uint8_t* xq, uint8_t* xsf, uint8_t* scratch,
+                               cudaStream_t s) {
+  const cudaError_t err = launch_permute_maps(c, idx, counts, offsets, row_of, token_of,
+                                              sel_offsets, sel_tokens, scratch, s);
+  if (err != cudaSuccess || c.T == 0) return err;
+  const int blocks = (c.T + 7) / 8, most = num_sms() * 8;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(blocks < most ? blocks : most, 1, 1);
+  lc.blockDim = dim3(256, 1, 1);
+  lc.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, permute_scatter8_kernel, codes, scales, (const int32_t*)row_of,
+                            (int)c.T, (int)c.H, (int)c.k, c.dtype == MOE_DTYPE_MXFP8 ? 32 : 128,
+                            xq, xsf);
 }
 
 cudaError_t launch_stash_release(const moe_config& c, const int32_t* table, int32_t* top,

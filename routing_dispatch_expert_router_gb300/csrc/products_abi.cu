@@ -1,0 +1,127 @@
+// C entry points of the norm before a layer, the dispatch of rows in 8 bits and the products
+// of free form: argument checks and launches.
+#include <limits.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "fp8_layout.cuh"
+#include "internal.h"
+
+using namespace moe;
+
+namespace {
+
+#define OP_TRY(expr)                   \
+  do {                                 \
+    const moe_status _s = (expr);      \
+    if (_s != MOE_OK) return _s;       \
+  } while (0)
+
+#define OP_CUDA(expr)                                                         \
+  do {                                                                        \
+    const cudaError_t _e = (expr);                                            \
+    if (_e != cudaSuccess)                                                    \
+      return _e == cudaErrorInvalidValue ? MOE_ERR_INVALID_ARG : MOE_ERR_CUDA; \
+  } while (0)
+
+#define OP_REQUIRE(cond)                       \
+  do {                                         \
+    if (!(cond)) return MOE_ERR_INVALID_ARG;   \
+  } while (0)
+
+bool al16(const void* p) { return p && ((uintptr_t)p & 15u) == 0; }
+bool al16_or_null(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool al4(const void* p) { return p && ((uintptr_t)p & 3u) == 0; }
+bool al4_or_null(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+// Rows of `cols` bf16 elements, ld apart, where the 16-byte accesses want them.
+bool rows_ok(const void* p, int64_t ld, int64_t cols) {
+  return al16(p) && ld >= cols && ld % 8 == 0 && ld <= INT_MAX;
+}
+bool rows_or_null(const void* p, int64_t ld, int64_t cols) { return !p || rows_ok(p, ld, cols); }
+
+moe_status check_norm(int64_t T, int64_t H, const void* gamma, int32_t gamma_dtype) {
+  OP_REQUIRE(T >= 0 && T <= INT_MAX && H >= 8 && H % 8 == 0);
+  if (H > 32768) return MOE_ERR_UNSUPPORTED;
+  OP_REQUIRE(gamma_dtype == MOE_GAMMA_BF16 || gamma_dtype == MOE_GAMMA_F32);
+  OP_REQUIRE(al16(gamma));
+  return MOE_OK;
+}
+
+const __nv_bfloat16* bf(const void* p) { return static_cast<const __nv_bfloat16*>(p); }
+__nv_bfloat16* bf(void* p) { return static_cast<__nv_bfloat16*>(p); }
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_rmsnorm_fwd(int64_t T, int64_t H, const void* x, int64_t ldx, const void* residual,
+                           int64_t ldr, const void* gamma, int32_t gamma_dtype, float eps,
+                           void* sum, int64_t lds, void* out, int64_t ldo, void* codes,
+                           void* scales, int32_t block, float* rstd, void* stream) {
+  OP_TRY(check_norm(T, H, gamma, gamma_dtype));
+  OP_REQUIRE(isfinite(eps) && eps >= 0.f && !codes == !scales && (out || codes || T == 0));
+  if (codes) {
+    OP_REQUIRE((block == 32 || block == 128) && H % block == 0);
+    OP_REQUIRE(al16(codes));
+  }
+  if (T == 0) return MOE_OK;
+  OP_REQUIRE(rows_ok(x, ldx, H) && rows_or_null(residual, ldr, H) && rows_or_null(sum, lds, H));
+  OP_REQUIRE(rows_or_null(out, ldo, H) && al4_or_null(rstd) && (residual || !sum));
+  const RmsNormFwd p{T, (int)H, bf(x), ldx, bf(residual), ldr, gamma,
+                     gamma_dtype == MOE_GAMMA_F32, eps, bf(sum), lds, bf(out), ldo,
+                     static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales),
+                     codes ? block : 32, rstd};
+  OP_CUDA(launch_rmsnorm_fwd(p, (cudaStream_t)stream));
+  return MOE_OK;
+}
+
+moe_status moe_rmsnorm_scratch_bytes(int64_t H, int64_t* bytes) {
+  OP_REQUIRE(bytes && H >= 8 && H % 8 == 0);
+  if (H > 32768) return MOE_ERR_UNSUPPORTED;
+  *bytes = (int64_t)kRmsNormParts * H * 4;
+  return MOE_OK;
+}
+
+moe_status moe_rmsnorm_bwd(int64_t T, int64_t H, const void* dy, int64_t lddy, const void* h,
+                           int64_t ldh, const float* rstd, const void* gamma, int32_t gamma_dtype,
+                           const void* dsum, int64_t ldds, void* dx, int64_t lddx, float* dgamma,
+                           void* scratch, void* stream) {
+  OP_TRY(check_norm(T, H, gamma, gamma_dtype));
+  OP_REQUIRE(!dgamma || (al4(dgamma) && al16(scratch)));
+  if (T > 0) {
+    OP_REQUIRE(rows_ok(dy, lddy, H) && rows_ok(h, ldh, H) && al4(rstd) && rows_ok(dx, lddx, H));
+    OP_REQUIRE(rows_or_null(dsum, ldds, H));
+  }
+  const RmsNormBwd p{T, (int)H, bf(dy), lddy, bf(h), ldh, rstd, gamma,
+                     gamma_dtype == MOE_GAMMA_F32, bf(dsum), ldds, bf(dx), lddx,
+                     dgamma ? static_cast<float*>(scratch) : nullptr};
+  OP_CUDA(launch_rmsnorm_bwd(p, dgamma, (cudaStream_t)stream));
+  return MOE_OK;
+}
+
+moe_status moe_permute_fp8(const moe_config* cfg, const void* codes, const void* scales,
+                           const int32_t* idx, int32_t* counts, int32_t* offsets, int32_t* row_of,
+                           int32_t* token_of, int32_t* sel_offsets, int32_t* sel_tokens,
+                           void* codes_perm, void* scales_perm, void* scratch, void* stream) {
+  OP_TRY(check_config(cfg));
+  OP_REQUIRE(cfg->dtype == MOE_DTYPE_FP8_E4M3_BLOCK || cfg->dtype == MOE_DTYPE_MXFP8);
+  if (cfg->stash_pool_pages) return MOE_ERR_UNSUPPORTED;
+  OP_REQUIRE(al4(counts) && al4(offsets) && al4(token_of) && al4(sel_offsets) && al16(scratch));
+  OP_REQUIRE(!codes_perm == !scales_perm && al16_or_null(codes_perm) && al16_or_null(scales_perm));
+  if (cfg->T > 0)
+    OP_REQUIRE(al16(codes) && scales && al4(idx) && al4(row_of) && al4(sel_tokens));
+  if (!codes_perm) {
+    const Fp8Scratch f = fp8_scratch(*cfg, scratch);
+    codes_perm = f.xq;
+    scales_perm = f.xsf;
+  }
+  OP_CUDA(launch_permute_fp8(*cfg, static_cast<const uint8_t*>(codes),
+                             static_cast<const uint8_t*>(scales), idx, counts, offsets, row_of,
+                             token_of, sel_offsets, sel_tokens, static_cast<uint8_t*>(codes_perm),
+                             static_cast<uint8_t*>(scales_perm), static_cast<uint8_t*>(scratch),
+                             (cudaStream_t)stream));
+  return MOE_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,115 @@
+"""Refusals of the norm, the dispatch of 8-bit rows and the products of free form: what does not
+fit is refused on the host (nothing is launched)."""
+import ctypes
+
+import pytest
+import torch
+
+import routing_dispatch_expert_router_gb300.binding as B
+from routing_dispatch_expert_router_gb300.build import build
+
+BF, U8, I32, F32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build()
+
+
+class OnGpu(torch.Tensor):
+    """A tensor that says it lies on the GPU: for checks that come before any launch."""
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return torch.cuda.current_device() if torch.cuda.is_available() else 0
+
+
+def gpu(*shape, dtype=BF):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+
+
+def wrong(t):
+    """Tensors that do not fit in t's place: another type, too few elements, gaps, the host."""
+    yield t.to(torch.float64)
+    yield t[:-1]
+    if t.dim() == 2:
+        yield t[:, :-8]
+    yield torch.zeros(*t.shape, dtype=t.dtype)
+
+
+def refused(call, args, **bad):
+    with pytest.raises((ValueError, B.MoEError)):
+        call(**{**args, **bad}, stream=0)
+
+
+T, H = 5, 256
+
+
+def test_norm_refuses_tensors_that_do_not_fit():
+    fwd = dict(x=gpu(T, H), gamma=gpu(H), out=gpu(T, H), residual=gpu(T, H), sum=gpu(T, H),
+               rstd=gpu(T, dtype=F32), codes=gpu(T, H, dtype=U8), scales=gpu(T, H // 32, dtype=U8))
+    for name in ("gamma", "out", "residual", "sum", "rstd", "codes", "scales"):
+        for bad in wrong(fwd[name]):
+            refused(B.moe_rmsnorm_fwd, fwd, **{name: bad})
+    for name, bad in (("scales", None), ("codes", None), ("scales", gpu(T, H // 64, dtype=U8)),
+                      ("residual", None), ("x", gpu(T, 2 * H)[:, ::2]), ("x", gpu(H, T).t()),
+                      ("x", gpu(1, H).expand(T, H)), ("out", gpu(T, H, dtype=torch.float16)),
+                      ("x", gpu(T, H + 4)[:, 4:])):
+        refused(B.moe_rmsnorm_fwd, fwd, **{name: bad})
+    refused(B.moe_rmsnorm_fwd, {**fwd, "codes": None, "scales": None}, out=None)
+    for eps in (-1e-6, float("nan"), float("inf")):
+        refused(B.moe_rmsnorm_fwd, fwd, eps=eps)
+    bwd = dict(dy=gpu(T, H), h=gpu(T, H), rstd=gpu(T, dtype=F32), gamma=gpu(H), dx=gpu(T, H),
+               dgamma=gpu(H, dtype=F32), dsum=gpu(T, H),
+               scratch=gpu(B.rmsnorm_scratch_bytes(H), dtype=U8))
+    for name in ("dy", "rstd", "gamma", "dx", "dgamma", "dsum"):
+        for bad in wrong(bwd[name]):
+            refused(B.moe_rmsnorm_bwd, bwd, **{name: bad})
+    for bad in (None, gpu(B.rmsnorm_scratch_bytes(H) - 1, dtype=U8)):
+        refused(B.moe_rmsnorm_bwd, bwd, scratch=bad)
+
+
+def test_norm_entry_refuses_sizes_and_addresses():
+    L, ok = B.lib(), 1024
+
+    def fwd(T=4, H=256, x=ok, ldx=256, r=0, ldr=0, g=ok, kind=0, eps=0.0, s=0, lds=0, o=ok, ldo=256,
+            c=0, sc=0, block=0, rstd=0):
+        return L.moe_rmsnorm_fwd(T, H, x, ldx, r, ldr, g, kind, eps, s, lds, o, ldo, c, sc, block, rstd, 0)
+
+    assert fwd(T=0) == 0
+    for bad in (dict(T=-1), dict(H=0), dict(H=252), dict(x=0), dict(x=8), dict(ldx=248), dict(ldx=260),
+                dict(r=8, ldr=256), dict(r=ok, ldr=8), dict(g=0), dict(g=4), dict(kind=2), dict(o=0),
+                dict(s=ok, lds=256), dict(c=ok), dict(c=ok, sc=ok, block=64), dict(rstd=2),
+                dict(H=264, ldx=264, ldo=264, c=ok, sc=ok, block=32)):
+        assert fwd(**bad) == 1, bad
+    assert fwd(H=32776, ldx=32776, ldo=32776) == 2
+    n = ctypes.c_int64(0)
+    assert L.moe_rmsnorm_scratch_bytes(4, ctypes.byref(n)) == 1
+    assert L.moe_rmsnorm_scratch_bytes(32776, ctypes.byref(n)) == 2
+
+
+def test_permute_fp8_refuses_what_does_not_fit():
+    cfg = B.MoEConfig(T=20, H=256, E=4, k=2, F=256, n_groups=1, topk_groups=1, route_scale=1.0,
+                      row_align=128, dtype=1)
+    sz = B.moe_query_sizes(cfg)
+    R = sz.rows_max
+    args = dict(cfg=cfg, codes=gpu(20, 256, dtype=U8), scales=gpu(20, 2, dtype=U8), idx=gpu(20, 2, dtype=I32),
+                counts=gpu(4, dtype=I32), offsets=gpu(5, dtype=I32), row_of=gpu(20, 2, dtype=I32),
+                token_of=gpu(R, dtype=I32), sel_offsets=gpu(5, dtype=I32), sel_tokens=gpu(40, dtype=I32),
+                scratch=gpu(sz.scratch_bytes, dtype=U8), codes_perm=gpu(R, 256, dtype=U8),
+                scales_perm=gpu(-(-R // 128), 1, 512, dtype=U8))
+    for name, t in args.items():
+        if name in ("cfg", "scratch"):
+            continue
+        for bad in wrong(t):
+            if bad.dim() == 3 and bad.is_cuda and bad.dtype == U8:
+                bad = bad[:, :, :500]
+            refused(B.moe_permute_fp8, args, **{name: bad})
+    refused(B.moe_permute_fp8, args, scratch=gpu(4000, dtype=U8))
+    refused(B.moe_permute_fp8, args, codes_perm=None)
+    refused(B.moe_permute_fp8, {**args, "codes_perm": None, "scales_perm": None}, scratch=gpu(1 << 16, dtype=U8))
+    bf = B.MoEConfig.from_buffer_copy(bytes(cfg))
+    bf.dtype = 0
+    refused(B.moe_permute_fp8, args, cfg=bf)
+    bf.dtype, bf.stash_pool_pages = 1, 4
+    refused(B.moe_permute_fp8, args, cfg=bf)
