@@ -729,6 +729,50 @@ MOE_API moe_status moe_permute_fp8(const moe_config* cfg, const void* codes, con
                                    int32_t* sel_tokens, void* codes_perm, void* scales_perm,
                                    void* scratch, void* stream);
 
+/* ------------------------------------------------------ products of free form
+ * Products of grouped rows whose sizes are ragged and lie one behind the other
+ * without padding: group g owns the rows offsets[g] .. offsets[g] + counts[g] - 1
+ * of the row tensors, at any offset (moe_permute's padded segments are one case);
+ * other rows are neither read into a result nor written. counts, offsets: int32
+ * [groups] on the device; NULL both: one group of all rows. Segments lie inside
+ * the rows (else the group counts as empty and MOE_ERR_DEVICE_CHECK is recorded)
+ * and do not overlap. rows 0 .. 2^31 - 1, groups 1..260. Accumulation is in fp32,
+ * results are rounded to bf16 once and do not depend on timing. Row tensors
+ * have ld* elements from row to row (a multiple of 8). scratch:
+ * moe_product_scratch_bytes bytes for any shape, zero-filled once by the caller
+ * and then left to the calls (its first word is the device status word); calls
+ * that may overlap need scratch each. Host only: */
+MOE_API moe_status moe_product_scratch_bytes(int64_t* bytes);
+
+/* Weights in 4-bit integers with a scale (and a zero point) for `group`
+ * consecutive elements along K: w = scale (code - zero). codes [groups, N, K / 2]
+ * bytes, the even element in the low four bits (0..15); scales [groups,
+ * K / group, N] bf16; zeros [groups, K / group, N] bytes 0..127, or NULL (8
+ * everywhere). group 32, 64 or 128; K a multiple of it, N of 16. */
+typedef struct moe_int4_tensor {
+    int32_t group;           /* 32, 64 or 128                                    */
+    int64_t groups;          /* experts                                          */
+    int64_t N, K;            /* outputs and inputs of an expert's product        */
+    const void* codes;       /* device, 16-byte aligned                          */
+    const void* scales;      /* device, 16-byte aligned                          */
+    const void* zeros;       /* device, 16-byte aligned, or NULL                 */
+} moe_int4_tensor;
+
+/* out[r, n] = bf16(sum_k x[r, k] w[g, n, k]) for the rows r of every group g,
+ * x [rows, K] and out [rows, N] bf16. swiglu = 1 (N a multiple of 32): out
+ * [rows, N / 2] = bf16(silu(a) b) of the product's columns a[n], b[n] = n and
+ * N / 2 + n, held in fp32. Made for few rows a group (decoding), where the codes'
+ * bytes decide; any number is right, every 16 rows reading the codes once more.
+ * For many rows moe_int4_dequantize and the products below. A row of x that
+ * holds an infinity or a NaN has NaN results; other rows are not touched by it. */
+MOE_API moe_status moe_int4_grouped_gemm(const moe_int4_tensor* w, int64_t rows, const void* x,
+                                         int64_t ldx, const int32_t* counts,
+                                         const int32_t* offsets, int32_t swiglu, void* out,
+                                         int64_t ldo, void* scratch, void* stream);
+
+/* The weights as bf16 (one rounding): out [groups, N, K]. */
+MOE_API moe_status moe_int4_dequantize(const moe_int4_tensor* w, void* out, void* stream);
+
 /* Synchronises `stream`, then copies the device status word from scratch to
  * *code (0 = no problem recorded). */
 MOE_API moe_status moe_last_device_status(const void* scratch, int32_t* code, void* stream);

@@ -32,6 +32,7 @@ ENTRY_POINTS = (
     "moe_fp4_query_sizes", "moe_fp4_scale_bytes", "moe_fp4_quantize", "moe_fp4_dequantize",
     "moe_fp4_grouped_gemm", "moe_fp4_ffn_fwd", "moe_fp4_ffn_bwd",
     "moe_rmsnorm_fwd", "moe_rmsnorm_bwd", "moe_rmsnorm_scratch_bytes", "moe_permute_fp8",
+    "moe_product_scratch_bytes", "moe_int4_grouped_gemm", "moe_int4_dequantize",
     "moe_last_device_status",
     "moe_clear_device_status", "moe_check_bounded_wait", "moe_status_string",
 )
@@ -577,7 +578,15 @@ def moe_fp4_ffn_bwd(cfg, experts: MoEFp4Experts, dO_perm, ckpt, ckpt_scale, coun
 # ---------------------------------- the norm before a layer, the dispatch of rows in 8 bits
 MOE_GAMMA_BF16, MOE_GAMMA_F32 = 0, 1
 
+class MoEInt4Tensor(ctypes.Structure):
+    _fields_ = [("group", ctypes.c_int32), ("groups", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("codes", _P), ("scales", _P), ("zeros", _P)]
+
+
 _PRODUCT_ARGS = {
+    "moe_product_scratch_bytes": [ctypes.POINTER(_I64)],
+    "moe_int4_grouped_gemm": [ctypes.POINTER(MoEInt4Tensor), _I64, _P, _I64, _P, _P, _I32, _P, _I64, _P, _P],
+    "moe_int4_dequantize": [ctypes.POINTER(MoEInt4Tensor), _P, _P],
     "moe_rmsnorm_fwd": [_I64, _I64, _P, _I64, _P, _I64, _P, _I32, ctypes.c_float, _P, _I64, _P, _I64,
                         _P, _P, _I32, _P, _P],
     "moe_rmsnorm_bwd": [_I64, _I64, _P, _I64, _P, _I64, _P, _P, _I32, _P, _I64, _P, _I64, _P, _P, _P],
@@ -702,6 +711,84 @@ def moe_permute_fp8(cfg, codes, scales, idx, counts, offsets, row_of, token_of, 
                                  _vector(scales_perm, -(-R // 128) * -(-blocks // 4) * 512,
                                          torch.uint8, "scales_perm"),
                                  _scratch(scratch, need), _stream(stream)))
+
+
+# ---------------------------------------------------------------- products of free form
+class Int4Tensor:
+    """Weights [groups, N, K] in 4-bit integers: codes [groups, N, K / 2] (uint8, the even element
+    in the low four bits), scales [groups, K / group, N] (bf16) and zeros (uint8, of the scales'
+    shape; None: 8 everywhere); w = scale * (code - zero)."""
+    __slots__ = ("codes", "scales", "zeros", "_struct")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None):
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+        if codes.dim() != 3 or codes.dtype is not torch.uint8 or not codes.is_contiguous():
+            raise ValueError("codes are contiguous uint8 [groups, N, K / 2]")
+        g, N, K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+        if scales.dim() != 3 or scales.dtype is not torch.bfloat16 or not scales.is_contiguous() or \
+                scales.shape[0] != g or scales.shape[2] != N or scales.shape[1] == 0 or \
+                K % scales.shape[1]:
+            raise ValueError("scales are contiguous bf16 [groups, K / group, N]")
+        if zeros is not None and (zeros.shape != scales.shape or zeros.dtype is not torch.uint8
+                                  or not zeros.is_contiguous()):
+            raise ValueError("zeros are contiguous uint8 of the scales' shape")
+        if not codes.is_cuda or not scales.is_cuda or not (zeros is None or zeros.is_cuda):
+            raise ValueError("codes, scales and zeros are on the GPU")
+        self._struct = MoEInt4Tensor(K // scales.shape[1], g, N, K, codes.data_ptr(),
+                                     scales.data_ptr(), None if zeros is None else zeros.data_ptr())
+
+    def struct(self) -> MoEInt4Tensor:
+        return self._struct
+
+
+_product_scratch_bytes = 0
+
+
+def product_scratch_bytes() -> int:
+    """Bytes of the products' scratch, for any shape (zero-filled once, as alloc_fp4_scratch's)."""
+    global _product_scratch_bytes
+    if not _product_scratch_bytes:
+        n = ctypes.c_int64(0)
+        _check("moe_product_scratch_bytes", lib().moe_product_scratch_bytes(ctypes.byref(n)))
+        _product_scratch_bytes = n.value
+    return _product_scratch_bytes
+
+
+def alloc_product_scratch(device="cuda") -> torch.Tensor:
+    return torch.zeros(product_scratch_bytes(), dtype=torch.uint8, device=device)
+
+
+def _segments(counts, offsets, groups: int):
+    if counts is not None and counts.numel() != groups:
+        raise ValueError("one count per group")
+    return (_vector(counts, groups, torch.int32, "counts"),
+            _vector(offsets, groups, torch.int32, "offsets"))
+
+
+def moe_int4_grouped_gemm(x, w: Int4Tensor, counts, offsets, out, scratch, swiglu: bool = False,
+                          stream=None):
+    """out [rows, N] = every group's rows of x [rows, K] by w [groups, N, K]; swiglu: out
+    [rows, N / 2] = silu(first half of the columns) * second half. counts, offsets: int32
+    [groups], or None for one group of all rows."""
+    s = w.struct()
+    rows = x.shape[0]
+    _here(x, w.codes, w.scales, w.zeros, counts, offsets, out, scratch)
+    px, ldx = _strided(x, rows, s.K, "x")
+    po, ldo = _strided(out, rows, s.N // 2 if swiglu else s.N, "out")
+    pc, pf = _segments(counts, offsets, s.groups)
+    _check("moe_int4_grouped_gemm",
+           lib().moe_int4_grouped_gemm(s, rows, px, ldx, pc, pf, 1 if swiglu else 0, po, ldo,
+                                       _scratch(scratch, product_scratch_bytes()), _stream(stream)))
+
+
+def moe_int4_dequantize(w: Int4Tensor, out, stream=None):
+    """out [groups, N, K] bf16 = the weights."""
+    s = w.struct()
+    _here(w.codes, w.scales, w.zeros, out)
+    if tuple(out.shape) != (s.groups, s.N, s.K) or out.dtype is not torch.bfloat16 or \
+            not out.is_contiguous() or not out.is_cuda:
+        raise ValueError("out is contiguous bf16 [groups, N, K], on the GPU")
+    _check("moe_int4_dequantize", lib().moe_int4_dequantize(s, out.data_ptr(), _stream(stream)))
 
 
 @functools.lru_cache(maxsize=64)

@@ -316,6 +316,39 @@ struct RmsNormBwd {
 constexpr int kRmsNormParts = 512;
 cudaError_t launch_rmsnorm_bwd(const RmsNormBwd& p, float* dgamma, cudaStream_t s);
 
+// Grouped products of few rows (product_few.cu): out[r] = x[r] W[g]^T (+ add) for the rows of
+// every group g (counts, offsets; null: one group of all rows). W [G, N, K] in bf16 (scales null),
+// or codes with scales [G, K / group, N] bf16 and zero points (null: 8) u8; swiglu (4-bit):
+// out [rows, N / 2] = silu(first half) second half.
+struct FewProduct {
+  int G;
+  int64_t rows;
+  int N, K;
+  const int32_t* counts;
+  const int32_t* offsets;
+  int group;                  // elements of K that share a scale (4-bit)
+  const __nv_bfloat16* add;
+  int64_t ldadd;
+  __nv_bfloat16* out;
+  int64_t ldo;
+  float* parts;               // [2 kFewCtas][kFewPart] fp32
+  uint32_t* arrived;          // [kFewCtas], zero before and after every launch
+  int32_t* status;
+  // set by the launcher
+  int F, slabs, steps, groups_per_step;
+  bool has_zeros;
+};
+constexpr int kFewCtas = 256;
+constexpr int kFewPart = 256 * 16;
+constexpr int kFewLeast = 4;
+bool few_fits(int64_t rows, int G, int64_t N);
+cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const void* w,
+                               const void* scales, const void* zeros, bool swiglu, cudaStream_t s);
+
+// The bf16 weights that 4-bit codes stand for: out [G, N, K].
+cudaError_t launch_int4_dequantize(const void* codes, const void* scales, const void* zeros, int G,
+                                   int N, int K, int group, void* out, cudaStream_t s);
+
 // Router logits for E % 128 == 0 on the tensor cores (W3 = W_r split in three bf16 parts).
 cudaError_t launch_router_logits_tc(const moe_config& c, const void* x, const void* W3,
                                     float* logits, int32_t* status, cudaStream_t s);

@@ -1,0 +1,626 @@
+// Grouped products of few rows: y[r] = x[r] W[g]^T with W in bf16 or in 4-bit integers with
+// group scales. Every byte that has to move is a weight's, so HBM bounds them, and the kernel
+// is a stream: one persistent CTA per SM takes an even share of all (expert, 256 output
+// columns, step of K) pieces in order, whatever their expert, and its weights come by TMA into
+// a ring of stages that never drains between experts.
+//
+//   warp 0         TMA producer (one lane): 256 weight rows x 128 bytes of K a stage, the same
+//                  step of the tokens' rows, and the group scales and zero points;
+//   warps 1-3      (4-bit) the tokens' elements in the order in which codes unpack, and their
+//                  sums over 32;
+//   the other 16   mma.sync m16n8k16, the weights as A: a warp has 32 weight rows and half of
+//                  the step's K. Tokens are B, eight to a tile, at most 16 a pass: with few
+//                  tokens tcgen05's 128-row tiles would multiply padding, and its operands
+//                  would have to be written back to shared memory as bf16 first, four times
+//                  the bytes of the codes.
+//
+// 4-bit weights are s (q - z). The codes become bf16 numbers 128 + q by placing their bits in
+// the mantissa (one logic operation for two), whose products with x are exact; the offset and
+// the zero point leave by s (sum (128 + q) x - (128 + z) sum x), in fp32, per group of K. (The
+// subtraction costs 2^-24 (128 + z) sum |x| of the group at most, far below the result's
+// rounding to bf16, unless all of a group's codes cancel its x.) Subtracting z from each code
+// first would be four more of eleven instructions a word, and instructions are what the SM
+// runs short of: 24 bytes a clock arrive, 48 codes.
+//
+// A (expert, columns) unit that two or more CTAs share is joined through scratch: every CTA
+// writes its fp32 part, the one that arrives last adds the parts in K's order. So results do
+// not depend on timing.
+#include "gemm_common.cuh"
+
+namespace moe {
+namespace {
+
+using gg::encode_fn;
+using gg::kWaitBudget;
+
+constexpr int kSlab = 256;                     // weight rows of a unit
+constexpr int kTok = 16;                       // tokens of a unit
+constexpr int kRowWarps = kSlab / 32;
+constexpr int kKWarps = 2;
+constexpr int kConsumers = kRowWarps * kKWarps;
+constexpr int kTileLd = kTok + 1;
+constexpr int kTileBytes = kSlab * kTileLd * 4;
+constexpr int kCtrl = 5120;
+
+template <bool W4>
+struct Cfg {
+  static constexpr int HELPERS = W4 ? 3 : 0;       // (five warps a scheduler: 96 registers)
+  static constexpr int THREADS = 32 * (1 + HELPERS + kConsumers);
+  static constexpr int STAGES = W4 ? 4 : 6;
+  static constexpr int STEP = W4 ? 256 : 64;           // elements of K a stage
+  static constexpr int XBOXES = STEP / 64;             // boxes of 64 elements x 8 tokens
+  static constexpr int X_OFF = kSlab * 128;
+  static constexpr int S_OFF = X_OFF + kTok / 8 * XBOXES * 1024;
+  static constexpr int Z_OFF = S_OFF + (W4 ? 8 * kSlab * 2 : 0);   // eight groups at most
+  static constexpr int SUM_OFF = Z_OFF + (W4 ? 8 * kSlab : 0);
+  static constexpr int STAGE = (SUM_OFF + (W4 ? 8 * kTok * 4 : 0) + 1023) / 1024 * 1024;
+  static constexpr int SMEM = STAGES * STAGE + kTileBytes + kCtrl + 1024;
+};
+static_assert(Cfg<true>::SMEM <= 232448 && Cfg<false>::SMEM <= 232448, "shared memory");
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
+               :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Elements i and i + 4 of a word of eight codes as the bf16 pair 128 + q.
+__device__ __forceinline__ uint32_t codes_pair(uint32_t w, int i) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(r) : "r"(w >> (4 * i)));
+  return r;
+}
+
+// What a step adds to a warp's 32 rows x 8 NTL tokens.
+template <int NTL>
+__device__ __forceinline__ void step_int4(float (&tot)[2][2][4], uint32_t st, const FewProduct& p,
+                                          int rg, int kw, int g, int t) {
+  using C = Cfg<true>;
+  const int row0 = rg * 32 + g;
+  const bool each = p.group == 32;               // a group is one chunk of 32, or covers both
+  // scales and zero points lie in two halves of 128 rows
+  const uint32_t half = (uint32_t)(rg >> 2) * p.groups_per_step;
+  const uint32_t r128 = row0 & 127;
+#pragma unroll
+  for (int cc = 0; cc < 4; cc += 2) {
+    float acc[2][NTL][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int n = 0; n < NTL; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+#pragma unroll
+    for (int c1 = 0; c1 < 2; ++c1) {
+      const int c = 4 * kw + cc + c1;            // the step's chunk of 32 elements
+      uint32_t w[2][2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = row0 + 16 * m + 8 * h;
+          w[m][h] = lds32(st + row * 128 + ((c ^ (row & 7)) << 4) + t * 4);
+        }
+      uint4 x[NTL];
+#pragma unroll
+      for (int n = 0; n < NTL; ++n)
+        x[n] = lds128(st + C::X_OFF + (n * C::XBOXES + (c >> 1)) * 1024 + g * 128 +
+                      ((((c & 1) * 4 + t) ^ ((g & 1) << 2)) << 4));
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const uint32_t a0 = codes_pair(w[m][0], 0), a1 = codes_pair(w[m][1], 0);
+        const uint32_t a2 = codes_pair(w[m][0], 1), a3 = codes_pair(w[m][1], 1);
+        const uint32_t b0 = codes_pair(w[m][0], 2), b1 = codes_pair(w[m][1], 2);
+        const uint32_t b2 = codes_pair(w[m][0], 3), b3 = codes_pair(w[m][1], 3);
+#pragma unroll
+        for (int n = 0; n < NTL; ++n) {
+          mma16816(acc[m][n], a0, a1, a2, a3, x[n].x, x[n].y);
+          mma16816(acc[m][n], b0, b1, b2, b3, x[n].z, x[n].w);
+        }
+      }
+      if (c1 == 0 && !each) continue;
+      // the group's scale and zero point: these rows' four, of this chunk's group
+      const uint32_t sg = half + (uint32_t)((c * 32) / p.group);
+      float2 sx[NTL];
+#pragma unroll
+      for (int n = 0; n < NTL; ++n) {
+        sx[n] = lds_f2(st + C::SUM_OFF + (c * kTok + n * 8 + 2 * t) * 4);
+        if (!each) {
+          const float2 o = lds_f2(st + C::SUM_OFF + ((c - 1) * kTok + n * 8 + 2 * t) * 4);
+          sx[n].x += o.x;
+          sx[n].y += o.y;
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t at = sg * 128 + r128 + 16 * m + 8 * h;
+          const float s = __uint_as_float(lds16(st + C::S_OFF + at * 2) << 16);
+          const float z = p.has_zeros ? (float)(128u + (lds8(st + C::Z_OFF + at) & 127u)) : 136.f;
+#pragma unroll
+          for (int n = 0; n < NTL; ++n) {
+            tot[m][n][2 * h] = fmaf(s, fmaf(-z, sx[n].x, acc[m][n][2 * h]), tot[m][n][2 * h]);
+            tot[m][n][2 * h + 1] =
+                fmaf(s, fmaf(-z, sx[n].y, acc[m][n][2 * h + 1]), tot[m][n][2 * h + 1]);
+            acc[m][n][2 * h] = acc[m][n][2 * h + 1] = 0.f;
+          }
+        }
+    }
+  }
+}
+
+template <int NTL>
+__device__ __forceinline__ void step_bf16(float (&tot)[2][2][4], uint32_t st, int rg, int kw,
+                                          int g, int t) {
+  using C = Cfg<false>;
+  const int row0 = rg * 32 + g;
+  uint4 w[2][2], x[NTL];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = row0 + 16 * m + 8 * h;
+      w[m][h] = lds128(st + row * 128 + (((4 * kw + t) ^ (row & 7)) << 4));
+    }
+#pragma unroll
+  for (int n = 0; n < NTL; ++n)
+    x[n] = lds128(st + C::X_OFF + n * 1024 + g * 128 + (((4 * kw + t) ^ g) << 4));
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int n = 0; n < NTL; ++n) {
+      mma16816(tot[m][n], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, x[n].x, x[n].y);
+      mma16816(tot[m][n], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, x[n].z, x[n].w);
+    }
+}
+
+// The unit u of a group: token tiles fastest, so that those of the same weights follow each
+// other and find them in L2.
+struct Unit {
+  int g, slab, tok0, ntok;                       // first token within the group, tokens
+};
+
+template <bool W4, bool SWIGLU>
+__global__ void __launch_bounds__(Cfg<W4>::THREADS, 1)
+product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                   const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmZ,
+                   const FewProduct p) {
+  using C = Cfg<W4>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  float* tile = reinterpret_cast<float*>(smem_raw + (base - raw) + C::STAGES * C::STAGE);
+  uint8_t* ctrl = reinterpret_cast<uint8_t*>(tile) + kTileBytes;
+  const uint32_t ctrl_u = base + C::STAGES * C::STAGE + kTileBytes;
+  const uint32_t bar_full = ctrl_u, bar_ready = ctrl_u + 64, bar_empty = ctrl_u + 128;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 192);
+  volatile int* s_last = reinterpret_cast<volatile int*>(ctrl + 196);
+  int* prefix = reinterpret_cast<int*>(ctrl + 256);        // [kMaxGroups + 1] units
+  int* s_off = reinterpret_cast<int*>(ctrl + 1536);        // [kMaxGroups]
+  int* s_cnt = reinterpret_cast<int*>(ctrl + 2688);        // [kMaxGroups]
+  int* tmp = reinterpret_cast<int*>(ctrl + 3840);          // [33]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int slabs = p.slabs;
+  for (int g = tid; g < p.G; g += C::THREADS) {
+    int c = (int)p.rows, o = 0;
+    if (p.counts) {
+      c = p.counts[g];
+      o = p.offsets[g];
+      if (c < 0 || o < 0 || (int64_t)o + c > p.rows) {
+        if (blockIdx.x == 0) record_status(p.status, MOE_ERR_DEVICE_CHECK);
+        c = 0;
+      }
+    }
+    s_cnt[g] = c;
+    s_off[g] = o;
+    prefix[g] = (c + kTok - 1) / kTok * slabs;
+  }
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < C::STAGES; ++s) {
+      ptx::mbar_init(bar_full + 8 * s, 1);
+      ptx::mbar_init(bar_ready + 8 * s, C::HELPERS > 0 ? C::HELPERS : 1);
+      ptx::mbar_init(bar_empty + 8 * s, kConsumers);
+    }
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  const int units = block_exclusive_scan(prefix, p.G, tmp);
+  if (tid == 0) prefix[p.G] = units;
+  __syncthreads();
+  // an even share of all steps, not under kFewLeast of them where there are few
+  const int64_t KC = p.steps, total = KC * units;
+  int64_t nb64 = total / kFewLeast;
+  if (nb64 < 1) nb64 = 1;
+  const int nb = nb64 < gridDim.x ? (int)nb64 : (int)gridDim.x;
+  if (total == 0 || (int)blockIdx.x >= nb) return;
+  auto first_of = [&](int b) { return total * b / nb; };
+  const int64_t begin = first_of(blockIdx.x), end = first_of(blockIdx.x + 1);
+  auto unit_at = [&](int u) {
+    Unit v;
+    v.g = gg::find_group(prefix, p.G, u);
+    const int local = u - prefix[v.g], cnt = s_cnt[v.g], tiles = (cnt + kTok - 1) / kTok;
+    v.slab = local / tiles;
+    v.tok0 = local % tiles * kTok;
+    v.ntok = min(kTok, cnt - v.tok0);
+    return v;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, issued = 0, issued_phase = 0;
+      bool ok = true;
+      for (int64_t at = begin; at < end && ok;) {
+        const int u = (int)(at / KC);
+        const int k0 = (int)(at - u * KC);
+        const int n = (int)min(KC - k0, end - at);
+        at += n;
+        const Unit v = unit_at(u);
+        const int ntl = (v.ntok + 7) >> 3;
+        const int row = s_off[v.g] + v.tok0;
+        // the slab's two halves of 128 rows: gate and up, or one behind the other
+        const int ra = v.slab * (SWIGLU ? 128 : 256), rb = SWIGLU ? p.F + ra : ra + 128;
+        const uint32_t bytes = kSlab * 128 + ntl * C::XBOXES * 1024 +
+                               (W4 ? p.groups_per_step * (p.has_zeros ? 768 : 512) : 0);
+        for (int k = k0; k < k0 + n; ++k) {
+          if (!ptx::mbar_wait(bar_empty + 8 * stage, phase ^ 1u, kWaitBudget, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = bar_full + 8 * stage, st = base + stage * C::STAGE;
+          ptx::mbar_arrive_expect_tx(fb, bytes);
+          const int kw = k * (W4 ? 128 : 64);            // in elements of the weights' map
+          ptx::tma_load_3d(st, &tmW, fb, kw, ra, v.g);
+          ptx::tma_load_3d(st + 128 * 128, &tmW, fb, kw, rb, v.g);
+          for (int i = 0; i < ntl; ++i)
+            for (int b = 0; b < C::XBOXES; ++b)
+              ptx::tma_load_2d(st + C::X_OFF + (i * C::XBOXES + b) * 1024, &tmX, fb,
+                               k * C::STEP + b * 64, row + 8 * i);
+          if (W4) {
+            const int gps = p.groups_per_step;
+            ptx::tma_load_3d(st + C::S_OFF, &tmS, fb, ra, k * gps, v.g);
+            ptx::tma_load_3d(st + C::S_OFF + gps * 256, &tmS, fb, rb, k * gps, v.g);
+            if (p.has_zeros) {
+              ptx::tma_load_3d(st + C::Z_OFF, &tmZ, fb, ra, k * gps, v.g);
+              ptx::tma_load_3d(st + C::Z_OFF + gps * 128, &tmZ, fb, rb, k * gps, v.g);
+            }
+          }
+          issued |= 1u << stage;
+          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        record_status(p.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // every load issued must land before the CTA may exit
+      for (int s = 0; s < C::STAGES; ++s)
+        if (issued & (1u << s))
+          ptx::mbar_wait(bar_full + 8 * s, (issued_phase >> s) & 1u, kWaitBudget, nullptr);
+    }
+    return;
+  }
+  if (W4 && warp <= C::HELPERS) {
+    // the tokens' elements in pairs (i, i + 4) of each eight, as the codes unpack, the 16-byte
+    // pieces of odd tokens four places on (so that two tokens' pieces are in all banks), and
+    // their sums over each 32
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int64_t at = begin; at < end && ok;) {
+      const int u = (int)(at / KC);
+      const int n = (int)min(KC - (at - u * KC), end - at);
+      at += n;
+      const int ntok = (unit_at(u).ntok + 7) & ~7;
+      for (int k = 0; k < n && ok; ++k) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget,
+                                                    abort_flag));
+        if (!ok) break;
+        const uint32_t st = base + stage * C::STAGE;
+        for (int tok = warp - 1; tok < ntok; tok += C::HELPERS) {
+          const uint32_t r = st + C::X_OFF + ((tok >> 3) * C::XBOXES + (lane >> 3)) * 1024 +
+                             (tok & 7) * 128;
+          const uint4 v = lds128(r + (((lane & 7) ^ (tok & 7)) << 4));
+          float f[8];
+          unpack8(v, f);
+          float s = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+          s += __shfl_xor_sync(0xffffffffu, s, 1);
+          s += __shfl_xor_sync(0xffffffffu, s, 2);
+          if ((lane & 3) == 0)
+            asm volatile("st.shared.f32 [%0], %1;"
+                         :: "r"(st + C::SUM_OFF + ((lane >> 2) * kTok + tok) * 4), "f"(s)
+                         : "memory");
+          __syncwarp();
+          sts128(r + (((lane & 7) ^ ((tok & 1) << 2)) << 4),
+                 make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                            __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)));
+        }
+        ptx::fence_proxy_async_smem();           // TMA writes here next
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar_ready + 8 * stage);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      record_status(p.status, MOE_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------- consumers
+  const int cw = warp - 1 - C::HELPERS, ctid = tid - 32 * (1 + C::HELPERS);
+  const int rg = cw >> 1, kw = cw & 1, g = lane >> 2, t = lane & 3;
+  constexpr int CT = 32 * kConsumers;
+  auto sync = [] { asm volatile("bar.sync 1, %0;" :: "n"(CT) : "memory"); };
+  uint32_t stage = 0, phase = 0;
+  bool ok = true;
+  for (int64_t at = begin; at < end;) {
+    const int u = (int)(at / KC);
+    const int k0 = (int)(at - u * KC);
+    const int n = (int)min(KC - k0, end - at);
+    at += n;
+    const Unit v = unit_at(u);
+    const bool two = v.ntok > 8;
+    float tot[2][2][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tot[m][j][i] = 0.f;
+    // (after a wait that ran out the pieces go on without their sums, so that the parts' counters
+    // come out as in any other launch)
+    for (int k = 0; k < n && ok; ++k) {
+      ok = ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget, abort_flag);
+      if (W4) ok = ok && ptx::mbar_wait(bar_ready + 8 * stage, phase, kWaitBudget, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        if (lane == 0) {
+          record_status(p.status, MOE_ERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+        break;
+      }
+      const uint32_t st = base + stage * C::STAGE;
+      if constexpr (W4) {
+        if (two) step_int4<2>(tot, st, p, rg, kw, g, t);
+        else step_int4<1>(tot, st, p, rg, kw, g, t);
+      } else {
+        if (two) step_bf16<2>(tot, st, rg, kw, g, t);
+        else step_bf16<1>(tot, st, rg, kw, g, t);
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar_empty + 8 * stage);
+      if (++stage == C::STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    // the two halves of K, then 256 rows x the unit's tokens in shared memory
+    auto at_tile = [&](int m, int j, int i) -> float& {
+      return tile[(rg * 32 + 16 * m + 8 * (i >> 1) + g) * kTileLd + 8 * j + 2 * t + (i & 1)];
+    };
+    sync();                                        // the tile's last readers are done
+    if (kw == 0) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) at_tile(m, j, i) = tot[m][j][i];
+    }
+    sync();
+    if (kw == 1) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) at_tile(m, j, i) += tot[m][j][i];
+    }
+    sync();
+    if (n < KC) {
+      // CTAs lo .. hi share the unit, each with one part: the first the one that it leaves
+      // unfinished, the others the one that they begin with
+      const int64_t s0 = u * KC, s1 = s0 + KC - 1;
+      auto cta_of = [&](int64_t s) {
+        int b = (int)(s * nb / total);
+        while (b > 0 && first_of(b) > s) --b;
+        while (first_of(b + 1) <= s) ++b;
+        return b;
+      };
+      const int lo = cta_of(s0), hi = cta_of(s1);
+      auto part = [&](int b) { return p.parts + ((int64_t)2 * b + (b == lo)) * (kSlab * kTok); };
+      float* mine = part(blockIdx.x);
+      for (int e = ctid; e < kSlab * v.ntok; e += CT)
+        __stcg(mine + e, tile[(e & (kSlab - 1)) * kTileLd + (e / kSlab)]);
+      __threadfence();
+      sync();
+      if (ctid == 0) *s_last = ptx::atom_add_acq_rel(p.arrived + lo, 1u) == (uint32_t)(hi - lo);
+      sync();
+      if (!*s_last) continue;
+      for (int e = ctid; e < kSlab * v.ntok; e += CT) {
+        float a = 0.f;
+        for (int b = lo; b <= hi; ++b) a += __ldcg(part(b) + e);
+        tile[(e & (kSlab - 1)) * kTileLd + (e / kSlab)] = a;
+      }
+      if (ctid == 0) p.arrived[lo] = 0u;           // as the next launch expects it
+      sync();
+    }
+    // two neighbouring columns a thread
+    constexpr int COLS = SWIGLU ? kSlab / 2 : kSlab;
+    const int n0 = v.slab * COLS, N = SWIGLU ? p.F : p.N;
+    for (int e = ctid; e < COLS / 2 * v.ntok; e += CT) {
+      const int c = e % (COLS / 2) * 2, tok = e / (COLS / 2);
+      if (n0 + c >= N) continue;
+      const int64_t row = s_off[v.g] + v.tok0 + tok;
+      float a = tile[c * kTileLd + tok], b = tile[(c + 1) * kTileLd + tok];
+      if (SWIGLU) {
+        a = gg::silu_f(a) * tile[(c + 128) * kTileLd + tok];
+        b = gg::silu_f(b) * tile[(c + 129) * kTileLd + tok];
+      }
+      if (p.add) {
+        const uint32_t d = *reinterpret_cast<const uint32_t*>(p.add + row * p.ldadd + n0 + c);
+        a += bf16_lo(d);
+        b += bf16_hi(d);
+      }
+      *reinterpret_cast<uint32_t*>(p.out + row * p.ldo + n0 + c) = pack_bf16x2(a, b);
+    }
+  }
+}
+
+// The bf16 weights that codes stand for: a warp takes a row, a lane eight consecutive codes at a
+// time; the rows of a CTA follow each other, so a line of scales serves all of them.
+__global__ void __launch_bounds__(256)
+int4_dequantize_kernel(const uint32_t* __restrict__ codes, const uint16_t* __restrict__ scales,
+                       const uint8_t* __restrict__ zeros, int64_t rows, int N, int K, int group,
+                       uint4* __restrict__ out) {
+  const int lane = threadIdx.x & 31, words = K >> 3, kg = K / group;
+  for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows;
+       row += (int64_t)gridDim.x * 8) {
+    const int64_t e = row / N;
+    const int64_t sbase = e * kg * N + (row - e * N);
+    for (int w = lane; w < words; w += 32) {
+      const uint32_t q = __ldg(codes + row * words + w);
+      const int64_t at = sbase + (int64_t)(8 * w / group) * N;
+      const float s = __uint_as_float((uint32_t)__ldg(scales + at) << 16);
+      const int z = zeros ? (__ldg(zeros + at) & 127) : 8;
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = (float)((int)((q >> (4 * i)) & 15u) - z) * s;
+      out[row * words + w] = pack8(f);
+    }
+  }
+}
+
+bool make_map3(CUtensorMap* m, CUtensorMapDataType type, int bytes, const void* ptr, uint64_t d0,
+               uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1, bool swizzle) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {d0, d1, d2};
+  cuuint64_t strides[2] = {d0 * bytes, d0 * d1 * bytes};
+  cuuint32_t box[3] = {b0, b1, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, type, 3, const_cast<void*>(ptr), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_rows_map(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t ld) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {ld * 2};
+  cuuint32_t box[2] = {64, 8};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool W4, bool SWIGLU>
+cudaError_t run_few(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& s,
+                    const CUtensorMap& z, const FewProduct& p, cudaStream_t stream) {
+  auto kern = product_few_kernel<W4, SWIGLU>;
+  static PerDevice set;
+  const cudaError_t e = set_smem_once(set, kern, Cfg<W4>::SMEM);
+  if (e != cudaSuccess) return e;
+  const int n = num_sms();
+  kern<<<n < kFewCtas ? n : kFewCtas, Cfg<W4>::THREADS, Cfg<W4>::SMEM, stream>>>(w, x, s, z, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_int4_dequantize(const void* codes, const void* scales, const void* zeros, int G,
+                                   int N, int K, int group, void* out, cudaStream_t s) {
+  const int64_t rows = (int64_t)G * N, blocks = (rows + 7) / 8;
+  const int64_t most = (int64_t)num_sms() * 8;
+  int4_dequantize_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, s>>>(
+      static_cast<const uint32_t*>(codes), static_cast<const uint16_t*>(scales),
+      static_cast<const uint8_t*>(zeros), rows, N, K, group, static_cast<uint4*>(out));
+  return cudaGetLastError();
+}
+
+static_assert(kFewPart == kSlab * kTok, "parts as the kernel writes them");
+
+// Units of 16 tokens and 256 weight rows that the kernel's 32-bit numbers hold.
+bool few_fits(int64_t rows, int G, int64_t N) {
+  return (rows / kTok + G + 1) * ((N + 127) / 128) < (1LL << 31);
+}
+
+cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const void* w,
+                               const void* scales, const void* zeros, bool swiglu,
+                               cudaStream_t s) {
+  const bool w4 = scales != nullptr;
+  const int64_t cols = swiglu ? p.N / 2 : p.N;
+  p.F = (int)(p.N / 2);
+  p.slabs = (int)((cols + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256));
+  p.steps = (p.K + (w4 ? 255 : 63)) / (w4 ? 256 : 64);
+  p.has_zeros = zeros != nullptr;
+  p.groups_per_step = w4 ? 256 / p.group : 0;
+  CUtensorMap tw, tx, ts, tz;
+  if (!make_rows_map(&tx, x, p.K, p.rows, ldx)) return cudaErrorInvalidValue;
+  if (w4) {
+    const uint64_t kg = p.K / p.group;
+    if (!make_map3(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, p.K / 2, p.N, p.G, 128, 128, true) ||
+        !make_map3(&ts, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, scales, p.N, kg, p.G, 128,
+                   p.groups_per_step, false))
+      return cudaErrorInvalidValue;
+    tz = ts;
+    if (zeros && !make_map3(&tz, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, zeros, p.N, kg, p.G, 128,
+                            p.groups_per_step, false))
+      return cudaErrorInvalidValue;
+    return swiglu ? run_few<true, true>(tw, tx, ts, tz, p, s)
+                  : run_few<true, false>(tw, tx, ts, tz, p, s);
+  }
+  if (!make_map3(&tw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w, p.K, p.N, p.G, 64, 128, true))
+    return cudaErrorInvalidValue;
+  return run_few<false, false>(tw, tx, tw, tw, p, s);
+}
+
+}  // namespace moe

@@ -48,6 +48,53 @@ moe_status check_norm(int64_t T, int64_t H, const void* gamma, int32_t gamma_dty
   return MOE_OK;
 }
 
+// Scratch of a product: the status word, the parts' counters, the parts.
+constexpr int64_t kArrivedOffset = 1024;
+constexpr int64_t kPartsOffset = 4096;
+constexpr int64_t kProductScratch = kPartsOffset + 2LL * kFewCtas * kFewPart * 4;
+static_assert(kArrivedOffset + kFewCtas * 4 <= kPartsOffset, "counters before the parts");
+
+moe_status check_segments(int64_t groups, int64_t rows, const int32_t* counts,
+                          const int32_t* offsets) {
+  OP_REQUIRE(groups >= 1 && rows >= 0 && rows <= INT_MAX);
+  if (groups > kMaxGroups) return MOE_ERR_UNSUPPORTED;
+  if (counts || offsets) OP_REQUIRE(al4(counts) && al4(offsets));
+  else OP_REQUIRE(groups == 1);
+  return MOE_OK;
+}
+
+// Sizes that the maps' and kernels' 32-bit numbers hold.
+bool matrix_ok(int64_t N, int64_t K, int unit) {
+  return N >= unit && K >= unit && N % unit == 0 && K % unit == 0 && N <= (1 << 24) &&
+         K <= (1 << 24);
+}
+
+moe_status check_int4(const moe_int4_tensor* w) {
+  OP_REQUIRE(w && (w->group == 32 || w->group == 64 || w->group == 128));
+  OP_REQUIRE(w->groups >= 1 && w->groups <= INT_MAX);
+  OP_REQUIRE(matrix_ok(w->N, w->K, 16) && w->K % w->group == 0);
+  OP_REQUIRE(al16(w->codes) && al16(w->scales) && al16_or_null(w->zeros));
+  return MOE_OK;
+}
+
+FewProduct few_product(int64_t groups, int64_t rows, int64_t N, int64_t K, const int32_t* counts,
+                       const int32_t* offsets, void* out, int64_t ldo, void* scratch) {
+  uint8_t* sc = static_cast<uint8_t*>(scratch);
+  FewProduct p{};
+  p.G = (int)groups;
+  p.rows = rows;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.counts = counts;
+  p.offsets = offsets;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.ldo = ldo;
+  p.parts = reinterpret_cast<float*>(sc + kPartsOffset);
+  p.arrived = reinterpret_cast<uint32_t*>(sc + kArrivedOffset);
+  p.status = reinterpret_cast<int32_t*>(sc);
+  return p;
+}
+
 const __nv_bfloat16* bf(const void* p) { return static_cast<const __nv_bfloat16*>(p); }
 __nv_bfloat16* bf(void* p) { return static_cast<__nv_bfloat16*>(p); }
 
@@ -121,6 +168,37 @@ moe_status moe_permute_fp8(const moe_config* cfg, const void* codes, const void*
                              token_of, sel_offsets, sel_tokens, static_cast<uint8_t*>(codes_perm),
                              static_cast<uint8_t*>(scales_perm), static_cast<uint8_t*>(scratch),
                              (cudaStream_t)stream));
+  return MOE_OK;
+}
+
+moe_status moe_product_scratch_bytes(int64_t* bytes) {
+  OP_REQUIRE(bytes);
+  *bytes = kProductScratch;
+  return MOE_OK;
+}
+
+moe_status moe_int4_grouped_gemm(const moe_int4_tensor* w, int64_t rows, const void* x, int64_t ldx,
+                                 const int32_t* counts, const int32_t* offsets, int32_t swiglu,
+                                 void* out, int64_t ldo, void* scratch, void* stream) {
+  OP_TRY(check_int4(w));
+  OP_TRY(check_segments(w->groups, rows, counts, offsets));
+  OP_REQUIRE(swiglu == 0 || (swiglu == 1 && w->N % 32 == 0));
+  OP_REQUIRE(al16(scratch));
+  if (!few_fits(rows, (int)w->groups, w->N)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  OP_REQUIRE(rows_ok(x, ldx, w->K) && rows_ok(out, ldo, swiglu ? w->N / 2 : w->N));
+  FewProduct p = few_product(w->groups, rows, w->N, w->K, counts, offsets, out, ldo, scratch);
+  p.group = w->group;
+  OP_CUDA(launch_product_few(p, x, ldx, w->codes, w->scales, w->zeros, swiglu != 0,
+                             (cudaStream_t)stream));
+  return MOE_OK;
+}
+
+moe_status moe_int4_dequantize(const moe_int4_tensor* w, void* out, void* stream) {
+  OP_TRY(check_int4(w));
+  OP_REQUIRE(al16(out) && w->groups <= kMaxGroups);
+  OP_CUDA(launch_int4_dequantize(w->codes, w->scales, w->zeros, (int)w->groups, (int)w->N,
+                                 (int)w->K, w->group, out, (cudaStream_t)stream));
   return MOE_OK;
 }
 

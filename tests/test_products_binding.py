@@ -113,3 +113,40 @@ def test_permute_fp8_refuses_what_does_not_fit():
     refused(B.moe_permute_fp8, args, cfg=bf)
     bf.dtype, bf.stash_pool_pages = 1, 4
     refused(B.moe_permute_fp8, args, cfg=bf)
+
+
+def int4(G, N, K, group, zeros=True):
+    return B.Int4Tensor(gpu(G, N, K // 2, dtype=U8), gpu(G, K // group, N),
+                        gpu(G, K // group, N, dtype=U8) if zeros else None)
+
+
+def test_int4_tensor_refuses_what_does_not_fit():
+    c, s, z = gpu(2, 32, 64, dtype=U8), gpu(2, 4, 32), gpu(2, 4, 32, dtype=U8)
+    B.Int4Tensor(c, s, z)
+    for bad in ((c.to(I32), s, z), (c[:, :, ::2], s, z), (c[0], s, z), (c, s.float(), z), (c, s[:1], z),
+                (c, s[:, :, :16], z), (c, gpu(2, 3, 32), z), (c, s, z.to(I32)), (c, s, z[:1]),
+                (torch.zeros(2, 32, 64, dtype=U8), s, z), (c, torch.zeros(2, 4, 32, dtype=BF), z)):
+        with pytest.raises(ValueError):
+            B.Int4Tensor(*bad)
+
+
+def test_int4_calls_refuse_what_does_not_fit():
+    args = dict(x=gpu(9, 128), w=int4(2, 32, 128, 32), counts=gpu(2, dtype=I32), offsets=gpu(2, dtype=I32),
+                out=gpu(9, 32), scratch=gpu(B.product_scratch_bytes(), dtype=U8))
+    for name in ("x", "counts", "offsets", "out", "scratch"):
+        for bad in wrong(args[name]):
+            if name == "scratch" and bad.element_size() == 8:
+                continue                                   # (it has no type of its own)
+            refused(B.moe_int4_grouped_gemm, args, **{name: bad})
+    refused(B.moe_int4_grouped_gemm, args, counts=None)
+    refused(B.moe_int4_grouped_gemm, args, counts=None, offsets=None)     # two groups
+    refused(B.moe_int4_grouped_gemm, args, swiglu=True)                   # out is [9, 16] then
+    refused(B.moe_int4_grouped_gemm, args, w=int4(2, 32, 128, 16))
+    refused(B.moe_int4_grouped_gemm, {**args, "out": gpu(9, 40)}, w=int4(2, 40, 128, 32))
+    refused(B.moe_int4_grouped_gemm, {**args, "out": gpu(9, 24)}, w=int4(2, 48, 128, 32), swiglu=True)
+    refused(B.moe_int4_dequantize, dict(w=args["w"], out=gpu(2, 32, 120)))
+    refused(B.moe_int4_dequantize, dict(w=args["w"], out=gpu(2, 32, 128, dtype=F32)))
+    many = dict(args, w=int4(261, 32, 128, 32), counts=gpu(261, dtype=I32), offsets=gpu(261, dtype=I32))
+    with pytest.raises(B.MoEError) as e:
+        B.moe_int4_grouped_gemm(**many, stream=0)
+    assert e.value.code == 2
