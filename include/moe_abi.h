@@ -773,6 +773,32 @@ MOE_API moe_status moe_int4_grouped_gemm(const moe_int4_tensor* w, int64_t rows,
 /* The weights as bf16 (one rounding): out [groups, N, K]. */
 MOE_API moe_status moe_int4_dequantize(const moe_int4_tensor* w, void* out, void* stream);
 
+/* Products with bf16 weights w [groups, N, K] (N, K multiples of 8), for experts of
+ * any form, adapters among them:
+ *   moe_grouped_gemm:        out[r, n] = bf16(sum_k x[r, k] w[g, n, k] + add[r, n]),
+ *   moe_grouped_gemm_dgrad:  dx[r, k]  = bf16(sum_n dy[r, n] w[g, n, k] + add[r, k]),
+ *   moe_grouped_gemm_wgrad:  dw[g, n, k] = bf16(sum over g's rows of dy[r, n] x[r, k])
+ *                            (zeros for a group without rows; every element written).
+ * add: bf16 rows of the output's shape, or NULL; it may be out itself.
+ * expected_rows: the most rows that the caller expects a group to have (tokens
+ * of a decoding step), a hint that chooses between the kernel that streams the
+ * weights and the one with tiles of 128 rows; 0: not known. */
+MOE_API moe_status moe_grouped_gemm(int64_t groups, int64_t rows, int64_t N, int64_t K,
+                                    const void* x, int64_t ldx, const void* w,
+                                    const int32_t* counts, const int32_t* offsets,
+                                    const void* add, int64_t ldadd, void* out, int64_t ldo,
+                                    int64_t expected_rows, void* scratch, void* stream);
+MOE_API moe_status moe_grouped_gemm_dgrad(int64_t groups, int64_t rows, int64_t N, int64_t K,
+                                          const void* dy, int64_t lddy, const void* w,
+                                          const int32_t* counts, const int32_t* offsets,
+                                          const void* add, int64_t ldadd, void* dx, int64_t lddx,
+                                          void* scratch, void* stream);
+MOE_API moe_status moe_grouped_gemm_wgrad(int64_t groups, int64_t rows, int64_t N, int64_t K,
+                                          const void* dy, int64_t lddy, const void* x,
+                                          int64_t ldx, const int32_t* counts,
+                                          const int32_t* offsets, void* dw, void* scratch,
+                                          void* stream);
+
 /* Synchronises `stream`, then copies the device status word from scratch to
  * *code (0 = no problem recorded). */
 MOE_API moe_status moe_last_device_status(const void* scratch, int32_t* code, void* stream);

@@ -33,6 +33,7 @@ ENTRY_POINTS = (
     "moe_fp4_grouped_gemm", "moe_fp4_ffn_fwd", "moe_fp4_ffn_bwd",
     "moe_rmsnorm_fwd", "moe_rmsnorm_bwd", "moe_rmsnorm_scratch_bytes", "moe_permute_fp8",
     "moe_product_scratch_bytes", "moe_int4_grouped_gemm", "moe_int4_dequantize",
+    "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad",
     "moe_last_device_status",
     "moe_clear_device_status", "moe_check_bounded_wait", "moe_status_string",
 )
@@ -587,6 +588,9 @@ _PRODUCT_ARGS = {
     "moe_product_scratch_bytes": [ctypes.POINTER(_I64)],
     "moe_int4_grouped_gemm": [ctypes.POINTER(MoEInt4Tensor), _I64, _P, _I64, _P, _P, _I32, _P, _I64, _P, _P],
     "moe_int4_dequantize": [ctypes.POINTER(MoEInt4Tensor), _P, _P],
+    "moe_grouped_gemm": [_I64] * 4 + [_P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _I64, _P, _P],
+    "moe_grouped_gemm_dgrad": [_I64] * 4 + [_P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P, _P],
+    "moe_grouped_gemm_wgrad": [_I64] * 4 + [_P, _I64, _P, _I64, _P, _P, _P, _P, _P],
     "moe_rmsnorm_fwd": [_I64, _I64, _P, _I64, _P, _I64, _P, _I32, ctypes.c_float, _P, _I64, _P, _I64,
                         _P, _P, _I32, _P, _P],
     "moe_rmsnorm_bwd": [_I64, _I64, _P, _I64, _P, _I64, _P, _P, _I32, _P, _I64, _P, _I64, _P, _P, _P],
@@ -789,6 +793,60 @@ def moe_int4_dequantize(w: Int4Tensor, out, stream=None):
             not out.is_contiguous() or not out.is_cuda:
         raise ValueError("out is contiguous bf16 [groups, N, K], on the GPU")
     _check("moe_int4_dequantize", lib().moe_int4_dequantize(s, out.data_ptr(), _stream(stream)))
+
+
+def _matrices(w, what: str):
+    """Address and sizes of contiguous bf16 [groups, N, K]."""
+    if w.dim() != 3 or w.dtype is not torch.bfloat16 or not w.is_contiguous() or not w.is_cuda:
+        raise ValueError(f"{what} is contiguous bf16 [groups, N, K], on the GPU")
+    return (w.data_ptr(), *w.shape)
+
+
+def moe_grouped_gemm(x, w, counts, offsets, out, scratch, add=None, expected_rows: int = 0,
+                     stream=None):
+    """out [rows, N] = every group's rows of x [rows, K] by w [groups, N, K] (+ add). counts,
+    offsets: int32 [groups], or None for one group of all rows; expected_rows: the most rows of
+    a group that the caller expects, 0 where it does not know."""
+    pw, G, N, K = _matrices(w, "w")
+    rows = x.shape[0]
+    _here(x, w, counts, offsets, out, scratch, add)
+    px, ldx = _strided(x, rows, K, "x")
+    po, ldo = _strided(out, rows, N, "out")
+    pa, lda = _strided(add, rows, N, "add")
+    pc, pf = _segments(counts, offsets, G)
+    _check("moe_grouped_gemm",
+           lib().moe_grouped_gemm(G, rows, N, K, px, ldx, pw, pc, pf, pa, lda, po, ldo,
+                                  expected_rows, _scratch(scratch, product_scratch_bytes()),
+                                  _stream(stream)))
+
+
+def moe_grouped_gemm_dgrad(dy, w, counts, offsets, dx, scratch, add=None, stream=None):
+    """dx [rows, K] = every group's rows of dy [rows, N] times w [groups, N, K] (+ add)."""
+    pw, G, N, K = _matrices(w, "w")
+    rows = dy.shape[0]
+    _here(dy, w, counts, offsets, dx, scratch, add)
+    py, ldy = _strided(dy, rows, N, "dy")
+    px, ldx = _strided(dx, rows, K, "dx")
+    pa, lda = _strided(add, rows, K, "add")
+    pc, pf = _segments(counts, offsets, G)
+    _check("moe_grouped_gemm_dgrad",
+           lib().moe_grouped_gemm_dgrad(G, rows, N, K, py, ldy, pw, pc, pf, pa, lda, px, ldx,
+                                        _scratch(scratch, product_scratch_bytes()),
+                                        _stream(stream)))
+
+
+def moe_grouped_gemm_wgrad(dy, x, counts, offsets, dw, scratch, stream=None):
+    """dw [groups, N, K] = the sum over every group's rows of dy [rows, N] by x [rows, K]."""
+    pw, G, N, K = _matrices(dw, "dw")
+    rows = dy.shape[0]
+    _here(dy, x, counts, offsets, dw, scratch)
+    py, ldy = _strided(dy, rows, N, "dy")
+    px, ldx = _strided(x, rows, K, "x")
+    pc, pf = _segments(counts, offsets, G)
+    _check("moe_grouped_gemm_wgrad",
+           lib().moe_grouped_gemm_wgrad(G, rows, N, K, py, ldy, px, ldx, pc, pf, pw,
+                                        _scratch(scratch, product_scratch_bytes()),
+                                        _stream(stream)))
 
 
 @functools.lru_cache(maxsize=64)

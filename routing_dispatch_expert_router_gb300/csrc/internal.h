@@ -340,7 +340,8 @@ struct FewProduct {
 };
 constexpr int kFewCtas = 256;
 constexpr int kFewPart = 256 * 16;
-constexpr int kFewLeast = 4;
+constexpr int kFewLeast = 4;  // steps of K a CTA takes at least
+constexpr int kFewRows = 64;  // rows a group up to which bf16 weights are streamed
 bool few_fits(int64_t rows, int G, int64_t N);
 cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const void* w,
                                const void* scales, const void* zeros, bool swiglu, cudaStream_t s);
@@ -348,6 +349,29 @@ cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const v
 // The bf16 weights that 4-bit codes stand for: out [G, N, K].
 cudaError_t launch_int4_dequantize(const void* codes, const void* scales, const void* zeros, int G,
                                    int N, int K, int group, void* out, cudaStream_t s);
+
+// Grouped products of ragged rows (grouped_gemm_ragged.cu): W [G, N, K] bf16; forward
+// [rows, K] -> [rows, N], data gradient [rows, N] -> [rows, K] (both + add, or null), weight
+// gradient -> [G, N, K] (zeros for an empty group).
+struct RaggedProduct {
+  int G;
+  int64_t rows;
+  const int32_t* counts;      // null: one group of all rows
+  const int32_t* offsets;
+  const __nv_bfloat16* add;
+  int64_t ldadd;
+  __nv_bfloat16* out;
+  int64_t ldo;
+  int32_t* status;
+  // set by the launchers: the output's columns, the length reduced over (not the weight
+  // gradient's), the weight gradient's output rows
+  int cols, red, out_rows;
+};
+bool ragged_fits(int64_t rows, int G, int64_t cols, int64_t out_rows);
+cudaError_t launch_ragged_gemm(RaggedProduct p, int dgrad, const void* x, int64_t ldx,
+                               const void* w, int N, int K, cudaStream_t s);
+cudaError_t launch_ragged_wgrad(RaggedProduct p, const void* dy, int64_t lddy, const void* x,
+                                int64_t ldx, int N, int K, cudaStream_t s);
 
 // Router logits for E % 128 == 0 on the tensor cores (W3 = W_r split in three bf16 parts).
 cudaError_t launch_router_logits_tc(const moe_config& c, const void* x, const void* W3,

@@ -95,6 +95,29 @@ FewProduct few_product(int64_t groups, int64_t rows, int64_t N, int64_t K, const
   return p;
 }
 
+moe_status check_product(int64_t groups, int64_t rows, int64_t N, int64_t K, const void* w,
+                         const int32_t* counts, const int32_t* offsets, const void* scratch) {
+  OP_TRY(check_segments(groups, rows, counts, offsets));
+  OP_REQUIRE(matrix_ok(N, K, 8) && al16(w) && al16(scratch));
+  return MOE_OK;
+}
+
+RaggedProduct ragged_product(int64_t groups, int64_t rows, const int32_t* counts,
+                             const int32_t* offsets, const void* add, int64_t ldadd, void* out,
+                             int64_t ldo, void* scratch) {
+  RaggedProduct p{};
+  p.G = (int)groups;
+  p.rows = rows;
+  p.counts = counts;
+  p.offsets = offsets;
+  p.add = static_cast<const __nv_bfloat16*>(add);
+  p.ldadd = ldadd;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.ldo = ldo;
+  p.status = static_cast<int32_t*>(scratch);
+  return p;
+}
+
 const __nv_bfloat16* bf(const void* p) { return static_cast<const __nv_bfloat16*>(p); }
 __nv_bfloat16* bf(void* p) { return static_cast<__nv_bfloat16*>(p); }
 
@@ -199,6 +222,57 @@ moe_status moe_int4_dequantize(const moe_int4_tensor* w, void* out, void* stream
   OP_REQUIRE(al16(out) && w->groups <= kMaxGroups);
   OP_CUDA(launch_int4_dequantize(w->codes, w->scales, w->zeros, (int)w->groups, (int)w->N,
                                  (int)w->K, w->group, out, (cudaStream_t)stream));
+  return MOE_OK;
+}
+
+moe_status moe_grouped_gemm(int64_t groups, int64_t rows, int64_t N, int64_t K, const void* x,
+                            int64_t ldx, const void* w, const int32_t* counts,
+                            const int32_t* offsets, const void* add, int64_t ldadd, void* out,
+                            int64_t ldo, int64_t expected_rows, void* scratch, void* stream) {
+  OP_TRY(check_product(groups, rows, N, K, w, counts, offsets, scratch));
+  OP_REQUIRE(expected_rows >= 0);
+  if (rows == 0) return MOE_OK;
+  OP_REQUIRE(rows_ok(x, ldx, K) && rows_ok(out, ldo, N) && rows_or_null(add, ldadd, N));
+  const int64_t most = expected_rows > 0 && expected_rows < rows ? expected_rows : rows;
+  if (most <= kFewRows && few_fits(rows, (int)groups, N)) {
+    FewProduct p = few_product(groups, rows, N, K, counts, offsets, out, ldo, scratch);
+    p.add = bf(add);
+    p.ldadd = ldadd;
+    OP_CUDA(launch_product_few(p, x, ldx, w, nullptr, nullptr, false, (cudaStream_t)stream));
+    return MOE_OK;
+  }
+  if (!ragged_fits(rows, (int)groups, N, 0)) return MOE_ERR_UNSUPPORTED;
+  OP_CUDA(launch_ragged_gemm(
+      ragged_product(groups, rows, counts, offsets, add, ldadd, out, ldo, scratch), 0, x, ldx, w,
+      (int)N, (int)K, (cudaStream_t)stream));
+  return MOE_OK;
+}
+
+moe_status moe_grouped_gemm_dgrad(int64_t groups, int64_t rows, int64_t N, int64_t K,
+                                  const void* dy, int64_t lddy, const void* w,
+                                  const int32_t* counts, const int32_t* offsets, const void* add,
+                                  int64_t ldadd, void* dx, int64_t lddx, void* scratch,
+                                  void* stream) {
+  OP_TRY(check_product(groups, rows, N, K, w, counts, offsets, scratch));
+  if (rows == 0) return MOE_OK;
+  OP_REQUIRE(rows_ok(dy, lddy, N) && rows_ok(dx, lddx, K) && rows_or_null(add, ldadd, K));
+  if (!ragged_fits(rows, (int)groups, K, 0)) return MOE_ERR_UNSUPPORTED;
+  OP_CUDA(launch_ragged_gemm(
+      ragged_product(groups, rows, counts, offsets, add, ldadd, dx, lddx, scratch), 1, dy, lddy, w,
+      (int)N, (int)K, (cudaStream_t)stream));
+  return MOE_OK;
+}
+
+moe_status moe_grouped_gemm_wgrad(int64_t groups, int64_t rows, int64_t N, int64_t K,
+                                  const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                  const int32_t* counts, const int32_t* offsets, void* dw,
+                                  void* scratch, void* stream) {
+  OP_TRY(check_product(groups, rows, N, K, dw, counts, offsets, scratch));
+  if (rows > 0) OP_REQUIRE(rows_ok(dy, lddy, N) && rows_ok(x, ldx, K));
+  if (!ragged_fits(rows, (int)groups, K, N)) return MOE_ERR_UNSUPPORTED;
+  OP_CUDA(launch_ragged_wgrad(
+      ragged_product(groups, rows, counts, offsets, nullptr, 0, dw, K, scratch), dy, lddy, x, ldx,
+      (int)N, (int)K, (cudaStream_t)stream));
   return MOE_OK;
 }
 

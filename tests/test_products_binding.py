@@ -150,3 +150,30 @@ def test_int4_calls_refuse_what_does_not_fit():
     with pytest.raises(B.MoEError) as e:
         B.moe_int4_grouped_gemm(**many, stream=0)
     assert e.value.code == 2
+
+
+def test_products_refuse_what_does_not_fit():
+    seg = dict(counts=gpu(2, dtype=I32), offsets=gpu(2, dtype=I32), scratch=gpu(B.product_scratch_bytes(), dtype=U8))
+    w = gpu(2, 32, 64)
+    calls = ((B.moe_grouped_gemm, dict(seg, x=gpu(9, 64), w=w, out=gpu(9, 32), add=gpu(9, 32))),
+             (B.moe_grouped_gemm_dgrad, dict(seg, dy=gpu(9, 32), w=w, dx=gpu(9, 64), add=gpu(9, 64))),
+             (B.moe_grouped_gemm_wgrad, dict(seg, dy=gpu(9, 32), x=gpu(9, 64), dw=gpu(2, 32, 64))))
+    for call, args in calls:
+        for name, t in args.items():
+            for bad in wrong(t):
+                if name == "scratch" and bad.element_size() == 8:
+                    continue                               # (it has no type of its own)
+                refused(call, args, **{name: bad})
+        refused(call, args, counts=None)
+        refused(call, args, counts=None, offsets=None)     # two groups
+        for name in ("w", "dw"):
+            if name in args:
+                refused(call, args, **{name: gpu(2, 64, 32).transpose(1, 2)})
+                refused(call, args, **{name: gpu(32, 64)})
+    refused(calls[0][0], calls[0][1], expected_rows=-1)
+    odd = dict(calls[0][1], x=gpu(9, 68), w=gpu(2, 32, 68))
+    refused(calls[0][0], odd)
+    many = dict(calls[0][1], w=gpu(261, 32, 64), counts=gpu(261, dtype=I32), offsets=gpu(261, dtype=I32))
+    with pytest.raises(B.MoEError) as e:
+        B.moe_grouped_gemm(**many, stream=0)
+    assert e.value.code == 2
