@@ -335,14 +335,14 @@ struct FewProduct {
   uint32_t* arrived;          // [kFewCtas], zero before and after every launch
   int32_t* status;
   // set by the launcher
-  int F, slabs, steps, groups_per_step;
+  int F, slabs, steps, groups_per_step, group_log2;
   bool has_zeros;
 };
 constexpr int kFewCtas = 256;
 constexpr int kFewPart = 256 * 16;
 constexpr int kFewLeast = 4;  // steps of K a CTA takes at least
 constexpr int kFewRows = 64;  // rows a group up to which bf16 weights are streamed
-bool few_fits(int64_t rows, int G, int64_t N);
+bool few_fits(int64_t rows, int G, int64_t N, int64_t K);
 cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const void* w,
                                const void* scales, const void* zeros, bool swiglu, cudaStream_t s);
 

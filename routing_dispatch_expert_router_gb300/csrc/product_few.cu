@@ -8,11 +8,11 @@
 //                  step of the tokens' rows, and the group scales and zero points;
 //   warps 1-3      (4-bit) the tokens' elements in the order in which codes unpack, and their
 //                  sums over 32;
-//   the other 16   mma.sync m16n8k16, the weights as A: a warp has 32 weight rows and half of
-//                  the step's K. Tokens are B, eight to a tile, at most 16 a pass: with few
-//                  tokens tcgen05's 128-row tiles would multiply padding, and its operands
-//                  would have to be written back to shared memory as bf16 first, four times
-//                  the bytes of the codes.
+//   eight warps    mma.sync m16n8k16, the weights as A: a warp has 32 weight rows. Tokens are
+//                  B, eight to a tile, at most 16 a pass: with few tokens tcgen05's 128-row
+//                  tiles would multiply padding, and its operands would have to be written
+//                  back to shared memory as bf16 first, four times the bytes of the codes;
+//   four warps     join units that CTAs share and write results, beside the next unit's sums.
 //
 // 4-bit weights are s (q - z). The codes become bf16 numbers 128 + q by placing their bits in
 // the mantissa (one logic operation for two), whose products with x are exact; the offset and
@@ -35,18 +35,17 @@ using gg::kWaitBudget;
 
 constexpr int kSlab = 256;                     // weight rows of a unit
 constexpr int kTok = 16;                       // tokens of a unit
-constexpr int kRowWarps = kSlab / 32;
-constexpr int kKWarps = 2;
-constexpr int kConsumers = kRowWarps * kKWarps;
+constexpr int kConsumers = kSlab / 32;
+constexpr int kJoiners = 4;                    // warps that write results
 constexpr int kTileLd = kTok + 1;
 constexpr int kTileBytes = kSlab * kTileLd * 4;
-constexpr int kCtrl = 5120;
+constexpr int kCtrl = 4096;
 
 template <bool W4>
 struct Cfg {
-  static constexpr int HELPERS = W4 ? 3 : 0;       // (five warps a scheduler: 96 registers)
-  static constexpr int THREADS = 32 * (1 + HELPERS + kConsumers);
-  static constexpr int STAGES = W4 ? 4 : 6;
+  static constexpr int HELPERS = W4 ? 3 : 0;       // (four warps a scheduler: 128 registers)
+  static constexpr int THREADS = 32 * (1 + HELPERS + kConsumers + kJoiners);
+  static constexpr int STAGES = W4 ? 4 : 5;
   static constexpr int STEP = W4 ? 256 : 64;           // elements of K a stage
   static constexpr int XBOXES = STEP / 64;             // boxes of 64 elements x 8 tokens
   static constexpr int X_OFF = kSlab * 128;
@@ -54,7 +53,7 @@ struct Cfg {
   static constexpr int Z_OFF = S_OFF + (W4 ? 8 * kSlab * 2 : 0);   // eight groups at most
   static constexpr int SUM_OFF = Z_OFF + (W4 ? 8 * kSlab : 0);
   static constexpr int STAGE = (SUM_OFF + (W4 ? 8 * kTok * 4 : 0) + 1023) / 1024 * 1024;
-  static constexpr int SMEM = STAGES * STAGE + kTileBytes + kCtrl + 1024;
+  static constexpr int SMEM = STAGES * STAGE + 2 * kTileBytes + kCtrl + 1024;
 };
 static_assert(Cfg<true>::SMEM <= 232448 && Cfg<false>::SMEM <= 232448, "shared memory");
 
@@ -105,18 +104,45 @@ __device__ __forceinline__ uint32_t codes_pair(uint32_t w, int i) {
   return r;
 }
 
-// What a step adds to a warp's 32 rows x 8 NTL tokens.
-template <int NTL>
-__device__ __forceinline__ void step_int4(float (&tot)[2][2][4], uint32_t st, const FewProduct& p,
-                                          int rg, int kw, int g, int t) {
-  using C = Cfg<true>;
-  const int row0 = rg * 32 + g;
-  const bool each = p.group == 32;               // a group is one chunk of 32, or covers both
-  // scales and zero points lie in two halves of 128 rows
-  const uint32_t half = (uint32_t)(rg >> 2) * p.groups_per_step;
-  const uint32_t r128 = row0 & 127;
+// A lane's places in a stage, without the stage's address: the weights' 16 bytes of a chunk of
+// 32 elements (4-bit: this thread's word of them), the tokens' pieces, sums, scales.
+struct Places {
+  uint32_t w[8], x[2], sum, s, z;
+};
+
+template <bool W4>
+__device__ __forceinline__ Places places(const FewProduct& p, int rg, int g, int t) {
+  using C = Cfg<W4>;
+  Places a;
+  const int row0 = rg * 32 + g;                  // and 8, 16, 24 on: the same low three bits
+  if constexpr (W4) {
 #pragma unroll
-  for (int cc = 0; cc < 4; cc += 2) {
+    for (int i = 0; i < 8; ++i) a.w[i] = row0 * 128 + ((i ^ g) << 4) + t * 4;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      a.x[b] = C::X_OFF + g * 128 + (((b * 4 + t) ^ ((g & 1) << 2)) << 4);
+    // (scales and zero points lie in two halves of 128 rows)
+    const int at = (rg >> 2) * p.groups_per_step * 128 + (row0 & 127);
+    a.sum = C::SUM_OFF + 2 * t * 4;
+    a.s = C::S_OFF + at * 2;
+    a.z = C::Z_OFF + at;
+  } else {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      a.w[b] = row0 * 128 + (((4 * b + t) ^ g) << 4);
+      a.x[b] = C::X_OFF + g * 128 + (((4 * b + t) ^ g) << 4);
+    }
+  }
+  return a;
+}
+
+// What a step adds to a warp's 32 rows x 8 NTL tokens. GC: chunks of 32 elements in a group.
+template <int NTL, int GC>
+__device__ __forceinline__ void step_int4(float (&tot)[2][2][4], uint32_t st, const Places& a,
+                                          bool has_zeros) {
+  using C = Cfg<true>;
+#pragma unroll
+  for (int c0 = 0; c0 < 8; c0 += GC) {
     float acc[2][NTL][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -125,21 +151,16 @@ __device__ __forceinline__ void step_int4(float (&tot)[2][2][4], uint32_t st, co
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
 #pragma unroll
-    for (int c1 = 0; c1 < 2; ++c1) {
-      const int c = 4 * kw + cc + c1;            // the step's chunk of 32 elements
+    for (int c = c0; c < c0 + GC; ++c) {
       uint32_t w[2][2];
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = row0 + 16 * m + 8 * h;
-          w[m][h] = lds32(st + row * 128 + ((c ^ (row & 7)) << 4) + t * 4);
-        }
+        for (int h = 0; h < 2; ++h) w[m][h] = lds32(st + a.w[c] + m * 2048 + h * 1024);
       uint4 x[NTL];
 #pragma unroll
       for (int n = 0; n < NTL; ++n)
-        x[n] = lds128(st + C::X_OFF + (n * C::XBOXES + (c >> 1)) * 1024 + g * 128 +
-                      ((((c & 1) * 4 + t) ^ ((g & 1) << 2)) << 4));
+        x[n] = lds128(st + a.x[c & 1] + n * (C::XBOXES * 1024) + (c >> 1) * 1024);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const uint32_t a0 = codes_pair(w[m][0], 0), a1 = codes_pair(w[m][1], 0);
@@ -152,61 +173,48 @@ __device__ __forceinline__ void step_int4(float (&tot)[2][2][4], uint32_t st, co
           mma16816(acc[m][n], b0, b1, b2, b3, x[n].z, x[n].w);
         }
       }
-      if (c1 == 0 && !each) continue;
-      // the group's scale and zero point: these rows' four, of this chunk's group
-      const uint32_t sg = half + (uint32_t)((c * 32) / p.group);
-      float2 sx[NTL];
+    }
+    // the group's scales, zero points and sums of x
+    const int q = c0 / GC;
+    float2 sx[NTL];
 #pragma unroll
-      for (int n = 0; n < NTL; ++n) {
-        sx[n] = lds_f2(st + C::SUM_OFF + (c * kTok + n * 8 + 2 * t) * 4);
-        if (!each) {
-          const float2 o = lds_f2(st + C::SUM_OFF + ((c - 1) * kTok + n * 8 + 2 * t) * 4);
-          sx[n].x += o.x;
-          sx[n].y += o.y;
+    for (int n = 0; n < NTL; ++n) sx[n] = lds_f2(st + a.sum + (q * kTok + n * 8) * 4);
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float s = __uint_as_float(lds16(st + a.s + (q * 128 + 16 * m + 8 * h) * 2) << 16);
+        const float z =
+            has_zeros ? (float)(128u + (lds8(st + a.z + q * 128 + 16 * m + 8 * h) & 127u)) : 136.f;
+#pragma unroll
+        for (int n = 0; n < NTL; ++n) {
+          tot[m][n][2 * h] = fmaf(s, fmaf(-z, sx[n].x, acc[m][n][2 * h]), tot[m][n][2 * h]);
+          tot[m][n][2 * h + 1] =
+              fmaf(s, fmaf(-z, sx[n].y, acc[m][n][2 * h + 1]), tot[m][n][2 * h + 1]);
         }
       }
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t at = sg * 128 + r128 + 16 * m + 8 * h;
-          const float s = __uint_as_float(lds16(st + C::S_OFF + at * 2) << 16);
-          const float z = p.has_zeros ? (float)(128u + (lds8(st + C::Z_OFF + at) & 127u)) : 136.f;
-#pragma unroll
-          for (int n = 0; n < NTL; ++n) {
-            tot[m][n][2 * h] = fmaf(s, fmaf(-z, sx[n].x, acc[m][n][2 * h]), tot[m][n][2 * h]);
-            tot[m][n][2 * h + 1] =
-                fmaf(s, fmaf(-z, sx[n].y, acc[m][n][2 * h + 1]), tot[m][n][2 * h + 1]);
-            acc[m][n][2 * h] = acc[m][n][2 * h + 1] = 0.f;
-          }
-        }
-    }
   }
 }
 
 template <int NTL>
-__device__ __forceinline__ void step_bf16(float (&tot)[2][2][4], uint32_t st, int rg, int kw,
-                                          int g, int t) {
-  using C = Cfg<false>;
-  const int row0 = rg * 32 + g;
-  uint4 w[2][2], x[NTL];
+__device__ __forceinline__ void step_bf16(float (&tot)[2][2][4], uint32_t st, const Places& a) {
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+  for (int c = 0; c < 2; ++c) {
+    uint4 w[2][2], x[NTL];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = row0 + 16 * m + 8 * h;
-      w[m][h] = lds128(st + row * 128 + (((4 * kw + t) ^ (row & 7)) << 4));
-    }
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-  for (int n = 0; n < NTL; ++n)
-    x[n] = lds128(st + C::X_OFF + n * 1024 + g * 128 + (((4 * kw + t) ^ g) << 4));
+      for (int h = 0; h < 2; ++h) w[m][h] = lds128(st + a.w[c] + m * 2048 + h * 1024);
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+    for (int n = 0; n < NTL; ++n) x[n] = lds128(st + a.x[c] + n * 1024);
 #pragma unroll
-    for (int n = 0; n < NTL; ++n) {
-      mma16816(tot[m][n], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, x[n].x, x[n].y);
-      mma16816(tot[m][n], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, x[n].z, x[n].w);
-    }
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int n = 0; n < NTL; ++n) {
+        mma16816(tot[m][n], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, x[n].x, x[n].y);
+        mma16816(tot[m][n], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, x[n].z, x[n].w);
+      }
+  }
 }
 
 // The unit u of a group: token tiles fastest, so that those of the same weights follow each
@@ -215,7 +223,8 @@ struct Unit {
   int g, slab, tok0, ntok;                       // first token within the group, tokens
 };
 
-template <bool W4, bool SWIGLU>
+// GC: chunks of 32 elements of K in a scale's group (4-bit).
+template <bool W4, bool SWIGLU, int GC>
 __global__ void __launch_bounds__(Cfg<W4>::THREADS, 1)
 product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmZ,
@@ -224,10 +233,11 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  float* tile = reinterpret_cast<float*>(smem_raw + (base - raw) + C::STAGES * C::STAGE);
-  uint8_t* ctrl = reinterpret_cast<uint8_t*>(tile) + kTileBytes;
-  const uint32_t ctrl_u = base + C::STAGES * C::STAGE + kTileBytes;
-  const uint32_t bar_full = ctrl_u, bar_ready = ctrl_u + 64, bar_empty = ctrl_u + 128;
+  float* tiles = reinterpret_cast<float*>(smem_raw + (base - raw) + C::STAGES * C::STAGE);
+  uint8_t* ctrl = reinterpret_cast<uint8_t*>(tiles) + 2 * kTileBytes;
+  const uint32_t ctrl_u = base + C::STAGES * C::STAGE + 2 * kTileBytes;
+  const uint32_t bar_full = ctrl_u, bar_ready = ctrl_u + 40, bar_empty = ctrl_u + 80;
+  const uint32_t bar_tile = ctrl_u + 120, bar_free = ctrl_u + 136;     // of the two tiles
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 192);
   volatile int* s_last = reinterpret_cast<volatile int*>(ctrl + 196);
   int* prefix = reinterpret_cast<int*>(ctrl + 256);        // [kMaxGroups + 1] units
@@ -258,20 +268,28 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
       ptx::mbar_init(bar_ready + 8 * s, C::HELPERS > 0 ? C::HELPERS : 1);
       ptx::mbar_init(bar_empty + 8 * s, kConsumers);
     }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bar_tile + 8 * i, kConsumers);
+      ptx::mbar_init(bar_free + 8 * i, kJoiners);
+    }
     ptx::fence_mbar_init();
   }
   __syncthreads();
   const int units = block_exclusive_scan(prefix, p.G, tmp);
   if (tid == 0) prefix[p.G] = units;
   __syncthreads();
-  // an even share of all steps, not under kFewLeast of them where there are few
-  const int64_t KC = p.steps, total = KC * units;
-  int64_t nb64 = total / kFewLeast;
-  if (nb64 < 1) nb64 = 1;
-  const int nb = nb64 < gridDim.x ? (int)nb64 : (int)gridDim.x;
+  // an even share of all steps, not under kFewLeast of them where there are few: the first
+  // `more` CTAs take one step above `share`
+  const int KC = p.steps, total = KC * units;
+  const int nb = max(1, min(total / kFewLeast, (int)gridDim.x));
   if (total == 0 || (int)blockIdx.x >= nb) return;
-  auto first_of = [&](int b) { return total * b / nb; };
-  const int64_t begin = first_of(blockIdx.x), end = first_of(blockIdx.x + 1);
+  const int share = total / nb, more = total - share * nb;
+  auto first_of = [&](int b) { return b * share + min(b, more); };
+  auto cta_of = [&](int step) {
+    const int long_ = more * (share + 1);
+    return step < long_ ? step / (share + 1) : more + (step - long_) / share;
+  };
+  const int begin = first_of(blockIdx.x), end = first_of(blockIdx.x + 1);
   auto unit_at = [&](int u) {
     Unit v;
     v.g = gg::find_group(prefix, p.G, u);
@@ -286,10 +304,8 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     if (lane == 0) {
       uint32_t stage = 0, phase = 0, issued = 0, issued_phase = 0;
       bool ok = true;
-      for (int64_t at = begin; at < end && ok;) {
-        const int u = (int)(at / KC);
-        const int k0 = (int)(at - u * KC);
-        const int n = (int)min(KC - k0, end - at);
+      for (int at = begin; at < end && ok;) {
+        const int u = at / KC, k0 = at - u * KC, n = min(KC - k0, end - at);
         at += n;
         const Unit v = unit_at(u);
         const int ntl = (v.ntok + 7) >> 3;
@@ -346,9 +362,8 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     // their sums over each 32
     uint32_t stage = 0, phase = 0;
     bool ok = true;
-    for (int64_t at = begin; at < end && ok;) {
-      const int u = (int)(at / KC);
-      const int n = (int)min(KC - (at - u * KC), end - at);
+    for (int at = begin; at < end && ok;) {
+      const int u = at / KC, n = min(KC - (at - u * KC), end - at);
       at += n;
       const int ntok = (unit_at(u).ntok + 7) & ~7;
       for (int k = 0; k < n && ok; ++k) {
@@ -356,23 +371,37 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                                                     abort_flag));
         if (!ok) break;
         const uint32_t st = base + stage * C::STAGE;
-        for (int tok = warp - 1; tok < ntok; tok += C::HELPERS) {
-          const uint32_t r = st + C::X_OFF + ((tok >> 3) * C::XBOXES + (lane >> 3)) * 1024 +
-                             (tok & 7) * 128;
-          const uint4 v = lds128(r + (((lane & 7) ^ (tok & 7)) << 4));
-          float f[8];
-          unpack8(v, f);
-          float s = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-          s += __shfl_xor_sync(0xffffffffu, s, 1);
-          s += __shfl_xor_sync(0xffffffffu, s, 2);
-          if ((lane & 3) == 0)
-            asm volatile("st.shared.f32 [%0], %1;"
-                         :: "r"(st + C::SUM_OFF + ((lane >> 2) * kTok + tok) * 4), "f"(s)
-                         : "memory");
+        // three tokens at a time: what bounds these warps is the shuffles' latency
+        for (int tok0 = warp - 1; tok0 < ntok; tok0 += 3 * C::HELPERS) {
+          uint4 v[3];
+          float s[3];
+          uint32_t r[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const int tok = min(tok0 + i * C::HELPERS, kTok - 1);
+            r[i] = st + C::X_OFF + ((tok >> 3) * C::XBOXES + (lane >> 3)) * 1024 + (tok & 7) * 128;
+            v[i] = lds128(r[i] + (((lane & 7) ^ (tok & 7)) << 4));
+            float f[8];
+            unpack8(v[i], f);
+            s[i] = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+          }
+#pragma unroll
+          for (int o = 1; o < 4 * GC; o *= 2)
+#pragma unroll
+            for (int i = 0; i < 3; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
           __syncwarp();
-          sts128(r + (((lane & 7) ^ ((tok & 1) << 2)) << 4),
-                 make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                            __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)));
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const int tok = tok0 + i * C::HELPERS;
+            if (tok >= ntok) break;
+            if (lane % (4 * GC) == 0)
+              asm volatile("st.shared.f32 [%0], %1;"
+                           :: "r"(st + C::SUM_OFF + (lane / (4 * GC) * kTok + tok) * 4), "f"(s[i])
+                           : "memory");
+            sts128(r[i] + (((lane & 7) ^ ((tok & 1) << 2)) << 4),
+                   make_uint4(__byte_perm(v[i].x, v[i].z, 0x5410), __byte_perm(v[i].x, v[i].z, 0x7632),
+                              __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632)));
+          }
         }
         ptx::fence_proxy_async_smem();           // TMA writes here next
         __syncwarp();
@@ -390,125 +419,166 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     return;
   }
 
-  // ------------------------------------------------------------- consumers
-  const int cw = warp - 1 - C::HELPERS, ctid = tid - 32 * (1 + C::HELPERS);
-  const int rg = cw >> 1, kw = cw & 1, g = lane >> 2, t = lane & 3;
-  constexpr int CT = 32 * kConsumers;
+  const int g = lane >> 2, t = lane & 3;
+  uint32_t buf = 0, buf_phase = 0;
+  if (warp <= C::HELPERS + kConsumers) {
+    const int rg = warp - 1 - C::HELPERS;
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    const Places here = places<W4>(p, rg, g, t);
+    for (int at = begin; at < end && ok;) {
+      const int u = at / KC, n = min(KC - (at - u * KC), end - at);
+      at += n;
+      const bool two = unit_at(u).ntok > 8;
+      float tot[2][2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tot[m][j][i] = 0.f;
+      for (int k = 0; k < n; ++k) {
+        ok = ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget, abort_flag);
+        if (W4) ok = ok && ptx::mbar_wait(bar_ready + 8 * stage, phase, kWaitBudget, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t st = base + stage * C::STAGE;
+        if constexpr (W4) {
+          if (two) step_int4<2, GC>(tot, st, here, p.has_zeros);
+          else step_int4<1, GC>(tot, st, here, p.has_zeros);
+        } else {
+          if (two) step_bf16<2>(tot, st, here);
+          else step_bf16<1>(tot, st, here);
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar_empty + 8 * stage);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(bar_free + 8 * buf, buf_phase ^ 1u,
+                                                        kWaitBudget, abort_flag));
+      if (!ok) break;
+      float* tile = tiles + buf * (kTileBytes / 4);
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            tile[(rg * 32 + 16 * m + 8 * (i >> 1) + g) * kTileLd + 8 * j + 2 * t + (i & 1)] =
+                tot[m][j][i];
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar_tile + 8 * buf);
+      buf ^= 1u;
+      buf_phase ^= buf ^ 1u;
+    }
+    if (!ok && lane == 0) {
+      record_status(p.status, MOE_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+    return;
+  }
+
+  // the results' warps, beside the consumers' next unit
+  constexpr int CT = 32 * kJoiners;
+  const int ctid = tid - (C::THREADS - CT);
   auto sync = [] { asm volatile("bar.sync 1, %0;" :: "n"(CT) : "memory"); };
-  uint32_t stage = 0, phase = 0;
   bool ok = true;
-  for (int64_t at = begin; at < end;) {
-    const int u = (int)(at / KC);
-    const int k0 = (int)(at - u * KC);
-    const int n = (int)min(KC - k0, end - at);
+  for (int at = begin; at < end;) {
+    const int u = at / KC, n = min(KC - (at - u * KC), end - at);
     at += n;
     const Unit v = unit_at(u);
-    const bool two = v.ntok > 8;
-    float tot[2][2][4];
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tot[m][j][i] = 0.f;
+    float* tile = tiles + buf * (kTileBytes / 4);
     // (after a wait that ran out the pieces go on without their sums, so that the parts' counters
     // come out as in any other launch)
-    for (int k = 0; k < n && ok; ++k) {
-      ok = ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget, abort_flag);
-      if (W4) ok = ok && ptx::mbar_wait(bar_ready + 8 * stage, phase, kWaitBudget, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) {
-        if (lane == 0) {
-          record_status(p.status, MOE_ERR_TIMEOUT);
-          *abort_flag = 1;
-        }
-        break;
-      }
-      const uint32_t st = base + stage * C::STAGE;
-      if constexpr (W4) {
-        if (two) step_int4<2>(tot, st, p, rg, kw, g, t);
-        else step_int4<1>(tot, st, p, rg, kw, g, t);
-      } else {
-        if (two) step_bf16<2>(tot, st, rg, kw, g, t);
-        else step_bf16<1>(tot, st, rg, kw, g, t);
-      }
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar_empty + 8 * stage);
-      if (++stage == C::STAGES) {
-        stage = 0;
-        phase ^= 1u;
-      }
+    if (ok && !ptx::mbar_wait(bar_tile + 8 * buf, buf_phase, kWaitBudget, abort_flag)) {
+      ok = false;
+      record_status(p.status, MOE_ERR_TIMEOUT);
+      *abort_flag = 1;
     }
-    // the two halves of K, then 256 rows x the unit's tokens in shared memory
-    auto at_tile = [&](int m, int j, int i) -> float& {
-      return tile[(rg * 32 + 16 * m + 8 * (i >> 1) + g) * kTileLd + 8 * j + 2 * t + (i & 1)];
-    };
-    sync();                                        // the tile's last readers are done
-    if (kw == 0) {
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) at_tile(m, j, i) = tot[m][j][i];
-    }
-    sync();
-    if (kw == 1) {
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) at_tile(m, j, i) += tot[m][j][i];
-    }
-    sync();
+    bool mine = true;                              // whether the results are this CTA's to write
     if (n < KC) {
       // CTAs lo .. hi share the unit, each with one part: the first the one that it leaves
       // unfinished, the others the one that they begin with
-      const int64_t s0 = u * KC, s1 = s0 + KC - 1;
-      auto cta_of = [&](int64_t s) {
-        int b = (int)(s * nb / total);
-        while (b > 0 && first_of(b) > s) --b;
-        while (first_of(b + 1) <= s) ++b;
-        return b;
-      };
-      const int lo = cta_of(s0), hi = cta_of(s1);
+      const int lo = cta_of(u * KC), hi = cta_of(u * KC + KC - 1);
       auto part = [&](int b) { return p.parts + ((int64_t)2 * b + (b == lo)) * (kSlab * kTok); };
-      float* mine = part(blockIdx.x);
-      for (int e = ctid; e < kSlab * v.ntok; e += CT)
-        __stcg(mine + e, tile[(e & (kSlab - 1)) * kTileLd + (e / kSlab)]);
+      float* to = part(blockIdx.x);
+      // four rows of a token a thread and turn, in the parts' order [token][row]
+      auto tile4 = [&](int e) { return tile + (e & (kSlab - 1)) * kTileLd + e / kSlab; };
+      const int all = kSlab * v.ntok;
+#pragma unroll 2
+      for (int e = 4 * ctid; e < all; e += 4 * CT) {
+        const float* f = tile4(e);
+        __stcg(reinterpret_cast<float4*>(to + e),
+               make_float4(f[0], f[kTileLd], f[2 * kTileLd], f[3 * kTileLd]));
+      }
       __threadfence();
       sync();
       if (ctid == 0) *s_last = ptx::atom_add_acq_rel(p.arrived + lo, 1u) == (uint32_t)(hi - lo);
       sync();
-      if (!*s_last) continue;
-      for (int e = ctid; e < kSlab * v.ntok; e += CT) {
-        float a = 0.f;
-        for (int b = lo; b <= hi; ++b) a += __ldcg(part(b) + e);
-        tile[(e & (kSlab - 1)) * kTileLd + (e / kSlab)] = a;
+      mine = *s_last;
+      if (mine) {
+        // (every load of a part in flight at once: a part costs one way to L2)
+        constexpr int V = kSlab * kTok / (4 * CT);
+        float4 sum[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int b = lo; b <= hi; ++b) {
+          const float* from = part(b) + 4 * ctid;
+          float4 d[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (4 * (ctid + i * CT) < all) d[i] = __ldcg(reinterpret_cast<const float4*>(from + 4 * i * CT));
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            if (4 * (ctid + i * CT) >= all) continue;
+            sum[i].x += d[i].x;
+            sum[i].y += d[i].y;
+            sum[i].z += d[i].z;
+            sum[i].w += d[i].w;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int e = 4 * (ctid + i * CT);
+          if (e >= all) continue;
+          float* f = tile4(e);
+          f[0] = sum[i].x;
+          f[kTileLd] = sum[i].y;
+          f[2 * kTileLd] = sum[i].z;
+          f[3 * kTileLd] = sum[i].w;
+        }
+        if (ctid == 0) p.arrived[lo] = 0u;         // as the next launch expects it
       }
-      if (ctid == 0) p.arrived[lo] = 0u;           // as the next launch expects it
       sync();
     }
-    // two neighbouring columns a thread
-    constexpr int COLS = SWIGLU ? kSlab / 2 : kSlab;
-    const int n0 = v.slab * COLS, N = SWIGLU ? p.F : p.N;
-    for (int e = ctid; e < COLS / 2 * v.ntok; e += CT) {
-      const int c = e % (COLS / 2) * 2, tok = e / (COLS / 2);
-      if (n0 + c >= N) continue;
-      const int64_t row = s_off[v.g] + v.tok0 + tok;
-      float a = tile[c * kTileLd + tok], b = tile[(c + 1) * kTileLd + tok];
-      if (SWIGLU) {
-        a = gg::silu_f(a) * tile[(c + 128) * kTileLd + tok];
-        b = gg::silu_f(b) * tile[(c + 129) * kTileLd + tok];
+    if (mine) {
+      // two neighbouring columns a thread
+      constexpr int COLS = SWIGLU ? kSlab / 2 : kSlab;
+      const int n0 = v.slab * COLS, N = SWIGLU ? p.F : p.N;
+      for (int e = ctid; e < COLS / 2 * v.ntok; e += CT) {
+        const int c = e % (COLS / 2) * 2, tok = e / (COLS / 2);
+        if (n0 + c >= N) continue;
+        const int64_t row = s_off[v.g] + v.tok0 + tok;
+        float a = tile[c * kTileLd + tok], b = tile[(c + 1) * kTileLd + tok];
+        if (SWIGLU) {
+          a = gg::silu_f(a) * tile[(c + 128) * kTileLd + tok];
+          b = gg::silu_f(b) * tile[(c + 129) * kTileLd + tok];
+        }
+        if (p.add) {
+          const uint32_t d = *reinterpret_cast<const uint32_t*>(p.add + row * p.ldadd + n0 + c);
+          a += bf16_lo(d);
+          b += bf16_hi(d);
+        }
+        *reinterpret_cast<uint32_t*>(p.out + row * p.ldo + n0 + c) = pack_bf16x2(a, b);
       }
-      if (p.add) {
-        const uint32_t d = *reinterpret_cast<const uint32_t*>(p.add + row * p.ldadd + n0 + c);
-        a += bf16_lo(d);
-        b += bf16_hi(d);
-      }
-      *reinterpret_cast<uint32_t*>(p.out + row * p.ldo + n0 + c) = pack_bf16x2(a, b);
     }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar_free + 8 * buf);
+    buf ^= 1u;
+    buf_phase ^= buf ^ 1u;
   }
 }
 
@@ -562,16 +632,24 @@ bool make_rows_map(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool W4, bool SWIGLU>
+template <bool W4, bool SWIGLU, int GC>
 cudaError_t run_few(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& s,
                     const CUtensorMap& z, const FewProduct& p, cudaStream_t stream) {
-  auto kern = product_few_kernel<W4, SWIGLU>;
+  auto kern = product_few_kernel<W4, SWIGLU, GC>;
   static PerDevice set;
   const cudaError_t e = set_smem_once(set, kern, Cfg<W4>::SMEM);
   if (e != cudaSuccess) return e;
   const int n = num_sms();
   kern<<<n < kFewCtas ? n : kFewCtas, Cfg<W4>::THREADS, Cfg<W4>::SMEM, stream>>>(w, x, s, z, p);
   return cudaGetLastError();
+}
+
+template <bool SWIGLU>
+cudaError_t run_int4(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& s,
+                     const CUtensorMap& z, const FewProduct& p, cudaStream_t stream) {
+  return p.group == 128  ? run_few<true, SWIGLU, 4>(w, x, s, z, p, stream)
+         : p.group == 64 ? run_few<true, SWIGLU, 2>(w, x, s, z, p, stream)
+                         : run_few<true, SWIGLU, 1>(w, x, s, z, p, stream);
 }
 
 }  // namespace
@@ -588,9 +666,9 @@ cudaError_t launch_int4_dequantize(const void* codes, const void* scales, const 
 
 static_assert(kFewPart == kSlab * kTok, "parts as the kernel writes them");
 
-// Units of 16 tokens and 256 weight rows that the kernel's 32-bit numbers hold.
-bool few_fits(int64_t rows, int G, int64_t N) {
-  return (rows / kTok + G + 1) * ((N + 127) / 128) < (1LL << 31);
+// Steps of units of 16 tokens and 256 weight rows that the kernel's 32-bit numbers hold.
+bool few_fits(int64_t rows, int G, int64_t N, int64_t K) {
+  return (rows / kTok + G + 1) * ((N + 127) / 128) * ((K + 63) / 64) < (1LL << 31);
 }
 
 cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const void* w,
@@ -603,6 +681,7 @@ cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const v
   p.steps = (p.K + (w4 ? 255 : 63)) / (w4 ? 256 : 64);
   p.has_zeros = zeros != nullptr;
   p.groups_per_step = w4 ? 256 / p.group : 0;
+  p.group_log2 = p.group == 128 ? 7 : p.group == 64 ? 6 : 5;
   CUtensorMap tw, tx, ts, tz;
   if (!make_rows_map(&tx, x, p.K, p.rows, ldx)) return cudaErrorInvalidValue;
   if (w4) {
@@ -615,12 +694,11 @@ cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const v
     if (zeros && !make_map3(&tz, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, zeros, p.N, kg, p.G, 128,
                             p.groups_per_step, false))
       return cudaErrorInvalidValue;
-    return swiglu ? run_few<true, true>(tw, tx, ts, tz, p, s)
-                  : run_few<true, false>(tw, tx, ts, tz, p, s);
+    return swiglu ? run_int4<true>(tw, tx, ts, tz, p, s) : run_int4<false>(tw, tx, ts, tz, p, s);
   }
   if (!make_map3(&tw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w, p.K, p.N, p.G, 64, 128, true))
     return cudaErrorInvalidValue;
-  return run_few<false, false>(tw, tx, tw, tw, p, s);
+  return run_few<false, false, 1>(tw, tx, tw, tw, p, s);
 }
 
 }  // namespace moe

@@ -207,7 +207,7 @@ moe_status moe_int4_grouped_gemm(const moe_int4_tensor* w, int64_t rows, const v
   OP_TRY(check_segments(w->groups, rows, counts, offsets));
   OP_REQUIRE(swiglu == 0 || (swiglu == 1 && w->N % 32 == 0));
   OP_REQUIRE(al16(scratch));
-  if (!few_fits(rows, (int)w->groups, w->N)) return MOE_ERR_UNSUPPORTED;
+  if (!few_fits(rows, (int)w->groups, w->N, w->K)) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   OP_REQUIRE(rows_ok(x, ldx, w->K) && rows_ok(out, ldo, swiglu ? w->N / 2 : w->N));
   FewProduct p = few_product(w->groups, rows, w->N, w->K, counts, offsets, out, ldo, scratch);
@@ -234,7 +234,7 @@ moe_status moe_grouped_gemm(int64_t groups, int64_t rows, int64_t N, int64_t K, 
   if (rows == 0) return MOE_OK;
   OP_REQUIRE(rows_ok(x, ldx, K) && rows_ok(out, ldo, N) && rows_or_null(add, ldadd, N));
   const int64_t most = expected_rows > 0 && expected_rows < rows ? expected_rows : rows;
-  if (most <= kFewRows && few_fits(rows, (int)groups, N)) {
+  if (most <= kFewRows && few_fits(rows, (int)groups, N, K)) {
     FewProduct p = few_product(groups, rows, N, K, counts, offsets, out, ldo, scratch);
     p.add = bf(add);
     p.ldadd = ldadd;
