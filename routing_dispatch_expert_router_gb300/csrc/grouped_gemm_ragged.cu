@@ -123,6 +123,24 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int NT = (p.cols + BN - 1) / BN;
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < STAGES; ++s) {
+      ptx::mbar_init(bar_full + 8 * s, 1);
+      ptx::mbar_init(bar_empty + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(bar_tfull + 8 * a, 1);
+      ptx::mbar_init(bar_tempty + 8 * a, 128);
+    }
+    ptx::mbar_init(bar_drain, 1);
+    ptx::fence_mbar_init();
+    ptx::tma_prefetch_desc(&tmA);
+    ptx::tma_prefetch_desc(&tmB);
+    ptx::tma_prefetch_desc(&tmC);
+  }
+  ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
   for (int g = tid; g < p.G; g += kThreads) {
     int c = (int)p.rows, o = 0;
     if (p.counts) {
@@ -137,27 +155,12 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     s_off[g] = o;
     prefix[g] = ((MODE == kWgrad ? p.out_rows : c) + BM - 1) / BM * NT;
   }
-  if (tid == 0) *abort_flag = 0;
   __syncthreads();
   const int total = block_exclusive_scan(prefix, p.G, tmp);
   if (tid == 0) prefix[p.G] = total;
   __syncthreads();
   if ((int)blockIdx.x >= total) return;
 
-  if (tid == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      ptx::mbar_init(bar_full + 8 * s, 1);
-      ptx::mbar_init(bar_empty + 8 * s, 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      ptx::mbar_init(bar_tfull + 8 * a, 1);
-      ptx::mbar_init(bar_tempty + 8 * a, 128);
-    }
-    ptx::mbar_init(bar_drain, 1);
-    ptx::fence_mbar_init();
-    ptx::tma_prefetch_desc(&tmA);
-    ptx::tma_prefetch_desc(&tmB);
-  }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 2 * BN);
     ptx::tmem_relinquish();
@@ -389,8 +392,7 @@ cudaError_t run_ragged(const CUtensorMap& a, const CUtensorMap& b, const CUtenso
   static PerDevice set;
   const cudaError_t e = set_smem_once(set, kern, Cfg<BN>::SMEM);
   if (e != cudaSuccess) return e;
-  kern<<<num_sms(), kThreads, Cfg<BN>::SMEM, s>>>(a, b, c, p);
-  return cudaGetLastError();
+  return launch_early(kern, (unsigned)num_sms(), dim3(kThreads, 1, 1), Cfg<BN>::SMEM, s, a, b, c, p);
 }
 
 // Columns of a tile: as wide as fills the SMs (a wider tile reads A less often, but few tiles

@@ -30,7 +30,25 @@ cudaError_t set_smem_once(PerDevice& set, Kernel kern, int bytes) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   });
 }
-// The same for a kernel of CTA pairs, and as many CTAs as can be resident at once (its tile
+// A launch that may be made ready while the kernel before it on the stream still runs (programmatic
+// dependent launch). Every thread of such a kernel waits for that one's end (ptx::grid_dependency_wait)
+// before its first access to memory: results are as in a plain launch, without its latency.
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*kern)(Params...), unsigned grid, dim3 block, int smem, cudaStream_t s,
+                         Args... args) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(grid, 1, 1);
+  lc.blockDim = block;
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kern, static_cast<Params>(args)...);
+}
+// set_smem_once for a kernel of CTA pairs, and as many CTAs as can be resident at once (its tile
 // loop strides over the pairs, so every launched pair must run).
 template <class Kernel>
 cudaError_t pair_grid_once(PerDevice& set, Kernel kern, int threads, int smem, int* grid) {

@@ -50,6 +50,8 @@ template <int V, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kRowWarps : 1024)
 rmsnorm_fwd_kernel(const RmsNormFwd p) {
   __shared__ float red[32];
+  ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
   const int64_t row = WARP ? (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5) : blockIdx.x;
   if (WARP && row >= p.T) return;
   const int lane = threadIdx.x & 31;
@@ -130,6 +132,8 @@ template <int V, int THREADS, bool WARP, int HOLD>
 __global__ void __launch_bounds__(THREADS)
 rmsnorm_bwd_kernel(const RmsNormBwd p) {
   __shared__ float red[2][32];
+  ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int first = WARP ? lane : threadIdx.x, step = WARP ? 32 : blockDim.x;
   const int nvec = p.H >> 3;
@@ -237,6 +241,7 @@ dgamma_kernel(const float* __restrict__ parts, int n, int H, float* __restrict__
   __shared__ float sum[16][32];
   const int c = blockIdx.x * 32 + threadIdx.x;
   ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
   float a = 0.f;
   if (c < H) {
 #pragma unroll 8
@@ -271,44 +276,34 @@ int bwd_ctas(int64_t T, int H) {
 }  // namespace
 
 cudaError_t launch_rmsnorm_fwd(const RmsNormFwd& p, cudaStream_t s) {
+  constexpr int W = 32 * kRowWarps;
   if (p.H <= kWarpColumns) {
     const unsigned grid = (unsigned)((p.T + kRowWarps - 1) / kRowWarps);
-    if (p.H <= 512) rmsnorm_fwd_kernel<2, true><<<grid, 32 * kRowWarps, 0, s>>>(p);
-    else rmsnorm_fwd_kernel<4, true><<<grid, 32 * kRowWarps, 0, s>>>(p);
-  } else if (p.H <= 16384) {
-    rmsnorm_fwd_kernel<2, false><<<(unsigned)p.T, row_threads(p.H, 2), 0, s>>>(p);
-  } else {
-    rmsnorm_fwd_kernel<4, false><<<(unsigned)p.T, row_threads(p.H, 4), 0, s>>>(p);
+    return launch_early(p.H <= 512 ? rmsnorm_fwd_kernel<2, true> : rmsnorm_fwd_kernel<4, true>, grid,
+                        dim3(W, 1, 1), 0, s, p);
   }
-  return cudaGetLastError();
+  const int V = p.H <= 16384 ? 2 : 4;
+  return launch_early(V == 2 ? rmsnorm_fwd_kernel<2, false> : rmsnorm_fwd_kernel<4, false>,
+                      (unsigned)p.T, dim3(row_threads(p.H, V), 1, 1), 0, s, p);
 }
 
 cudaError_t launch_rmsnorm_bwd(const RmsNormBwd& p, float* dgamma, cudaStream_t s) {
+  constexpr int W = 32 * kRowWarps;
   const int n = bwd_ctas(p.T, p.H);
   if (n > 0) {
-    constexpr int W = 32 * kRowWarps;
-    const int threads = row_threads(p.H, p.H <= 8192 ? 2 : 4);
-    if (p.H <= 512) rmsnorm_bwd_kernel<2, W, true, 2><<<n, W, 0, s>>>(p);
-    else if (p.H <= kWarpColumns) rmsnorm_bwd_kernel<4, W, true, 1><<<n, W, 0, s>>>(p);
-    else if (p.H <= 8192) rmsnorm_bwd_kernel<2, 512, false, 2><<<n, threads, 0, s>>>(p);
-    else if (p.H <= 16384) rmsnorm_bwd_kernel<4, 512, false, 1><<<n, threads, 0, s>>>(p);
-    else rmsnorm_bwd_kernel<4, 1024, false, 0><<<n, threads, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const int threads = p.H <= kWarpColumns ? W : row_threads(p.H, p.H <= 8192 ? 2 : 4);
+    const cudaError_t e = launch_early(p.H <= 512            ? rmsnorm_bwd_kernel<2, W, true, 2>
+                                       : p.H <= kWarpColumns ? rmsnorm_bwd_kernel<4, W, true, 1>
+                                       : p.H <= 8192         ? rmsnorm_bwd_kernel<2, 512, false, 2>
+                                       : p.H <= 16384        ? rmsnorm_bwd_kernel<4, 512, false, 1>
+                                                             : rmsnorm_bwd_kernel<4, 1024, false, 0>,
+                                       (unsigned)n, dim3(threads, 1, 1), 0, s, p);
     if (e != cudaSuccess) return e;
   }
   if (!dgamma) return cudaSuccess;
   // (without rows there are no shares, and dgamma is zero)
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((p.H + 31) / 32, 1, 1);
-  lc.blockDim = dim3(32, 16, 1);
-  lc.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = at;
-  lc.numAttrs = 1;
-  const float* parts = p.parts;
-  return cudaLaunchKernelEx(&lc, dgamma_kernel, parts, n, p.H, dgamma);
+  return launch_early(dgamma_kernel, (unsigned)((p.H + 31) / 32), dim3(32, 16, 1), 0, s, p.parts, n,
+                      p.H, dgamma);
 }
 
 }  // namespace moe

@@ -341,6 +341,7 @@ permute_scatter8_kernel(const uint8_t* __restrict__ codes, const uint8_t* __rest
                         const int32_t* __restrict__ row_of, int T, int H, int k, int block,
                         uint8_t* __restrict__ xq, uint8_t* __restrict__ xsf) {
   ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int nvec = H >> 4, n = H / block;
   const int words = (n + 3) >> 2;                  // atoms along the row, in either layout
@@ -444,18 +445,9 @@ cudaError_t launch_permute_fp8(const moe_config& c, const uint8_t* codes, const 
                                               sel_offsets, sel_tokens, scratch, s);
   if (err != cudaSuccess || c.T == 0) return err;
   const int blocks = (c.T + 7) / 8, most = num_sms() * 8;
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(blocks < most ? blocks : most, 1, 1);
-  lc.blockDim = dim3(256, 1, 1);
-  lc.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = at;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, permute_scatter8_kernel, codes, scales, (const int32_t*)row_of,
-                            (int)c.T, (int)c.H, (int)c.k, c.dtype == MOE_DTYPE_MXFP8 ? 32 : 128,
-                            xq, xsf);
+  return launch_early(permute_scatter8_kernel, (unsigned)(blocks < most ? blocks : most),
+                      dim3(256, 1, 1), 0, s, codes, scales, row_of, c.T, c.H, c.k,
+                      c.dtype == MOE_DTYPE_MXFP8 ? 32 : 128, xq, xsf);
 }
 
 cudaError_t launch_stash_release(const moe_config& c, const int32_t* table, int32_t* top,

@@ -247,6 +247,25 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slabs = p.slabs;
+  if (tid == 0) {
+    ptx::tma_prefetch_desc(&tmW);
+    ptx::tma_prefetch_desc(&tmX);
+    if (W4) ptx::tma_prefetch_desc(&tmS);
+    if (W4 && p.has_zeros) ptx::tma_prefetch_desc(&tmZ);
+    *abort_flag = 0;
+    for (int s = 0; s < C::STAGES; ++s) {
+      ptx::mbar_init(bar_full + 8 * s, 1);
+      ptx::mbar_init(bar_ready + 8 * s, C::HELPERS > 0 ? C::HELPERS : 1);
+      ptx::mbar_init(bar_empty + 8 * s, kConsumers);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bar_tile + 8 * i, kConsumers);
+      ptx::mbar_init(bar_free + 8 * i, kJoiners);
+    }
+    ptx::fence_mbar_init();
+  }
+  ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
   for (int g = tid; g < p.G; g += C::THREADS) {
     int c = (int)p.rows, o = 0;
     if (p.counts) {
@@ -260,19 +279,6 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     s_cnt[g] = c;
     s_off[g] = o;
     prefix[g] = (c + kTok - 1) / kTok * slabs;
-  }
-  if (tid == 0) {
-    *abort_flag = 0;
-    for (int s = 0; s < C::STAGES; ++s) {
-      ptx::mbar_init(bar_full + 8 * s, 1);
-      ptx::mbar_init(bar_ready + 8 * s, C::HELPERS > 0 ? C::HELPERS : 1);
-      ptx::mbar_init(bar_empty + 8 * s, kConsumers);
-    }
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(bar_tile + 8 * i, kConsumers);
-      ptx::mbar_init(bar_free + 8 * i, kJoiners);
-    }
-    ptx::fence_mbar_init();
   }
   __syncthreads();
   const int units = block_exclusive_scan(prefix, p.G, tmp);
@@ -640,8 +646,8 @@ cudaError_t run_few(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMa
   const cudaError_t e = set_smem_once(set, kern, Cfg<W4>::SMEM);
   if (e != cudaSuccess) return e;
   const int n = num_sms();
-  kern<<<n < kFewCtas ? n : kFewCtas, Cfg<W4>::THREADS, Cfg<W4>::SMEM, stream>>>(w, x, s, z, p);
-  return cudaGetLastError();
+  return launch_early(kern, n < kFewCtas ? n : kFewCtas, dim3(Cfg<W4>::THREADS, 1, 1), Cfg<W4>::SMEM,
+                      stream, w, x, s, z, p);
 }
 
 template <bool SWIGLU>
