@@ -9,11 +9,13 @@
 // deterministic and bit-identical from run to run.
 //
 // Three launches (four with a paged stash):
-//   hist    one block per chunk of 256 tokens: per-expert counts of the chunk;
+//   hist    one block per chunk of 256 tokens, a thread per token: per-expert
+//           counts of the chunk (not with a single chunk);
 //   rank    one block per chunk: global counts, segment offsets, and the rank
 //           of every assignment = (assignments of its expert in earlier
 //           chunks) + (earlier tokens of this chunk that chose the same
 //           expert, read from a per-expert bitmap of the chunk's tokens);
+//           8192 tokens to 8 of 256 experts: RANKTIME;
 //   alloc   (paged stash) one block: the layer's stash pages and page table;
 //   scatter one warp per token: reads the row once, writes it to each of its
 //           rows with 16-byte stores; padding rows are zero-filled.
@@ -24,63 +26,104 @@
 
 namespace moe {
 
-// Whether assignment i = t*k + j names the same expert as an earlier slot of
-// token t. Such a repeat (possible only in a caller-given idx, e.g. a replayed
-// one) is reported and dropped like an out-of-range id, so that every counted
-// row of an expert segment is written exactly once.
-__device__ __forceinline__ bool repeats_earlier_slot(const int32_t* __restrict__ idx, int i, int k,
-                                                     int e) {
-  for (int i0 = i - i % k; i0 < i; ++i0)
-    if (idx[i0] == e) return true;
-  return false;
+// The k experts of token t, in registers: -1 where an entry is out of range or names the same
+// expert as an earlier slot of the token (possible only in a caller-given idx, e.g. a replayed
+// one). Such entries are reported and dropped, so that every counted row of an expert segment
+// is written exactly once.
+__device__ __forceinline__ bool token_experts(const int32_t* __restrict__ idx, int t, int k, int E,
+                                              int (&e)[kMaxK]) {
+  int raw[kMaxK];
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) raw[j] = j < k ? __ldg(idx + (size_t)t * k + j) : -1;
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) {
+    bool ok = (unsigned)raw[j] < (unsigned)E;
+#pragma unroll
+    for (int i = 0; i < j; ++i) ok = ok && raw[i] != raw[j];
+    e[j] = ok && j < k ? raw[j] : -1;
+    bad = bad || (j < k && !ok);
+  }
+  return bad;
 }
+
+static_assert(kChunkTokens == 256, "a thread of the dispatch's kernels has one token");
 
 __global__ void __launch_bounds__(256)
 permute_hist_kernel(const int32_t* __restrict__ idx, int32_t* __restrict__ hist, int T, int k,
                     int E, int32_t* status) {
   __shared__ int cnt[kMaxExperts];
-  for (int e = threadIdx.x; e < E; e += blockDim.x) cnt[e] = 0;
+  cnt[threadIdx.x] = 0;
   __syncthreads();
-  const int c = blockIdx.x;
-  const int t0 = c * kChunkTokens, t1 = min(T, t0 + kChunkTokens);
-  for (int i = t0 * k + threadIdx.x; i < t1 * k; i += blockDim.x) {
-    const int e = idx[i];
-    if ((unsigned)e < (unsigned)E && !repeats_earlier_slot(idx, i, k, e)) atomicAdd(&cnt[e], 1);
-    else record_status(status, MOE_ERR_DEVICE_CHECK);
+  const int t = blockIdx.x * kChunkTokens + threadIdx.x;
+  if (t < T) {
+    int e[kMaxK];
+    if (token_experts(idx, t, k, E, e)) record_status(status, MOE_ERR_DEVICE_CHECK);
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j)
+      if (e[j] >= 0) atomicAdd(&cnt[e[j]], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += blockDim.x) hist[(size_t)c * E + e] = cnt[e];
+  if ((int)threadIdx.x < E) hist[(size_t)blockIdx.x * E + threadIdx.x] = cnt[threadIdx.x];
 }
 
+// One chunk (T <= 256) needs no histogram: its own bitmap has the counts.
 __global__ void __launch_bounds__(256)
 permute_rank_kernel(const int32_t* __restrict__ idx, const int32_t* __restrict__ hist,
                     int n_chunk, int T, int k, int E, int S, int align, int C,
                     int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                     int32_t* __restrict__ row_of, int32_t* __restrict__ token_of,
                     int32_t* __restrict__ sel_offsets, int32_t* __restrict__ sel_tokens,
-                    int32_t* __restrict__ pad_prefix) {
+                    int32_t* __restrict__ pad_prefix, int32_t* status) {
+  constexpr int W = kChunkTokens / 32;
   __shared__ int tot[kMaxExperts];
   __shared__ int before[kMaxExperts];
   __shared__ int seg[kMaxGroups + 1];
   __shared__ int kept[kMaxGroups];
   __shared__ int pad[kMaxGroups + 1];
   __shared__ int soff[kMaxExperts + 1];
-  __shared__ uint32_t bm[kMaxExperts][kChunkTokens / 32];
+  __shared__ __align__(16) uint32_t bm[kMaxExperts][W];        // tokens of the chunk, per expert
+  __shared__ __align__(8) uint8_t pre[kMaxExperts][W];         // how many in the words before
   __shared__ int tmp[33];
   const int c = blockIdx.x, G = E + S, tid = threadIdx.x, nt = blockDim.x;
+  const int t = c * kChunkTokens + tid;
 
-  for (int e = tid; e < E; e += nt) {
+  for (int i = tid; i < E * W; i += nt) (&bm[0][0])[i] = 0u;
+  int e[kMaxK];
+  const bool bad = t < T && token_experts(idx, t, k, E, e);
+  ptx::grid_dependency_wait();                   // (idx is older than the histogram's launch)
+  if (bad && n_chunk == 1) record_status(status, MOE_ERR_DEVICE_CHECK);
+  if (tid < E && n_chunk > 1) {
     int a = 0, b = 0;
+#pragma unroll 8
     for (int cc = 0; cc < n_chunk; ++cc) {
-      const int h = hist[(size_t)cc * E + e];
+      const int h = __ldcg(hist + (size_t)cc * E + tid);
       a += h;
       if (cc < c) b += h;
     }
-    tot[e] = a;
-    before[e] = b;
-    soff[e] = a;
+    tot[tid] = a;
+    before[tid] = b;
+    soff[tid] = a;
   }
-  for (int i = tid; i < E * (kChunkTokens / 32); i += nt) (&bm[0][0])[i] = 0u;
+  __syncthreads();
+  if (t < T) {
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j)
+      if (e[j] >= 0) atomicOr(&bm[e[j]][tid >> 5], 1u << (tid & 31));
+  }
+  __syncthreads();
+  if (tid < E) {
+    int n = 0;
+#pragma unroll
+    for (int q = 0; q < W; ++q) {
+      pre[tid][q] = (uint8_t)n;                  // (at most 224)
+      n += __popc(bm[tid][q]);
+    }
+    if (n_chunk <= 1) {
+      tot[tid] = soff[tid] = n;
+      before[tid] = 0;
+    }
+  }
   __syncthreads();
   for (int g = tid; g < G; g += nt) {
     int kp, sl;
@@ -113,39 +156,29 @@ permute_rank_kernel(const int32_t* __restrict__ idx, const int32_t* __restrict__
       offsets[g] = seg[g];
       pad_prefix[g] = pad[g];
     }
-    for (int e = tid; e <= E; e += nt) sel_offsets[e] = soff[e];
+    for (int q = tid; q <= E; q += nt) sel_offsets[q] = soff[q];
   }
-  const int t0 = c * kChunkTokens, t1 = min(T, t0 + kChunkTokens);
-  for (int i = t0 * k + tid; i < t1 * k; i += nt) {
-    const int e = idx[i];
-    if ((unsigned)e >= (unsigned)E || repeats_earlier_slot(idx, i, k, e)) continue;
-    const int tl = i / k - t0;
-    atomicOr(&bm[e][tl >> 5], 1u << (tl & 31));
-  }
-  __syncthreads();
-  for (int i = t0 * k + tid; i < t1 * k; i += nt) {
-    const int e = idx[i];
-    if ((unsigned)e >= (unsigned)E || repeats_earlier_slot(idx, i, k, e)) {
-      row_of[i] = -1;
-      continue;
+  if (t < T) {
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j) {
+      if (j >= k) break;
+      int row = -1;
+      if (e[j] >= 0) {
+        const int rank = before[e[j]] + pre[e[j]][tid >> 5] +
+                         __popc(bm[e[j]][tid >> 5] & ((1u << (tid & 31)) - 1u));
+        sel_tokens[soff[e[j]] + rank] = t;
+        if (C == 0 || rank < C) {
+          row = seg[e[j]] + rank;
+          token_of[row] = t;
+        }
+      }
+      row_of[(size_t)t * k + j] = row;
     }
-    const int t = i / k, tl = t - t0, wd = tl >> 5;
-    int local = __popc(bm[e][wd] & ((1u << (tl & 31)) - 1u));
-    for (int q = 0; q < wd; ++q) local += __popc(bm[e][q]);
-    const int rank = before[e] + local;
-    sel_tokens[soff[e] + rank] = t;
-    int row = -1;
-    if (C == 0 || rank < C) {
-      row = seg[e] + rank;
-      token_of[row] = t;
-    }
-    row_of[i] = row;
+    for (int s = 0; s < S; ++s) token_of[seg[E + s] + t] = t;
   }
-  for (int s = 0; s < S; ++s)
-    for (int t = t0 + tid; t < t1; t += nt) token_of[seg[E + s] + t] = t;
-  // padding rows of groups g = c, c + gridDim.x, ... (gridDim.x >= 1 even when T == 0)
-  for (int g = c; g < G; g += gridDim.x)
-    for (int r = seg[g] + kept[g] + tid; r < seg[g + 1]; r += nt) token_of[r] = -1;
+  // padding rows of groups g = c, c + gridDim.x, ..., a warp each (gridDim.x >= 1 even when T == 0)
+  for (int g = c + (tid >> 5) * gridDim.x; g < G; g += gridDim.x * (nt >> 5))
+    for (int r = seg[g] + kept[g] + (tid & 31); r < seg[g + 1]; r += 32) token_of[r] = -1;
 }
 
 // Paged stashing (es summary §2.3.C: the dynamic buffers are managed inside
@@ -391,14 +424,17 @@ static cudaError_t launch_permute_maps(const moe_config& c, const int32_t* idx, 
   int32_t* pad_prefix = reinterpret_cast<int32_t*>(scratch + kScratchPadPrefix);
   int32_t* hist = reinterpret_cast<int32_t*>(scratch + kScratchHist);
   const int nc = n_chunks(c);
-  if (nc > 0) {
+  if (nc > 1) {
     permute_hist_kernel<<<nc, 256, 0, s>>>(idx, hist, c.T, c.k, c.E, status);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
+    return launch_early(permute_rank_kernel, (unsigned)nc, dim3(256, 1, 1), 0, s, idx, hist, nc, c.T,
+                        c.k, c.E, c.n_shared, c.row_align, (int)capacity_rows(c), counts, offsets,
+                        row_of, token_of, sel_offsets, sel_tokens, pad_prefix, status);
   }
-  permute_rank_kernel<<<nc > 0 ? nc : 1, 256, 0, s>>>(idx, hist, nc, c.T, c.k, c.E, c.n_shared, c.row_align,
-                                         (int)capacity_rows(c), counts, offsets, row_of,
-                                         token_of, sel_offsets, sel_tokens, pad_prefix);
+  permute_rank_kernel<<<1, 256, 0, s>>>(idx, hist, nc, c.T, c.k, c.E, c.n_shared, c.row_align,
+                                        (int)capacity_rows(c), counts, offsets, row_of, token_of,
+                                        sel_offsets, sel_tokens, pad_prefix, status);
   return cudaGetLastError();
 }
 
