@@ -599,32 +599,64 @@ _PRODUCT_ARGS = {
 }
 
 
-def _strided(t, rows: int, cols: int, what: str):
+# These calls can be shorter than the checks of their arguments, so the checks ask a tensor
+# each thing once: its place (the current device, whose stream the call takes), type and sizes.
+_has_cuda = None
+
+
+def _device() -> int:
+    global _has_cuda
+    if _has_cuda is None:
+        _has_cuda = torch.cuda.is_available()
+    return torch._C._cuda_getDevice() if _has_cuda else 0
+
+
+def _on(stream, dev: int):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _strided(t, rows: int, cols: int, what: str, dev: int):
     """Address and elements from row to row of bf16 [rows, cols] with contiguous rows."""
     if t is None:
         return None, 0
-    shape, stride = t.shape, t.stride()
-    if t.dtype is not torch.bfloat16 or len(shape) != 2 or shape[0] != rows or shape[1] != cols \
-            or (stride[1] != 1 and cols > 1) or not t.is_cuda:
-        raise ValueError(f"{what} is bf16 [{rows}, {cols}] with contiguous rows, on the GPU")
-    ld = stride[0] if rows > 1 else cols + -cols % 8   # (the stride of a single row says nothing)
-    if ld < cols:
-        raise ValueError(f"{what}'s rows lie one after the other")
-    return t.data_ptr(), ld
+    if t.dtype is torch.bfloat16 and t.get_device() == dev and t.dim() == 2:
+        r, c = t.shape
+        ld, one = t.stride()
+        # (the stride of a single row says nothing)
+        if r == rows and c == cols and one == 1 and (ld >= cols or rows <= 1):
+            return t.data_ptr(), ld if rows > 1 else cols + -cols % 8
+    raise ValueError(f"{what} is bf16 [{rows}, {cols}] with contiguous rows, on the current GPU")
 
 
-def _gamma(t, H: int):
+def _flat(t, n: int, dtype, what: str, dev: int):
+    """At least n elements in a row; dtype None: bytes in all."""
+    if t is None:
+        return None
+    if t.get_device() == dev and t.is_contiguous() and (
+            t.numel() >= n if t.dtype is dtype else
+            dtype is None and t.numel() * t.element_size() >= n):
+        return t.data_ptr()
+    raise ValueError(f"{what} is contiguous {dtype or 'memory'} of {n} "
+                     f"{'elements' if dtype else 'bytes'}, on the current GPU")
+
+
+def _bytes2(t, rows: int, cols: int, what: str, dev: int, exact: bool = True):
+    """[rows (or more), cols] of one byte each."""
+    if t is None:
+        return None
+    if t.dim() == 2 and t.element_size() == 1 and t.get_device() == dev and t.is_contiguous():
+        r, c = t.shape
+        if c == cols and (r == rows or (r > rows and not exact)):
+            return t.data_ptr()
+    raise ValueError(f"{what} is contiguous bytes [{rows}, {cols}], on the current GPU")
+
+
+def _gamma(t, H: int, dev: int):
     if t.dtype is torch.float32:
-        return _vector(t, H, torch.float32, "gamma"), MOE_GAMMA_F32
-    return _vector(t, H, torch.bfloat16, "gamma"), MOE_GAMMA_BF16
-
-
-def _here(*tensors):
-    """Every tensor lies on the current device, whose stream the call takes."""
-    here = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for t in tensors:
-        if t is not None and here is not None and t.get_device() != here:
-            raise ValueError(f"tensors are on the current device, {here}")
+        return _flat(t, H, torch.float32, "gamma", dev), MOE_GAMMA_F32
+    return _flat(t, H, torch.bfloat16, "gamma", dev), MOE_GAMMA_BF16
 
 
 def moe_rmsnorm_fwd(x, gamma, out, residual=None, sum=None, rstd=None, codes=None, scales=None,
@@ -633,32 +665,22 @@ def moe_rmsnorm_fwd(x, gamma, out, residual=None, sum=None, rstd=None, codes=Non
     fp32 [H]); codes [T, H] and scales [T, H / 32 or H / 128]: its E4M3 form, with which out may
     be None; rstd [T] fp32 for the backward. x, residual, sum, out: bf16, contiguous rows."""
     T, H = x.shape
-    _here(x, gamma, out, residual, sum, rstd, codes, scales)
-    g, kind = _gamma(gamma, H)
-    block = 0
-    if scales is not None:
-        block = H // scales.shape[1] if scales.dim() == 2 and scales.shape[1] else 0
-        if codes is None or block not in (32, 128) or scales.shape[1] * block != H:
+    dev = _device()
+    g, kind = _gamma(gamma, H, dev)
+    px, ldx = _strided(x, T, H, "x", dev)
+    pr, ldr = _strided(residual, T, H, "residual", dev)
+    ps, lds = _strided(sum, T, H, "sum", dev)
+    po, ldo = _strided(out, T, H, "out", dev)
+    pc, pq, block = None, None, 0
+    if codes is not None or scales is not None:
+        if codes is None or scales is None or scales.dim() != 2 or \
+                scales.shape[1] * 32 != H and scales.shape[1] * 128 != H:
             raise ValueError("codes [T, H] have scales [T, H / 32] or [T, H / 128]")
-    if codes is not None and scales is None:
-        raise ValueError("codes have scales")
-    px, ldx = _strided(x, T, H, "x")
-    pr, ldr = _strided(residual, T, H, "residual")
-    ps, lds = _strided(sum, T, H, "sum")
-    po, ldo = _strided(out, T, H, "out")
+        block = H // scales.shape[1]
+        pc, pq = _bytes2(codes, T, H, "codes", dev), _bytes2(scales, T, H // block, "scales", dev)
     _check("moe_rmsnorm_fwd",
-           lib().moe_rmsnorm_fwd(T, H, px, ldx, pr, ldr, g, kind, eps, ps, lds, po, ldo,
-                                 None if codes is None else _exactly(codes, T, H, "codes"),
-                                 None if codes is None else
-                                 _exactly(scales, T, H // block, "scales"), block,
-                                 _vector(rstd, T, torch.float32, "rstd"), _stream(stream)))
-
-
-def _exactly(t, rows: int, cols: int, what: str):
-    """[rows, cols] of one byte each, contiguous."""
-    if t.shape[0] != rows:
-        raise ValueError(f"{what} has {rows} rows")
-    return _rows(t, rows, cols, None, what)
+           lib().moe_rmsnorm_fwd(T, H, px, ldx, pr, ldr, g, kind, eps, ps, lds, po, ldo, pc, pq, block,
+                                 _flat(rstd, T, torch.float32, "rstd", dev), _on(stream, dev)))
 
 
 def rmsnorm_scratch_bytes(H: int) -> int:
@@ -672,20 +694,20 @@ def moe_rmsnorm_bwd(dy, h, rstd, gamma, dx, dgamma=None, dsum=None, scratch=None
     or its x) and rstd; dsum: the gradient that reaches h past the norm. scratch:
     rmsnorm_scratch_bytes(H) bytes, with dgamma."""
     T, H = h.shape
-    _here(dy, h, rstd, gamma, dx, dgamma, dsum, scratch)
-    g, kind = _gamma(gamma, H)
-    pdy, lddy = _strided(dy, T, H, "dy")
-    ph, ldh = _strided(h, T, H, "h")
-    pds, ldds = _strided(dsum, T, H, "dsum")
-    pdx, lddx = _strided(dx, T, H, "dx")
+    dev = _device()
+    g, kind = _gamma(gamma, H, dev)
+    pdy, lddy = _strided(dy, T, H, "dy", dev)
+    ph, ldh = _strided(h, T, H, "h", dev)
+    pds, ldds = _strided(dsum, T, H, "dsum", dev)
+    pdx, lddx = _strided(dx, T, H, "dx", dev)
     if dgamma is not None and scratch is None:
         raise ValueError("dgamma is summed through scratch")
     _check("moe_rmsnorm_bwd",
-           lib().moe_rmsnorm_bwd(T, H, pdy, lddy, ph, ldh,
-                                 _vector(rstd, T, torch.float32, "rstd"), g, kind, pds, ldds, pdx,
-                                 lddx, _vector(dgamma, H, torch.float32, "dgamma"),
-                                 _scratch(scratch, 0 if dgamma is None else 2048 * H),
-                                 _stream(stream)))
+           lib().moe_rmsnorm_bwd(T, H, pdy, lddy, ph, ldh, _flat(rstd, T, torch.float32, "rstd", dev),
+                                 g, kind, pds, ldds, pdx, lddx,
+                                 _flat(dgamma, H, torch.float32, "dgamma", dev),
+                                 _flat(scratch, 0 if dgamma is None else 2048 * H, None, "scratch",
+                                       dev), _on(stream, dev)))
 
 
 def moe_permute_fp8(cfg, codes, scales, idx, counts, offsets, row_of, token_of, sel_offsets,
@@ -694,27 +716,33 @@ def moe_permute_fp8(cfg, codes, scales, idx, counts, offsets, row_of, token_of, 
     [T, H / 128] (MXFP8: [T, H / 32]) into the layer's place in scratch, or into codes_perm
     [R, H] and scales_perm (the atoms of R rows)."""
     c = _cfg(cfg)
-    _here(codes, scales, idx, counts, offsets, row_of, token_of, sel_offsets, sel_tokens, scratch,
-          codes_perm, scales_perm)
+    dev, i32 = _device(), torch.int32
     R, need = _fp8_sizes(bytes(c))
-    mx, i32, T, E = c.dtype == 2, torch.int32, c.T, c.E
+    T, E, H, k = c.T, c.E, c.H, c.k
+    blocks = H // (32 if c.dtype == 2 else 128)
     if codes_perm is not None:
         need = 4352 + 4 * E * (-(-T // 256))
-    blocks = c.H // (32 if mx else 128)
     _check("moe_permute_fp8",
-           lib().moe_permute_fp8(c, _exactly(codes, T, c.H, "codes"),
-                                 _exactly(scales, T, blocks, "scales"),
-                                 _vector(idx, T * c.k, i32, "idx"),
-                                 _vector(counts, E, i32, "counts"),
-                                 _vector(offsets, E + 1, i32, "offsets"),
-                                 _vector(row_of, T * c.k, i32, "row_of"),
-                                 _vector(token_of, R, i32, "token_of"),
-                                 _vector(sel_offsets, E + 1, i32, "sel_offsets"),
-                                 _vector(sel_tokens, T * c.k, i32, "sel_tokens"),
-                                 _rows(codes_perm, R, c.H, None, "codes_perm"),
-                                 _vector(scales_perm, -(-R // 128) * -(-blocks // 4) * 512,
-                                         torch.uint8, "scales_perm"),
-                                 _scratch(scratch, need), _stream(stream)))
+           lib().moe_permute_fp8(c, _bytes2(codes, T, H, "codes", dev),
+                                 _bytes2(scales, T, blocks, "scales", dev),
+                                 _flat(idx, T * k, i32, "idx", dev),
+                                 _flat(counts, E, i32, "counts", dev),
+                                 _flat(offsets, E + 1, i32, "offsets", dev),
+                                 _flat(row_of, T * k, i32, "row_of", dev),
+                                 _flat(token_of, R, i32, "token_of", dev),
+                                 _flat(sel_offsets, E + 1, i32, "sel_offsets", dev),
+                                 _flat(sel_tokens, T * k, i32, "sel_tokens", dev),
+                                 _bytes2(codes_perm, R, H, "codes_perm", dev, exact=False),
+                                 _flat(scales_perm, -(-R // 128) * -(-blocks // 4) * 512,
+                                       torch.uint8, "scales_perm", dev),
+                                 _flat(scratch, need, None, "scratch", dev), _on(stream, dev)))
+
+
+@functools.lru_cache(maxsize=64)
+def _fp8_sizes(config: bytes):
+    """Rows of an FP8 layer's buffers and its scratch."""
+    s = moe_query_sizes(MoEConfig.from_buffer_copy(config))
+    return s.rows_max, s.scratch_bytes
 
 
 # ---------------------------------------------------------------- products of free form
@@ -722,7 +750,7 @@ class Int4Tensor:
     """Weights [groups, N, K] in 4-bit integers: codes [groups, N, K / 2] (uint8, the even element
     in the low four bits), scales [groups, K / group, N] (bf16) and zeros (uint8, of the scales'
     shape; None: 8 everywhere); w = scale * (code - zero)."""
-    __slots__ = ("codes", "scales", "zeros", "_struct")
+    __slots__ = ("codes", "scales", "zeros", "_struct", "_device")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None):
         self.codes, self.scales, self.zeros = codes, scales, zeros
@@ -738,10 +766,16 @@ class Int4Tensor:
             raise ValueError("zeros are contiguous uint8 of the scales' shape")
         if not codes.is_cuda or not scales.is_cuda or not (zeros is None or zeros.is_cuda):
             raise ValueError("codes, scales and zeros are on the GPU")
+        self._device = codes.get_device()
+        if scales.get_device() != self._device or \
+                zeros is not None and zeros.get_device() != self._device:
+            raise ValueError("codes, scales and zeros are on one GPU")
         self._struct = MoEInt4Tensor(K // scales.shape[1], g, N, K, codes.data_ptr(),
                                      scales.data_ptr(), None if zeros is None else zeros.data_ptr())
 
-    def struct(self) -> MoEInt4Tensor:
+    def struct(self, dev: int) -> MoEInt4Tensor:
+        if self._device != dev:
+            raise ValueError("codes, scales and zeros are on the current GPU")
         return self._struct
 
 
@@ -762,11 +796,11 @@ def alloc_product_scratch(device="cuda") -> torch.Tensor:
     return torch.zeros(product_scratch_bytes(), dtype=torch.uint8, device=device)
 
 
-def _segments(counts, offsets, groups: int):
+def _segments(counts, offsets, groups: int, dev: int):
     if counts is not None and counts.numel() != groups:
         raise ValueError("one count per group")
-    return (_vector(counts, groups, torch.int32, "counts"),
-            _vector(offsets, groups, torch.int32, "offsets"))
+    return (_flat(counts, groups, torch.int32, "counts", dev),
+            _flat(offsets, groups, torch.int32, "offsets", dev))
 
 
 def moe_int4_grouped_gemm(x, w: Int4Tensor, counts, offsets, out, scratch, swiglu: bool = False,
@@ -774,31 +808,33 @@ def moe_int4_grouped_gemm(x, w: Int4Tensor, counts, offsets, out, scratch, swigl
     """out [rows, N] = every group's rows of x [rows, K] by w [groups, N, K]; swiglu: out
     [rows, N / 2] = silu(first half of the columns) * second half. counts, offsets: int32
     [groups], or None for one group of all rows."""
-    s = w.struct()
-    rows = x.shape[0]
-    _here(x, w.codes, w.scales, w.zeros, counts, offsets, out, scratch)
-    px, ldx = _strided(x, rows, s.K, "x")
-    po, ldo = _strided(out, rows, s.N // 2 if swiglu else s.N, "out")
-    pc, pf = _segments(counts, offsets, s.groups)
+    dev = _device()
+    s = w.struct(dev)
+    rows, N = x.shape[0], s.N
+    px, ldx = _strided(x, rows, s.K, "x", dev)
+    po, ldo = _strided(out, rows, N // 2 if swiglu else N, "out", dev)
+    pc, pf = _segments(counts, offsets, s.groups, dev)
     _check("moe_int4_grouped_gemm",
            lib().moe_int4_grouped_gemm(s, rows, px, ldx, pc, pf, 1 if swiglu else 0, po, ldo,
-                                       _scratch(scratch, product_scratch_bytes()), _stream(stream)))
+                                       _flat(scratch, product_scratch_bytes(), None, "scratch", dev),
+                                       _on(stream, dev)))
 
 
 def moe_int4_dequantize(w: Int4Tensor, out, stream=None):
     """out [groups, N, K] bf16 = the weights."""
-    s = w.struct()
-    _here(w.codes, w.scales, w.zeros, out)
-    if tuple(out.shape) != (s.groups, s.N, s.K) or out.dtype is not torch.bfloat16 or \
-            not out.is_contiguous() or not out.is_cuda:
-        raise ValueError("out is contiguous bf16 [groups, N, K], on the GPU")
-    _check("moe_int4_dequantize", lib().moe_int4_dequantize(s, out.data_ptr(), _stream(stream)))
+    dev = _device()
+    s = w.struct(dev)
+    if tuple(out.shape) != (s.groups, s.N, s.K):
+        raise ValueError("out is bf16 [groups, N, K]")
+    _check("moe_int4_dequantize",
+           lib().moe_int4_dequantize(s, _flat(out, 0, torch.bfloat16, "out", dev), _on(stream, dev)))
 
 
-def _matrices(w, what: str):
+def _matrices(w, what: str, dev: int):
     """Address and sizes of contiguous bf16 [groups, N, K]."""
-    if w.dim() != 3 or w.dtype is not torch.bfloat16 or not w.is_contiguous() or not w.is_cuda:
-        raise ValueError(f"{what} is contiguous bf16 [groups, N, K], on the GPU")
+    if w.dim() != 3 or w.dtype is not torch.bfloat16 or not w.is_contiguous() or \
+            w.get_device() != dev:
+        raise ValueError(f"{what} is contiguous bf16 [groups, N, K], on the current GPU")
     return (w.data_ptr(), *w.shape)
 
 
@@ -807,53 +843,46 @@ def moe_grouped_gemm(x, w, counts, offsets, out, scratch, add=None, expected_row
     """out [rows, N] = every group's rows of x [rows, K] by w [groups, N, K] (+ add). counts,
     offsets: int32 [groups], or None for one group of all rows; expected_rows: the most rows of
     a group that the caller expects, 0 where it does not know."""
-    pw, G, N, K = _matrices(w, "w")
+    dev = _device()
+    pw, G, N, K = _matrices(w, "w", dev)
     rows = x.shape[0]
-    _here(x, w, counts, offsets, out, scratch, add)
-    px, ldx = _strided(x, rows, K, "x")
-    po, ldo = _strided(out, rows, N, "out")
-    pa, lda = _strided(add, rows, N, "add")
-    pc, pf = _segments(counts, offsets, G)
+    px, ldx = _strided(x, rows, K, "x", dev)
+    po, ldo = _strided(out, rows, N, "out", dev)
+    pa, lda = _strided(add, rows, N, "add", dev)
+    pc, pf = _segments(counts, offsets, G, dev)
     _check("moe_grouped_gemm",
-           lib().moe_grouped_gemm(G, rows, N, K, px, ldx, pw, pc, pf, pa, lda, po, ldo,
-                                  expected_rows, _scratch(scratch, product_scratch_bytes()),
-                                  _stream(stream)))
+           lib().moe_grouped_gemm(G, rows, N, K, px, ldx, pw, pc, pf, pa, lda, po, ldo, expected_rows,
+                                  _flat(scratch, product_scratch_bytes(), None, "scratch", dev),
+                                  _on(stream, dev)))
 
 
 def moe_grouped_gemm_dgrad(dy, w, counts, offsets, dx, scratch, add=None, stream=None):
     """dx [rows, K] = every group's rows of dy [rows, N] times w [groups, N, K] (+ add)."""
-    pw, G, N, K = _matrices(w, "w")
+    dev = _device()
+    pw, G, N, K = _matrices(w, "w", dev)
     rows = dy.shape[0]
-    _here(dy, w, counts, offsets, dx, scratch, add)
-    py, ldy = _strided(dy, rows, N, "dy")
-    px, ldx = _strided(dx, rows, K, "dx")
-    pa, lda = _strided(add, rows, K, "add")
-    pc, pf = _segments(counts, offsets, G)
+    py, ldy = _strided(dy, rows, N, "dy", dev)
+    px, ldx = _strided(dx, rows, K, "dx", dev)
+    pa, lda = _strided(add, rows, K, "add", dev)
+    pc, pf = _segments(counts, offsets, G, dev)
     _check("moe_grouped_gemm_dgrad",
            lib().moe_grouped_gemm_dgrad(G, rows, N, K, py, ldy, pw, pc, pf, pa, lda, px, ldx,
-                                        _scratch(scratch, product_scratch_bytes()),
-                                        _stream(stream)))
+                                        _flat(scratch, product_scratch_bytes(), None, "scratch", dev),
+                                        _on(stream, dev)))
 
 
 def moe_grouped_gemm_wgrad(dy, x, counts, offsets, dw, scratch, stream=None):
     """dw [groups, N, K] = the sum over every group's rows of dy [rows, N] by x [rows, K]."""
-    pw, G, N, K = _matrices(dw, "dw")
+    dev = _device()
+    pw, G, N, K = _matrices(dw, "dw", dev)
     rows = dy.shape[0]
-    _here(dy, x, counts, offsets, dw, scratch)
-    py, ldy = _strided(dy, rows, N, "dy")
-    px, ldx = _strided(x, rows, K, "x")
-    pc, pf = _segments(counts, offsets, G)
+    py, ldy = _strided(dy, rows, N, "dy", dev)
+    px, ldx = _strided(x, rows, K, "x", dev)
+    pc, pf = _segments(counts, offsets, G, dev)
     _check("moe_grouped_gemm_wgrad",
            lib().moe_grouped_gemm_wgrad(G, rows, N, K, py, ldy, px, ldx, pc, pf, pw,
-                                        _scratch(scratch, product_scratch_bytes()),
-                                        _stream(stream)))
-
-
-@functools.lru_cache(maxsize=64)
-def _fp8_sizes(config: bytes):
-    """Rows of an FP8 layer's buffers and its scratch."""
-    s = moe_query_sizes(MoEConfig.from_buffer_copy(config))
-    return s.rows_max, s.scratch_bytes
+                                        _flat(scratch, product_scratch_bytes(), None, "scratch", dev),
+                                        _on(stream, dev)))
 
 
 def moe_last_device_status(scratch, stream=None) -> int:

@@ -1,147 +1,101 @@
 // Grouped products of ragged rows on the fifth-generation tensor cores: for the rows r of every
 // group g, which follow each other without padding at any offset,
-//   forward          y[r] = x[r] W[g]^T         (A x, B W, both K-major)
-//   data gradient    dx[r] = dy[r] W[g]         (B MN-major: W read as it lies)
-//   weight gradient  dW[g] = sum of dy[r]^T x[r] (both MN-major, the rows reduced over)
-// in one kernel, a persistent CTA per SM: TMA producer, MMA issuer, four epilogue warps, two
-// accumulators in tensor memory, as in the experts' FFN. What the raggedness adds:
+//   forward          y[r] = x[r] W[g]^T
+//   data gradient    dx[r] = dy[r] W[g]
+//   weight gradient  dW[g] = sum of dy[r]^T x[r]
+// by CTA pairs (tcgen05 cta_group::2, M = 256, accumulators of up to 256 columns, two of them in
+// tensor memory so that one is drained while the next is summed).
+//
+// The first two take W's features as M and the rows as N: the instruction's N is any multiple
+// of 16, so a group's rows are cut into equal tiles of at most 256 without padding (512 rows an
+// expert on average: tiles of 128 rows as M multiplied an eighth of padding), and the features
+// are the dimension that is a multiple of the tile. What that costs is a transposed epilogue:
+// a thread holds one feature of 32 rows, and the tile is turned in shared memory on its way to
+// plain 16-byte stores, which need no wait and are masked row by row.
+//
+// A TMA request costs its issuer some 200 clocks whatever its size, and a k-block of a 256 x 256
+// tile lasts 512: each operand comes in one request a CTA (a map of its own for every height of
+// the row tile, chunked maps for operands that lie along M or N), issued by a warp each.
+//
+// What the raggedness adds:
 //   - the weights' maps have the expert as a dimension of their own, so that a box that passes
 //     an expert's last row or column reads zeros and not the next expert's;
-//   - a tile's rows past its group's end are the next group's (each row of A makes its own row
-//     of the product alone); the epilogue leaves them out: 32 rows that are all the group's go
-//     by TMA, the last few lane by lane;
-//   - the weight gradient's last block of rows holds the next group's rows in both operands:
-//     the issuing warp zeroes them in shared memory (both: zero times a NaN is one).
+//   - a tile's rows past its group's end are the next group's; each makes its own row of the
+//     product alone, which is not stored;
+//   - the weight gradient reduces over the rows: a warp of each CTA zeroes the next group's rows
+//     of the last block in both operands (zero times a NaN is one) before it hands the stage to
+//     the pair's MMAs.
 #include "gemm_common.cuh"
 
 namespace moe {
 namespace {
 
 using gg::BK;
-using gg::BM;
-using gg::kThreads;
 using gg::kWaitBudget;
 
 enum Mode : int { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 
-constexpr int kCtrl = 5120;
-constexpr int kOutBox = 32 * 128;               // 32 rows x 64 bf16
+constexpr int kPairThreads = 256;               // A's loads, MMAs, fixer, B's loads, four epilogue warps
+constexpr int kM = 256;                         // features of a pair tile
+constexpr int kStages = 6;
+constexpr int kABytes = 128 * BK * 2;           // of each CTA
+constexpr int kStageBytes = 2 * kABytes;
+constexpr int kBox = 4096;                      // an epilogue warp's: 32 x 32 fp32 or 32 x 64 bf16
+constexpr int kEpiWarps = 4;
+constexpr int kCtrl = 4096;
+constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kBox + kCtrl + 1024;
+static_assert(kSmem <= 232448, "shared memory");
 
-template <int BN>
-struct Cfg {
-  static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-  static constexpr int A_BYTES = BM * BK * 2;
-  static constexpr int STAGE = A_BYTES + BN * BK * 2;
-  static constexpr int SMEM = STAGES * STAGE + kCtrl + 4 * kOutBox + 1024;
+// a, b: one request a k-block and CTA: 128 features; 16 (i + 1) rows (b[i]), or all of a weight
+// gradient's columns (b[0]). a2, b2: 64 columns of an operand that lies along M or N, where the
+// last ones are not a whole chunk of 64.
+struct Maps {
+  CUtensorMap a, a2, b2, b[8];
 };
-static_assert(Cfg<256>::SMEM <= 232448 && Cfg<128>::SMEM <= 232448 && Cfg<64>::SMEM <= 232448,
-              "shared memory");
 
-// 64 columns of 32 rows, one row a lane, from tensor memory to the output.
 template <int MODE>
-__device__ __forceinline__ void store64(const RaggedProduct& p, const CUtensorMap* tmC,
-                                        uint32_t taddr, bool zero, int g, int64_t row, int rows_left,
-                                        int out_row, int col, int lane, uint8_t* stage,
-                                        uint32_t stage_u32) {
-  uint32_t r0[32], r1[32];
-  if (zero) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) r0[i] = r1[i] = 0u;
-  } else {
-    ptx::tmem_ld32(taddr, r0);
-    ptx::tmem_ld32(taddr + 32, r1);
-    ptx::tmem_ld_wait();
-  }
-  if (MODE != kWgrad && p.add && lane < rows_left) {
-    const __nv_bfloat16* src = p.add + (row + lane) * p.ldadd + col;
-#pragma unroll
-    for (int v = 0; v < 8; ++v) {
-      if (col + 8 * v >= p.cols) break;
-      float f[8];
-      unpack8(*reinterpret_cast<const uint4*>(src + 8 * v), f);
-      uint32_t* r = v < 4 ? r0 + 8 * v : r1 + 8 * (v - 4);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + f[i]);
-    }
-  }
-  uint4 o[8];
-  {
-    uint4 a[4], b[4];
-    gg::pack_slice(r0, a);
-    gg::pack_slice(r1, b);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      o[v] = a[v];
-      o[4 + v] = b[v];
-    }
-  }
-  if (MODE != kWgrad && rows_left < 32) {
-    if (lane < rows_left) {
-      __nv_bfloat16* dst = p.out + (row + lane) * p.ldo + col;
-#pragma unroll
-      for (int v = 0; v < 8; ++v)
-        if (col + 8 * v < p.cols) stg_v4(dst + 8 * v, o[v]);
-    }
-    return;
-  }
-  // the staging box is free once TMA has read the previous one
-  if (lane == 0) ptx::tma_store_wait_read();
-  __syncwarp();
-  uint8_t* rowp = stage + lane * 128;             // chunk j of row r at j ^ (r & 7)
-#pragma unroll
-  for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) = o[j];
-  ptx::fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    if (MODE == kWgrad) ptx::tma_store_3d(tmC, stage_u32, col, out_row, g);
-    else ptx::tma_store_2d(tmC, stage_u32, col, (int)row);
-    ptx::tma_store_commit();
-  }
-}
-
-template <int MODE, int BN>
-__global__ void __launch_bounds__(kThreads, 1)
-ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmC, const RaggedProduct p) {
-  using C = Cfg<BN>;
-  constexpr int STAGES = C::STAGES;
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* out_stage = smem_raw + (base - raw) + STAGES * C::STAGE;
-  const uint32_t out_stage_u32 = base + STAGES * C::STAGE;
-  uint8_t* ctrl = out_stage + 4 * kOutBox;
-  const uint32_t ctrl_u = out_stage_u32 + 4 * kOutBox;
-  const uint32_t bar_full = ctrl_u, bar_empty = ctrl_u + 64;       // [STAGES] each
-  const uint32_t bar_tfull = ctrl_u + 128, bar_tempty = ctrl_u + 144, bar_drain = ctrl_u + 160;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 192);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 196);
-  int* prefix = reinterpret_cast<int*>(ctrl + 256);       // [kMaxGroups + 1] tiles
-  int* s_off = reinterpret_cast<int*>(ctrl + 1536);       // [kMaxGroups]
-  int* s_cnt = reinterpret_cast<int*>(ctrl + 2688);       // [kMaxGroups]
-  int* tmp = reinterpret_cast<int*>(ctrl + 3840);         // [33]
+  uint8_t* boxes = smem_raw + (base - raw) + kStages * kStageBytes;
+  uint8_t* ctrl = boxes + kEpiWarps * kBox;
+  const uint32_t ctrl_u = base + kStages * kStageBytes + kEpiWarps * kBox;
+  // per stage: loaded (what the MMAs wait for, in the even CTA), read, loaded for the fixer
+  const uint32_t bar_full = ctrl_u, bar_empty = ctrl_u + 48, bar_tail = ctrl_u + 96;
+  const uint32_t bar_tfull = ctrl_u + 144, bar_tempty = ctrl_u + 160, bar_drain = ctrl_u + 176;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 352);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 356);
+  int* prefix = reinterpret_cast<int*>(ctrl + 384);        // [kMaxGroups + 1] pair tiles
+  int* s_off = reinterpret_cast<int*>(ctrl + 1440);        // [kMaxGroups]
+  int* s_cnt = reinterpret_cast<int*>(ctrl + 2496);        // [kMaxGroups]
+  int* tmp = reinterpret_cast<int*>(ctrl + 3552);          // [33]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int NT = (p.cols + BN - 1) / BN;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
   if (tid == 0) {
     *abort_flag = 0;
-    for (int s = 0; s < STAGES; ++s) {
-      ptx::mbar_init(bar_full + 8 * s, 1);
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(bar_full + 8 * s, 2);                 // A's loader twice, or both fixers
       ptx::mbar_init(bar_empty + 8 * s, 1);
+      ptx::mbar_init(bar_tail + 8 * s, 1);
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(bar_tfull + 8 * a, 1);
-      ptx::mbar_init(bar_tempty + 8 * a, 128);
+      ptx::mbar_init(bar_tempty + 8 * a, 2 * kEpiWarps);
     }
     ptx::mbar_init(bar_drain, 1);
     ptx::fence_mbar_init();
-    ptx::tma_prefetch_desc(&tmA);
-    ptx::tma_prefetch_desc(&tmB);
-    ptx::tma_prefetch_desc(&tmC);
+    ptx::tma_prefetch_desc(&maps.a);
+    ptx::tma_prefetch_desc(&maps.b[MODE == kWgrad ? 0 : 7]);
   }
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
-  for (int g = tid; g < p.G; g += kThreads) {
+  // features: M tiles; columns: what N runs over (rows of the group, or the gradient's columns)
+  const int FT = (p.feat + kM - 1) / kM, CT = (p.cols + p.tile - 1) / p.tile;
+  for (int g = tid; g < p.G; g += kPairThreads) {
     int c = (int)p.rows, o = 0;
     if (p.counts) {
       c = p.counts[g];
@@ -153,81 +107,109 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     }
     s_cnt[g] = c;
     s_off[g] = o;
-    prefix[g] = ((MODE == kWgrad ? p.out_rows : c) + BM - 1) / BM * NT;
+    prefix[g] = FT * (MODE == kWgrad ? CT : (c + p.tile - 1) / p.tile);
   }
   __syncthreads();
   const int total = block_exclusive_scan(prefix, p.G, tmp);
   if (tid == 0) prefix[p.G] = total;
   __syncthreads();
-  if ((int)blockIdx.x >= total) return;
+  if (cluster >= total) return;                            // both CTAs of the pair leave together
 
   if (warp == 1) {
-    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 2 * BN);
-    ptx::tmem_relinquish();
+    ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish_pair();
   }
   ptx::tc_fence_before();
   __syncthreads();
+  ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
   struct Tile {
-    int g, mt, nt, nk;
+    int g, f0, n0, n, nk;           // features from f0, columns (rows of the group) n0 .. n0 + n - 1
   };
   auto tile_at = [&](int tile) {
     Tile t;
     t.g = gg::find_group(prefix, p.G, tile);
-    const int local = tile - prefix[t.g];
-    if (MODE == kWgrad) {
-      // n fastest: tiles that run together share A's columns
-      t.nt = local % NT;
-      t.mt = local / NT;
-      t.nk = (s_cnt[t.g] + BK - 1) / BK;
+    const int local = tile - prefix[t.g], c = s_cnt[t.g];
+    if constexpr (MODE == kWgrad) {
+      // columns fastest: pairs that run together share A's columns
+      t.f0 = local / CT * kM;
+      t.n0 = local % CT * p.tile;
+      t.n = p.tile;
+      t.nk = (c + BK - 1) / BK;
     } else {
-      // m fastest: they share the expert's weights
-      const int mt = (s_cnt[t.g] + BM - 1) / BM;
-      t.mt = local % mt;
-      t.nt = local / mt;
+      // rows fastest (they share the expert's weights), cut into equal tiles of whole 32s
+      const int nt = (c + p.tile - 1) / p.tile, size = ((c + nt - 1) / nt + 31) & ~31;
+      t.f0 = local / nt * kM;
+      t.n0 = local % nt * size;
+      t.n = min(size, ((c - t.n0) + 31) & ~31);
       t.nk = (p.red + BK - 1) / BK;
     }
     return t;
   };
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
+    // A's loader, B's loader
+    const bool is_a = warp == 0;
     if (lane == 0) {
-      uint32_t stage = 0, phase = 0, issued = 0, issued_phase = 0;
+      uint32_t stage = 0, phase = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-        const Tile t = tile_at(tile);
+      uint32_t leader_full[kStages];
+#pragma unroll
+      for (int s = 0; s < kStages; ++s) leader_full[s] = ptx::mapa_shared(bar_full + 8 * s, 0);
+      for (int pt = cluster; pt < total && ok; pt += nclusters) {
+        const Tile t = tile_at(pt);
+        const int half = t.n >> 1, r = s_off[t.g];
+        const int f0 = t.f0 + (int)rank * 128, c0 = t.n0 + (int)rank * half;
+        const uint32_t bytes = kABytes + half * BK * 2;
+        // whole chunks of 64 columns come together (also where none of the 128 is the tensor's)
+        const bool a_whole = MODE == kFwd || f0 + 128 <= (p.feat & ~63) || (f0 >= p.feat && p.feat >= 64);
+        const bool b_whole = MODE != kWgrad || c0 + half <= (p.cols & ~63) || (c0 >= p.cols && p.cols >= 64);
         for (int kb = 0; kb < t.nk; ++kb) {
           if (!ptx::mbar_wait(bar_empty + 8 * stage, phase ^ 1u, kWaitBudget, abort_flag)) {
             ok = false;
             break;
           }
-          const uint32_t fb = bar_full + 8 * stage;
-          ptx::mbar_arrive_expect_tx(fb, C::STAGE);
-          const uint32_t sA = base + stage * C::STAGE, sB = sA + C::A_BYTES;
+          const uint32_t sA = base + stage * kStageBytes, sB = sA + kABytes;
           const int k0 = kb * BK;
-          if (MODE == kWgrad) {
-            const int r = s_off[t.g] + k0;
-#pragma unroll
-            for (int j = 0; j < BM / 64; ++j)
-              ptx::tma_load_2d(sA + j * 8192, &tmA, fb, t.mt * BM + 64 * j, r);
-#pragma unroll
-            for (int j = 0; j < BN / 64; ++j)
-              ptx::tma_load_2d(sB + j * 8192, &tmB, fb, t.nt * BN + 64 * j, r);
-          } else {
-            ptx::tma_load_2d(sA, &tmA, fb, k0, s_off[t.g] + t.mt * BM);
-            if (MODE == kFwd) {
-              ptx::tma_load_3d(sB, &tmB, fb, k0, t.nt * BN, t.g);
-            } else {
-#pragma unroll
-              for (int j = 0; j < BN / 64; ++j)
-                ptx::tma_load_3d(sB + j * 8192, &tmB, fb, t.nt * BN + 64 * j, k0, t.g);
+          // both CTAs' loads count on the even CTA's barrier; a weight gradient's last block goes
+          // to each CTA's own fixer first
+          const bool tail = MODE == kWgrad && s_cnt[t.g] - k0 < BK;
+          const uint32_t fb = tail ? bar_tail + 8 * stage : leader_full[stage];
+          if (is_a) {
+            if (tail) {
+              ptx::mbar_arrive_expect_tx(fb, bytes);
+            } else if (rank == 0) {
+              ptx::mbar_arrive_expect_tx(bar_full + 8 * stage, 2 * bytes);
+              ptx::mbar_arrive(bar_full + 8 * stage);
             }
           }
-          issued |= 1u << stage;
-          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-          if (++stage == STAGES) {
+          if constexpr (MODE == kWgrad) {
+            const CUtensorMap* m = is_a ? &maps.a : &maps.b[0];
+            const CUtensorMap* m2 = is_a ? &maps.a2 : &maps.b2;
+            const uint32_t to = is_a ? sA : sB;
+            const int col = is_a ? f0 : c0;
+            if (is_a ? a_whole : b_whole) {
+              if (tail) ptx::tma_load_3d(to, m, fb, 0, r + k0, col / 64);
+              else ptx::tma_load_3d_pair(to, m, fb, 0, r + k0, col / 64);
+            } else {
+              for (int j = 0; j < (is_a ? 2 : half / 64); ++j)
+                if (tail) ptx::tma_load_2d(to + j * 8192, m2, fb, col + 64 * j, r + k0);
+                else ptx::tma_load_2d_pair(to + j * 8192, m2, fb, col + 64 * j, r + k0);
+            }
+          } else if (!is_a) {
+            ptx::tma_load_2d_pair(sB, &maps.b[half / 16 - 1], fb, k0, r + c0);
+          } else if (MODE == kFwd) {
+            ptx::tma_load_3d_pair(sA, &maps.a, fb, k0, f0, t.g);
+          } else if (a_whole) {
+            ptx::tma_load_4d_pair(sA, &maps.a, fb, 0, k0, f0 / 64, t.g);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              ptx::tma_load_3d_pair(sA + j * 8192, &maps.a2, fb, f0 + 64 * j, k0, t.g);
+          }
+          if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -236,91 +218,136 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
       if (!ok) {
         record_status(p.status, MOE_ERR_TIMEOUT);
         *abort_flag = 1;
+        // loads already issued land within microseconds; give them time
+        const long long t0 = clock64();
+        while (clock64() - t0 < 200000) {
+        }
       }
-      // every load issued must land before the CTA may exit
-      for (int s = 0; s < STAGES; ++s)
-        if (issued & (1u << s))
-          ptx::mbar_wait(bar_full + 8 * s, (issued_phase >> s) & 1u, kWaitBudget, nullptr);
     }
   } else if (warp == 1) {
-    // the whole warp walks the blocks (a weight gradient's last one is zeroed by all lanes),
-    // one lane issues
-    constexpr int A_MN = MODE == kWgrad, B_MN = MODE != kFwd;
-    constexpr uint32_t IDESC = ptx::idesc_bf16(BM, BN, A_MN, B_MN);
-    uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
-    bool ok = true, issued = false;
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const Tile t = tile_at(tile);
-      ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_tempty + 8 * acc, acc_phase ^ 1u, kWaitBudget,
-                                                  abort_flag));
-      if (!ok) break;
-      ptx::tc_fence_after();
-      const uint32_t d = tmem_base + acc * BN;
-      for (int kb = 0; kb < t.nk; ++kb) {
-        ok = __all_sync(0xffffffffu,
-                        ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget, abort_flag));
-        if (!ok) break;
-        const uint32_t sA = base + stage * C::STAGE, sB = sA + C::A_BYTES;
-        if (MODE == kWgrad) {
-          const int valid = s_cnt[t.g] - kb * BK;
-          if (valid < BK) {
-            // rows valid .. 63 of every 64-column chunk of A and B (128 bytes a row)
-            for (int j = 0; j < (BM + BN) / 64; ++j)
-              for (int b = valid * 128 + lane * 16; b < 8192; b += 512)
-                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};"
-                             :: "r"(sA + j * 8192 + b), "r"(0u) : "memory");
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-          }
+    if (lane == 0 && rank == 0) {
+      constexpr int A_MN = MODE != kFwd, B_MN = MODE == kWgrad;
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+      bool ok = true, issued = false;
+      const uint32_t peer_tfull[2] = {ptx::mapa_shared(bar_tfull, 1),
+                                      ptx::mapa_shared(bar_tfull + 8, 1)};
+      for (int pt = cluster; pt < total && ok; pt += nclusters) {
+        const Tile t = tile_at(pt);
+        const uint32_t idesc = ptx::idesc_bf16(kM, t.n, A_MN, B_MN);
+        if (!ptx::mbar_wait_cluster(bar_tempty + 8 * acc, acc_phase ^ 1u, kWaitBudget, abort_flag)) {
+          ok = false;
+          break;
         }
         ptx::tc_fence_after();
-        if (lane == 0) {
+        const uint32_t d = tmem_base + acc * 256;
+        for (int kb = 0; kb < t.nk; ++kb) {
+          ok = MODE == kWgrad
+                   ? ptx::mbar_wait_cluster(bar_full + 8 * stage, phase, kWaitBudget, abort_flag)
+                   : ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget, abort_flag);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t sA = base + stage * kStageBytes, sB = sA + kABytes;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk) {
             const uint64_t ad = A_MN ? ptx::smem_desc_sw128(sA + kk * 2048, 8192, 1024)
                                      : ptx::smem_desc_sw128(sA + kk * 32, 16, 1024);
             const uint64_t bd = B_MN ? ptx::smem_desc_sw128(sB + kk * 2048, 8192, 1024)
                                      : ptx::smem_desc_sw128(sB + kk * 32, 16, 1024);
-            ptx::mma_bf16(d, ad, bd, IDESC, (kb | kk) ? 1u : 0u);
+            ptx::mma_bf16_pair(d, ad, bd, idesc, (kb | kk) ? 1u : 0u);
           }
-          ptx::mma_commit(bar_empty + 8 * stage);
+          issued = true;
+          ptx::mma_commit_pair(bar_empty + 8 * stage, 3);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
-        __syncwarp();
-        issued = true;
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
+        if (!ok) break;
+        if (t.nk > 0) {
+          ptx::mma_commit_pair(bar_tfull + 8 * acc, 3);
+        } else {                                           // an empty group: nothing to wait for
+          ptx::mbar_arrive(bar_tfull + 8 * acc);
+          ptx::mbar_arrive_cluster(peer_tfull[acc]);
+        }
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
         }
       }
-      if (!ok) break;
-      if (lane == 0) {
-        if (t.nk > 0) ptx::mma_commit(bar_tfull + 8 * acc);
-        else ptx::mbar_arrive(bar_tfull + 8 * acc);     // an empty group: nothing to wait for
+      if (!ok) {
+        record_status(p.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
       }
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1u;
+      // every MMA issued by this thread is waited for before tensor memory is freed
+      if (issued) {
+        ptx::mma_commit_pair(bar_drain, 1);
+        ptx::mbar_wait(bar_drain, 0, kWaitBudget, nullptr);
       }
-    }
-    if (!ok && lane == 0) {
-      record_status(p.status, MOE_ERR_TIMEOUT);
-      *abort_flag = 1;
-    }
-    // every MMA issued by this thread is waited for before tensor memory is freed
-    if (issued && lane == 0) {
-      ptx::mma_commit(bar_drain);
-      ptx::mbar_wait(bar_drain, 0, kWaitBudget, nullptr);
     }
     __syncwarp();
+  } else if (warp == 2) {
+    if constexpr (MODE == kWgrad) {
+      uint32_t stage = 0, phases = 0;                      // phases: a bit per stage, of bar_tail
+      bool ok = true;
+      for (int pt = cluster; pt < total && ok; pt += nclusters) {
+        const Tile t = tile_at(pt);
+        const int valid = s_cnt[t.g] & (BK - 1);
+        if (valid) {
+          stage = (stage + t.nk - 1) % kStages;
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_tail + 8 * stage, (phases >> stage) & 1u,
+                                                      kWaitBudget, abort_flag));
+          if (!ok) break;
+          phases ^= 1u << stage;
+          // rows valid .. 63 of every 64-column chunk of A and B (128 bytes a row)
+          const uint32_t sA = base + stage * kStageBytes;
+          for (int j = 0; j < 2 + t.n / 128; ++j)
+            for (int b = valid * 128 + lane * 16; b < 8192; b += 512)
+              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};"
+                           :: "r"(sA + j * 8192 + b), "r"(0u) : "memory");
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(bar_full + 8 * stage, 0));
+          stage = (stage + 1) % kStages;
+        } else {
+          stage = (stage + t.nk) % kStages;
+        }
+      }
+      if (!ok && lane == 0) {
+        record_status(p.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+    }
   } else {
-    const int q = warp & 3;                              // tensor-memory lane quarter
-    uint8_t* stage = out_stage + (warp - 2) * kOutBox;
-    const uint32_t stage_u32 = out_stage_u32 + (warp - 2) * kOutBox;
+    // lane = feature
+    const int q = warp & 3;
+    uint8_t* box = boxes + q * kBox;
+    const uint32_t leader_tempty[2] = {ptx::mapa_shared(bar_tempty, 0),
+                                       ptx::mapa_shared(bar_tempty + 8, 0)};
+    const int fq = (int)rank * 128 + q * 32;               // this warp's features in a tile
     uint32_t acc = 0, acc_phase = 0;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-      const Tile t = tile_at(tile);
-      bool ok = ptx::mbar_wait(bar_tfull + 8 * acc, acc_phase, kWaitBudget, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
+    for (int pt = cluster; pt < total; pt += nclusters) {
+      const Tile t = tile_at(pt);
+      const int f = t.f0 + fq;
+      const int64_t row0 = (int64_t)s_off[t.g] + t.n0;
+      const int rows = MODE == kWgrad ? 0 : min(s_cnt[t.g] - t.n0, t.n);
+      // rows i0 + 8 v of a box, sixteen bytes (features fl .. fl + 7) each
+      const int i0 = lane >> 2, fl = f + 8 * (lane & 3);
+      const bool mine = MODE != kWgrad && fl < p.feat;
+      uint4 add[4];
+      auto fetch = [&](int j) {
+        if constexpr (MODE != kWgrad) {
+          if (!p.add) return;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int i = 32 * j + i0 + 8 * v;
+            if (mine && i < rows)
+              add[v] = *reinterpret_cast<const uint4*>(p.add + (row0 + i) * p.ldadd + fl);
+          }
+        }
+      };
+      fetch(0);
+      const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_tfull + 8 * acc, acc_phase,
+                                                             kWaitBudget, abort_flag));
       if (!ok) {
         if (lane == 0) {
           record_status(p.status, MOE_ERR_TIMEOUT);
@@ -329,33 +356,98 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         break;
       }
       ptx::tc_fence_after();
-      const int m0 = t.mt * BM + q * 32;
-      const int rows_left = (MODE == kWgrad ? p.out_rows : s_cnt[t.g]) - m0;
-      const int64_t row = (int64_t)s_off[t.g] + m0;
-      const uint32_t tbase = tmem_base + acc * BN + ((uint32_t)(q * 32) << 16);
-      if (rows_left > 0) {
+      const uint32_t tbase = tmem_base + acc * 256 + ((uint32_t)(q * 32) << 16);
+      if constexpr (MODE == kWgrad) {
+        // 32 features x 64 columns, a row a lane; 16-byte chunk j of row r at j ^ (r & 7)
 #pragma unroll 1
-        for (int c = 0; c < BN; c += 64) {
-          const int col = t.nt * BN + c;
-          if (col >= p.cols) break;
-          store64<MODE>(p, &tmC, tbase + c, t.nk == 0, t.g, row, rows_left, m0, col, lane, stage,
-                        stage_u32);
+        for (int c = 0; c < t.n; c += 64) {
+          const int col = t.n0 + c;
+          if (f >= p.feat || col >= p.cols) break;
+          uint32_t r0[32], r1[32];
+          if (t.nk == 0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r0[i] = r1[i] = 0u;
+          } else {
+            ptx::tmem_ld32(tbase + c, r0);
+            ptx::tmem_ld32(tbase + c + 32, r1);
+            ptx::tmem_ld_wait();
+          }
+          uint4 a[4], b[4];
+          gg::pack_slice(r0, a);
+          gg::pack_slice(r1, b);
+          uint8_t* rowp = box + lane * 128;
+          __syncwarp();                                    // the box before has been read
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) = a[j];
+            *reinterpret_cast<uint4*>(rowp + (((j + 4) ^ (lane & 7)) << 4)) = b[j];
+          }
+          __syncwarp();
+          // eight lanes a row of 128 bytes
+          __nv_bfloat16* out = p.out + ((int64_t)t.g * p.feat + f) * p.cols + col + 8 * (lane & 7);
+          if (col + 8 * (lane & 7) < p.cols) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+              const int i = (lane >> 3) + 4 * v;
+              if (f + i < p.feat)
+                stg_v4(out + (int64_t)i * p.cols,
+                       *reinterpret_cast<const uint4*>(box + i * 128 + (((lane & 7) ^ (i & 7)) << 4)));
+            }
+          }
+        }
+      } else if (f < p.feat) {
+        // 32 rows x 32 features in fp32, 128 bytes a row, 16-byte chunk c of row i at c ^ (i & 1):
+        // a feature's 32 stores and a row's eight-feature loads meet every bank once
+#pragma unroll 1
+        for (int j = 0; 32 * j < rows; ++j) {
+          uint32_t r[32];
+          ptx::tmem_ld32(tbase + 32 * j, r);
+          ptx::tmem_ld_wait();
+          __syncwarp();                                    // the box before has been read
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            *reinterpret_cast<uint32_t*>(box + i * 128 + (((lane >> 2) ^ (i & 1)) << 4) +
+                                         (lane & 3) * 4) = r[i];
+          __syncwarp();
+          uint4 o[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const uint8_t* b = box + (i0 + 8 * v) * 128;
+            const int c = 2 * (lane & 3), x = i0 & 1;
+            const float4 lo = *reinterpret_cast<const float4*>(b + ((c ^ x) << 4));
+            const float4 hi = *reinterpret_cast<const float4*>(b + (((c + 1) ^ x) << 4));
+            float e[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            if (p.add) {
+              float d[8];
+              unpack8(add[v], d);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) e[i] += d[i];
+            }
+            o[v] = pack8(e);
+          }
+          fetch(j + 1);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int i = 32 * j + i0 + 8 * v;
+            if (mine && i < rows) stg_v4(p.out + (row0 + i) * p.ldo + fl, o[v]);
+          }
         }
       }
       ptx::tc_fence_before();
-      ptx::mbar_arrive(bar_tempty + 8 * acc);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(leader_tempty[acc]);
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
       }
     }
-    if (lane == 0) ptx::tma_store_wait_all();
   }
   ptx::tc_fence_before();
   __syncthreads();
+  ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem_base, 2 * BN);
+    ptx::tmem_dealloc_pair(tmem_base, 512);
   }
 }
 
@@ -385,70 +477,83 @@ bool map3(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, int BN>
-cudaError_t run_ragged(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
-                       const RaggedProduct& p, cudaStream_t s) {
-  auto kern = ragged_gemm_kernel<MODE, BN>;
-  static PerDevice set;
-  const cudaError_t e = set_smem_once(set, kern, Cfg<BN>::SMEM);
-  if (e != cudaSuccess) return e;
-  return launch_early(kern, (unsigned)num_sms(), dim3(kThreads, 1, 1), Cfg<BN>::SMEM, s, a, b, c, p);
+// Columns of an operand that lies along M or N, 64 to a chunk, `chunks` of them and 64 rows to a
+// box: {64 columns of a chunk, rows, chunk, group}. Columns past the last whole chunk are not in it.
+bool chunk_map(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t ld,
+               uint64_t groups, uint32_t chunks) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = gg::encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {64, rows, cols / 64, groups};
+  cuuint64_t strides[3] = {ld * 2, 128, ld * rows * 2};
+  cuuint32_t box[4] = {64, 64, chunks, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, groups ? 4 : 3, const_cast<void*>(ptr), dims,
+            strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Columns of a tile: as wide as fills the SMs (a wider tile reads A less often, but few tiles
-// leave SMs without one, and a narrow output multiplies nothing by padding).
-int tile_columns(int cols, int64_t row_tiles) {
-  const int sms = num_sms();
-  for (int bn = 256; bn > 64; bn /= 2)
-    if (cols > bn / 2 && row_tiles * ((cols + bn - 1) / bn) >= sms) return bn;
-  return 64;
+template <int MODE>
+cudaError_t run_ragged(const Maps& m, const RaggedProduct& p, cudaStream_t s) {
+  auto kern = ragged_pair_kernel<MODE>;
+  static PerDevice set;
+  int grid = 0;
+  const cudaError_t e = pair_grid_once(set, kern, kPairThreads, kSmem, &grid);
+  if (e != cudaSuccess) return e;
+  return launch_early(kern, (unsigned)grid, dim3(kPairThreads, 1, 1), kSmem, s, m, p);
+}
+
+// Columns of a tile, 256 where that makes a tile for every pair of SMs, else fewer: a wide tile
+// reads the features' operand less often, few tiles leave SMs without one.
+int tile_columns(int64_t columns, int64_t others, int least) {
+  const int pairs = num_sms() / 2;
+  int tile = 256;
+  while (tile > least && others * ((columns + tile - 1) / tile) < pairs) tile /= 2;
+  return tile;
 }
 
 }  // namespace
 
-// Tiles of 128 rows and 64 columns at least, in 32 bits.
-bool ragged_fits(int64_t rows, int G, int64_t cols, int64_t out_rows) {
-  const int64_t m = out_rows ? (out_rows + 127) / 128 * G : rows / 128 + G;
-  return m * ((cols + 63) / 64) < (1LL << 31);
+// Tiles of 256 features and 64 columns at least, in 32 bits.
+bool ragged_fits(int64_t rows, int G, int64_t feat, int64_t cols) {
+  const int64_t n = cols ? (cols + 127) / 128 * G : rows / 64 + G;
+  return n * ((feat + kM - 1) / kM) < (1LL << 31);
 }
 
 cudaError_t launch_ragged_gemm(RaggedProduct p, int dgrad, const void* x, int64_t ldx,
                                const void* w, int N, int K, cudaStream_t s) {
-  p.cols = dgrad ? K : N;
+  p.feat = dgrad ? K : N;
   p.red = dgrad ? N : K;
-  p.out_rows = 0;
-  const int64_t tiles = p.rows / BM + (p.rows < p.G ? p.rows : p.G);
-  const int bn = tile_columns(p.cols, tiles);
-  CUtensorMap a, b, c;
-  if (!map2(&a, x, p.red, p.rows, ldx, 64, BM) || !map2(&c, p.out, p.cols, p.rows, p.ldo, 64, 32) ||
-      !map3(&b, w, K, N, p.G, 64, dgrad ? 64 : bn))
-    return cudaErrorInvalidValue;
-  if (dgrad)
-    return bn == 256   ? run_ragged<kDgrad, 256>(a, b, c, p, s)
-           : bn == 128 ? run_ragged<kDgrad, 128>(a, b, c, p, s)
-                       : run_ragged<kDgrad, 64>(a, b, c, p, s);
-  return bn == 256   ? run_ragged<kFwd, 256>(a, b, c, p, s)
-         : bn == 128 ? run_ragged<kFwd, 128>(a, b, c, p, s)
-                     : run_ragged<kFwd, 64>(a, b, c, p, s);
+  p.cols = 0;
+  p.tile = tile_columns(p.rows, (p.feat + kM - 1) / kM, 64);
+  Maps m;
+  for (int i = 0; i < 8; ++i)
+    if (!map2(&m.b[i], x, p.red, p.rows, ldx, 64, 16 * (i + 1))) return cudaErrorInvalidValue;
+  if (!map3(&m.a2, w, K, N, p.G, 64, dgrad ? 64 : 128)) return cudaErrorInvalidValue;
+  m.a = m.b2 = m.a2;
+  if (dgrad && K >= 64 && !chunk_map(&m.a, w, K, N, K, p.G, 2)) return cudaErrorInvalidValue;
+  return dgrad ? run_ragged<kDgrad>(m, p, s) : run_ragged<kFwd>(m, p, s);
 }
 
 cudaError_t launch_ragged_wgrad(RaggedProduct p, const void* dy, int64_t lddy, const void* x,
                                 int64_t ldx, int N, int K, cudaStream_t s) {
+  p.feat = N;
   p.cols = K;
-  p.out_rows = N;
   p.red = 0;
   p.add = nullptr;
-  const int bn = tile_columns(K, (int64_t)p.G * ((N + BM - 1) / BM));
-  CUtensorMap a, b, c;
+  p.tile = tile_columns(K, (int64_t)p.G * ((N + kM - 1) / kM), 128);
   // (without rows nothing is loaded: the maps are then of any valid extent)
-  const int64_t rows = p.rows > 0 ? p.rows : 1;
-  if (!map2(&a, p.rows > 0 ? dy : p.out, N, rows, p.rows > 0 ? lddy : (N + 7) / 8 * 8, 64, 64) ||
-      !map2(&b, p.rows > 0 ? x : p.out, K, rows, p.rows > 0 ? ldx : (K + 7) / 8 * 8, 64, 64) ||
-      !map3(&c, p.out, K, N, p.G, 64, 32))
+  const bool some = p.rows > 0;
+  const void *pa = some ? dy : p.out, *pb = some ? x : p.out;
+  const int64_t rows = some ? p.rows : 1, lda = some ? lddy : N, ldb = some ? ldx : K;
+  Maps m;
+  if (!map2(&m.a2, pa, N, rows, lda, 64, 64) || !map2(&m.b2, pb, K, rows, ldb, 64, 64))
     return cudaErrorInvalidValue;
-  return bn == 256   ? run_ragged<kWgrad, 256>(a, b, c, p, s)
-         : bn == 128 ? run_ragged<kWgrad, 128>(a, b, c, p, s)
-                     : run_ragged<kWgrad, 64>(a, b, c, p, s);
+  m.a = m.a2;
+  for (int i = 0; i < 8; ++i) m.b[i] = m.b2;
+  if ((N >= 64 && !chunk_map(&m.a, pa, N, rows, lda, 0, 2)) ||
+      (K >= 64 && !chunk_map(&m.b[0], pb, K, rows, ldb, 0, p.tile / 128)))
+    return cudaErrorInvalidValue;
+  return run_ragged<kWgrad>(m, p, s);
 }
 
 }  // namespace moe

@@ -381,11 +381,12 @@ struct RaggedProduct {
   __nv_bfloat16* out;
   int64_t ldo;
   int32_t* status;
-  // set by the launchers: the output's columns, the length reduced over (not the weight
-  // gradient's), the weight gradient's output rows
-  int cols, red, out_rows;
+  // set by the launchers: features (the output's columns; the weight gradient's rows), the length
+  // reduced over (not the weight gradient's), the weight gradient's columns, columns of a tile
+  int feat, red, cols, tile;
 };
-bool ragged_fits(int64_t rows, int G, int64_t cols, int64_t out_rows);
+// cols: of a weight gradient, else 0.
+bool ragged_fits(int64_t rows, int G, int64_t feat, int64_t cols);
 cudaError_t launch_ragged_gemm(RaggedProduct p, int dgrad, const void* x, int64_t ldx,
                                const void* w, int N, int K, cudaStream_t s);
 cudaError_t launch_ragged_wgrad(RaggedProduct p, const void* dy, int64_t lddy, const void* x,

@@ -269,7 +269,7 @@ moe_status moe_grouped_gemm_wgrad(int64_t groups, int64_t rows, int64_t N, int64
                                   void* scratch, void* stream) {
   OP_TRY(check_product(groups, rows, N, K, dw, counts, offsets, scratch));
   if (rows > 0) OP_REQUIRE(rows_ok(dy, lddy, N) && rows_ok(x, ldx, K));
-  if (!ragged_fits(rows, (int)groups, K, N)) return MOE_ERR_UNSUPPORTED;
+  if (!ragged_fits(rows, (int)groups, N, K)) return MOE_ERR_UNSUPPORTED;
   OP_CUDA(launch_ragged_wgrad(
       ragged_product(groups, rows, counts, offsets, nullptr, 0, dw, K, scratch), dy, lddy, x, ldx,
       (int)N, (int)K, (cudaStream_t)stream));
