@@ -35,13 +35,13 @@ using gg::kWaitBudget;
 
 enum Mode : int { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 
-constexpr int kPairThreads = 256;               // A's loads, MMAs, fixer, B's loads, four epilogue warps
+constexpr int kPairThreads = 384;               // A's loads, MMAs, fixer, B's loads, eight epilogue warps
 constexpr int kM = 256;                         // features of a pair tile
 constexpr int kStages = 6;
 constexpr int kABytes = 128 * BK * 2;           // of each CTA
 constexpr int kStageBytes = 2 * kABytes;
-constexpr int kBox = 4096;                      // an epilogue warp's: 32 x 32 fp32 or 32 x 64 bf16
-constexpr int kEpiWarps = 4;
+constexpr int kBox = 2048;                      // an epilogue warp's: 16 x 32 fp32 or 32 x 32 bf16
+constexpr int kEpiWarps = 8;
 constexpr int kCtrl = 4096;
 constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kBox + kCtrl + 1024;
 static_assert(kSmem <= 232448, "shared memory");
@@ -318,34 +318,35 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
       }
     }
   } else {
-    // lane = feature
-    const int q = warp & 3;
-    uint8_t* box = boxes + q * kBox;
+    // lane = feature; warps 4-7 take the even boxes of 32 columns, 8-11 the odd ones
+    const int q = warp & 3, odd = (warp - 4) >> 2;
+    uint8_t* box = boxes + (warp - 4) * kBox;
     const uint32_t leader_tempty[2] = {ptx::mapa_shared(bar_tempty, 0),
                                        ptx::mapa_shared(bar_tempty + 8, 0)};
     const int fq = (int)rank * 128 + q * 32;               // this warp's features in a tile
+    const int lr = lane >> 2, lc = lane & 3;               // four lanes a row of a box
     uint32_t acc = 0, acc_phase = 0;
     for (int pt = cluster; pt < total; pt += nclusters) {
       const Tile t = tile_at(pt);
       const int f = t.f0 + fq;
       const int64_t row0 = (int64_t)s_off[t.g] + t.n0;
-      const int rows = MODE == kWgrad ? 0 : min(s_cnt[t.g] - t.n0, t.n);
-      // rows i0 + 8 v of a box, sixteen bytes (features fl .. fl + 7) each
-      const int i0 = lane >> 2, fl = f + 8 * (lane & 3);
-      const bool mine = MODE != kWgrad && fl < p.feat;
-      uint4 add[4];
-      auto fetch = [&](int j) {
-        if constexpr (MODE != kWgrad) {
-          if (!p.add) return;
+      // rows of the tile that are this warp's to write, sixteen bytes (features fl .. fl + 7) a lane
+      const int fl = f + 8 * lc;
+      const int rows = MODE != kWgrad && fl < p.feat ? min(s_cnt[t.g] - t.n0, t.n) : 0;
+      uint4 add[4][4];
+      if constexpr (MODE != kWgrad) {
+        // every load of the tile is under way before its sums are waited for
+        if (p.add) {
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int i = 32 * j + i0 + 8 * v;
-            if (mine && i < rows)
-              add[v] = *reinterpret_cast<const uint4*>(p.add + (row0 + i) * p.ldadd + fl);
-          }
+          for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const int i = 64 * b + 32 * odd + 8 * v + lr;
+              if (i < rows)
+                add[b][v] = *reinterpret_cast<const uint4*>(p.add + (row0 + i) * p.ldadd + fl);
+            }
         }
-      };
-      fetch(0);
+      }
       const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_tfull + 8 * acc, acc_phase,
                                                              kWaitBudget, abort_flag));
       if (!ok) {
@@ -358,78 +359,78 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
       ptx::tc_fence_after();
       const uint32_t tbase = tmem_base + acc * 256 + ((uint32_t)(q * 32) << 16);
       if constexpr (MODE == kWgrad) {
-        // 32 features x 64 columns, a row a lane; 16-byte chunk j of row r at j ^ (r & 7)
-#pragma unroll 1
-        for (int c = 0; c < t.n; c += 64) {
-          const int col = t.n0 + c;
-          if (f >= p.feat || col >= p.cols) break;
-          uint32_t r0[32], r1[32];
+        // 32 features x 32 columns, a row a lane; 16-byte chunk j of row r at j ^ ((r >> 1) & 3). The
+        // next columns leave tensor memory while these are on their way.
+        const int end = f < p.feat ? min(t.n, p.cols - t.n0) : 0;
+        uint32_t r[32];
+        auto take = [&](int c) {
+          if (c >= end) return;
           if (t.nk == 0) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r0[i] = r1[i] = 0u;
+            for (int i = 0; i < 32; ++i) r[i] = 0u;
           } else {
-            ptx::tmem_ld32(tbase + c, r0);
-            ptx::tmem_ld32(tbase + c + 32, r1);
-            ptx::tmem_ld_wait();
+            ptx::tmem_ld32(tbase + c, r);
           }
-          uint4 a[4], b[4];
-          gg::pack_slice(r0, a);
-          gg::pack_slice(r1, b);
-          uint8_t* rowp = box + lane * 128;
+        };
+        take(32 * odd);
+#pragma unroll 1
+        for (int c = 32 * odd; c < end; c += 64) {
+          const int col = t.n0 + c + 8 * lc;
+          ptx::tmem_ld_wait();
+          uint4 a[4];
+          gg::pack_slice(r, a);
+          take(c + 64);
           __syncwarp();                                    // the box before has been read
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) = a[j];
-            *reinterpret_cast<uint4*>(rowp + (((j + 4) ^ (lane & 7)) << 4)) = b[j];
-          }
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = a[j];
           __syncwarp();
-          // eight lanes a row of 128 bytes
-          __nv_bfloat16* out = p.out + ((int64_t)t.g * p.feat + f) * p.cols + col + 8 * (lane & 7);
-          if (col + 8 * (lane & 7) < p.cols) {
+          if (col < p.cols) {
+            __nv_bfloat16* out = p.out + ((int64_t)t.g * p.feat + f + lr) * p.cols + col;
 #pragma unroll
-            for (int v = 0; v < 8; ++v) {
-              const int i = (lane >> 3) + 4 * v;
+            for (int v = 0; v < 4; ++v) {
+              const int i = lr + 8 * v;
               if (f + i < p.feat)
-                stg_v4(out + (int64_t)i * p.cols,
-                       *reinterpret_cast<const uint4*>(box + i * 128 + (((lane & 7) ^ (i & 7)) << 4)));
+                stg_v4(out + (int64_t)(8 * v) * p.cols,
+                       *reinterpret_cast<const uint4*>(box + i * 64 + ((lc ^ ((i >> 1) & 3)) << 4)));
             }
           }
         }
       } else if (f < p.feat) {
-        // 32 rows x 32 features in fp32, 128 bytes a row, 16-byte chunk c of row i at c ^ (i & 1):
-        // a feature's 32 stores and a row's eight-feature loads meet every bank once
-#pragma unroll 1
-        for (int j = 0; 32 * j < rows; ++j) {
+        // 16 rows x 32 features in fp32 at a time, 128 bytes a row, 16-byte chunk c of row i at
+        // c ^ (i & 1): a feature's stores and a row's eight-feature loads meet every bank once
+        const int here = min(s_cnt[t.g] - t.n0, t.n);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int j = 64 * b + 32 * odd;                 // the box's first row
+          if (j >= here) break;
           uint32_t r[32];
-          ptx::tmem_ld32(tbase + 32 * j, r);
+          ptx::tmem_ld32(tbase + j, r);
           ptx::tmem_ld_wait();
-          __syncwarp();                                    // the box before has been read
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            *reinterpret_cast<uint32_t*>(box + i * 128 + (((lane >> 2) ^ (i & 1)) << 4) +
-                                         (lane & 3) * 4) = r[i];
-          __syncwarp();
-          uint4 o[4];
+          for (int h = 0; h < 2; ++h) {
+            __syncwarp();                                  // the box before has been read
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const uint8_t* b = box + (i0 + 8 * v) * 128;
-            const int c = 2 * (lane & 3), x = i0 & 1;
-            const float4 lo = *reinterpret_cast<const float4*>(b + ((c ^ x) << 4));
-            const float4 hi = *reinterpret_cast<const float4*>(b + (((c + 1) ^ x) << 4));
-            float e[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            if (p.add) {
-              float d[8];
-              unpack8(add[v], d);
+            for (int i = 0; i < 16; ++i)
+              *reinterpret_cast<uint32_t*>(box + i * 128 + (((lane >> 2) ^ (i & 1)) << 4) +
+                                           (lane & 3) * 4) = r[16 * h + i];
+            __syncwarp();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) e[i] += d[i];
+            for (int v = 0; v < 2; ++v) {
+              const uint8_t* from = box + (lr + 8 * v) * 128;
+              const float4 lo = *reinterpret_cast<const float4*>(from + (((2 * lc) ^ (lr & 1)) << 4));
+              const float4 hi = *reinterpret_cast<const float4*>(from + (((2 * lc + 1) ^ (lr & 1)) << 4));
+              float e[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+              const int i = j + 16 * h + 8 * v + lr;
+              if (i >= rows) continue;
+              if (p.add) {
+                float d[8];
+                unpack8(add[b][2 * h + v], d);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) e[x] += d[x];
+              }
+              stg_v4(p.out + (row0 + i) * p.ldo + fl, pack8(e));
             }
-            o[v] = pack8(e);
-          }
-          fetch(j + 1);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int i = 32 * j + i0 + 8 * v;
-            if (mine && i < rows) stg_v4(p.out + (row0 + i) * p.ldo + fl, o[v]);
           }
         }
       }
