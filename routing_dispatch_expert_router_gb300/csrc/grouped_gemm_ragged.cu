@@ -318,19 +318,19 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
       }
     }
   } else {
-    // lane = feature; warps 4-7 take the even boxes of 32 columns, 8-11 the odd ones
+    // lane = feature; warps 4-7 take the even boxes of columns, 8-11 the odd ones
     const int q = warp & 3, odd = (warp - 4) >> 2;
     uint8_t* box = boxes + (warp - 4) * kBox;
     const uint32_t leader_tempty[2] = {ptx::mapa_shared(bar_tempty, 0),
                                        ptx::mapa_shared(bar_tempty + 8, 0)};
     const int fq = (int)rank * 128 + q * 32;               // this warp's features in a tile
-    const int lr = lane >> 2, lc = lane & 3;               // four lanes a row of a box
+    const int lr = lane >> 2, lc = lane & 3, l8 = lane & 7;
     uint32_t acc = 0, acc_phase = 0;
     for (int pt = cluster; pt < total; pt += nclusters) {
       const Tile t = tile_at(pt);
       const int f = t.f0 + fq;
       const int64_t row0 = (int64_t)s_off[t.g] + t.n0;
-      // rows of the tile that are this warp's to write, sixteen bytes (features fl .. fl + 7) a lane
+      // rows of the tile that are this lane's to write, sixteen bytes (features fl .. fl + 7) each
       const int fl = f + 8 * lc;
       const int rows = MODE != kWgrad && fl < p.feat ? min(s_cnt[t.g] - t.n0, t.n) : 0;
       uint4 add[4][4];
@@ -347,6 +347,13 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
             }
         }
       }
+      // hands the accumulator back (what this publishes is tensor memory alone: a release would
+      // wait for the stores, 5000 clocks a tile)
+      auto give = [&] {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster_tmem(leader_tempty[acc]);
+      };
       const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_tfull + 8 * acc, acc_phase,
                                                              kWaitBudget, abort_flag));
       if (!ok) {
@@ -359,47 +366,58 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
       ptx::tc_fence_after();
       const uint32_t tbase = tmem_base + acc * 256 + ((uint32_t)(q * 32) << 16);
       if constexpr (MODE == kWgrad) {
-        // 32 features x 32 columns, a row a lane; 16-byte chunk j of row r at j ^ ((r >> 1) & 3). The
+        // 32 features x 64 columns, a row a lane, 16 rows at a time: whole lines leave the SM (half
+        // lines cost as much). 16-byte chunk j of row r at j ^ (r & 7). The
         // next columns leave tensor memory while these are on their way.
         const int end = f < p.feat ? min(t.n, p.cols - t.n0) : 0;
-        uint32_t r[32];
+        uint32_t r0[32], r1[32];
         auto take = [&](int c) {
           if (c >= end) return;
           if (t.nk == 0) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = 0u;
+            for (int i = 0; i < 32; ++i) r0[i] = r1[i] = 0u;
           } else {
-            ptx::tmem_ld32(tbase + c, r);
+            ptx::tmem_ld32(tbase + c, r0);
+            ptx::tmem_ld32(tbase + c + 32, r1);
           }
         };
-        take(32 * odd);
+        take(64 * odd);
+        if (64 * odd >= end) give();
 #pragma unroll 1
-        for (int c = 32 * odd; c < end; c += 64) {
-          const int col = t.n0 + c + 8 * lc;
+        for (int c = 64 * odd; c < end; c += 128) {
+          const int col = t.n0 + c + 8 * l8;
           ptx::tmem_ld_wait();
-          uint4 a[4];
-          gg::pack_slice(r, a);
-          take(c + 64);
-          __syncwarp();                                    // the box before has been read
+          uint4 a[4], b[4];
+          gg::pack_slice(r0, a);
+          gg::pack_slice(r1, b);
+          take(c + 128);
+          if (c + 128 >= end) give();
+          __nv_bfloat16* out = p.out + ((int64_t)t.g * p.feat + f) * p.cols + col;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = a[j];
-          __syncwarp();
-          if (col < p.cols) {
-            __nv_bfloat16* out = p.out + ((int64_t)t.g * p.feat + f + lr) * p.cols + col;
+          for (int h = 0; h < 2; ++h) {
+            __syncwarp();                                  // the box before has been read
+            if ((lane >> 4) == h) {
+              uint8_t* rowp = box + (lane & 15) * 128;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                *reinterpret_cast<uint4*>(rowp + ((j ^ l8) << 4)) = a[j];
+                *reinterpret_cast<uint4*>(rowp + (((j + 4) ^ l8) << 4)) = b[j];
+              }
+            }
+            __syncwarp();
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-              const int i = lr + 8 * v;
-              if (f + i < p.feat)
-                stg_v4(out + (int64_t)(8 * v) * p.cols,
-                       *reinterpret_cast<const uint4*>(box + i * 64 + ((lc ^ ((i >> 1) & 3)) << 4)));
+              const int i = (lane >> 3) + 4 * v;
+              if (col < p.cols && f + 16 * h + i < p.feat)
+                stg_v4(out + (int64_t)(16 * h + i) * p.cols,
+                       *reinterpret_cast<const uint4*>(box + i * 128 + ((l8 ^ (i & 7)) << 4)));
             }
           }
         }
-      } else if (f < p.feat) {
+      } else {
         // 16 rows x 32 features in fp32 at a time, 128 bytes a row, 16-byte chunk c of row i at
         // c ^ (i & 1): a feature's stores and a row's eight-feature loads meet every bank once
-        const int here = min(s_cnt[t.g] - t.n0, t.n);
+        const int here = f < p.feat ? min(s_cnt[t.g] - t.n0, t.n) : 0;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const int j = 64 * b + 32 * odd;                 // the box's first row
@@ -433,10 +451,8 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
             }
           }
         }
+        give();
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(leader_tempty[acc]);
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
