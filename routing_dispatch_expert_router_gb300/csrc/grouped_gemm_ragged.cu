@@ -128,21 +128,28 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
   struct Tile {
     int g, f0, n0, n, nk;           // features from f0, columns (rows of the group) n0 .. n0 + n - 1
   };
-  auto tile_at = [&](int tile) {
+  // A role's walk over its pair's tiles: the next one is found while the present one is worked on
+  // (its group from the present one's on), so that no role stands still between tiles.
+  auto tile_at = [&](int tile, int g) {
     Tile t;
-    t.g = gg::find_group(prefix, p.G, tile);
-    const int local = tile - prefix[t.g], c = s_cnt[t.g];
+    while (prefix[g + 1] <= tile) ++g;
+    t.g = g;
+    const unsigned local = tile - prefix[g];
+    const int c = s_cnt[g];
     if constexpr (MODE == kWgrad) {
       // columns fastest: pairs that run together share A's columns
-      t.f0 = local / CT * kM;
-      t.n0 = local % CT * p.tile;
+      const unsigned m = local / (unsigned)CT;
+      t.f0 = m * kM;
+      t.n0 = (local - m * CT) * p.tile;
       t.n = p.tile;
       t.nk = (c + BK - 1) / BK;
     } else {
       // rows fastest (they share the expert's weights), cut into equal tiles of whole 32s
-      const int nt = (c + p.tile - 1) / p.tile, size = ((c + nt - 1) / nt + 31) & ~31;
-      t.f0 = local / nt * kM;
-      t.n0 = local % nt * size;
+      const unsigned nt = (unsigned)(prefix[g + 1] - prefix[g]) / (unsigned)FT;
+      const int size = ((c + nt - 1) / nt + 31) & ~31u;
+      const unsigned m = local / nt;
+      t.f0 = m * kM;
+      t.n0 = (local - m * nt) * size;
       t.n = min(size, ((c - t.n0) + 31) & ~31);
       t.nk = (p.red + BK - 1) / BK;
     }
@@ -158,8 +165,8 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
       uint32_t leader_full[kStages];
 #pragma unroll
       for (int s = 0; s < kStages; ++s) leader_full[s] = ptx::mapa_shared(bar_full + 8 * s, 0);
-      for (int pt = cluster; pt < total && ok; pt += nclusters) {
-        const Tile t = tile_at(pt);
+      Tile t = tile_at(cluster, 0), next = t;
+      for (int pt = cluster; pt < total && ok; pt += nclusters, t = next) {
         const int half = t.n >> 1, r = s_off[t.g];
         const int f0 = t.f0 + (int)rank * 128, c0 = t.n0 + (int)rank * half;
         const uint32_t bytes = kABytes + half * BK * 2;
@@ -214,6 +221,7 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
             phase ^= 1u;
           }
         }
+        if (pt + nclusters < total) next = tile_at(pt + nclusters, t.g);
       }
       if (!ok) {
         record_status(p.status, MOE_ERR_TIMEOUT);
@@ -231,8 +239,8 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
       bool ok = true, issued = false;
       const uint32_t peer_tfull[2] = {ptx::mapa_shared(bar_tfull, 1),
                                       ptx::mapa_shared(bar_tfull + 8, 1)};
-      for (int pt = cluster; pt < total && ok; pt += nclusters) {
-        const Tile t = tile_at(pt);
+      Tile t = tile_at(cluster, 0), next = t;
+      for (int pt = cluster; pt < total && ok; pt += nclusters, t = next) {
         const uint32_t idesc = ptx::idesc_bf16(kM, t.n, A_MN, B_MN);
         if (!ptx::mbar_wait_cluster(bar_tempty + 8 * acc, acc_phase ^ 1u, kWaitBudget, abort_flag)) {
           ok = false;
@@ -257,6 +265,7 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
           }
           issued = true;
           ptx::mma_commit_pair(bar_empty + 8 * stage, 3);
+          if (kb == 0 && pt + nclusters < total) next = tile_at(pt + nclusters, t.g);
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
@@ -268,6 +277,7 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
         } else {                                           // an empty group: nothing to wait for
           ptx::mbar_arrive(bar_tfull + 8 * acc);
           ptx::mbar_arrive_cluster(peer_tfull[acc]);
+          if (pt + nclusters < total) next = tile_at(pt + nclusters, t.g);
         }
         if (++acc == 2) {
           acc = 0;
@@ -289,8 +299,10 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
     if constexpr (MODE == kWgrad) {
       uint32_t stage = 0, phases = 0;                      // phases: a bit per stage, of bar_tail
       bool ok = true;
+      int g = 0;
       for (int pt = cluster; pt < total && ok; pt += nclusters) {
-        const Tile t = tile_at(pt);
+        const Tile t = tile_at(pt, g);
+        g = t.g;
         const int valid = s_cnt[t.g] & (BK - 1);
         if (valid) {
           stage = (stage + t.nk - 1) % kStages;
@@ -326,8 +338,10 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
     const int fq = (int)rank * 128 + q * 32;               // this warp's features in a tile
     const int lr = lane >> 2, lc = lane & 3, l8 = lane & 7;
     uint32_t acc = 0, acc_phase = 0;
+    Tile next = tile_at(cluster, 0);
     for (int pt = cluster; pt < total; pt += nclusters) {
-      const Tile t = tile_at(pt);
+      const Tile t = next;
+      if (pt + nclusters < total) next = tile_at(pt + nclusters, t.g);
       const int f = t.f0 + fq;
       const int64_t row0 = (int64_t)s_off[t.g] + t.n0;
       // rows of the tile that are this lane's to write, sixteen bytes (features fl .. fl + 7) each
@@ -367,8 +381,8 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
       const uint32_t tbase = tmem_base + acc * 256 + ((uint32_t)(q * 32) << 16);
       if constexpr (MODE == kWgrad) {
         // 32 features x 64 columns, a row a lane, 16 rows at a time: whole lines leave the SM (half
-        // lines cost as much). 16-byte chunk j of row r at j ^ (r & 7). The
-        // next columns leave tensor memory while these are on their way.
+        // lines cost as much). 16-byte chunk j of row r at j ^ (r & 7). The next
+        // columns leave tensor memory while these are on their way.
         const int end = f < p.feat ? min(t.n, p.cols - t.n0) : 0;
         uint32_t r0[32], r1[32];
         auto take = [&](int c) {
