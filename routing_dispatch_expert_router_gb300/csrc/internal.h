@@ -358,7 +358,7 @@ struct FewProduct {
 };
 constexpr int kFewCtas = 256;
 constexpr int kFewPart = 256 * 16;
-constexpr int kFewLeast = 4;  // steps of K a CTA takes at least
+constexpr int kFewLeast = 2;  // steps of K a CTA takes at least (they must weigh more than one)
 constexpr int kFewRows = 64;  // rows a group up to which bf16 weights are streamed
 bool few_fits(int64_t rows, int G, int64_t N, int64_t K);
 cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const void* w,

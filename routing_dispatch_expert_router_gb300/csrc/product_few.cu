@@ -47,6 +47,8 @@ struct Cfg {
   static constexpr int THREADS = 32 * (1 + HELPERS + kConsumers + kJoiners);
   static constexpr int STAGES = W4 ? 4 : 5;
   static constexpr int STEP = W4 ? 256 : 64;           // elements of K a stage
+  // what a step of one and of two token tiles takes, as measured (codes: 1510 and 2100 clocks)
+  static constexpr int W1 = W4 ? 5 : 1, W2 = W4 ? 7 : 1;
   static constexpr int XBOXES = STEP / 64;             // boxes of 64 elements x 8 tokens
   static constexpr int X_OFF = kSlab * 128;
   static constexpr int S_OFF = X_OFF + kTok / 8 * XBOXES * 1024;
@@ -217,10 +219,10 @@ __device__ __forceinline__ void step_bf16(float (&tot)[2][2][4], uint32_t st, co
   }
 }
 
-// The unit u of a group: token tiles fastest, so that those of the same weights follow each
-// other and find them in L2.
-struct Unit {
-  int g, slab, tok0, ntok;                       // first token within the group, tokens
+// A place in the stream: step `step` of the unit (group, slab of columns, tile of tokens). Token
+// tiles are fastest, so that those of the same weights follow each other and find them in L2.
+struct Place {
+  int g, slab, tile, step;
 };
 
 // GC: chunks of 32 elements of K in a scale's group (4-bit).
@@ -240,13 +242,19 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
   const uint32_t bar_tile = ctrl_u + 120, bar_free = ctrl_u + 136;     // of the two tiles
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 192);
   volatile int* s_last = reinterpret_cast<volatile int*>(ctrl + 196);
-  int* prefix = reinterpret_cast<int*>(ctrl + 256);        // [kMaxGroups + 1] units
+  Place* s_ends = reinterpret_cast<Place*>(ctrl + 208);    // [2]
+  int* prefix = reinterpret_cast<int*>(ctrl + 256);        // [kMaxGroups + 1] weights
   int* s_off = reinterpret_cast<int*>(ctrl + 1536);        // [kMaxGroups]
   int* s_cnt = reinterpret_cast<int*>(ctrl + 2688);        // [kMaxGroups]
   int* tmp = reinterpret_cast<int*>(ctrl + 3840);          // [33]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slabs = p.slabs;
+  // what the steps of a slab of columns weigh: two token tiles of eight cost more than one
+  auto slab_weight = [](int c) {
+    const int rest = c % kTok;
+    return c / kTok * C::W2 + (rest == 0 ? 0 : rest <= 8 ? C::W1 : C::W2);
+  };
   if (tid == 0) {
     ptx::tma_prefetch_desc(&tmW);
     ptx::tma_prefetch_desc(&tmX);
@@ -278,44 +286,76 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     }
     s_cnt[g] = c;
     s_off[g] = o;
-    prefix[g] = (c + kTok - 1) / kTok * slabs;
+    prefix[g] = slab_weight(c) * slabs;
   }
   __syncthreads();
-  const int units = block_exclusive_scan(prefix, p.G, tmp);
-  if (tid == 0) prefix[p.G] = units;
+  const int weight = block_exclusive_scan(prefix, p.G, tmp);
+  if (tid == 0) prefix[p.G] = weight;
   __syncthreads();
-  // an even share of all steps, not under kFewLeast of them where there are few: the first
-  // `more` CTAs take one step above `share`
-  const int KC = p.steps, total = KC * units;
-  const int nb = max(1, min(total / kFewLeast, (int)gridDim.x));
+  // An even share of the steps, weighed by what they take, for each CTA, not under kFewLeast
+  // steps where there are few. CTA b begins with the first step at or behind its share's start.
+  const int KC = p.steps;
+  const int64_t total = (int64_t)weight * KC;
+  const int nb = max(1, (int)min(total / (kFewLeast * C::W1), (int64_t)gridDim.x));
   if (total == 0 || (int)blockIdx.x >= nb) return;
-  const int share = total / nb, more = total - share * nb;
-  auto first_of = [&](int b) { return b * share + min(b, more); };
-  auto cta_of = [&](int step) {
-    const int long_ = more * (share + 1);
-    return step < long_ ? step / (share + 1) : more + (step - long_) / share;
-  };
-  const int begin = first_of(blockIdx.x), end = first_of(blockIdx.x + 1);
-  auto unit_at = [&](int u) {
-    Unit v;
-    v.g = gg::find_group(prefix, p.G, u);
-    const int local = u - prefix[v.g], cnt = s_cnt[v.g], tiles = (cnt + kTok - 1) / kTok;
-    v.slab = local / tiles;
-    v.tok0 = local % tiles * kTok;
-    v.ntok = min(kTok, cnt - v.tok0);
+  auto first_of = [&](int b) {
+    const int64_t at = total * b / nb;
+    Place v{p.G, 0, 0, 0};
+    if (at >= total) return v;
+    v.g = gg::find_group(prefix, p.G, (int)(at / KC));
+    const int c = s_cnt[v.g];
+    int64_t rest = at - (int64_t)prefix[v.g] * KC;
+    const int64_t slab = (int64_t)slab_weight(c) * KC;
+    v.slab = (int)(rest / slab);
+    rest -= v.slab * slab;
+    v.tile = min((int)(rest / (C::W2 * KC)), (c - 1) / kTok);
+    rest -= (int64_t)v.tile * C::W2 * KC;
+    const int w = c - v.tile * kTok <= 8 ? C::W1 : C::W2;
+    v.step = (int)((rest + w - 1) / w);
     return v;
+  };
+  // the CTA of a step: the last whose share starts at or before it
+  auto cta_of = [&](const Place& v, int step) {
+    const int c = s_cnt[v.g], w = c - v.tile * kTok <= 8 ? C::W1 : C::W2;
+    const int64_t at =
+        ((int64_t)prefix[v.g] + v.slab * slab_weight(c) + v.tile * C::W2) * KC + (int64_t)step * w;
+    return (int)(((at + 1) * nb - 1) / total);
+  };
+  auto next_unit = [&](Place& v) {
+    v.step = 0;
+    if ((++v.tile) * kTok < s_cnt[v.g]) return;
+    v.tile = 0;
+    if (++v.slab < slabs) return;
+    v.slab = 0;
+    do ++v.g;
+    while (v.g < p.G && s_cnt[v.g] == 0);
+  };
+  if (tid < 64 && lane == 0) {
+    Place v = first_of(blockIdx.x + warp);
+    if (v.step == KC) next_unit(v);
+    s_ends[warp] = v;
+  }
+  __syncthreads();
+  const Place begin = s_ends[0], end = s_ends[1];
+  // steps of the unit at v that are this CTA's, 0 at its end; and the way there
+  auto at_end = [&](const Place& v) {
+    return v.g == end.g && v.slab == end.slab && v.tile == end.tile;
+  };
+  auto steps_at = [&](const Place& v) { return (at_end(v) ? end.step : KC) - v.step; };
+  auto advance = [&](Place& v) {
+    if (at_end(v)) v.step = end.step;
+    else next_unit(v);
   };
 
   if (warp == 0) {
     if (lane == 0) {
       uint32_t stage = 0, phase = 0, issued = 0, issued_phase = 0;
       bool ok = true;
-      for (int at = begin; at < end && ok;) {
-        const int u = at / KC, k0 = at - u * KC, n = min(KC - k0, end - at);
-        at += n;
-        const Unit v = unit_at(u);
-        const int ntl = (v.ntok + 7) >> 3;
-        const int row = s_off[v.g] + v.tok0;
+      for (Place v = begin; ok; advance(v)) {
+        const int n = steps_at(v), k0 = v.step;
+        if (n <= 0) break;
+        const int ntl = min(2, (s_cnt[v.g] - v.tile * kTok + 7) >> 3);
+        const int row = s_off[v.g] + v.tile * kTok;
         // the slab's two halves of 128 rows: gate and up, or one behind the other
         const int ra = v.slab * (SWIGLU ? 128 : 256), rb = SWIGLU ? p.F + ra : ra + 128;
         const uint32_t bytes = kSlab * 128 + ntl * C::XBOXES * 1024 +
@@ -368,10 +408,10 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     // their sums over each 32
     uint32_t stage = 0, phase = 0;
     bool ok = true;
-    for (int at = begin; at < end && ok;) {
-      const int u = at / KC, n = min(KC - (at - u * KC), end - at);
-      at += n;
-      const int ntok = (unit_at(u).ntok + 7) & ~7;
+    for (Place v = begin; ok; advance(v)) {
+      const int n = steps_at(v);
+      if (n <= 0) break;
+      const int ntok = (min(kTok, s_cnt[v.g] - v.tile * kTok) + 7) & ~7;
       for (int k = 0; k < n && ok; ++k) {
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget,
                                                     abort_flag));
@@ -379,16 +419,16 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         const uint32_t st = base + stage * C::STAGE;
         // three tokens at a time: what bounds these warps is the shuffles' latency
         for (int tok0 = warp - 1; tok0 < ntok; tok0 += 3 * C::HELPERS) {
-          uint4 v[3];
+          uint4 q[3];
           float s[3];
           uint32_t r[3];
 #pragma unroll
           for (int i = 0; i < 3; ++i) {
             const int tok = min(tok0 + i * C::HELPERS, kTok - 1);
             r[i] = st + C::X_OFF + ((tok >> 3) * C::XBOXES + (lane >> 3)) * 1024 + (tok & 7) * 128;
-            v[i] = lds128(r[i] + (((lane & 7) ^ (tok & 7)) << 4));
+            q[i] = lds128(r[i] + (((lane & 7) ^ (tok & 7)) << 4));
             float f[8];
-            unpack8(v[i], f);
+            unpack8(q[i], f);
             s[i] = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
           }
 #pragma unroll
@@ -405,8 +445,8 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                            :: "r"(st + C::SUM_OFF + (lane / (4 * GC) * kTok + tok) * 4), "f"(s[i])
                            : "memory");
             sts128(r[i] + (((lane & 7) ^ ((tok & 1) << 2)) << 4),
-                   make_uint4(__byte_perm(v[i].x, v[i].z, 0x5410), __byte_perm(v[i].x, v[i].z, 0x7632),
-                              __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632)));
+                   make_uint4(__byte_perm(q[i].x, q[i].z, 0x5410), __byte_perm(q[i].x, q[i].z, 0x7632),
+                              __byte_perm(q[i].y, q[i].w, 0x5410), __byte_perm(q[i].y, q[i].w, 0x7632)));
           }
         }
         ptx::fence_proxy_async_smem();           // TMA writes here next
@@ -432,10 +472,10 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     const Places here = places<W4>(p, rg, g, t);
-    for (int at = begin; at < end && ok;) {
-      const int u = at / KC, n = min(KC - (at - u * KC), end - at);
-      at += n;
-      const bool two = unit_at(u).ntok > 8;
+    for (Place v = begin; ok; advance(v)) {
+      const int n = steps_at(v);
+      if (n <= 0) break;
+      const bool two = s_cnt[v.g] - v.tile * kTok > 8;
       float tot[2][2][4];
 #pragma unroll
       for (int m = 0; m < 2; ++m)
@@ -492,10 +532,10 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
   const int ctid = tid - (C::THREADS - CT);
   auto sync = [] { asm volatile("bar.sync 1, %0;" :: "n"(CT) : "memory"); };
   bool ok = true;
-  for (int at = begin; at < end;) {
-    const int u = at / KC, n = min(KC - (at - u * KC), end - at);
-    at += n;
-    const Unit v = unit_at(u);
+  for (Place v = begin;; advance(v)) {
+    const int n = steps_at(v);
+    if (n <= 0) break;
+    const int ntok = min(kTok, s_cnt[v.g] - v.tile * kTok);
     float* tile = tiles + buf * (kTileBytes / 4);
     // (after a wait that ran out the pieces go on without their sums, so that the parts' counters
     // come out as in any other launch)
@@ -508,12 +548,12 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     if (n < KC) {
       // CTAs lo .. hi share the unit, each with one part: the first the one that it leaves
       // unfinished, the others the one that they begin with
-      const int lo = cta_of(u * KC), hi = cta_of(u * KC + KC - 1);
+      const int lo = cta_of(v, 0), hi = cta_of(v, KC - 1);
       auto part = [&](int b) { return p.parts + ((int64_t)2 * b + (b == lo)) * (kSlab * kTok); };
       float* to = part(blockIdx.x);
       // four rows of a token a thread and turn, in the parts' order [token][row]
       auto tile4 = [&](int e) { return tile + (e & (kSlab - 1)) * kTileLd + e / kSlab; };
-      const int all = kSlab * v.ntok;
+      const int all = kSlab * ntok;
 #pragma unroll 2
       for (int e = 4 * ctid; e < all; e += 4 * CT) {
         const float* f = tile4(e);
@@ -564,10 +604,10 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
       // two neighbouring columns a thread
       constexpr int COLS = SWIGLU ? kSlab / 2 : kSlab;
       const int n0 = v.slab * COLS, N = SWIGLU ? p.F : p.N;
-      for (int e = ctid; e < COLS / 2 * v.ntok; e += CT) {
+      for (int e = ctid; e < COLS / 2 * ntok; e += CT) {
         const int c = e % (COLS / 2) * 2, tok = e / (COLS / 2);
         if (n0 + c >= N) continue;
-        const int64_t row = s_off[v.g] + v.tok0 + tok;
+        const int64_t row = s_off[v.g] + v.tile * kTok + tok;
         float a = tile[c * kTileLd + tok], b = tile[(c + 1) * kTileLd + tok];
         if (SWIGLU) {
           a = gg::silu_f(a) * tile[(c + 128) * kTileLd + tok];
@@ -672,9 +712,9 @@ cudaError_t launch_int4_dequantize(const void* codes, const void* scales, const 
 
 static_assert(kFewPart == kSlab * kTok, "parts as the kernel writes them");
 
-// Steps of units of 16 tokens and 256 weight rows that the kernel's 32-bit numbers hold.
+// Units of 16 tokens and 256 weight rows, weighed, that the kernel's 32-bit numbers hold.
 bool few_fits(int64_t rows, int G, int64_t N, int64_t K) {
-  return (rows / kTok + G + 1) * ((N + 127) / 128) * ((K + 63) / 64) < (1LL << 31);
+  return (rows / kTok + G + 1) * ((N + 127) / 128) * 7 < (1LL << 31) && K < (1LL << 24);
 }
 
 cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const void* w,
