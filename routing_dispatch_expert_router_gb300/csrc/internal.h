@@ -354,7 +354,7 @@ struct FewProduct {
   int32_t* status;
   // set by the launcher
   int F, slabs, steps, groups_per_step, group_log2;
-  bool has_zeros;
+  bool has_zeros, x_whole;
 };
 constexpr int kFewCtas = 256;
 constexpr int kFewPart = 256 * 16;

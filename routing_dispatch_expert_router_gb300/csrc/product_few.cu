@@ -106,32 +106,56 @@ __device__ __forceinline__ uint32_t codes_pair(uint32_t w, int i) {
   return r;
 }
 
-// A lane's places in a stage, without the stage's address: the weights' 16 bytes of a chunk of
-// 32 elements (4-bit: this thread's word of them), the tokens' pieces, sums, scales.
+// The weight row of a warp's eight that lane group g of the MMA has. With 16-byte loads the
+// eight lanes that go together have rows four apart, whose swizzled places are in all banks.
+template <bool W4, int GC>
+__device__ __forceinline__ int weight_row(int g) {
+  return W4 && GC == 4 ? ((g & 1) << 2) | (g >> 1) : g;
+}
+// Where the helpers put 16-byte piece `piece` of box `box` of a token's 256 elements, so that
+// the pieces that eight lanes read together are in all banks.
+template <int GC>
+__device__ __forceinline__ int token_place(int tok, int box, int piece) {
+  return GC == 4 ? piece ^ (box & 1) ^ ((tok & 1) << 1) : piece ^ ((tok & 1) << 2);
+}
+
+// A lane's places in a stage, without the stage's address: weights, tokens' pieces, sums, scales.
+// In an MMA a lane has any 16-bit pairs of K as long as A's and B's are the same and all lanes'
+// are of one group: with groups of 128 elements lane t has elements 32 t .. 32 t + 31 of the group
+// (16 bytes of codes), else 8 t .. 8 t + 7 of each 32 (a word).
 struct Places {
-  uint32_t w[8], x[2], sum, s, z;
+  uint32_t w[8], x[4], sum, s, z;
 };
 
-template <bool W4>
+template <bool W4, bool SWIGLU, int GC>
 __device__ __forceinline__ Places places(const FewProduct& p, int rg, int g, int t) {
   using C = Cfg<W4>;
   Places a;
-  const int row0 = rg * 32 + g;                  // and 8, 16, 24 on: the same low three bits
+  const int r = weight_row<W4, GC>(g);
+  const int row0 = rg * 32 + r;                  // and 8, 16, 24 on: the same low three bits
   if constexpr (W4) {
+    if constexpr (GC == 4) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a.w[i] = row0 * 128 + ((i ^ g) << 4) + t * 4;
+      for (int q = 0; q < 2; ++q) a.w[q] = row0 * 128 + (((4 * q + t) ^ r) << 4);
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-      a.x[b] = C::X_OFF + g * 128 + (((b * 4 + t) ^ ((g & 1) << 2)) << 4);
-    // (scales and zero points lie in two halves of 128 rows)
-    const int at = (rg >> 2) * p.groups_per_step * 128 + (row0 & 127);
+      for (int j = 0; j < 4; ++j)
+        a.x[j] = C::X_OFF + g * 128 + (token_place<GC>(g, t >> 1, 4 * (t & 1) + j) << 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a.w[i] = row0 * 128 + ((i ^ r) << 4) + t * 4;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        a.x[b] = C::X_OFF + g * 128 + (token_place<GC>(g, 0, b * 4 + t) << 4);
+    }
+    // (scales and zero points: gate's and up's rows apart, or 256 rows a group)
+    const int at = SWIGLU ? (rg >> 2) * p.groups_per_step * 128 + (row0 & 127) : row0;
     a.sum = C::SUM_OFF + 2 * t * 4;
     a.s = C::S_OFF + at * 2;
     a.z = C::Z_OFF + at;
   } else {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      a.w[b] = row0 * 128 + (((4 * b + t) ^ g) << 4);
+      a.w[b] = row0 * 128 + (((4 * b + t) ^ r) << 4);
       a.x[b] = C::X_OFF + g * 128 + (((4 * b + t) ^ g) << 4);
     }
   }
@@ -139,10 +163,12 @@ __device__ __forceinline__ Places places(const FewProduct& p, int rg, int g, int
 }
 
 // What a step adds to a warp's 32 rows x 8 NTL tokens. GC: chunks of 32 elements in a group.
-template <int NTL, int GC>
+template <int NTL, bool SWIGLU, int GC>
 __device__ __forceinline__ void step_int4(float (&tot)[2][2][4], uint32_t st, const Places& a,
-                                          bool has_zeros) {
+                                          bool has_zeros, int t) {
   using C = Cfg<true>;
+  constexpr int GS = SWIGLU ? 128 : 256;         // from one group's scales to the next's
+  const uint32_t stx = GC == 4 ? st + (t >> 1) * (NTL * 1024) : st;
 #pragma unroll
   for (int c0 = 0; c0 < 8; c0 += GC) {
     float acc[2][NTL][4];
@@ -152,17 +178,32 @@ __device__ __forceinline__ void step_int4(float (&tot)[2][2][4], uint32_t st, co
       for (int n = 0; n < NTL; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+    uint4 w4[2][2];
+    if (GC == 4) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) w4[m][h] = lds128(st + a.w[c0 / 4] + m * 2048 + h * 1024);
+    }
 #pragma unroll
     for (int c = c0; c < c0 + GC; ++c) {
       uint32_t w[2][2];
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) w[m][h] = lds32(st + a.w[c] + m * 2048 + h * 1024);
+        for (int h = 0; h < 2; ++h) {
+          const uint4& v = w4[m][h];
+          w[m][h] = GC == 4 ? (c & 3) == 0   ? v.x
+                              : (c & 3) == 1 ? v.y
+                              : (c & 3) == 2 ? v.z
+                                             : v.w
+                            : lds32(st + a.w[c] + m * 2048 + h * 1024);
+        }
       uint4 x[NTL];
 #pragma unroll
       for (int n = 0; n < NTL; ++n)
-        x[n] = lds128(st + a.x[c & 1] + n * (C::XBOXES * 1024) + (c >> 1) * 1024);
+        x[n] = GC == 4 ? lds128(stx + a.x[c & 3] + n * 1024 + (c >> 2) * (2 * NTL * 1024))
+                       : lds128(stx + a.x[c & 1] + n * 1024 + (c >> 1) * (NTL * 1024));
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const uint32_t a0 = codes_pair(w[m][0], 0), a1 = codes_pair(w[m][1], 0);
@@ -185,9 +226,9 @@ __device__ __forceinline__ void step_int4(float (&tot)[2][2][4], uint32_t st, co
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float s = __uint_as_float(lds16(st + a.s + (q * 128 + 16 * m + 8 * h) * 2) << 16);
+        const float s = __uint_as_float(lds16(st + a.s + (q * GS + 16 * m + 8 * h) * 2) << 16);
         const float z =
-            has_zeros ? (float)(128u + (lds8(st + a.z + q * 128 + 16 * m + 8 * h) & 127u)) : 136.f;
+            has_zeros ? (float)(128u + (lds8(st + a.z + q * GS + 16 * m + 8 * h) & 127u)) : 136.f;
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
           tot[m][n][2 * h] = fmaf(s, fmaf(-z, sx[n].x, acc[m][n][2 * h]), tot[m][n][2 * h]);
@@ -225,12 +266,17 @@ struct Place {
   int g, slab, tile, step;
 };
 
+// A TMA request costs its issuer some 200 clocks whatever its size, and a stage's bytes come in
+// 1400: each operand is one request. w: 256 rows, or 128 of the gate and of the up half; x: 8 and
+// 16 tokens, all of a stage's K (in boxes of 64 elements, where K is not whole boxes); s, z.
+struct Maps {
+  CUtensorMap w, x[2], s, z;
+};
+
 // GC: chunks of 32 elements of K in a scale's group (4-bit).
 template <bool W4, bool SWIGLU, int GC>
 __global__ void __launch_bounds__(Cfg<W4>::THREADS, 1)
-product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                   const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmZ,
-                   const FewProduct p) {
+product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
   using C = Cfg<W4>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
@@ -256,10 +302,9 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     return c / kTok * C::W2 + (rest == 0 ? 0 : rest <= 8 ? C::W1 : C::W2);
   };
   if (tid == 0) {
-    ptx::tma_prefetch_desc(&tmW);
-    ptx::tma_prefetch_desc(&tmX);
-    if (W4) ptx::tma_prefetch_desc(&tmS);
-    if (W4 && p.has_zeros) ptx::tma_prefetch_desc(&tmZ);
+    ptx::tma_prefetch_desc(&maps.w);
+    ptx::tma_prefetch_desc(&maps.x[0]);
+    if (W4) ptx::tma_prefetch_desc(&maps.s);
     *abort_flag = 0;
     for (int s = 0; s < C::STAGES; ++s) {
       ptx::mbar_init(bar_full + 8 * s, 1);
@@ -356,8 +401,8 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         if (n <= 0) break;
         const int ntl = min(2, (s_cnt[v.g] - v.tile * kTok + 7) >> 3);
         const int row = s_off[v.g] + v.tile * kTok;
-        // the slab's two halves of 128 rows: gate and up, or one behind the other
-        const int ra = v.slab * (SWIGLU ? 128 : 256), rb = SWIGLU ? p.F + ra : ra + 128;
+        const int n0 = v.slab * (SWIGLU ? 128 : 256);
+        const CUtensorMap* x = &maps.x[ntl - 1];
         const uint32_t bytes = kSlab * 128 + ntl * C::XBOXES * 1024 +
                                (W4 ? p.groups_per_step * (p.has_zeros ? 768 : 512) : 0);
         for (int k = k0; k < k0 + n; ++k) {
@@ -368,19 +413,21 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
           const uint32_t fb = bar_full + 8 * stage, st = base + stage * C::STAGE;
           ptx::mbar_arrive_expect_tx(fb, bytes);
           const int kw = k * (W4 ? 128 : 64);            // in elements of the weights' map
-          ptx::tma_load_3d(st, &tmW, fb, kw, ra, v.g);
-          ptx::tma_load_3d(st + 128 * 128, &tmW, fb, kw, rb, v.g);
-          for (int i = 0; i < ntl; ++i)
+          if (SWIGLU) ptx::tma_load_4d(st, &maps.w, fb, kw, n0, 0, v.g);
+          else ptx::tma_load_3d(st, &maps.w, fb, kw, n0, v.g);
+          if (W4 && p.x_whole) {
+            ptx::tma_load_3d(st + C::X_OFF, x, fb, 0, row, k * C::XBOXES);
+          } else {
             for (int b = 0; b < C::XBOXES; ++b)
-              ptx::tma_load_2d(st + C::X_OFF + (i * C::XBOXES + b) * 1024, &tmX, fb,
-                               k * C::STEP + b * 64, row + 8 * i);
+              ptx::tma_load_2d(st + C::X_OFF + b * ntl * 1024, x, fb, k * C::STEP + b * 64, row);
+          }
           if (W4) {
-            const int gps = p.groups_per_step;
-            ptx::tma_load_3d(st + C::S_OFF, &tmS, fb, ra, k * gps, v.g);
-            ptx::tma_load_3d(st + C::S_OFF + gps * 256, &tmS, fb, rb, k * gps, v.g);
+            const int k1 = k * p.groups_per_step;
+            if (SWIGLU) ptx::tma_load_4d(st + C::S_OFF, &maps.s, fb, n0, k1, 0, v.g);
+            else ptx::tma_load_3d(st + C::S_OFF, &maps.s, fb, n0, k1, v.g);
             if (p.has_zeros) {
-              ptx::tma_load_3d(st + C::Z_OFF, &tmZ, fb, ra, k * gps, v.g);
-              ptx::tma_load_3d(st + C::Z_OFF + gps * 128, &tmZ, fb, rb, k * gps, v.g);
+              if (SWIGLU) ptx::tma_load_4d(st + C::Z_OFF, &maps.z, fb, n0, k1, 0, v.g);
+              else ptx::tma_load_3d(st + C::Z_OFF, &maps.z, fb, n0, k1, v.g);
             }
           }
           issued |= 1u << stage;
@@ -424,8 +471,8 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
           uint32_t r[3];
 #pragma unroll
           for (int i = 0; i < 3; ++i) {
-            const int tok = min(tok0 + i * C::HELPERS, kTok - 1);
-            r[i] = st + C::X_OFF + ((tok >> 3) * C::XBOXES + (lane >> 3)) * 1024 + (tok & 7) * 128;
+            const int tok = min(tok0 + i * C::HELPERS, ntok - 1);
+            r[i] = st + C::X_OFF + (lane >> 3) * (ntok * 128) + tok * 128;
             q[i] = lds128(r[i] + (((lane & 7) ^ (tok & 7)) << 4));
             float f[8];
             unpack8(q[i], f);
@@ -444,7 +491,7 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
               asm volatile("st.shared.f32 [%0], %1;"
                            :: "r"(st + C::SUM_OFF + (lane / (4 * GC) * kTok + tok) * 4), "f"(s[i])
                            : "memory");
-            sts128(r[i] + (((lane & 7) ^ ((tok & 1) << 2)) << 4),
+            sts128(r[i] + (token_place<GC>(tok, lane >> 3, lane & 7) << 4),
                    make_uint4(__byte_perm(q[i].x, q[i].z, 0x5410), __byte_perm(q[i].x, q[i].z, 0x7632),
                               __byte_perm(q[i].y, q[i].w, 0x5410), __byte_perm(q[i].y, q[i].w, 0x7632)));
           }
@@ -471,7 +518,7 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     const int rg = warp - 1 - C::HELPERS;
     uint32_t stage = 0, phase = 0;
     bool ok = true;
-    const Places here = places<W4>(p, rg, g, t);
+    const Places here = places<W4, SWIGLU, GC>(p, rg, g, t);
     for (Place v = begin; ok; advance(v)) {
       const int n = steps_at(v);
       if (n <= 0) break;
@@ -490,8 +537,8 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         if (!ok) break;
         const uint32_t st = base + stage * C::STAGE;
         if constexpr (W4) {
-          if (two) step_int4<2, GC>(tot, st, here, p.has_zeros);
-          else step_int4<1, GC>(tot, st, here, p.has_zeros);
+          if (two) step_int4<2, SWIGLU, GC>(tot, st, here, p.has_zeros, t);
+          else step_int4<1, SWIGLU, GC>(tot, st, here, p.has_zeros, t);
         } else {
           if (two) step_bf16<2>(tot, st, here);
           else step_bf16<1>(tot, st, here);
@@ -513,7 +560,8 @@ product_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            tile[(rg * 32 + 16 * m + 8 * (i >> 1) + g) * kTileLd + 8 * j + 2 * t + (i & 1)] =
+            tile[(rg * 32 + 16 * m + 8 * (i >> 1) + weight_row<W4, GC>(g)) * kTileLd + 8 * j +
+                 2 * t + (i & 1)] =
                 tot[m][j][i];
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar_tile + 8 * buf);
@@ -652,50 +700,52 @@ int4_dequantize_kernel(const uint32_t* __restrict__ codes, const uint16_t* __res
   }
 }
 
-bool make_map3(CUtensorMap* m, CUtensorMapDataType type, int bytes, const void* ptr, uint64_t d0,
-               uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1, bool swizzle) {
+// A tensor map of 2 to 4 dimensions: dims and box from the innermost on, strides in bytes.
+bool make_tensor_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, int rank,
+                     const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                     bool swizzle) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[3] = {d0, d1, d2};
-  cuuint64_t strides[2] = {d0 * bytes, d0 * d1 * bytes};
-  cuuint32_t box[3] = {b0, b1, 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  return fn(m, type, 3, const_cast<void*>(ptr), dims, strides, box, es,
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, type, rank, const_cast<void*>(ptr), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE,
             swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_rows_map(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t ld) {
-  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {ld * 2};
-  cuuint32_t box[2] = {64, 8};
-  cuuint32_t es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+// A matrix of d1 x d0 elements for every group; halves: its columns (scales) or rows (weights) cut
+// into the gate's and the up half, so that a box has both.
+bool make_group_map(CUtensorMap* m, CUtensorMapDataType type, uint64_t bytes, const void* ptr,
+                    uint64_t d0, uint64_t d1, uint64_t groups, uint32_t b0, uint32_t b1,
+                    int halved, bool swizzle) {
+  const cuuint64_t row = d0 * bytes, group = d0 * d1 * bytes;
+  if (halved < 0) {
+    const cuuint64_t dims[3] = {d0, d1, groups}, strides[2] = {row, group};
+    const cuuint32_t box[3] = {b0, b1, 1};
+    return make_tensor_map(m, type, ptr, 3, dims, strides, box, swizzle);
+  }
+  const cuuint64_t dims[4] = {halved == 0 ? d0 / 2 : d0, halved == 1 ? d1 / 2 : d1, 2, groups};
+  const cuuint64_t strides[3] = {row, halved == 0 ? row / 2 : group / 2, group};
+  const cuuint32_t box[4] = {b0, b1, 2, 1};
+  return make_tensor_map(m, type, ptr, 4, dims, strides, box, swizzle);
 }
 
 template <bool W4, bool SWIGLU, int GC>
-cudaError_t run_few(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& s,
-                    const CUtensorMap& z, const FewProduct& p, cudaStream_t stream) {
+cudaError_t run_few(const Maps& m, const FewProduct& p, cudaStream_t stream) {
   auto kern = product_few_kernel<W4, SWIGLU, GC>;
   static PerDevice set;
   const cudaError_t e = set_smem_once(set, kern, Cfg<W4>::SMEM);
   if (e != cudaSuccess) return e;
   const int n = num_sms();
   return launch_early(kern, n < kFewCtas ? n : kFewCtas, dim3(Cfg<W4>::THREADS, 1, 1), Cfg<W4>::SMEM,
-                      stream, w, x, s, z, p);
+                      stream, m, p);
 }
 
 template <bool SWIGLU>
-cudaError_t run_int4(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& s,
-                     const CUtensorMap& z, const FewProduct& p, cudaStream_t stream) {
-  return p.group == 128  ? run_few<true, SWIGLU, 4>(w, x, s, z, p, stream)
-         : p.group == 64 ? run_few<true, SWIGLU, 2>(w, x, s, z, p, stream)
-                         : run_few<true, SWIGLU, 1>(w, x, s, z, p, stream);
+cudaError_t run_int4(const Maps& m, const FewProduct& p, cudaStream_t stream) {
+  return p.group == 128  ? run_few<true, SWIGLU, 4>(m, p, stream)
+         : p.group == 64 ? run_few<true, SWIGLU, 2>(m, p, stream)
+                         : run_few<true, SWIGLU, 1>(m, p, stream);
 }
 
 }  // namespace
@@ -728,23 +778,33 @@ cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const v
   p.has_zeros = zeros != nullptr;
   p.groups_per_step = w4 ? 256 / p.group : 0;
   p.group_log2 = p.group == 128 ? 7 : p.group == 64 ? 6 : 5;
-  CUtensorMap tw, tx, ts, tz;
-  if (!make_rows_map(&tx, x, p.K, p.rows, ldx)) return cudaErrorInvalidValue;
-  if (w4) {
-    const uint64_t kg = p.K / p.group;
-    if (!make_map3(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, p.K / 2, p.N, p.G, 128, 128, true) ||
-        !make_map3(&ts, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, scales, p.N, kg, p.G, 128,
-                   p.groups_per_step, false))
+  p.x_whole = w4 && p.K % 64 == 0;
+  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const uint64_t N = p.N, K = p.K, ld = ldx;
+  Maps m;
+  for (int i = 0; i < 2; ++i) {
+    const cuuint32_t rows = 8 * (i + 1);
+    const cuuint64_t dims[3] = {64, (cuuint64_t)p.rows, K / 64}, strides[2] = {ld * 2, 128};
+    const cuuint64_t flat[2] = {K, (cuuint64_t)p.rows};
+    const cuuint32_t box[3] = {64, rows, 4};
+    if (!make_tensor_map(&m.x[i], bf16, x, p.x_whole ? 3 : 2, p.x_whole ? dims : flat, strides, box,
+                         true))
       return cudaErrorInvalidValue;
-    tz = ts;
-    if (zeros && !make_map3(&tz, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, zeros, p.N, kg, p.G, 128,
-                            p.groups_per_step, false))
-      return cudaErrorInvalidValue;
-    return swiglu ? run_int4<true>(tw, tx, ts, tz, p, s) : run_int4<false>(tw, tx, ts, tz, p, s);
   }
-  if (!make_map3(&tw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w, p.K, p.N, p.G, 64, 128, true))
+  if (!w4) {
+    if (!make_group_map(&m.w, bf16, 2, w, K, N, p.G, 64, 256, -1, true)) return cudaErrorInvalidValue;
+    m.s = m.z = m.w;
+    return run_few<false, false, 1>(m, p, s);
+  }
+  const uint64_t kg = K / p.group;
+  const uint32_t rows = swiglu ? 128 : 256, gps = p.groups_per_step;
+  if (!make_group_map(&m.w, u8, 1, w, K / 2, N, p.G, 128, rows, swiglu ? 1 : -1, true) ||
+      !make_group_map(&m.s, bf16, 2, scales, N, kg, p.G, rows, gps, swiglu ? 0 : -1, false))
     return cudaErrorInvalidValue;
-  return run_few<false, false, 1>(tw, tx, tw, tw, p, s);
+  m.z = m.s;
+  if (zeros && !make_group_map(&m.z, u8, 1, zeros, N, kg, p.G, rows, gps, swiglu ? 0 : -1, false))
+    return cudaErrorInvalidValue;
+  return swiglu ? run_int4<true>(m, p, s) : run_int4<false>(m, p, s);
 }
 
 }  // namespace moe
