@@ -68,35 +68,21 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
+// Loads of a stage: its address the same in all lanes, the lane's place and a constant beside it,
+// which one load instruction takes.
+template <class T>
+__device__ __forceinline__ T at(const uint8_t* st, uint32_t place, int offset) {
+  return *reinterpret_cast<const T*>(st + place + offset);
 }
-__device__ __forceinline__ float2 lds_f2(uint32_t a) {
-  float2 v;
-  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
-  return v;
+
+// s + the low or the high bf16 of a pair, without a conversion of its own.
+__device__ __forceinline__ float add_lo(float s, uint32_t pair) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.f32.bf16 %0, l, %0;\n\t}" : "+f"(s) : "r"(pair));
+  return s;
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
-               :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+__device__ __forceinline__ float add_hi(float s, uint32_t pair) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.f32.bf16 %0, h, %0;\n\t}" : "+f"(s) : "r"(pair));
+  return s;
 }
 
 // Elements i and i + 4 of a word of eight codes as the bf16 pair 128 + q.
@@ -124,7 +110,7 @@ __device__ __forceinline__ int token_place(int tok, int box, int piece) {
 // are of one group: with groups of 128 elements lane t has elements 32 t .. 32 t + 31 of the group
 // (16 bytes of codes), else 8 t .. 8 t + 7 of each 32 (a word).
 struct Places {
-  uint32_t w[8], x[4], sum, s, z;
+  uint32_t w[8], x[2][4], sum, s, z;            // x: for one tile of eight tokens, for two
 };
 
 template <bool W4, bool SWIGLU, int GC>
@@ -138,14 +124,17 @@ __device__ __forceinline__ Places places(const FewProduct& p, int rg, int g, int
 #pragma unroll
       for (int q = 0; q < 2; ++q) a.w[q] = row0 * 128 + (((4 * q + t) ^ r) << 4);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        a.x[j] = C::X_OFF + g * 128 + (token_place<GC>(g, t >> 1, 4 * (t & 1) + j) << 4);
+      for (int j = 0; j < 4; ++j) {
+        a.x[0][j] = C::X_OFF + g * 128 + (token_place<GC>(g, t >> 1, 4 * (t & 1) + j) << 4) +
+                    (t >> 1) * 1024;
+        a.x[1][j] = a.x[0][j] + (t >> 1) * 1024;
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) a.w[i] = row0 * 128 + ((i ^ r) << 4) + t * 4;
 #pragma unroll
       for (int b = 0; b < 2; ++b)
-        a.x[b] = C::X_OFF + g * 128 + (token_place<GC>(g, 0, b * 4 + t) << 4);
+        a.x[0][b] = C::X_OFF + g * 128 + (token_place<GC>(g, 0, b * 4 + t) << 4);
     }
     // (scales and zero points: gate's and up's rows apart, or 256 rows a group)
     const int at = SWIGLU ? (rg >> 2) * p.groups_per_step * 128 + (row0 & 127) : row0;
@@ -156,7 +145,7 @@ __device__ __forceinline__ Places places(const FewProduct& p, int rg, int g, int
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       a.w[b] = row0 * 128 + (((4 * b + t) ^ r) << 4);
-      a.x[b] = C::X_OFF + g * 128 + (((4 * b + t) ^ g) << 4);
+      a.x[0][b] = C::X_OFF + g * 128 + (((4 * b + t) ^ g) << 4);
     }
   }
   return a;
@@ -164,11 +153,11 @@ __device__ __forceinline__ Places places(const FewProduct& p, int rg, int g, int
 
 // What a step adds to a warp's 32 rows x 8 NTL tokens. GC: chunks of 32 elements in a group.
 template <int NTL, bool SWIGLU, int GC>
-__device__ __forceinline__ void step_int4(float (&tot)[2][2][4], uint32_t st, const Places& a,
-                                          bool has_zeros, int t) {
+__device__ __forceinline__ void step_int4(float (&tot)[2][2][4], const uint8_t* st, const Places& a,
+                                          bool has_zeros) {
   using C = Cfg<true>;
   constexpr int GS = SWIGLU ? 128 : 256;         // from one group's scales to the next's
-  const uint32_t stx = GC == 4 ? st + (t >> 1) * (NTL * 1024) : st;
+  constexpr int XB = NTL * 1024;                 // from one box of the tokens to the next
 #pragma unroll
   for (int c0 = 0; c0 < 8; c0 += GC) {
     float acc[2][NTL][4];
@@ -183,7 +172,7 @@ __device__ __forceinline__ void step_int4(float (&tot)[2][2][4], uint32_t st, co
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) w4[m][h] = lds128(st + a.w[c0 / 4] + m * 2048 + h * 1024);
+        for (int h = 0; h < 2; ++h) w4[m][h] = at<uint4>(st, a.w[c0 / 4], m * 2048 + h * 1024);
     }
 #pragma unroll
     for (int c = c0; c < c0 + GC; ++c) {
@@ -197,13 +186,13 @@ __device__ __forceinline__ void step_int4(float (&tot)[2][2][4], uint32_t st, co
                               : (c & 3) == 1 ? v.y
                               : (c & 3) == 2 ? v.z
                                              : v.w
-                            : lds32(st + a.w[c] + m * 2048 + h * 1024);
+                            : at<uint32_t>(st, a.w[c], m * 2048 + h * 1024);
         }
       uint4 x[NTL];
 #pragma unroll
       for (int n = 0; n < NTL; ++n)
-        x[n] = GC == 4 ? lds128(stx + a.x[c & 3] + n * 1024 + (c >> 2) * (2 * NTL * 1024))
-                       : lds128(stx + a.x[c & 1] + n * 1024 + (c >> 1) * (NTL * 1024));
+        x[n] = GC == 4 ? at<uint4>(st, a.x[NTL - 1][c & 3], n * 1024 + (c >> 2) * 2 * XB)
+                       : at<uint4>(st, a.x[0][c & 1], n * 1024 + (c >> 1) * XB);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const uint32_t a0 = codes_pair(w[m][0], 0), a1 = codes_pair(w[m][1], 0);
@@ -221,14 +210,15 @@ __device__ __forceinline__ void step_int4(float (&tot)[2][2][4], uint32_t st, co
     const int q = c0 / GC;
     float2 sx[NTL];
 #pragma unroll
-    for (int n = 0; n < NTL; ++n) sx[n] = lds_f2(st + a.sum + (q * kTok + n * 8) * 4);
+    for (int n = 0; n < NTL; ++n) sx[n] = at<float2>(st, a.sum, (q * kTok + n * 8) * 4);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float s = __uint_as_float(lds16(st + a.s + (q * GS + 16 * m + 8 * h) * 2) << 16);
+        const float s = __uint_as_float(
+            (uint32_t)at<uint16_t>(st, a.s, (q * GS + 16 * m + 8 * h) * 2) << 16);
         const float z =
-            has_zeros ? (float)(128u + (lds8(st + a.z + q * GS + 16 * m + 8 * h) & 127u)) : 136.f;
+            has_zeros ? (float)(128u + (at<uint8_t>(st, a.z, q * GS + 16 * m + 8 * h) & 127u)) : 136.f;
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
           tot[m][n][2 * h] = fmaf(s, fmaf(-z, sx[n].x, acc[m][n][2 * h]), tot[m][n][2 * h]);
@@ -240,16 +230,16 @@ __device__ __forceinline__ void step_int4(float (&tot)[2][2][4], uint32_t st, co
 }
 
 template <int NTL>
-__device__ __forceinline__ void step_bf16(float (&tot)[2][2][4], uint32_t st, const Places& a) {
+__device__ __forceinline__ void step_bf16(float (&tot)[2][2][4], const uint8_t* st, const Places& a) {
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     uint4 w[2][2], x[NTL];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) w[m][h] = lds128(st + a.w[c] + m * 2048 + h * 1024);
+      for (int h = 0; h < 2; ++h) w[m][h] = at<uint4>(st, a.w[c], m * 2048 + h * 1024);
 #pragma unroll
-    for (int n = 0; n < NTL; ++n) x[n] = lds128(st + a.x[c] + n * 1024);
+    for (int n = 0; n < NTL; ++n) x[n] = at<uint4>(st, a.x[0][c], n * 1024);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -281,7 +271,8 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  float* tiles = reinterpret_cast<float*>(smem_raw + (base - raw) + C::STAGES * C::STAGE);
+  uint8_t* stages = smem_raw + (base - raw);
+  float* tiles = reinterpret_cast<float*>(stages + C::STAGES * C::STAGE);
   uint8_t* ctrl = reinterpret_cast<uint8_t*>(tiles) + 2 * kTileBytes;
   const uint32_t ctrl_u = base + C::STAGES * C::STAGE + 2 * kTileBytes;
   const uint32_t bar_full = ctrl_u, bar_ready = ctrl_u + 40, bar_empty = ctrl_u + 80;
@@ -463,20 +454,19 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget,
                                                     abort_flag));
         if (!ok) break;
-        const uint32_t st = base + stage * C::STAGE;
+        uint8_t* st = stages + stage * C::STAGE;
         // three tokens at a time: what bounds these warps is the shuffles' latency
         for (int tok0 = warp - 1; tok0 < ntok; tok0 += 3 * C::HELPERS) {
           uint4 q[3];
           float s[3];
-          uint32_t r[3];
+          uint8_t* r[3];
 #pragma unroll
           for (int i = 0; i < 3; ++i) {
             const int tok = min(tok0 + i * C::HELPERS, ntok - 1);
             r[i] = st + C::X_OFF + (lane >> 3) * (ntok * 128) + tok * 128;
-            q[i] = lds128(r[i] + (((lane & 7) ^ (tok & 7)) << 4));
-            float f[8];
-            unpack8(q[i], f);
-            s[i] = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+            q[i] = *reinterpret_cast<const uint4*>(r[i] + (((lane & 7) ^ (tok & 7)) << 4));
+            s[i] = add_hi(add_lo(add_hi(add_lo(0.f, q[i].x), q[i].x), q[i].y), q[i].y) +
+                   add_hi(add_lo(add_hi(add_lo(0.f, q[i].z), q[i].z), q[i].w), q[i].w);
           }
 #pragma unroll
           for (int o = 1; o < 4 * GC; o *= 2)
@@ -488,12 +478,10 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
             const int tok = tok0 + i * C::HELPERS;
             if (tok >= ntok) break;
             if (lane % (4 * GC) == 0)
-              asm volatile("st.shared.f32 [%0], %1;"
-                           :: "r"(st + C::SUM_OFF + (lane / (4 * GC) * kTok + tok) * 4), "f"(s[i])
-                           : "memory");
-            sts128(r[i] + (token_place<GC>(tok, lane >> 3, lane & 7) << 4),
-                   make_uint4(__byte_perm(q[i].x, q[i].z, 0x5410), __byte_perm(q[i].x, q[i].z, 0x7632),
-                              __byte_perm(q[i].y, q[i].w, 0x5410), __byte_perm(q[i].y, q[i].w, 0x7632)));
+              *reinterpret_cast<float*>(st + C::SUM_OFF + (lane / (4 * GC) * kTok + tok) * 4) = s[i];
+            *reinterpret_cast<uint4*>(r[i] + (token_place<GC>(tok, lane >> 3, lane & 7) << 4)) =
+                make_uint4(__byte_perm(q[i].x, q[i].z, 0x5410), __byte_perm(q[i].x, q[i].z, 0x7632),
+                           __byte_perm(q[i].y, q[i].w, 0x5410), __byte_perm(q[i].y, q[i].w, 0x7632));
           }
         }
         ptx::fence_proxy_async_smem();           // TMA writes here next
@@ -531,14 +519,14 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) tot[m][j][i] = 0.f;
       for (int k = 0; k < n; ++k) {
-        ok = ptx::mbar_wait(bar_full + 8 * stage, phase, kWaitBudget, abort_flag);
-        if (W4) ok = ok && ptx::mbar_wait(bar_ready + 8 * stage, phase, kWaitBudget, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
+        // (the helpers arrive after they have seen the stage's loads land)
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait((W4 ? bar_ready : bar_full) + 8 * stage, phase,
+                                                    kWaitBudget, abort_flag));
         if (!ok) break;
-        const uint32_t st = base + stage * C::STAGE;
+        const uint8_t* st = stages + stage * C::STAGE;
         if constexpr (W4) {
-          if (two) step_int4<2, SWIGLU, GC>(tot, st, here, p.has_zeros, t);
-          else step_int4<1, SWIGLU, GC>(tot, st, here, p.has_zeros, t);
+          if (two) step_int4<2, SWIGLU, GC>(tot, st, here, p.has_zeros);
+          else step_int4<1, SWIGLU, GC>(tot, st, here, p.has_zeros);
         } else {
           if (two) step_bf16<2>(tot, st, here);
           else step_bf16<1>(tot, st, here);
