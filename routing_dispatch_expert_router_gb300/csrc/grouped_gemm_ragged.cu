@@ -25,6 +25,8 @@
 //   - the weight gradient reduces over the rows: a warp of each CTA zeroes the next group's rows
 //     of the last block in both operands (zero times a NaN is one) before it hands the stage to
 //     the pair's MMAs.
+#include <math.h>
+
 #include "gemm_common.cuh"
 
 namespace moe {
@@ -533,13 +535,23 @@ cudaError_t run_ragged(const Maps& m, const RaggedProduct& p, cudaStream_t s) {
   return launch_early(kern, (unsigned)grid, dim3(kPairThreads, 1, 1), kSmem, s, m, p);
 }
 
-// Columns of a tile, 256 where that makes a tile for every pair of SMs, else fewer: a wide tile
-// reads the features' operand less often, few tiles leave SMs without one.
-int tile_columns(int64_t columns, int64_t others, int least) {
+// Columns of a tile: rounds of tiles over the pairs of SMs times what a tile takes, which is its
+// columns and about 64 more (the features' operand, filling and draining). `others`: tiles in the
+// other dimension; `groups`: each cuts `columns` once more (half a tile on average), or 0.
+int tile_columns(int64_t columns, int64_t others, int64_t groups, int least) {
   const int pairs = num_sms() / 2;
-  int tile = 256;
-  while (tile > least && others * ((columns + tile - 1) / tile) < pairs) tile /= 2;
-  return tile;
+  int best = 256;
+  double cost = 0;
+  for (int tile = 256; tile >= least; tile -= least) {
+    const double tiles = others * (groups ? (double)columns / tile + 0.5 * groups
+                                          : (double)((columns + tile - 1) / tile));
+    const double c = ceil(tiles / pairs) * (tile + 64);
+    if (tile == 256 || c < 0.95 * cost) {
+      best = tile;
+      cost = c;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -555,7 +567,7 @@ cudaError_t launch_ragged_gemm(RaggedProduct p, int dgrad, const void* x, int64_
   p.feat = dgrad ? K : N;
   p.red = dgrad ? N : K;
   p.cols = 0;
-  p.tile = tile_columns(p.rows, (p.feat + kM - 1) / kM, 64);
+  p.tile = tile_columns(p.rows, (p.feat + kM - 1) / kM, p.rows < p.G ? p.rows : p.G, 64);
   Maps m;
   for (int i = 0; i < 8; ++i)
     if (!map2(&m.b[i], x, p.red, p.rows, ldx, 64, 16 * (i + 1))) return cudaErrorInvalidValue;
@@ -571,7 +583,7 @@ cudaError_t launch_ragged_wgrad(RaggedProduct p, const void* dy, int64_t lddy, c
   p.cols = K;
   p.red = 0;
   p.add = nullptr;
-  p.tile = tile_columns(K, (int64_t)p.G * ((N + kM - 1) / kM), 128);
+  p.tile = tile_columns(K, (int64_t)p.G * ((N + kM - 1) / kM), 0, 128);
   // (without rows nothing is loaded: the maps are then of any valid extent)
   const bool some = p.rows > 0;
   const void *pa = some ? dy : p.out, *pb = some ? x : p.out;

@@ -359,8 +359,10 @@ struct FewProduct {
 constexpr int kFewCtas = 256;
 constexpr int kFewPart = 256 * 16;
 constexpr int kFewLeast = 2;  // steps of K a CTA takes at least (they must weigh more than one)
-constexpr int kFewRows = 64;  // rows a group up to which bf16 weights are streamed
+constexpr int kFewJoin = 2;   // steps that joining a unit's parts takes the time of
 bool few_fits(int64_t rows, int G, int64_t N, int64_t K);
+// Whether bf16 weights are streamed, groups having about `most` rows at most.
+bool few_rows(int64_t most, int G, int64_t N);
 cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const void* w,
                                const void* scales, const void* zeros, bool swiglu, cudaStream_t s);
 

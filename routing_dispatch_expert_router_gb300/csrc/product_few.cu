@@ -328,11 +328,16 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
   const int weight = block_exclusive_scan(prefix, p.G, tmp);
   if (tid == 0) prefix[p.G] = weight;
   __syncthreads();
-  // An even share of the steps, weighed by what they take, for each CTA, not under kFewLeast
-  // steps where there are few. CTA b begins with the first step at or behind its share's start.
+  // An even share of the steps, weighed by what they take, for each CTA: not under kFewLeast steps
+  // where there are few, and no unit shared where whole ones leave the fullest CTA kFewJoin steps
+  // more at most, which is what a join costs. CTA b begins with the first step (the first unit) at
+  // or behind its share's start.
   const int KC = p.steps;
   const int64_t total = (int64_t)weight * KC;
-  const int nb = max(1, (int)min(total / (kFewLeast * C::W1), (int64_t)gridDim.x));
+  int nb = max(1, (int)min(total / (kFewLeast * C::W1), (int64_t)gridDim.x));
+  const bool whole = (int64_t)((weight + (int)gridDim.x * C::W2 - 1) / ((int)gridDim.x * C::W2)) *
+                         C::W2 * KC <= total / nb + kFewJoin * C::W1;
+  if (whole) nb = gridDim.x;
   if (total == 0 || (int)blockIdx.x >= nb) return;
   auto first_of = [&](int b) {
     const int64_t at = total * b / nb;
@@ -368,7 +373,7 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
   };
   if (tid < 64 && lane == 0) {
     Place v = first_of(blockIdx.x + warp);
-    if (v.step == KC) next_unit(v);
+    if (v.step == KC || (whole && v.step > 0)) next_unit(v);
     s_ends[warp] = v;
   }
   __syncthreads();
@@ -753,6 +758,15 @@ static_assert(kFewPart == kSlab * kTok, "parts as the kernel writes them");
 // Units of 16 tokens and 256 weight rows, weighed, that the kernel's 32-bit numbers hold.
 bool few_fits(int64_t rows, int G, int64_t N, int64_t K) {
   return (rows / kTok + G + 1) * ((N + 127) / 128) * 7 < (1LL << 31) && K < (1LL << 24);
+}
+
+// A pass of the stream has 16 tokens, a tile of the tensor cores' kernel up to 256. With more than
+// 16 the stream reads the weights again (4.5 TB/s a pass); the other kernel reads them once, 75
+// GB/s a tile of 256 features, of which 60 are as fast as one pass. (21 rows for each of 4 experts,
+// 1128 x 7776: 31 us against 45; 60 for each of two, 4096 x 4096: 41 against 29.)
+bool few_rows(int64_t most, int G, int64_t N) {
+  const int64_t passes = (most + kTok - 1) / kTok;
+  return passes <= 1 || (passes <= 4 && passes * G * ((N + 255) / 256) < num_sms() * 2 / 5);
 }
 
 cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const void* w,

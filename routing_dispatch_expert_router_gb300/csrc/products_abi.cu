@@ -234,7 +234,7 @@ moe_status moe_grouped_gemm(int64_t groups, int64_t rows, int64_t N, int64_t K, 
   if (rows == 0) return MOE_OK;
   OP_REQUIRE(rows_ok(x, ldx, K) && rows_ok(out, ldo, N) && rows_or_null(add, ldadd, N));
   const int64_t most = expected_rows > 0 && expected_rows < rows ? expected_rows : rows;
-  if (most <= kFewRows && few_fits(rows, (int)groups, N, K)) {
+  if (few_rows(most, (int)groups, N) && few_fits(rows, (int)groups, N, K)) {
     FewProduct p = few_product(groups, rows, N, K, counts, offsets, out, ldo, scratch);
     p.add = bf(add);
     p.ldadd = ldadd;
