@@ -115,7 +115,19 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
   const int total = block_exclusive_scan(prefix, p.G, tmp);
   if (tid == 0) prefix[p.G] = total;
   __syncthreads();
-  if (cluster >= total) return;                            // both CTAs of the pair leave together
+  // Few tiles: the reduction of each is cut among several pairs. (A step takes some 600 clocks, a
+  // part about 12 a column to join, one after the other: sqrt(nk tile / 50) steps make the least
+  // of both.) Every pair then has one unit, and so has its part of the scratch for itself.
+  int splits = 1;
+  const int most = min(nclusters, kRaggedPairs);
+  if (total > 0 && 2 * total <= most) {
+    int nk = (p.red + BK - 1) / BK;
+    if (MODE == kWgrad)
+      for (int g = 0; g < p.G; ++g) nk = max(nk, (s_cnt[g] + BK - 1) / BK);
+    splits = max(1, min(most / total, nk / max(2, (int)sqrtf(nk * p.tile * 0.02f))));
+  }
+  const int units = total * splits;
+  if (cluster >= units) return;                            // both CTAs of the pair leave together
 
   if (warp == 1) {
     ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), 512);
@@ -128,12 +140,18 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
   const uint32_t tmem_base = *tmem_slot;
 
   struct Tile {
-    int g, f0, n0, n, nk;           // features from f0, columns (rows of the group) n0 .. n0 + n - 1
+    int g, f0, n0, n, k0, nk;       // features from f0, columns (rows of the group) n0 .. n0 + n - 1,
+    bool ends;                      // blocks k0 .. k0 + nk - 1 of the reduction, whether to its end
   };
   // A role's walk over its pair's tiles: the next one is found while the present one is worked on
   // (its group from the present one's on), so that no role stands still between tiles.
   auto tile_at = [&](int tile, int g) {
     Tile t;
+    unsigned split = 0;
+    if (splits > 1) {
+      split = tile / total;
+      tile -= split * total;
+    }
     while (prefix[g + 1] <= tile) ++g;
     t.g = g;
     const unsigned local = tile - prefix[g];
@@ -155,6 +173,14 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
       t.n = min(size, ((c - t.n0) + 31) & ~31);
       t.nk = (p.red + BK - 1) / BK;
     }
+    t.k0 = 0;
+    t.ends = true;
+    if (splits > 1) {
+      const unsigned nk = t.nk;
+      t.k0 = nk * split / splits;
+      t.nk = nk * (split + 1) / splits - t.k0;
+      t.ends = t.k0 + t.nk == (int)nk && t.nk > 0;
+    }
     return t;
   };
 
@@ -168,7 +194,7 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
 #pragma unroll
       for (int s = 0; s < kStages; ++s) leader_full[s] = ptx::mapa_shared(bar_full + 8 * s, 0);
       Tile t = tile_at(cluster, 0), next = t;
-      for (int pt = cluster; pt < total && ok; pt += nclusters, t = next) {
+      for (int pt = cluster; pt < units && ok; pt += nclusters, t = next) {
         const int half = t.n >> 1, r = s_off[t.g];
         const int f0 = t.f0 + (int)rank * 128, c0 = t.n0 + (int)rank * half;
         const uint32_t bytes = kABytes + half * BK * 2;
@@ -181,7 +207,7 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
             break;
           }
           const uint32_t sA = base + stage * kStageBytes, sB = sA + kABytes;
-          const int k0 = kb * BK;
+          const int k0 = (t.k0 + kb) * BK;
           // both CTAs' loads count on the even CTA's barrier; a weight gradient's last block goes
           // to each CTA's own fixer first
           const bool tail = MODE == kWgrad && s_cnt[t.g] - k0 < BK;
@@ -223,7 +249,7 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
             phase ^= 1u;
           }
         }
-        if (pt + nclusters < total) next = tile_at(pt + nclusters, t.g);
+        if (pt + nclusters < units) next = tile_at(pt + nclusters, t.g);
       }
       if (!ok) {
         record_status(p.status, MOE_ERR_TIMEOUT);
@@ -242,7 +268,7 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
       const uint32_t peer_tfull[2] = {ptx::mapa_shared(bar_tfull, 1),
                                       ptx::mapa_shared(bar_tfull + 8, 1)};
       Tile t = tile_at(cluster, 0), next = t;
-      for (int pt = cluster; pt < total && ok; pt += nclusters, t = next) {
+      for (int pt = cluster; pt < units && ok; pt += nclusters, t = next) {
         const uint32_t idesc = ptx::idesc_bf16(kM, t.n, A_MN, B_MN);
         if (!ptx::mbar_wait_cluster(bar_tempty + 8 * acc, acc_phase ^ 1u, kWaitBudget, abort_flag)) {
           ok = false;
@@ -267,7 +293,7 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
           }
           issued = true;
           ptx::mma_commit_pair(bar_empty + 8 * stage, 3);
-          if (kb == 0 && pt + nclusters < total) next = tile_at(pt + nclusters, t.g);
+          if (kb == 0 && pt + nclusters < units) next = tile_at(pt + nclusters, t.g);
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
@@ -279,7 +305,7 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
         } else {                                           // an empty group: nothing to wait for
           ptx::mbar_arrive(bar_tfull + 8 * acc);
           ptx::mbar_arrive_cluster(peer_tfull[acc]);
-          if (pt + nclusters < total) next = tile_at(pt + nclusters, t.g);
+          if (pt + nclusters < units) next = tile_at(pt + nclusters, t.g);
         }
         if (++acc == 2) {
           acc = 0;
@@ -302,10 +328,10 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
       uint32_t stage = 0, phases = 0;                      // phases: a bit per stage, of bar_tail
       bool ok = true;
       int g = 0;
-      for (int pt = cluster; pt < total && ok; pt += nclusters) {
+      for (int pt = cluster; pt < units && ok; pt += nclusters) {
         const Tile t = tile_at(pt, g);
         g = t.g;
-        const int valid = s_cnt[t.g] & (BK - 1);
+        const int valid = t.ends ? s_cnt[t.g] & (BK - 1) : 0;
         if (valid) {
           stage = (stage + t.nk - 1) % kStages;
           ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_tail + 8 * stage, (phases >> stage) & 1u,
@@ -341,17 +367,16 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
     const int lr = lane >> 2, lc = lane & 3, l8 = lane & 7;
     uint32_t acc = 0, acc_phase = 0;
     Tile next = tile_at(cluster, 0);
-    for (int pt = cluster; pt < total; pt += nclusters) {
+    for (int pt = cluster; pt < units; pt += nclusters) {
       const Tile t = next;
-      if (pt + nclusters < total) next = tile_at(pt + nclusters, t.g);
+      if (pt + nclusters < units) next = tile_at(pt + nclusters, t.g);
       const int f = t.f0 + fq;
       const int64_t row0 = (int64_t)s_off[t.g] + t.n0;
       // rows of the tile that are this lane's to write, sixteen bytes (features fl .. fl + 7) each
       const int fl = f + 8 * lc;
       const int rows = MODE != kWgrad && fl < p.feat ? min(s_cnt[t.g] - t.n0, t.n) : 0;
       uint4 add[4][4];
-      if constexpr (MODE != kWgrad) {
-        // every load of the tile is under way before its sums are waited for
+      auto fetch_add = [&] {
         if (p.add) {
 #pragma unroll
           for (int b = 0; b < 4; ++b)
@@ -362,7 +387,9 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
                 add[b][v] = *reinterpret_cast<const uint4*>(p.add + (row0 + i) * p.ldadd + fl);
             }
         }
-      }
+      };
+      // every load of the tile is under way before its sums are waited for
+      if (MODE != kWgrad && splits == 1) fetch_add();
       // hands the accumulator back (what this publishes is tensor memory alone: a release would
       // wait for the stores, 5000 clocks a tile)
       auto give = [&] {
@@ -370,9 +397,65 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_cluster_tmem(leader_tempty[acc]);
       };
+      // Parts of a tile that several pairs share: 4096 sums of a warp behind each other, by pair;
+      // the warp that arrives last of those with the same piece adds them, in K's order.
+      const int piece = (int)rank * kEpiWarps + warp - 4;
+      auto part = [&](int unit, int b) {
+        return reinterpret_cast<float4*>(p.parts) +
+               ((int64_t)(unit * 2 * kEpiWarps + piece) * 4 + b) * 256 + lane;
+      };
+      auto put = [&](int b, const uint32_t (&r)[32]) {
+        float4* to = part(pt, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          __stcg(to + 32 * i, make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                          __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])));
+      };
+      auto last = [&] {
+        uint32_t n = 0;
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) {
+          uint32_t* arrived = p.arrived + (pt % total) * 2 * kEpiWarps + piece;
+          n = ptx::atom_add_acq_rel(arrived, 1u);
+          if (n + 1 == splits) *arrived = 0u;              // as the next launch expects it
+        }
+        n = __shfl_sync(0xffffffffu, n, 0);
+        __threadfence();
+        return n + 1 == splits;
+      };
+      auto get = [&](int unit, int b, uint32_t (&r)[32]) {
+        const float4* from = part(unit, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 d = __ldcg(from + 32 * i);
+          r[4 * i] = __float_as_uint(d.x);
+          r[4 * i + 1] = __float_as_uint(d.y);
+          r[4 * i + 2] = __float_as_uint(d.z);
+          r[4 * i + 3] = __float_as_uint(d.w);
+        }
+      };
+      // the sum of box b's parts takes the place of this pair's
+      auto join = [&](int b) {
+        float sum[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[i] = 0.f;
+#pragma unroll 2
+        for (int u = pt % total; u < units; u += total) {
+          uint32_t d[32];
+          get(u, b, d);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[i] += __uint_as_float(d[i]);
+        }
+        uint32_t r[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(sum[i]);
+        put(b, r);
+      };
       const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_tfull + 8 * acc, acc_phase,
                                                              kWaitBudget, abort_flag));
       if (!ok) {
+        if (splits > 1) last();                            // (the counters as after any launch)
         if (lane == 0) {
           record_status(p.status, MOE_ERR_TIMEOUT);
           *abort_flag = 1;
@@ -387,9 +470,12 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
         // columns leave tensor memory while these are on their way.
         const int end = f < p.feat ? min(t.n, p.cols - t.n0) : 0;
         uint32_t r0[32], r1[32];
-        auto take = [&](int c) {
+        auto take = [&](int c, bool shared) {
           if (c >= end) return;
-          if (t.nk == 0) {
+          if (shared) {
+            get(pt, c >> 7 << 1, r0);
+            get(pt, (c >> 7 << 1) + 1, r1);
+          } else if (t.nk == 0) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) r0[i] = r1[i] = 0u;
           } else {
@@ -397,7 +483,19 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
             ptx::tmem_ld32(tbase + c + 32, r1);
           }
         };
-        take(64 * odd);
+        if (splits > 1) {
+#pragma unroll 1
+          for (int c = 64 * odd; c < end; c += 128) {
+            take(c, false);
+            ptx::tmem_ld_wait();
+            put(c >> 7 << 1, r0);
+            put((c >> 7 << 1) + 1, r1);
+          }
+          if (!last()) break;                              // (a pair has one unit)
+#pragma unroll 1
+          for (int b = 0; 128 * (b >> 1) + 64 * odd < end; ++b) join(b);
+        }
+        take(64 * odd, splits > 1);
         if (64 * odd >= end) give();
 #pragma unroll 1
         for (int c = 64 * odd; c < end; c += 128) {
@@ -406,7 +504,7 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
           uint4 a[4], b[4];
           gg::pack_slice(r0, a);
           gg::pack_slice(r1, b);
-          take(c + 128);
+          take(c + 128, splits > 1);
           if (c + 128 >= end) give();
           __nv_bfloat16* out = p.out + ((int64_t)t.g * p.feat + f) * p.cols + col;
 #pragma unroll
@@ -434,13 +532,30 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
         // 16 rows x 32 features in fp32 at a time, 128 bytes a row, 16-byte chunk c of row i at
         // c ^ (i & 1): a feature's stores and a row's eight-feature loads meet every bank once
         const int here = f < p.feat ? min(s_cnt[t.g] - t.n0, t.n) : 0;
+        if (splits > 1) {
+#pragma unroll 1
+          for (int b = 0; 64 * b + 32 * odd < here; ++b) {
+            uint32_t r[32];
+            ptx::tmem_ld32(tbase + 64 * b + 32 * odd, r);
+            ptx::tmem_ld_wait();
+            put(b, r);
+          }
+          if (!last()) break;                              // (a pair has one unit)
+#pragma unroll 1
+          for (int b = 0; 64 * b + 32 * odd < here; ++b) join(b);
+          fetch_add();
+        }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const int j = 64 * b + 32 * odd;                 // the box's first row
           if (j >= here) break;
           uint32_t r[32];
-          ptx::tmem_ld32(tbase + j, r);
-          ptx::tmem_ld_wait();
+          if (splits > 1) {
+            get(pt, b, r);
+          } else {
+            ptx::tmem_ld32(tbase + j, r);
+            ptx::tmem_ld_wait();
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             __syncwarp();                                  // the box before has been read

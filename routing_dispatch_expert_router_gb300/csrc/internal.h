@@ -382,11 +382,14 @@ struct RaggedProduct {
   int64_t ldadd;
   __nv_bfloat16* out;
   int64_t ldo;
+  float* parts;               // [kRaggedPairs][256 x 256] fp32
+  uint32_t* arrived;          // [kRaggedPairs / 2][16], zero before and after every launch
   int32_t* status;
   // set by the launchers: features (the output's columns; the weight gradient's rows), the length
   // reduced over (not the weight gradient's), the weight gradient's columns, columns of a tile
   int feat, red, cols, tile;
 };
+constexpr int kRaggedPairs = 80;   // pairs of SMs, at most, that share reductions
 // cols: of a weight gradient, else 0.
 bool ragged_fits(int64_t rows, int G, int64_t feat, int64_t cols);
 cudaError_t launch_ragged_gemm(RaggedProduct p, int dgrad, const void* x, int64_t ldx,

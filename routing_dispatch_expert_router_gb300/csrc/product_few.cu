@@ -329,12 +329,14 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
   if (tid == 0) prefix[p.G] = weight;
   __syncthreads();
   // An even share of the steps, weighed by what they take, for each CTA: not under kFewLeast steps
-  // where there are few, and no unit shared where whole ones leave the fullest CTA kFewJoin steps
+  // where there are few, nor under what makes a unit's steps in one CTA and the parts that the last
+  // one joins the least together (a part costs half a step), and no unit shared where whole ones leave the fullest CTA kFewJoin steps
   // more at most, which is what a join costs. CTA b begins with the first step (the first unit) at
   // or behind its share's start.
   const int KC = p.steps;
   const int64_t total = (int64_t)weight * KC;
-  int nb = max(1, (int)min(total / (kFewLeast * C::W1), (int64_t)gridDim.x));
+  const int least = max(kFewLeast, (int)sqrtf(0.5f * KC));
+  int nb = max(1, (int)min(total / (least * C::W1), (int64_t)gridDim.x));
   const bool whole = (int64_t)((weight + (int)gridDim.x * C::W2 - 1) / ((int)gridDim.x * C::W2)) *
                          C::W2 * KC <= total / nb + kFewJoin * C::W1;
   if (whole) nb = gridDim.x;
@@ -607,35 +609,39 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
       sync();
       mine = *s_last;
       if (mine) {
-        // (every load of a part in flight at once: a part costs one way to L2)
-        constexpr int V = kSlab * kTok / (4 * CT);
-        float4 sum[V];
+        // (four parts' loads in flight at once: a round of them costs one way to L2)
+        for (int e = 4 * ctid; e < all; e += 16 * CT) {
+          float4 sum[4];
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int b = lo; b <= hi; ++b) {
-          const float* from = part(b) + 4 * ctid;
-          float4 d[V];
+          for (int i = 0; i < 4; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int b = lo; b <= hi; b += 4) {
+            float4 d[4][4];
 #pragma unroll
-          for (int i = 0; i < V; ++i)
-            if (4 * (ctid + i * CT) < all) d[i] = __ldcg(reinterpret_cast<const float4*>(from + 4 * i * CT));
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            if (4 * (ctid + i * CT) >= all) continue;
-            sum[i].x += d[i].x;
-            sum[i].y += d[i].y;
-            sum[i].z += d[i].z;
-            sum[i].w += d[i].w;
+              for (int i = 0; i < 4; ++i)
+                if (b + j <= hi && e + 4 * i * CT < all)
+                  d[j][i] = __ldcg(reinterpret_cast<const float4*>(part(b + j) + e + 4 * i * CT));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (b + j > hi || e + 4 * i * CT >= all) continue;
+                sum[i].x += d[j][i].x;
+                sum[i].y += d[j][i].y;
+                sum[i].z += d[j][i].z;
+                sum[i].w += d[j][i].w;
+              }
           }
-        }
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int e = 4 * (ctid + i * CT);
-          if (e >= all) continue;
-          float* f = tile4(e);
-          f[0] = sum[i].x;
-          f[kTileLd] = sum[i].y;
-          f[2 * kTileLd] = sum[i].z;
-          f[3 * kTileLd] = sum[i].w;
+          for (int i = 0; i < 4; ++i) {
+            if (e + 4 * i * CT >= all) continue;
+            float* f = tile4(e + 4 * i * CT);
+            f[0] = sum[i].x;
+            f[kTileLd] = sum[i].y;
+            f[2 * kTileLd] = sum[i].z;
+            f[3 * kTileLd] = sum[i].w;
+          }
         }
         if (ctid == 0) p.arrived[lo] = 0u;         // as the next launch expects it
       }

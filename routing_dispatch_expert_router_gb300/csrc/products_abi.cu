@@ -48,11 +48,13 @@ moe_status check_norm(int64_t T, int64_t H, const void* gamma, int32_t gamma_dty
   return MOE_OK;
 }
 
-// Scratch of a product: the status word, the parts' counters, the parts.
+// Scratch of a product: the status word, the parts' counters (of each kernel its own), the parts.
 constexpr int64_t kArrivedOffset = 1024;
-constexpr int64_t kPartsOffset = 4096;
-constexpr int64_t kProductScratch = kPartsOffset + 2LL * kFewCtas * kFewPart * 4;
-static_assert(kArrivedOffset + kFewCtas * 4 <= kPartsOffset, "counters before the parts");
+constexpr int64_t kRaggedArrivedOffset = kArrivedOffset + kFewCtas * 4;
+constexpr int64_t kPartsOffset = 8192;
+constexpr int64_t kFewBytes = 2LL * kFewCtas * kFewPart * 4, kRaggedBytes = kRaggedPairs * (256LL << 10);
+constexpr int64_t kProductScratch = kPartsOffset + (kFewBytes > kRaggedBytes ? kFewBytes : kRaggedBytes);
+static_assert(kRaggedArrivedOffset + kRaggedPairs / 2 * 16 * 4 <= kPartsOffset, "counters before the parts");
 
 moe_status check_segments(int64_t groups, int64_t rows, const int32_t* counts,
                           const int32_t* offsets) {
@@ -105,6 +107,7 @@ moe_status check_product(int64_t groups, int64_t rows, int64_t N, int64_t K, con
 RaggedProduct ragged_product(int64_t groups, int64_t rows, const int32_t* counts,
                              const int32_t* offsets, const void* add, int64_t ldadd, void* out,
                              int64_t ldo, void* scratch) {
+  uint8_t* sc = static_cast<uint8_t*>(scratch);
   RaggedProduct p{};
   p.G = (int)groups;
   p.rows = rows;
@@ -114,6 +117,8 @@ RaggedProduct ragged_product(int64_t groups, int64_t rows, const int32_t* counts
   p.ldadd = ldadd;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.ldo = ldo;
+  p.parts = reinterpret_cast<float*>(sc + kPartsOffset);
+  p.arrived = reinterpret_cast<uint32_t*>(sc + kRaggedArrivedOffset);
   p.status = static_cast<int32_t*>(scratch);
   return p;
 }
