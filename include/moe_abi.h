@@ -782,7 +782,7 @@ MOE_API moe_status moe_int4_dequantize(const moe_int4_tensor* w, void* out, void
  * add: bf16 rows of the output's shape, or NULL; it may be out itself.
  * expected_rows: the most rows that the caller expects a group to have (tokens
  * of a decoding step), a hint that chooses between the kernel that streams the
- * weights and the one with tiles of 128 rows; 0: not known. */
+ * weights (16 rows at a time) and the one with tiles of up to 256; 0: not known. */
 MOE_API moe_status moe_grouped_gemm(int64_t groups, int64_t rows, int64_t N, int64_t K,
                                     const void* x, int64_t ldx, const void* w,
                                     const int32_t* counts, const int32_t* offsets,

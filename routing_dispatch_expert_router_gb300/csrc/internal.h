@@ -362,7 +362,7 @@ constexpr int kFewLeast = 2;  // steps of K a CTA takes at least (they must weig
 constexpr int kFewJoin = 2;   // steps that joining a unit's parts takes the time of
 bool few_fits(int64_t rows, int G, int64_t N, int64_t K);
 // Whether bf16 weights are streamed, groups having about `most` rows at most.
-bool few_rows(int64_t most, int G, int64_t N);
+bool few_rows(int64_t most);
 cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const void* w,
                                const void* scales, const void* zeros, bool swiglu, cudaStream_t s);
 
@@ -394,6 +394,10 @@ constexpr int kRaggedPairs = 80;   // pairs of SMs, at most, that share reductio
 bool ragged_fits(int64_t rows, int G, int64_t feat, int64_t cols);
 cudaError_t launch_ragged_gemm(RaggedProduct p, int dgrad, const void* x, int64_t ldx,
                                const void* w, int N, int K, cudaStream_t s);
+// The two of a reduction of 64 at most (product_short.cu).
+bool short_fits(int64_t rows, int G, int64_t feat, int64_t red, bool add);
+cudaError_t launch_product_short(RaggedProduct p, int dgrad, const void* x, int64_t ldx,
+                                 const void* w, int N, int K, cudaStream_t s);
 cudaError_t launch_ragged_wgrad(RaggedProduct p, const void* dy, int64_t lddy, const void* x,
                                 int64_t ldx, int N, int K, cudaStream_t s);
 

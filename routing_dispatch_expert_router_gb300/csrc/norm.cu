@@ -177,18 +177,6 @@ rmsnorm_fwd_kernel(const RmsNormFwd p) {
 // Many rows: a persistent CTA keeps the loads of S rows in flight. Each thread copies its own
 // columns into its own places of shared memory (cp.async) and reads them back alone, so the
 // ring needs no barrier, and the rows in flight take no registers.
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
-}
-__device__ __forceinline__ void copies_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-__device__ __forceinline__ void copy16(uint4* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-               :: "r"(ptx::smem_u32(to)), "l"(from) : "memory");
-}
-
 template <int V, int S, int THREADS>
 __global__ void __launch_bounds__(THREADS)
 rmsnorm_fwd_ring_kernel(const RmsNormFwd p) {
@@ -210,11 +198,11 @@ rmsnorm_fwd_ring_kernel(const RmsNormFwd p) {
       for (int i = 0; i < V; ++i) {
         const int v = tid + i * step;
         if (v >= nvec) continue;
-        copy16(place(s, 0, i), x + 8 * v);
-        if (p.residual) copy16(place(s, 1, i), r + 8 * v);
+        ptx::cp_async16(place(s, 0, i), x + 8 * v);
+        if (p.residual) ptx::cp_async16(place(s, 1, i), r + 8 * v);
       }
     }
-    copies_commit();
+    ptx::cp_async_commit();
   };
   int64_t ahead = blockIdx.x;
 #pragma unroll
@@ -222,7 +210,7 @@ rmsnorm_fwd_ring_kernel(const RmsNormFwd p) {
   int s = 0, turn = 0;
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, ahead += gridDim.x, turn ^= 1) {
     issue(ahead, s == 0 ? S - 1 : s - 1);
-    copies_wait<S - 1>();
+    ptx::cp_async_wait<S - 1>();
     __nv_bfloat16* sum = p.sum ? p.sum + row * p.lds : nullptr;
     uint4 h[V];
     uint64_t s2 = ptx::f2_pack(0.f, 0.f);
@@ -235,7 +223,7 @@ rmsnorm_fwd_ring_kernel(const RmsNormFwd p) {
     finish_row<V>(p, row, h, g, block_sum(sum_of(s2), red[turn]), tid, step, lane);
     if (++s == S) s = 0;
   }
-  copies_wait<0>();
+  ptx::cp_async_wait<0>();
 }
 
 // The backward, persistent too: a thread keeps the same columns of every row that its CTA (its
@@ -275,12 +263,12 @@ rmsnorm_bwd_kernel(const RmsNormBwd p) {
       for (int i = 0; i < V; ++i) {
         const int v = first + i * step;
         if (v >= nvec) continue;
-        copy16(place(s, 0, i), dy + 8 * v);
-        copy16(place(s, 1, i), h + 8 * v);
-        if (p.dsum) copy16(place(s, 2, i), ds + 8 * v);
+        ptx::cp_async16(place(s, 0, i), dy + 8 * v);
+        ptx::cp_async16(place(s, 1, i), h + 8 * v);
+        if (p.dsum) ptx::cp_async16(place(s, 2, i), ds + 8 * v);
       }
     }
-    copies_commit();
+    ptx::cp_async_commit();
   };
   int64_t ahead = row0;
 #pragma unroll
@@ -291,7 +279,7 @@ rmsnorm_bwd_kernel(const RmsNormBwd p) {
     issue(ahead, s == 0 ? S - 1 : s - 1);
     const float rs = rs_next;
     if (row + rows < p.T) rs_next = __ldg(p.rstd + row + rows);
-    copies_wait<S - 1>();
+    ptx::cp_async_wait<S - 1>();
     const uint64_t rs2 = ptx::f2_pack(rs, rs);
     uint64_t dot = zero2;
     Eight t[KEEP ? V : 1], n[KEEP ? V : 1];
@@ -337,7 +325,7 @@ rmsnorm_bwd_kernel(const RmsNormBwd p) {
     }
     if (++s == S) s = 0;
   }
-  copies_wait<0>();
+  ptx::cp_async_wait<0>();
   if (!p.parts) return;
   float* part = p.parts + (int64_t)blockIdx.x * p.H;
   if (WARP) {

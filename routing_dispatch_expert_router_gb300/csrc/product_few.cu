@@ -767,13 +767,10 @@ bool few_fits(int64_t rows, int G, int64_t N, int64_t K) {
 }
 
 // A pass of the stream has 16 tokens, a tile of the tensor cores' kernel up to 256. With more than
-// 16 the stream reads the weights again (4.5 TB/s a pass); the other kernel reads them once, 75
-// GB/s a tile of 256 features, of which 60 are as fast as one pass. (21 rows for each of 4 experts,
-// 1128 x 7776: 31 us against 45; 60 for each of two, 4096 x 4096: 41 against 29.)
-bool few_rows(int64_t most, int G, int64_t N) {
-  const int64_t passes = (most + kTok - 1) / kTok;
-  return passes <= 1 || (passes <= 4 && passes * G * ((N + 255) / 256) < num_sms() * 2 / 5);
-}
+// 16 the stream reads the weights again. (us, stream and tiles: 4 rows for each of 64 experts,
+// 512 x 512: 10.4 and 14.4; 24 for each of 8, 1024 x 1024: 16.6 and 14.4; 48 for each of 4,
+// 1128 x 7776: 32.9 and 25.0; 60 for each of two, 4096 x 4096: 35.0 and 22.6.)
+bool few_rows(int64_t most) { return most <= kTok; }
 
 cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const void* w,
                                const void* scales, const void* zeros, bool swiglu,

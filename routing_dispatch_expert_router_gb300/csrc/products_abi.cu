@@ -239,7 +239,12 @@ moe_status moe_grouped_gemm(int64_t groups, int64_t rows, int64_t N, int64_t K, 
   if (rows == 0) return MOE_OK;
   OP_REQUIRE(rows_ok(x, ldx, K) && rows_ok(out, ldo, N) && rows_or_null(add, ldadd, N));
   const int64_t most = expected_rows > 0 && expected_rows < rows ? expected_rows : rows;
-  if (few_rows(most, (int)groups, N) && few_fits(rows, (int)groups, N, K)) {
+  const RaggedProduct rp = ragged_product(groups, rows, counts, offsets, add, ldadd, out, ldo, scratch);
+  if (short_fits(rows, (int)groups, N, K, add != nullptr)) {
+    OP_CUDA(launch_product_short(rp, 0, x, ldx, w, (int)N, (int)K, (cudaStream_t)stream));
+    return MOE_OK;
+  }
+  if (few_rows(most) && few_fits(rows, (int)groups, N, K)) {
     FewProduct p = few_product(groups, rows, N, K, counts, offsets, out, ldo, scratch);
     p.add = bf(add);
     p.ldadd = ldadd;
@@ -247,9 +252,7 @@ moe_status moe_grouped_gemm(int64_t groups, int64_t rows, int64_t N, int64_t K, 
     return MOE_OK;
   }
   if (!ragged_fits(rows, (int)groups, N, 0)) return MOE_ERR_UNSUPPORTED;
-  OP_CUDA(launch_ragged_gemm(
-      ragged_product(groups, rows, counts, offsets, add, ldadd, out, ldo, scratch), 0, x, ldx, w,
-      (int)N, (int)K, (cudaStream_t)stream));
+  OP_CUDA(launch_ragged_gemm(rp, 0, x, ldx, w, (int)N, (int)K, (cudaStream_t)stream));
   return MOE_OK;
 }
 
@@ -261,10 +264,14 @@ moe_status moe_grouped_gemm_dgrad(int64_t groups, int64_t rows, int64_t N, int64
   OP_TRY(check_product(groups, rows, N, K, w, counts, offsets, scratch));
   if (rows == 0) return MOE_OK;
   OP_REQUIRE(rows_ok(dy, lddy, N) && rows_ok(dx, lddx, K) && rows_or_null(add, ldadd, K));
+  const RaggedProduct rp =
+      ragged_product(groups, rows, counts, offsets, add, ldadd, dx, lddx, scratch);
+  if (short_fits(rows, (int)groups, K, N, add != nullptr)) {
+    OP_CUDA(launch_product_short(rp, 1, dy, lddy, w, (int)N, (int)K, (cudaStream_t)stream));
+    return MOE_OK;
+  }
   if (!ragged_fits(rows, (int)groups, K, 0)) return MOE_ERR_UNSUPPORTED;
-  OP_CUDA(launch_ragged_gemm(
-      ragged_product(groups, rows, counts, offsets, add, ldadd, dx, lddx, scratch), 1, dy, lddy, w,
-      (int)N, (int)K, (cudaStream_t)stream));
+  OP_CUDA(launch_ragged_gemm(rp, 1, dy, lddy, w, (int)N, (int)K, (cudaStream_t)stream));
   return MOE_OK;
 }
 

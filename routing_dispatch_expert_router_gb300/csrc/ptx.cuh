@@ -107,6 +107,27 @@ __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A thread's own copies global -> shared, in groups; those of eight bytes write zeros (and read
+// nothing) where !some.
+__device__ __forceinline__ void cp_async16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void cp_async16(void* to, const void* from) {
+  cp_async16((uint32_t)__cvta_generic_to_shared(to), from);
+}
+__device__ __forceinline__ void cp_async8_or_zero(uint32_t to, const void* from, bool some) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;"
+               :: "r"(to), "l"(from), "r"(some ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All of a thread's groups but the last N have landed.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
+
 // 2D tiled store shared -> global of one box (bulk-group completion).
 __device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int32_t c0,
                                              int32_t c1) {

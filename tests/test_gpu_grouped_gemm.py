@@ -73,6 +73,11 @@ CASES = [
     ([700, 650, 130, 20], 4096, 264),
     ([0, 0], 64, 64),
     ([0] * 250 + [70, 1] + [0] * 7 + [30], 72, 128),
+    # short reductions
+    ([700, 0, 33, 5, 128], 1000, 48),
+    ([50, 2000, 1], 56, 328),
+    ([129, 16, 15], 64, 64),
+    ([0, 1], 24, 30000),
     # few tiles, a long reduction: several pairs share a tile
     ([17, 0, 30], 200, 4104),
     ([420], 4104, 120),
