@@ -736,7 +736,7 @@ MOE_API moe_status moe_permute_fp8(const moe_config* cfg, const void* codes, con
  * other rows are neither read into a result nor written. counts, offsets: int32
  * [groups] on the device; NULL both: one group of all rows. Segments lie inside
  * the rows (else the group counts as empty and MOE_ERR_DEVICE_CHECK is recorded)
- * and do not overlap. rows 0 .. 2^31 - 1, groups 1..260. Accumulation is in fp32,
+ * and do not overlap. rows 0 .. 2^31 - 1024, groups 1..260. Accumulation is in fp32,
  * results are rounded to bf16 once and do not depend on timing. Row tensors
  * have ld* elements from row to row (a multiple of 8). scratch:
  * moe_product_scratch_bytes bytes for any shape, zero-filled once by the caller

@@ -337,8 +337,8 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
   const int64_t total = (int64_t)weight * KC;
   const int least = max(kFewLeast, (int)sqrtf(0.5f * KC));
   int nb = max(1, (int)min(total / (least * C::W1), (int64_t)gridDim.x));
-  const bool whole = (int64_t)((weight + (int)gridDim.x * C::W2 - 1) / ((int)gridDim.x * C::W2)) *
-                         C::W2 * KC <= total / nb + kFewJoin * C::W1;
+  const int64_t round = (int64_t)gridDim.x * C::W2;
+  const bool whole = (weight + round - 1) / round * C::W2 * KC <= total / nb + kFewJoin * C::W1;
   if (whole) nb = gridDim.x;
   if (total == 0 || (int)blockIdx.x >= nb) return;
   auto first_of = [&](int b) {

@@ -56,10 +56,13 @@ constexpr int64_t kFewBytes = 2LL * kFewCtas * kFewPart * 4, kRaggedBytes = kRag
 constexpr int64_t kProductScratch = kPartsOffset + (kFewBytes > kRaggedBytes ? kFewBytes : kRaggedBytes);
 static_assert(kRaggedArrivedOffset + kRaggedPairs / 2 * 16 * 4 <= kPartsOffset, "counters before the parts");
 
+// (a tile past the last row is counted in 32 bits)
+constexpr int64_t kMaxRows = INT_MAX - 1023;
+
 moe_status check_segments(int64_t groups, int64_t rows, const int32_t* counts,
                           const int32_t* offsets) {
   OP_REQUIRE(groups >= 1 && rows >= 0 && rows <= INT_MAX);
-  if (groups > kMaxGroups) return MOE_ERR_UNSUPPORTED;
+  if (groups > kMaxGroups || rows > kMaxRows) return MOE_ERR_UNSUPPORTED;
   if (counts || offsets) OP_REQUIRE(al4(counts) && al4(offsets));
   else OP_REQUIRE(groups == 1);
   return MOE_OK;
@@ -224,7 +227,8 @@ moe_status moe_int4_grouped_gemm(const moe_int4_tensor* w, int64_t rows, const v
 
 moe_status moe_int4_dequantize(const moe_int4_tensor* w, void* out, void* stream) {
   OP_TRY(check_int4(w));
-  OP_REQUIRE(al16(out) && w->groups <= kMaxGroups);
+  if (w->groups > kMaxGroups) return MOE_ERR_UNSUPPORTED;
+  OP_REQUIRE(al16(out));
   OP_CUDA(launch_int4_dequantize(w->codes, w->scales, w->zeros, (int)w->groups, (int)w->N,
                                  (int)w->K, w->group, out, (cudaStream_t)stream));
   return MOE_OK;

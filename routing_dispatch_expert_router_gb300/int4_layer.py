@@ -26,7 +26,9 @@ from .fp4_layer import ROOT, _time_graph
 
 # Rows an expert expects up to which the products read the codes once for every 16 rows. Beyond it
 # the experts become bf16 first, which costs 4.5 bytes of traffic a weight, eight readings of codes.
-STREAM_ROWS = 64
+# (A step of eight experts 28672 x 4096, 2 of them a token, us, streamed and not: 128 tokens 473 and
+# 1104, 256: 816 and 1102, 384: 1154 and about 1150, 512: 1472 and 1195.)
+STREAM_ROWS = 96
 
 
 def quantize_int4(W: torch.Tensor, group: int = 128, zeros: bool = True) -> B.Int4Tensor:

@@ -177,3 +177,22 @@ def test_products_refuse_what_does_not_fit():
     with pytest.raises(B.MoEError) as e:
         B.moe_grouped_gemm(**many, stream=0)
     assert e.value.code == 2
+
+
+def test_product_entries_refuse_sizes():
+    L, ok = B.lib(), 1024
+
+    def gemm(groups=1, rows=4, N=32, K=64, hint=0):
+        return L.moe_grouped_gemm(groups, rows, N, K, ok, K, ok, ok, ok, 0, 0, ok, N, hint, ok, 0)
+
+    assert gemm(rows=0) == 0
+    for bad in (dict(rows=-1), dict(rows=2 ** 31), dict(groups=0), dict(N=0), dict(N=12), dict(K=4), dict(hint=-1)):
+        assert gemm(**bad) == 1, bad
+    for far in (dict(rows=2 ** 31 - 1), dict(rows=2 ** 31 - 1023), dict(groups=261)):
+        assert gemm(**far) == 2, far
+    assert gemm(rows=2 ** 31 - 1024, N=1 << 24, K=128) == 2            # more tiles than 32 bits hold
+    w = B.MoEInt4Tensor(32, 261, 32, 64, ok, ok, ok)
+    assert L.moe_int4_dequantize(w, ok, 0) == 2
+    assert L.moe_int4_grouped_gemm(w, 4, ok, 64, ok, ok, 0, ok, 32, ok, 0) == 2
+    w = B.MoEInt4Tensor(32, 1, 32, 64, ok, ok, ok)
+    assert L.moe_int4_grouped_gemm(w, 2 ** 31 - 1, ok, 64, ok, ok, 0, ok, 32, ok, 0) == 2
