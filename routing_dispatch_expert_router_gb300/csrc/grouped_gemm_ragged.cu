@@ -55,6 +55,15 @@ struct Maps {
   CUtensorMap a, a2, b2, b[8];
 };
 
+// Pairs that share a tile's reduction of nk steps, `most` at most. A step takes some 600 clocks, a
+// part about 12 a column to join, one after the other: sqrt(nk tile / 50) steps make the least of
+// both. Joining at all costs the time of some 16 steps.
+__host__ __device__ inline int shares(int most, int nk, int tile) {
+  if (nk < 24) return 1;
+  const int least = (int)sqrtf(nk * tile * 0.02f), n = nk / (least < 2 ? 2 : least);
+  return n < 1 ? 1 : n < most ? n : most;
+}
+
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
@@ -115,16 +124,15 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
   const int total = block_exclusive_scan(prefix, p.G, tmp);
   if (tid == 0) prefix[p.G] = total;
   __syncthreads();
-  // Few tiles: the reduction of each is cut among several pairs. (A step takes some 600 clocks, a
-  // part about 12 a column to join, one after the other: sqrt(nk tile / 50) steps make the least
-  // of both.) Every pair then has one unit, and so has its part of the scratch for itself.
+  // Few tiles: the reduction of each is cut among several pairs. Every pair then has one unit, and
+  // so has its part of the scratch for itself.
   int splits = 1;
   const int most = min(nclusters, kRaggedPairs);
   if (total > 0 && 2 * total <= most) {
     int nk = (p.red + BK - 1) / BK;
     if (MODE == kWgrad)
       for (int g = 0; g < p.G; ++g) nk = max(nk, (s_cnt[g] + BK - 1) / BK);
-    splits = max(1, min(most / total, nk / max(2, (int)sqrtf(nk * p.tile * 0.02f))));
+    splits = shares(most / total, nk, p.tile);
   }
   const int units = total * splits;
   if (cluster >= units) return;                            // both CTAs of the pair leave together
@@ -650,17 +658,22 @@ cudaError_t run_ragged(const Maps& m, const RaggedProduct& p, cudaStream_t s) {
   return launch_early(kern, (unsigned)grid, dim3(kPairThreads, 1, 1), kSmem, s, m, p);
 }
 
-// Columns of a tile: rounds of tiles over the pairs of SMs times what a tile takes, which is its
-// columns and about 64 more (the features' operand, filling and draining). `others`: tiles in the
-// other dimension; `groups`: each cuts `columns` once more (half a tile on average), or 0.
-int tile_columns(int64_t columns, int64_t others, int64_t groups, int least) {
-  const int pairs = num_sms() / 2;
+// Columns of a tile, from what it takes in clocks: steps of 450 + 1.75 a column, an epilogue of 1280
+// + 20 a column beside the next tile's steps; in rounds over the pairs of SMs, or shared among them.
+// `others`: tiles in the other dimension; `groups`: each cuts `columns` once more (half a tile on
+// average), or 0; nk: steps.
+int tile_columns(int64_t columns, int64_t others, int64_t groups, int nk, int least) {
+  const int pairs = num_sms() / 2 < kRaggedPairs ? num_sms() / 2 : kRaggedPairs;
   int best = 256;
   double cost = 0;
   for (int tile = 256; tile >= least; tile -= least) {
     const double tiles = others * (groups ? (double)columns / tile + 0.5 * groups
                                           : (double)((columns + tile - 1) / tile));
-    const double c = ceil(tiles / pairs) * (tile + 64);
+    const double step = 450 + 1.75 * tile, epilogue = 20 * (tile + 64);
+    const int n = shares((int)(pairs / (tiles < 1 ? 1 : tiles)), nk, tile);
+    const double c = 2 * tiles <= pairs && n > 1
+                         ? nk * step / n + 12.0 * tile * n + 10000 + epilogue
+                         : ceil(tiles / pairs) * fmax(nk * step, epilogue) + epilogue;
     if (tile == 256 || c < 0.95 * cost) {
       best = tile;
       cost = c;
@@ -682,7 +695,8 @@ cudaError_t launch_ragged_gemm(RaggedProduct p, int dgrad, const void* x, int64_
   p.feat = dgrad ? K : N;
   p.red = dgrad ? N : K;
   p.cols = 0;
-  p.tile = tile_columns(p.rows, (p.feat + kM - 1) / kM, p.rows < p.G ? p.rows : p.G, 64);
+  p.tile = tile_columns(p.rows, (p.feat + kM - 1) / kM, p.rows < p.G ? p.rows : p.G,
+                        (p.red + BK - 1) / BK, 64);
   Maps m;
   for (int i = 0; i < 8; ++i)
     if (!map2(&m.b[i], x, p.red, p.rows, ldx, 64, 16 * (i + 1))) return cudaErrorInvalidValue;
@@ -698,7 +712,7 @@ cudaError_t launch_ragged_wgrad(RaggedProduct p, const void* dy, int64_t lddy, c
   p.cols = K;
   p.red = 0;
   p.add = nullptr;
-  p.tile = tile_columns(K, (int64_t)p.G * ((N + kM - 1) / kM), 0, 128);
+  p.tile = tile_columns(K, (int64_t)p.G * ((N + kM - 1) / kM), 0, (int)(p.rows / p.G / BK) + 1, 128);
   // (without rows nothing is loaded: the maps are then of any valid extent)
   const bool some = p.rows > 0;
   const void *pa = some ? dy : p.out, *pb = some ? x : p.out;
