@@ -336,9 +336,10 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
   const int KC = p.steps;
   const int64_t total = (int64_t)weight * KC;
   const int least = max(kFewLeast, (int)sqrtf(0.5f * KC));
-  int nb = max(1, (int)min(total / (least * C::W1), (int64_t)gridDim.x));
-  const int64_t round = (int64_t)gridDim.x * C::W2;
-  const bool whole = (weight + round - 1) / round * C::W2 * KC <= total / nb + kFewJoin * C::W1;
+  int nb = (int)fminf(fmaxf((float)total / (least * C::W1), 1.f), (float)gridDim.x);
+  const unsigned round = gridDim.x * C::W2;
+  const int64_t most = (int64_t)((weight + round - 1) / round) * C::W2 * KC;
+  const bool whole = (most - kFewJoin * C::W1) * nb <= total;
   if (whole) nb = gridDim.x;
   if (total == 0 || (int)blockIdx.x >= nb) return;
   auto first_of = [&](int b) {
@@ -609,21 +610,21 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
       sync();
       mine = *s_last;
       if (mine) {
-        // (four parts' loads in flight at once: a round of them costs one way to L2)
+        // (two parts' loads in flight at once: they cost one way to L2; code for four costs small calls more)
         for (int e = 4 * ctid; e < all; e += 16 * CT) {
           float4 sum[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int b = lo; b <= hi; b += 4) {
-            float4 d[4][4];
+          for (int b = lo; b <= hi; b += 2) {
+            float4 d[2][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 if (b + j <= hi && e + 4 * i * CT < all)
                   d[j][i] = __ldcg(reinterpret_cast<const float4*>(part(b + j) + e + 4 * i * CT));
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 if (b + j > hi || e + 4 * i * CT >= all) continue;
