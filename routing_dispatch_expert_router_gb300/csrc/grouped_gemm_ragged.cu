@@ -25,6 +25,10 @@
 //   - the weight gradient reduces over the rows: a warp of each CTA zeroes the next group's rows
 //     of the last block in both operands (zero times a NaN is one) before it hands the stage to
 //     the pair's MMAs.
+//
+// 32768 rows of 64 experts, 4096 x 2040 (0.55 PFLOP): data gradient 420 us, 1.31 PFLOP/s; weight
+// gradient 525, whose operands pass from L2 to the SMs at 10.6 TB/s (without MMAs and stores 424
+// are left, without stores 452). 8192^3 in one group: 1.65 to 1.70 PFLOP/s in each of the three.
 #include <math.h>
 
 #include "gemm_common.cuh"

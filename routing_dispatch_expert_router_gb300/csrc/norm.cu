@@ -8,6 +8,11 @@
 // HBM bounds both: a row is read once, stays in registers between the sum and its use, and is
 // written once. A row belongs to a CTA (to a warp up to 1024 columns, eight rows to a CTA, so
 // that short rows need no barrier); a thread holds 8 x V columns. Sums are fp32.
+//
+// 8192 rows of 7168 with residual, sum, bf16 output and MXFP8 codes: 80 us, 6.6 TB/s (a row a CTA with
+// loads that wait for nothing but themselves: 101, with instructions in 73 % of the issue slots and
+// HBM 63 % busy; the ring and packed arithmetic brought it here). 8192 rows of 4096 backward with
+// dsum and dgamma: 45 us, 5.9 TB/s (67 before). One row of 7168: 4.3 us, a launch.
 #include "common.cuh"
 #include "fp8_layout.cuh"
 #include "internal.h"
