@@ -106,6 +106,16 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
     ptx::tma_prefetch_desc(&maps.a);
     ptx::tma_prefetch_desc(&maps.b[MODE == kWgrad ? 0 : 7]);
   }
+  // what needs no memory comes before the wait for the kernel in front
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
   // features: M tiles; columns: what N runs over (rows of the group, or the gradient's columns)
@@ -139,17 +149,11 @@ ragged_pair_kernel(const __grid_constant__ Maps maps, const RaggedProduct p) {
     splits = shares(most / total, nk, p.tile);
   }
   const int units = total * splits;
-  if (cluster >= units) return;                            // both CTAs of the pair leave together
-
-  if (warp == 1) {
-    ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), 512);
-    ptx::tmem_relinquish_pair();
+  if (cluster >= units) {                                  // both CTAs of the pair leave together
+    ptx::cluster_sync();
+    if (warp == 1) ptx::tmem_dealloc_pair(tmem_base, 512);
+    return;
   }
-  ptx::tc_fence_before();
-  __syncthreads();
-  ptx::cluster_sync();
-  ptx::tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
 
   struct Tile {
     int g, f0, n0, n, k0, nk;       // features from f0, columns (rows of the group) n0 .. n0 + n - 1,

@@ -54,6 +54,8 @@ __global__ void __launch_bounds__(256)
 permute_hist_kernel(const int32_t* __restrict__ idx, int32_t* __restrict__ hist, int T, int k,
                     int E, int32_t* status) {
   __shared__ int cnt[kMaxExperts];
+  ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
   cnt[threadIdx.x] = 0;
   __syncthreads();
   const int t = blockIdx.x * kChunkTokens + threadIdx.x;
@@ -85,15 +87,17 @@ permute_rank_kernel(const int32_t* __restrict__ idx, const int32_t* __restrict__
   __shared__ int soff[kMaxExperts + 1];
   __shared__ __align__(16) uint32_t bm[kMaxExperts][W];        // tokens of the chunk, per expert
   __shared__ __align__(8) uint8_t pre[kMaxExperts][W];         // how many in the words before
-  __shared__ int tmp[33];
-  const int c = blockIdx.x, G = E + S, tid = threadIdx.x, nt = blockDim.x;
+  // (with a single chunk the CTAs behind the first share its padding rows alone)
+  const int c = n_chunk > 1 ? blockIdx.x : 0, G = E + S, tid = threadIdx.x, nt = blockDim.x;
   const int t = c * kChunkTokens + tid;
 
   for (int i = tid; i < E * W; i += nt) (&bm[0][0])[i] = 0u;
+  if (n_chunk <= 1) ptx::grid_dependency_wait();
   int e[kMaxK];
   const bool bad = t < T && token_experts(idx, t, k, E, e);
-  ptx::grid_dependency_wait();                   // (idx is older than the histogram's launch)
-  if (bad && n_chunk == 1) record_status(status, MOE_ERR_DEVICE_CHECK);
+  if (n_chunk > 1) ptx::grid_dependency_wait();  // (idx is older than the histogram's launch)
+  ptx::grid_launch_dependents();
+  if (bad && n_chunk == 1 && blockIdx.x == 0) record_status(status, MOE_ERR_DEVICE_CHECK);
   if (tid < E && n_chunk > 1) {
     int a = 0, b = 0;
 #pragma unroll 8
@@ -142,16 +146,28 @@ permute_rank_kernel(const int32_t* __restrict__ idx, const int32_t* __restrict__
     pad[g] = min(sl, (kp + 127) / 128 * 128) - kp;
   }
   __syncthreads();
-  const int R = block_exclusive_scan(seg, G, tmp);
-  const int P = block_exclusive_scan(pad, G, tmp);
-  const int A = block_exclusive_scan(soff, E, tmp);
-  if (tid == 0) {
-    seg[G] = R;
-    pad[G] = P;
-    soff[E] = A;
+  // exclusive sums of the three side by side, by a warp each, a lane neighbouring groups
+  if (tid < 96) {
+    int* a = tid < 32 ? seg : tid < 64 ? pad : soff;
+    const int n = tid < 64 ? G : E, lane = tid & 31, per = (n + 31) / 32, from = lane * per;
+    int own = 0;
+    for (int i = from; i < min(from + per, n); ++i) own += a[i];
+    int run = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += y;
+    }
+    if (lane == 31) a[n] = run;
+    run -= own;
+    for (int i = from; i < min(from + per, n); ++i) {
+      const int v = a[i];
+      a[i] = run;
+      run += v;
+    }
   }
   __syncthreads();
-  if (c == 0) {
+  if (blockIdx.x == 0) {
     for (int g = tid; g < G; g += nt) counts[g] = kept[g];
     for (int g = tid; g <= G; g += nt) {
       offsets[g] = seg[g];
@@ -159,7 +175,7 @@ permute_rank_kernel(const int32_t* __restrict__ idx, const int32_t* __restrict__
     }
     for (int q = tid; q <= E; q += nt) sel_offsets[q] = soff[q];
   }
-  if (t < T) {
+  if (t < T && (n_chunk > 1 || blockIdx.x == 0)) {
 #pragma unroll
     for (int j = 0; j < kMaxK; ++j) {
       if (j >= k) break;
@@ -177,8 +193,8 @@ permute_rank_kernel(const int32_t* __restrict__ idx, const int32_t* __restrict__
     }
     for (int s = 0; s < S; ++s) token_of[seg[E + s] + t] = t;
   }
-  // padding rows of groups g = c, c + gridDim.x, ..., a warp each (gridDim.x >= 1 even when T == 0)
-  for (int g = c + (tid >> 5) * gridDim.x; g < G; g += gridDim.x * (nt >> 5))
+  // padding rows of groups g = blockIdx.x, + gridDim.x, .., a warp each (gridDim.x >= 1 even when T == 0)
+  for (int g = blockIdx.x + (tid >> 5) * gridDim.x; g < G; g += gridDim.x * (nt >> 5))
     for (int r = seg[g] + kept[g] + (tid & 31); r < seg[g + 1]; r += 32) token_of[r] = -1;
 }
 
@@ -426,17 +442,15 @@ static cudaError_t launch_permute_maps(const moe_config& c, const int32_t* idx, 
   int32_t* hist = reinterpret_cast<int32_t*>(scratch + kScratchHist);
   const int nc = n_chunks(c);
   if (nc > 1) {
-    permute_hist_kernel<<<nc, 256, 0, s>>>(idx, hist, c.T, c.k, c.E, status);
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = launch_early(permute_hist_kernel, (unsigned)nc, dim3(256, 1, 1), 0, s,
+                                         idx, hist, c.T, c.k, c.E, status);
     if (err != cudaSuccess) return err;
-    return launch_early(permute_rank_kernel, (unsigned)nc, dim3(256, 1, 1), 0, s, idx, hist, nc, c.T,
-                        c.k, c.E, c.n_shared, c.row_align, (int)capacity_rows(c), counts, offsets,
-                        row_of, token_of, sel_offsets, sel_tokens, pad_prefix, status);
   }
-  permute_rank_kernel<<<1, 256, 0, s>>>(idx, hist, nc, c.T, c.k, c.E, c.n_shared, c.row_align,
-                                        (int)capacity_rows(c), counts, offsets, row_of, token_of,
-                                        sel_offsets, sel_tokens, pad_prefix, status);
-  return cudaGetLastError();
+  // (a single chunk: a warp a group for the padding rows)
+  const unsigned ctas = nc > 1 ? nc : (c.E + c.n_shared + 7) / 8;
+  return launch_early(permute_rank_kernel, ctas, dim3(256, 1, 1), 0, s, idx, hist, nc, c.T, c.k, c.E,
+                      c.n_shared, c.row_align, (int)capacity_rows(c), counts, offsets, row_of,
+                      token_of, sel_offsets, sel_tokens, pad_prefix, status);
 }
 
 cudaError_t launch_permute(const moe_config& c, const void* x, const int32_t* idx,
