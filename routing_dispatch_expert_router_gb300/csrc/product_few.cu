@@ -214,25 +214,27 @@ __device__ __forceinline__ void step_int4(float (&tot)[2][2][4], const uint8_t* 
     }
     // the group's scales, zero points and sums of x
     const int q = c0 / GC;
-    float2 sx[NTL];
+    uint64_t sx[NTL];
 #pragma unroll
-    for (int n = 0; n < NTL; ++n) sx[n] = at<float2>(st, a.sum, (q * kTok + n * 8) * 4);
+    for (int n = 0; n < NTL; ++n) sx[n] = at<uint64_t>(st, a.sum, (q * kTok + n * 8) * 4);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float s = __uint_as_float(
             (uint32_t)at<uint16_t>(st, a.s, (q * GS + 16 * m + 8 * h) * 2) << 16);
-        // (128 + z as the codes' bf16 numbers are made: a conversion takes eight times as long)
+        // -(128 + z) as the codes' bf16 numbers are made: a conversion takes eight times as long
         const float z =
             has_zeros ? __uint_as_float(
-                            ((uint32_t)at<uint8_t>(st, a.z, q * GS + 16 * m + 8 * h) & 127u | 0x4300u) << 16)
-                      : 136.f;
+                            ((uint32_t)at<uint8_t>(st, a.z, q * GS + 16 * m + 8 * h) & 127u | 0xc300u) << 16)
+                      : -136.f;
+        const uint64_t s2 = ptx::f2_pack(s, s), z2 = ptx::f2_pack(z, z);
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
-          tot[m][n][2 * h] = fmaf(s, fmaf(-z, sx[n].x, acc[m][n][2 * h]), tot[m][n][2 * h]);
-          tot[m][n][2 * h + 1] =
-              fmaf(s, fmaf(-z, sx[n].y, acc[m][n][2 * h + 1]), tot[m][n][2 * h + 1]);
+          const uint64_t d = ptx::f2_pack(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
+          float(&t)[4] = tot[m][n];
+          ptx::f2_unpack(ptx::f2_fma(s2, ptx::f2_fma(z2, sx[n], d), ptx::f2_pack(t[2 * h], t[2 * h + 1])),
+                         t[2 * h], t[2 * h + 1]);
         }
       }
   }
