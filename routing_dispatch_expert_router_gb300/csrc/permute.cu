@@ -15,8 +15,8 @@
 //           of every assignment = (assignments of its expert in earlier
 //           chunks) + (earlier tokens of this chunk that chose the same
 //           expert, read from a per-expert bitmap of the chunk's tokens);
-//           8192 tokens to 8 of 256 experts: 12 us, 61 to 8 of 128: 9.5, whose idx loads, three
-//           scans and stores wait for one another;
+//           8192 tokens to 8 of 256 experts: 10.4 us, 61 to 8 of 128: 5.4 (three scans by the
+//           whole CTA, one after the other, and one CTA for the padding rows: 9.5);
 //   alloc   (paged stash) one block: the layer's stash pages and page table;
 //   scatter one warp per token: reads the row once, writes it to each of its
 //           rows with 16-byte stores; padding rows are zero-filled.
@@ -386,7 +386,7 @@ permute_scatter_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __res
 // lane; its scale bytes go into the atoms four at a time (fp8_layout.cuh: both layouts keep four
 // consecutive blocks of a row in one word). Rows without a token are not written: a product's rows
 // depend on their own row alone, and only the combine's rows are read behind it. HBM bounds it:
-// 8192 tokens of 7168 to 8 of 256 experts 65 us (of 81 with the maps).
+// 8192 tokens of 7168 to 8 of 256 experts 65 us (of 78 with the maps).
 __global__ void __launch_bounds__(256)
 permute_scatter8_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                         const int32_t* __restrict__ row_of, int T, int H, int k, int block,

@@ -26,11 +26,11 @@
 // writes its fp32 part, the one that arrives last adds the parts in K's order. So results do
 // not depend on timing.
 //
-// Two rows of two of eight experts through 28672 x 4096 in 4 bits (121 MB): 31 us, 3.9 TB/s; loads
-// alone take 27.6, the launch, the shares and the last joins the rest. 512 rows of 64 experts through
-// 4096 x 2048 (287 MB): 76 us, 3.8 TB/s: a step whose unit has two tiles of tokens takes 2100 clocks,
-// in which HBM would bring three halves of it. bf16, 8 rows of 5 experts through 4096 x 14336
-// (587 MB): 86 us, 6.8 TB/s.
+// A row of each of two experts through 28672 x 4096 in 4 bits (121 MB): 31 us, 3.9 TB/s; loads alone
+// take 27.6, the launch, the shares and the last joins the rest. 512 rows of 64 experts through
+// 4096 x 2048 (287 MB): 75 us, 3.8 TB/s: a step whose unit has two tiles of tokens takes some 2050
+// clocks, in which HBM would bring three halves of it. bf16, 8 rows of five experts through
+// 4096 x 14336 (587 MB): 86 us, 6.8 TB/s.
 #include "gemm_common.cuh"
 
 namespace moe {
