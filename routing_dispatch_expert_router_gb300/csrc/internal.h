@@ -366,6 +366,11 @@ bool few_rows(int64_t most);
 cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const void* w,
                                const void* scales, const void* zeros, bool swiglu, cudaStream_t s);
 
+// The same kernel for few outputs: the rows stream, the weights are what few there is of.
+bool narrow_fits(int64_t rows, int G, int64_t outputs, int64_t reduction);
+cudaError_t launch_product_narrow(FewProduct p, int dgrad, const void* x, int64_t ldx, const void* w,
+                                  int N, int K, cudaStream_t s);
+
 // The bf16 weights that 4-bit codes stand for: out [G, N, K].
 cudaError_t launch_int4_dequantize(const void* codes, const void* scales, const void* zeros, int G,
                                    int N, int K, int group, void* out, cudaStream_t s);

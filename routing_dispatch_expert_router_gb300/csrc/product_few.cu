@@ -26,6 +26,10 @@
 // writes its fp32 part, the one that arrives last adds the parts in K's order. So results do
 // not depend on timing.
 //
+// With many rows and few outputs (an adapter's products into its rank) the roles change: 256 rows are
+// the operand that streams, the expert's weights the one of 16, turned by ldmatrix where the
+// reduction runs over their rows. 8192 rows of 4096 to 16: 21.9 us.
+//
 // A row of each of two experts through 28672 x 4096 in 4 bits (121 MB): 31 us, 3.9 TB/s; loads alone
 // take 27.6, the launch, the shares and the last joins the rest. 512 rows of 64 experts through
 // 4096 x 2048 (287 MB): 75 us, 3.8 TB/s: a step whose unit has two tiles of tokens takes some 2050
@@ -45,7 +49,13 @@ constexpr int kConsumers = kSlab / 32;
 constexpr int kJoiners = 4;                    // warps that write results
 constexpr int kTileLd = kTok + 1;
 constexpr int kTileBytes = kSlab * kTileLd * 4;
-constexpr int kCtrl = 4096;
+
+// What streams as the 256-row operand, and what is the other one, of 16 rows a pass.
+enum Roles : int {
+  kWeightsStream = 0,      // an expert's weights; its rows
+  kRowsStream = 1,         // an expert's rows; its weights, of few outputs
+  kRowsStreamT = 2,        // the same where the reduction runs over the weights' rows
+};
 
 template <bool W4>
 struct Cfg {
@@ -61,7 +71,8 @@ struct Cfg {
   static constexpr int Z_OFF = S_OFF + (W4 ? 8 * kSlab * 2 : 0);   // eight groups at most
   static constexpr int SUM_OFF = Z_OFF + (W4 ? 8 * kSlab : 0);
   static constexpr int STAGE = (SUM_OFF + (W4 ? 8 * kTok * 4 : 0) + 1023) / 1024 * 1024;
-  static constexpr int SMEM = STAGES * STAGE + 2 * kTileBytes + kCtrl + 1024;
+  static constexpr int CTRL = W4 ? 4096 : 5376;
+  static constexpr int SMEM = STAGES * STAGE + 2 * kTileBytes + CTRL + 1024;
 };
 static_assert(Cfg<true>::SMEM <= 232448 && Cfg<false>::SMEM <= 232448, "shared memory");
 
@@ -240,8 +251,13 @@ __device__ __forceinline__ void step_int4(float (&tot)[2][2][4], const uint8_t* 
   }
 }
 
-template <int NTL>
+// TR: the tokens' operand lies [64 of K][8 NTL columns], and is turned on its way to registers (row
+// i of matrix j of a 32: element 8 (i / 2) + i % 2 + 2 j, as the lanes have the other operand's).
+template <int NTL, bool TR>
 __device__ __forceinline__ void step_bf16(float (&tot)[2][2][4], const uint8_t* st, const Places& a) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t turned = ptx::smem_u32(st) + Cfg<false>::X_OFF +
+                          (8 * ((lane & 7) >> 1) + (lane & 1) + 2 * (lane >> 3)) * (16 * NTL);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     uint4 w[2][2], x[NTL];
@@ -250,7 +266,14 @@ __device__ __forceinline__ void step_bf16(float (&tot)[2][2][4], const uint8_t* 
 #pragma unroll
       for (int h = 0; h < 2; ++h) w[m][h] = at<uint4>(st, a.w[c], m * 2048 + h * 1024);
 #pragma unroll
-    for (int n = 0; n < NTL; ++n) x[n] = at<uint4>(st, a.x[0][c], n * 1024);
+    for (int n = 0; n < NTL; ++n) {
+      if (TR)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(x[n].x), "=r"(x[n].y), "=r"(x[n].z), "=r"(x[n].w)
+                     : "r"(turned + c * 32 * 16 * NTL + n * 16) : "memory");
+      else
+        x[n] = at<uint4>(st, a.x[0][c], n * 1024);
+    }
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -275,7 +298,7 @@ struct Maps {
 };
 
 // GC: chunks of 32 elements of K in a scale's group (4-bit).
-template <bool W4, bool SWIGLU, int GC>
+template <bool W4, bool SWIGLU, int GC, int ROLES>
 __global__ void __launch_bounds__(Cfg<W4>::THREADS, 1)
 product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
   using C = Cfg<W4>;
@@ -295,9 +318,9 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
   int* s_off = reinterpret_cast<int*>(ctrl + 1536);        // [kMaxGroups]
   int* s_cnt = reinterpret_cast<int*>(ctrl + 2688);        // [kMaxGroups]
   int* tmp = reinterpret_cast<int*>(ctrl + 3840);          // [33]
+  int* s_rows = reinterpret_cast<int*>(ctrl + 4096);       // [kMaxGroups] (rows that stream)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slabs = p.slabs;
   // what the steps of a slab of columns weigh: two token tiles of eight cost more than one
   auto slab_weight = [](int c) {
     const int rest = c % kTok;
@@ -331,14 +354,23 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
         c = 0;
       }
     }
-    s_cnt[g] = c;
     s_off[g] = o;
+    int slabs = p.slabs;
+    if (ROLES != kWeightsStream) {
+      s_rows[g] = c;
+      slabs = (c + kSlab - 1) / kSlab;
+      c = c > 0 ? p.N : 0;
+    }
+    s_cnt[g] = c;
     prefix[g] = slab_weight(c) * slabs;
   }
   __syncthreads();
   const int weight = block_exclusive_scan(prefix, p.G, tmp);
   if (tid == 0) prefix[p.G] = weight;
   __syncthreads();
+  auto slabs_of = [&](int g) {
+    return ROLES != kWeightsStream ? (s_rows[g] + kSlab - 1) / kSlab : p.slabs;
+  };
   // An even share of the steps, weighed by what they take, for each CTA: not under kFewLeast steps
   // where there are few, nor under what makes a unit's steps in one CTA and the parts that the last
   // one joins the least together (a part costs half a step), and no unit shared where whole ones leave the fullest CTA kFewJoin steps
@@ -380,7 +412,7 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
     v.step = 0;
     if ((++v.tile) * kTok < s_cnt[v.g]) return;
     v.tile = 0;
-    if (++v.slab < slabs) return;
+    if (++v.slab < slabs_of(v.g)) return;
     v.slab = 0;
     do ++v.g;
     while (v.g < p.G && s_cnt[v.g] == 0);
@@ -410,8 +442,8 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
         const int n = steps_at(v), k0 = v.step;
         if (n <= 0) break;
         const int ntl = min(2, (s_cnt[v.g] - v.tile * kTok + 7) >> 3);
-        const int row = s_off[v.g] + v.tile * kTok;
-        const int n0 = v.slab * (SWIGLU ? 128 : 256);
+        const int row = (ROLES != kWeightsStream ? v.g * p.N : s_off[v.g]) + v.tile * kTok;
+        const int n0 = v.slab * (SWIGLU ? 128 : 256) + (ROLES != kWeightsStream ? s_off[v.g] : 0);
         const CUtensorMap* x = &maps.x[ntl - 1];
         const uint32_t bytes = kSlab * 128 + ntl * C::XBOXES * 1024 +
                                (W4 ? p.groups_per_step * (p.has_zeros ? 768 : 512) : 0);
@@ -424,8 +456,11 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
           ptx::mbar_arrive_expect_tx(fb, bytes);
           const int kw = k * (W4 ? 128 : 64);            // in elements of the weights' map
           if (SWIGLU) ptx::tma_load_4d(st, &maps.w, fb, kw, n0, 0, v.g);
+          else if (ROLES != kWeightsStream) ptx::tma_load_2d(st, &maps.w, fb, kw, n0);
           else ptx::tma_load_3d(st, &maps.w, fb, kw, n0, v.g);
-          if (W4 && p.x_whole) {
+          if (ROLES == kRowsStreamT) {
+            ptx::tma_load_3d(st + C::X_OFF, x, fb, v.tile * kTok, k * C::STEP, v.g);
+          } else if (W4 && p.x_whole) {
             ptx::tma_load_3d(st + C::X_OFF, x, fb, 0, row, k * C::XBOXES);
           } else {
             for (int b = 0; b < C::XBOXES; ++b)
@@ -547,8 +582,8 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
           if (two) step_int4<2, SWIGLU, GC>(tot, st, here, p.has_zeros);
           else step_int4<1, SWIGLU, GC>(tot, st, here, p.has_zeros);
         } else {
-          if (two) step_bf16<2>(tot, st, here);
-          else step_bf16<1>(tot, st, here);
+          if (two) step_bf16<2, ROLES == kRowsStreamT>(tot, st, here);
+          else step_bf16<1, ROLES == kRowsStreamT>(tot, st, here);
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar_empty + 8 * stage);
@@ -659,7 +694,21 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
       }
       sync();
     }
-    if (mine) {
+    if (mine && ROLES != kWeightsStream) {
+      // two neighbouring outputs of a row a thread
+      const int pairs = ntok >> 1, rows = min(kSlab, s_rows[v.g] - v.slab * kSlab);
+      const int64_t row0 = (int64_t)s_off[v.g] + v.slab * kSlab;
+      for (int e = ctid; e < rows * pairs; e += CT) {
+        const int r = e / pairs, tok = (e - r * pairs) * 2, col = v.tile * kTok + tok;
+        float a = tile[r * kTileLd + tok], b = tile[r * kTileLd + tok + 1];
+        if (p.add) {
+          const uint32_t d = *reinterpret_cast<const uint32_t*>(p.add + (row0 + r) * p.ldadd + col);
+          a += bf16_lo(d);
+          b += bf16_hi(d);
+        }
+        *reinterpret_cast<uint32_t*>(p.out + (row0 + r) * p.ldo + col) = pack_bf16x2(a, b);
+      }
+    } else if (mine) {
       // two neighbouring columns a thread
       constexpr int COLS = SWIGLU ? kSlab / 2 : kSlab;
       const int n0 = v.slab * COLS, N = SWIGLU ? p.F : p.N;
@@ -741,9 +790,9 @@ bool make_group_map(CUtensorMap* m, CUtensorMapDataType type, uint64_t bytes, co
   return make_tensor_map(m, type, ptr, 4, dims, strides, box, swizzle);
 }
 
-template <bool W4, bool SWIGLU, int GC>
+template <bool W4, bool SWIGLU, int GC, int ROLES = kWeightsStream>
 cudaError_t run_few(const Maps& m, const FewProduct& p, cudaStream_t stream) {
-  auto kern = product_few_kernel<W4, SWIGLU, GC>;
+  auto kern = product_few_kernel<W4, SWIGLU, GC, ROLES>;
   static PerDevice set;
   const cudaError_t e = set_smem_once(set, kern, Cfg<W4>::SMEM);
   if (e != cudaSuccess) return e;
@@ -783,6 +832,38 @@ bool few_fits(int64_t rows, int G, int64_t N, int64_t K) {
 // 512 x 512: 10.4 and 14.4; 24 for each of 8, 1024 x 1024: 16.6 and 14.4; 48 for each of 4,
 // 1128 x 7776: 32.9 and 25.0; 60 for each of two, 4096 x 4096: 35.0 and 22.6.)
 bool few_rows(int64_t most) { return most <= kTok; }
+
+// Whether a product's rows stream: few outputs, six steps a CTA at least (fewer make many parts of
+// 256 rows to join), and units in 32 bits. (us, this way and by tensor tiles, 16 outputs: 8192 rows
+// of 4096 21.9 and 28.8, 4096 of them 20.6 and 22.7, 2048 25 and 20.6, 512 20.5 and 16.6.)
+bool narrow_fits(int64_t rows, int G, int64_t outputs, int64_t reduction) {
+  return outputs <= kTok && rows / kSlab + G < (1LL << 28) &&
+         rows / kSlab * ((reduction + 63) / 64) >= 6 * num_sms();
+}
+
+cudaError_t launch_product_narrow(FewProduct p, int dgrad, const void* x, int64_t ldx, const void* w,
+                                  int N, int K, cudaStream_t s) {
+  // p.N: outputs, p.K: the reduction
+  p.N = dgrad ? K : N;
+  p.K = dgrad ? N : K;
+  p.steps = (p.K + 63) / 64;
+  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint64_t row[1] = {(cuuint64_t)ldx * 2}, wide[2] = {(cuuint64_t)p.K, (cuuint64_t)p.rows};
+  const cuuint32_t slab[2] = {64, kSlab};
+  Maps m;
+  if (!make_tensor_map(&m.w, bf16, x, 2, wide, row, slab, true)) return cudaErrorInvalidValue;
+  m.s = m.z = m.w;
+  for (int i = 0; i < 2; ++i) {
+    const cuuint32_t n = 8 * (i + 1), box[2] = {64, n}, turned[3] = {n, 64, 1};
+    const cuuint64_t flat[2] = {(cuuint64_t)K, (cuuint64_t)p.G * N}, ld[1] = {(cuuint64_t)K * 2};
+    const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)p.G};
+    const cuuint64_t strides[2] = {(cuuint64_t)K * 2, (cuuint64_t)K * N * 2};
+    if (!(dgrad ? make_tensor_map(&m.x[i], bf16, w, 3, dims, strides, turned, false)
+                : make_tensor_map(&m.x[i], bf16, w, 2, flat, ld, box, true)))
+      return cudaErrorInvalidValue;
+  }
+  return dgrad ? run_few<false, false, 1, kRowsStreamT>(m, p, s) : run_few<false, false, 1, kRowsStream>(m, p, s);
+}
 
 cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const void* w,
                                const void* scales, const void* zeros, bool swiglu,

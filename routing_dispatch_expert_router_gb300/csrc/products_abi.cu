@@ -248,11 +248,15 @@ moe_status moe_grouped_gemm(int64_t groups, int64_t rows, int64_t N, int64_t K, 
     OP_CUDA(launch_product_short(rp, 0, x, ldx, w, (int)N, (int)K, (cudaStream_t)stream));
     return MOE_OK;
   }
+  FewProduct p = few_product(groups, rows, N, K, counts, offsets, out, ldo, scratch);
+  p.add = bf(add);
+  p.ldadd = ldadd;
   if (few_rows(most) && few_fits(rows, (int)groups, N, K)) {
-    FewProduct p = few_product(groups, rows, N, K, counts, offsets, out, ldo, scratch);
-    p.add = bf(add);
-    p.ldadd = ldadd;
     OP_CUDA(launch_product_few(p, x, ldx, w, nullptr, nullptr, false, (cudaStream_t)stream));
+    return MOE_OK;
+  }
+  if (narrow_fits(rows, (int)groups, N, K)) {
+    OP_CUDA(launch_product_narrow(p, 0, x, ldx, w, (int)N, (int)K, (cudaStream_t)stream));
     return MOE_OK;
   }
   if (!ragged_fits(rows, (int)groups, N, 0)) return MOE_ERR_UNSUPPORTED;
@@ -272,6 +276,13 @@ moe_status moe_grouped_gemm_dgrad(int64_t groups, int64_t rows, int64_t N, int64
       ragged_product(groups, rows, counts, offsets, add, ldadd, dx, lddx, scratch);
   if (short_fits(rows, (int)groups, K, N, add != nullptr)) {
     OP_CUDA(launch_product_short(rp, 1, dy, lddy, w, (int)N, (int)K, (cudaStream_t)stream));
+    return MOE_OK;
+  }
+  if (narrow_fits(rows, (int)groups, K, N)) {
+    FewProduct p = few_product(groups, rows, N, K, counts, offsets, dx, lddx, scratch);
+    p.add = bf(add);
+    p.ldadd = ldadd;
+    OP_CUDA(launch_product_narrow(p, 1, dy, lddy, w, (int)N, (int)K, (cudaStream_t)stream));
     return MOE_OK;
   }
   if (!ragged_fits(rows, (int)groups, K, 0)) return MOE_ERR_UNSUPPORTED;

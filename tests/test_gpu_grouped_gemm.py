@@ -78,6 +78,11 @@ CASES = [
     ([50, 2000, 1], 56, 328),
     ([129, 16, 15], 64, 64),
     ([0, 1], 24, 30000),
+    # few outputs of many rows, forward and data gradient
+    ([3000, 0, 3, 1160], 8, 4104),
+    ([17, 2257, 256, 1, 2900], 4104, 8),
+    ([14600], 1032, 16),
+    ([0, 9000, 90, 6000], 16, 1096),
     # few tiles, a long reduction: several pairs share a tile
     ([17, 0, 30], 200, 4104),
     ([420], 4104, 120),
