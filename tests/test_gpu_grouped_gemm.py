@@ -263,6 +263,24 @@ def test_rows_behind_2_to_the_31_elements():
     check_wgrad(dw, out, x, counts, off)
 
 
+@pytest.mark.parametrize("R,N,K", [(600_000, 16, 4096), (600_000, 4096, 16), (140_000_000, 24, 16)])
+def test_narrow_products_of_rows_behind_2_to_the_31_elements(R, N, K):
+    w, counts, off = randn(2, N, K, seed=19, scale=0.1), [135, 5], [R - 140, R - 5]
+    c, o, sc = dev(counts), dev(off), B.alloc_product_scratch()
+    for dgrad in (False, True):
+        ka, kc = (N, K) if dgrad else (K, N)
+        a = torch.zeros(R, ka, dtype=BF, device="cuda")
+        a[-140:] = randn(140, ka, seed=18)
+        out = torch.zeros(R, kc, dtype=BF, device="cuda")
+        if dgrad:
+            B.moe_grouped_gemm_dgrad(a, w, c, o, out, sc, add=out)
+        else:
+            B.moe_grouped_gemm(a, w, c, o, out, sc, add=out)
+        check_rows(out, a, w, counts, off, dgrad=dgrad)
+        assert bool((out[:-140] == 0).all()) and B.moe_last_device_status(sc) == 0
+        del a, out
+
+
 def test_captured_and_replayed_with_other_counts():
     R, N, K = 400, 256, 320
     x, w, dy = randn(R, K, seed=20), randn(3, N, K, seed=21), randn(R, N, seed=22)

@@ -192,3 +192,34 @@ def test_quantised_weights():
             # a scale off by 2^-8 of itself moves the outermost of 15 codes (8 of them from zero)
             # by that much more, and the zero point by half a step of the lower end
             assert (np.abs(values(q) - f64(W)) <= step * (0.5 + 15 * 2.0 ** -8 + (0.5 if zeros else 0)) + 1e-6).all()
+
+
+def test_two_layers_at_once():
+    """A serving and a training layer on streams of their own, with buffers of their own, give the bits
+    that they give alone."""
+    serve, inp, more = prepared(SHAPES[0], training=False)
+    train, inp2, more2 = prepared(SHAPES[3], training=True)
+
+    def step():
+        train.forward(inp2["x"], more2)
+        return train.backward(inp2["x"], inp2["dY"], residual=more2)
+
+    out = serve.forward(inp["x"], more).clone()
+    kept = [t.clone() for t in (step(), train.out, train.dA, train.dB, train.dgamma, train.dW_r)]
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        for t in (serve.out, train.out, train.dA, train.dB, train.dgamma, train.dx):
+            t.zero_()
+        torch.cuda.synchronize()
+        for _ in range(4):
+            with torch.cuda.stream(a):
+                serve.forward(inp["x"], more)
+            with torch.cuda.stream(b):
+                step()
+        torch.cuda.synchronize()
+        assert torch.equal(serve.out, out)
+        for t, v in zip((train.dx, train.out, train.dA, train.dB, train.dgamma, train.dW_r), kept):
+            assert torch.equal(t, v)
+    serve.check()
+    train.check()
