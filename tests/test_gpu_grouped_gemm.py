@@ -205,6 +205,32 @@ def test_other_rows_values_stay_out(N, K):
     check_rows(few, x, w, [70, 0, 65], off)
 
 
+@pytest.mark.parametrize("N,K,times", [(1000, 24, 1), (40, 1000, 1), (16, 4104, 17), (4104, 8, 17)])
+def test_other_values_stay_out_of_short_and_narrow_products(N, K, times):
+    """The same where the reduction is short or the outputs few, and NaN behind every row's end."""
+    counts = [70 * times, 130 * times, 65 * times]
+    off, R = [1, 1 + counts[0], 2 + counts[0] + counts[1]], 5 + sum(counts)
+    c, o, sc = dev(counts), dev(off), B.alloc_product_scratch()
+    w = randn(3, N, K, seed=11)
+    for dgrad in (False, True):
+        ka, kc = (N, K) if dgrad else (K, N)
+        wide, more = randn(R, ka + 8, seed=9), randn(R, kc, seed=12)
+        want, got = torch.zeros(R, kc, dtype=BF, device="cuda"), torch.zeros(R, kc, dtype=BF, device="cuda")
+        call = B.moe_grouped_gemm_dgrad if dgrad else B.moe_grouped_gemm
+        call(wide[:, :ka], w, c, o, want, sc, add=more)
+        check_rows(want, wide[:, :ka], w, counts, off, more, dgrad)
+        wide[:, ka:] = float("nan")
+        wide[0], wide[off[2] - 1], wide[-3:] = float("nan"), float("inf"), float("nan")
+        wide[off[1]:off[2]] = float("nan")
+        bad = w.clone()
+        bad[1] = float("nan")
+        call(wide[:, :ka], bad, c, o, got, sc, add=more)
+        for e in (0, 2):
+            r = slice(off[e], off[e] + counts[e])
+            assert torch.equal(got[r], want[r])
+        assert bool((got[0] == 0).all()) and bool((got[-3:] == 0).all())
+
+
 def test_one_group_of_all_rows_and_no_rows():
     x, w, dy = randn(130, 64, seed=12), randn(1, 72, 64, seed=13), randn(130, 72, seed=14)
     sc = B.alloc_product_scratch()
