@@ -622,6 +622,8 @@ def _strided(t, rows: int, cols: int, what: str, dev: int):
     if t is None:
         return None, 0
     if t.dtype is torch.bfloat16 and t.get_device() == dev and t.dim() == 2:
+        if t.shape == (rows, cols) and t.is_contiguous():
+            return t.data_ptr(), cols if rows > 1 else cols + -cols % 8
         r, c = t.shape
         ld, one = t.stride()
         # (the stride of a single row says nothing)
@@ -634,10 +636,9 @@ def _flat(t, n: int, dtype, what: str, dev: int):
     """At least n elements in a row; dtype None: bytes in all."""
     if t is None:
         return None
-    if t.get_device() == dev and t.is_contiguous() and (
-            t.numel() >= n if t.dtype is dtype else
-            dtype is None and t.numel() * t.element_size() >= n):
-        return t.data_ptr()
+    if t.get_device() == dev and t.is_contiguous():
+        if t.numel() >= n if t.dtype is dtype else dtype is None and t.numel() * t.element_size() >= n:
+            return t.data_ptr()
     raise ValueError(f"{what} is contiguous {dtype or 'memory'} of {n} "
                      f"{'elements' if dtype else 'bytes'}, on the current GPU")
 

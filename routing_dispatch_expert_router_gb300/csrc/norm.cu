@@ -388,21 +388,19 @@ dgamma_kernel(const float* __restrict__ parts, int n, int H, float* __restrict__
 int row_threads(int H, int V) { return ((H / 8 + V - 1) / V + 31) / 32 * 32; }
 
 // CTAs of a kernel that walks the rows: as many as are resident together, the same number on
-// every SM, no more than one a row (a turn of the CTA) and `most`.
+// every SM, no more than one a row (a turn of the CTA) and `most`. set: of the kernel, by its warps
+// (which decide its shared memory).
 template <class Kernel>
-cudaError_t resident(PerDevice& set, Kernel kern, int threads, int smem, int64_t turns, int most,
+cudaError_t resident(PerDevice (&set)[33], Kernel kern, int threads, int smem, int64_t turns, int most,
                      int* grid) {
   int per_sm = 0;
-  const cudaError_t e = set.get(current_device(), &per_sm, [&](int* v) {
+  const cudaError_t e = set[threads / 32].get(current_device(), &per_sm, [&](int* v) {
     cudaError_t err =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
     if (err != cudaSuccess) return err;
-    *v = 1;
-    return cudaSuccess;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kern, threads, smem);
   });
   if (e != cudaSuccess) return e;
-  const cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
-  if (err != cudaSuccess) return err;
   const int sms = num_sms();
   if (per_sm > most / sms) per_sm = most / sms;
   const int64_t n = per_sm > 0 ? (int64_t)sms * per_sm : most;
@@ -413,7 +411,7 @@ cudaError_t resident(PerDevice& set, Kernel kern, int threads, int smem, int64_t
 template <int V, int S, int THREADS>
 cudaError_t run_fwd_ring(const RmsNormFwd& p, cudaStream_t s) {
   auto kern = rmsnorm_fwd_ring_kernel<V, S, THREADS>;
-  static PerDevice set;
+  static PerDevice set[33];
   const int threads = row_threads(p.H, V), smem = S * 2 * V * threads * 16;
   int grid = 0;
   const cudaError_t e = resident(set, kern, threads, smem, p.T, 1 << 20, &grid);
@@ -424,7 +422,7 @@ cudaError_t run_fwd_ring(const RmsNormFwd& p, cudaStream_t s) {
 template <int V, int S, int THREADS, bool WARP, bool KEEP>
 cudaError_t run_bwd(const RmsNormBwd& p, int* parts, cudaStream_t s) {
   auto kern = rmsnorm_bwd_kernel<V, S, THREADS, WARP, KEEP>;
-  static PerDevice set;
+  static PerDevice set[33];
   const int threads = WARP ? 32 * kRowWarps : row_threads(p.H, V);
   const int smem = S * 3 * V * threads * 16;
   const int64_t turns = WARP ? (p.T + kRowWarps - 1) / kRowWarps : p.T;
