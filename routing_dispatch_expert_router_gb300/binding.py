@@ -718,31 +718,33 @@ def moe_permute_fp8(cfg, codes, scales, idx, counts, offsets, row_of, token_of, 
     [R, H] and scales_perm (the atoms of R rows)."""
     c = _cfg(cfg)
     dev, i32 = _device(), torch.int32
-    R, need = _fp8_sizes(bytes(c))
-    T, E, H, k = c.T, c.E, c.H, c.k
-    blocks = H // (32 if c.dtype == 2 else 128)
-    if codes_perm is not None:
-        need = 4352 + 4 * E * (-(-T // 256))
+    T, H, R, blocks, atoms, need, small, maps = _fp8_sizes(bytes(c))
     # (_flat's checks without its calls, a third of this function's time)
     at = [t.data_ptr() if t is not None and t.dtype is i32 and t.numel() >= n and
           t.get_device() == dev and t.is_contiguous() else _flat(t, n, i32, what, dev)
-          for t, n, what in ((idx, T * k, "idx"), (counts, E, "counts"), (offsets, E + 1, "offsets"),
-                             (row_of, T * k, "row_of"), (token_of, R, "token_of"),
-                             (sel_offsets, E + 1, "sel_offsets"), (sel_tokens, T * k, "sel_tokens"))]
+          for t, (n, what) in zip((idx, counts, offsets, row_of, token_of, sel_offsets, sel_tokens),
+                                  maps)]
     _check("moe_permute_fp8",
            lib().moe_permute_fp8(c, _bytes2(codes, T, H, "codes", dev),
                                  _bytes2(scales, T, blocks, "scales", dev), *at,
                                  _bytes2(codes_perm, R, H, "codes_perm", dev, exact=False),
-                                 _flat(scales_perm, -(-R // 128) * -(-blocks // 4) * 512,
-                                       torch.uint8, "scales_perm", dev),
-                                 _flat(scratch, need, None, "scratch", dev), _on(stream, dev)))
+                                 _flat(scales_perm, atoms, torch.uint8, "scales_perm", dev),
+                                 _flat(scratch, need if codes_perm is None else small, None,
+                                       "scratch", dev), _on(stream, dev)))
 
 
 @functools.lru_cache(maxsize=64)
 def _fp8_sizes(config: bytes):
-    """Rows of an FP8 layer's buffers and its scratch."""
-    s = moe_query_sizes(MoEConfig.from_buffer_copy(config))
-    return s.rows_max, s.scratch_bytes
+    """What an FP8 dispatch's tensors hold: T, H, rows, scales of a row, bytes of all rows' scale
+    atoms, of scratch with the layer's rows and without, and its maps."""
+    c = MoEConfig.from_buffer_copy(config)
+    s = moe_query_sizes(c)
+    T, E, k, R = c.T, c.E, c.k, s.rows_max
+    blocks = c.H // (32 if c.dtype == 2 else 128)
+    return (T, c.H, R, blocks, -(-R // 128) * -(-blocks // 4) * 512, s.scratch_bytes,
+            4352 + 4 * E * (-(-T // 256)),
+            ((T * k, "idx"), (E, "counts"), (E + 1, "offsets"), (T * k, "row_of"), (R, "token_of"),
+             (E + 1, "sel_offsets"), (T * k, "sel_tokens")))
 
 
 # ---------------------------------------------------------------- products of free form
