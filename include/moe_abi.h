@@ -763,8 +763,11 @@ typedef struct moe_int4_tensor {
  * [rows, N / 2] = bf16(silu(a) b) of the product's columns a[n], b[n] = n and
  * N / 2 + n, held in fp32. Made for few rows a group (decoding), where the codes'
  * bytes decide; any number is right, every 16 rows reading the codes once more.
- * For many rows moe_int4_dequantize and the products below. A row of x that
- * holds an infinity or a NaN has NaN results; other rows are not touched by it. */
+ * For many rows moe_int4_dequantize and the products below. A group's sum of
+ * (code - zero) x is taken in fp32 before its scale (which never overflows for
+ * |x| below 2^114); a code that is its zero point takes its x out whatever its
+ * size. Infinities and NaN of a row of x go into that row's results as they
+ * do in any sum (zero times one is NaN); other rows are not touched by them. */
 MOE_API moe_status moe_int4_grouped_gemm(const moe_int4_tensor* w, int64_t rows, const void* x,
                                          int64_t ldx, const int32_t* counts,
                                          const int32_t* offsets, int32_t swiglu, void* out,

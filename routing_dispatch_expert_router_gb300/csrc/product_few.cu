@@ -6,8 +6,7 @@
 //
 //   warp 0         TMA producer (one lane): 256 weight rows x 128 bytes of K a stage, the same
 //                  step of the tokens' rows, and the group scales and zero points;
-//   warps 1-3      (4-bit) the tokens' elements in the order in which codes unpack, and their
-//                  sums over 32;
+//   warps 1-3      (4-bit) the tokens' elements in the order in which codes unpack;
 //   eight warps    mma.sync m16n8k16, the weights as A: a warp has 32 weight rows. Tokens are
 //                  B, eight to a tile, at most 16 a pass: with few tokens tcgen05's 128-row
 //                  tiles would multiply padding, and its operands would have to be written
@@ -15,12 +14,11 @@
 //   four warps     join units that CTAs share and write results, beside the next unit's sums.
 //
 // 4-bit weights are s (q - z). The codes become bf16 numbers 128 + q by placing their bits in
-// the mantissa (one logic operation for two), whose products with x are exact; the offset and
-// the zero point leave by s (sum (128 + q) x - (128 + z) sum x), in fp32, per group of K. (The
-// subtraction costs 2^-24 (128 + z) sum |x| of the group at most, far below the result's
-// rounding to bf16, unless all of a group's codes cancel its x.) Subtracting z from each code
-// first would be four more of eleven instructions a word, and instructions are what the SM
-// runs short of: 24 bytes a clock arrive, 48 codes.
+// the mantissa (one logic operation for two), and one packed addition takes 128 + z off again:
+// q - z is exact in bf16, so what is summed is (q - z) x itself, in fp32 per group of K, and s is
+// applied to the group's sum. (Sums of (128 + q) x with (128 + z) sum x taken off behind them need no
+// such addition, but their roundings are those of 128 x: a channel 1000 times the others whose
+// code is its zero point left an error of 2e-3 of the group's result, and values above 2^120 a NaN.)
 //
 // A (expert, columns) unit that two or more CTAs share is joined through scratch: every CTA
 // writes its fp32 part, the one that arrives last adds the parts in K's order. So results do
@@ -30,10 +28,10 @@
 // the operand that streams, the expert's weights the one of 16, turned by ldmatrix where the
 // reduction runs over their rows. 8192 rows of 4096 to 16: 21.9 us.
 //
-// A row of each of two experts through 28672 x 4096 in 4 bits (121 MB): 31 us, 3.9 TB/s; loads alone
+// A row of each of two experts through 28672 x 4096 in 4 bits (121 MB): 31.5 us, 3.8 TB/s; loads alone
 // take 27.6, the launch, the shares and the last joins the rest. 512 rows of 64 experts through
-// 4096 x 2048 (287 MB): 75 us, 3.8 TB/s: a step whose unit has two tiles of tokens takes some 2050
-// clocks, in which HBM would bring three halves of it. bf16, 8 rows of five experts through
+// 4096 x 2048 (287 MB): 75 us, 3.8 TB/s: a step whose unit has two tiles of tokens takes
+// 1.24 us (2560 clocks), for whose bytes HBM takes 0.77. bf16, 8 rows of five experts through
 // 4096 x 14336 (587 MB): 86 us, 6.8 TB/s.
 #include "gemm_common.cuh"
 
@@ -63,14 +61,14 @@ struct Cfg {
   static constexpr int THREADS = 32 * (1 + HELPERS + kConsumers + kJoiners);
   static constexpr int STAGES = W4 ? 4 : 5;
   static constexpr int STEP = W4 ? 256 : 64;           // elements of K a stage
-  // what a step of one and of two token tiles takes, as measured (codes: 1510 and 2100 clocks)
-  static constexpr int W1 = W4 ? 5 : 1, W2 = W4 ? 7 : 1;
+  // what a step of one and of two token tiles takes, as measured (codes in L2, groups of 128, 64 and
+  // 32 with zero points: 2070 and 2560 clocks, 2260 and 2790, 2640 and 3280)
+  static constexpr int W1 = W4 ? 4 : 1, W2 = W4 ? 5 : 1;
   static constexpr int XBOXES = STEP / 64;             // boxes of 64 elements x 8 tokens
   static constexpr int X_OFF = kSlab * 128;
   static constexpr int S_OFF = X_OFF + kTok / 8 * XBOXES * 1024;
   static constexpr int Z_OFF = S_OFF + (W4 ? 8 * kSlab * 2 : 0);   // eight groups at most
-  static constexpr int SUM_OFF = Z_OFF + (W4 ? 8 * kSlab : 0);
-  static constexpr int STAGE = (SUM_OFF + (W4 ? 8 * kTok * 4 : 0) + 1023) / 1024 * 1024;
+  static constexpr int STAGE = (Z_OFF + (W4 ? 8 * kSlab : 0) + 1023) / 1024 * 1024;
   static constexpr int CTRL = W4 ? 4096 : 5376;
   static constexpr int SMEM = STAGES * STAGE + 2 * kTileBytes + CTRL + 1024;
 };
@@ -92,20 +90,11 @@ __device__ __forceinline__ T at(const uint8_t* st, uint32_t place, int offset) {
   return *reinterpret_cast<const T*>(st + place + offset);
 }
 
-// s + the low or the high bf16 of a pair, without a conversion of its own.
-__device__ __forceinline__ float add_lo(float s, uint32_t pair) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.f32.bf16 %0, l, %0;\n\t}" : "+f"(s) : "r"(pair));
-  return s;
-}
-__device__ __forceinline__ float add_hi(float s, uint32_t pair) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.f32.bf16 %0, h, %0;\n\t}" : "+f"(s) : "r"(pair));
-  return s;
-}
-
-// Elements i and i + 4 of a word of eight codes as the bf16 pair 128 + q.
-__device__ __forceinline__ uint32_t codes_pair(uint32_t w, int i) {
+// Elements i and i + 4 of a word of eight codes as the bf16 pair q - z; z: the pair -(128 + z).
+__device__ __forceinline__ uint32_t codes_pair(uint32_t w, int i, uint32_t z) {
   uint32_t r;
   asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(r) : "r"(w >> (4 * i)));
+  asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(z));
   return r;
 }
 
@@ -122,12 +111,12 @@ __device__ __forceinline__ int token_place(int tok, int box, int piece) {
   return GC == 4 ? piece ^ (box & 1) ^ ((tok & 1) << 1) : piece ^ ((tok & 1) << 2);
 }
 
-// A lane's places in a stage, without the stage's address: weights, tokens' pieces, sums, scales.
+// A lane's places in a stage, without the stage's address: weights, tokens' pieces, scales, zero points.
 // In an MMA a lane has any 16-bit pairs of K as long as A's and B's are the same and all lanes'
 // are of one group: with groups of 128 elements lane t has elements 32 t .. 32 t + 31 of the group
 // (16 bytes of codes), else 8 t .. 8 t + 7 of each 32 (a word).
 struct Places {
-  uint32_t w[8], x[2][4], sum, s, z;            // x: for one tile of eight tokens, for two
+  uint32_t w[8], x[2][4], s, z;                 // x: for one tile of eight tokens, for two
 };
 
 template <bool W4, bool SWIGLU, int GC>
@@ -155,7 +144,6 @@ __device__ __forceinline__ Places places(const FewProduct& p, int rg, int g, int
     }
     // (scales and zero points: gate's and up's rows apart, or 256 rows a group)
     const int at = SWIGLU ? (rg >> 2) * p.groups_per_step * 128 + (row0 & 127) : row0;
-    a.sum = C::SUM_OFF + 2 * t * 4;
     a.s = C::S_OFF + at * 2;
     a.z = C::Z_OFF + at;
   } else {
@@ -184,6 +172,15 @@ __device__ __forceinline__ void step_int4(float (&tot)[2][2][4], const uint8_t* 
       for (int n = 0; n < NTL; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+    // -(128 + z) of the group, made as the codes' bf16 numbers are
+    const int q = c0 / GC;
+    uint32_t z[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        z[m][h] = has_zeros ? (at<uint8_t>(st, a.z, q * GS + 16 * m + 8 * h) & 127u) * 0x10001u | 0xc300c300u
+                            : 0xc308c308u;
     uint4 w4[2][2];
     if (GC == 4) {
 #pragma unroll
@@ -212,10 +209,10 @@ __device__ __forceinline__ void step_int4(float (&tot)[2][2][4], const uint8_t* 
                        : at<uint4>(st, a.x[0][c & 1], n * 1024 + (c >> 1) * XB);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const uint32_t a0 = codes_pair(w[m][0], 0), a1 = codes_pair(w[m][1], 0);
-        const uint32_t a2 = codes_pair(w[m][0], 1), a3 = codes_pair(w[m][1], 1);
-        const uint32_t b0 = codes_pair(w[m][0], 2), b1 = codes_pair(w[m][1], 2);
-        const uint32_t b2 = codes_pair(w[m][0], 3), b3 = codes_pair(w[m][1], 3);
+        const uint32_t a0 = codes_pair(w[m][0], 0, z[m][0]), a1 = codes_pair(w[m][1], 0, z[m][1]);
+        const uint32_t a2 = codes_pair(w[m][0], 1, z[m][0]), a3 = codes_pair(w[m][1], 1, z[m][1]);
+        const uint32_t b0 = codes_pair(w[m][0], 2, z[m][0]), b1 = codes_pair(w[m][1], 2, z[m][1]);
+        const uint32_t b2 = codes_pair(w[m][0], 3, z[m][0]), b3 = codes_pair(w[m][1], 3, z[m][1]);
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
           mma16816(acc[m][n], a0, a1, a2, a3, x[n].x, x[n].y);
@@ -223,29 +220,19 @@ __device__ __forceinline__ void step_int4(float (&tot)[2][2][4], const uint8_t* 
         }
       }
     }
-    // the group's scales, zero points and sums of x
-    const int q = c0 / GC;
-    uint64_t sx[NTL];
-#pragma unroll
-    for (int n = 0; n < NTL; ++n) sx[n] = at<uint64_t>(st, a.sum, (q * kTok + n * 8) * 4);
+    // the group's sums by its scales
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float s = __uint_as_float(
             (uint32_t)at<uint16_t>(st, a.s, (q * GS + 16 * m + 8 * h) * 2) << 16);
-        // -(128 + z) as the codes' bf16 numbers are made: a conversion takes eight times as long
-        const float z =
-            has_zeros ? __uint_as_float(
-                            ((uint32_t)at<uint8_t>(st, a.z, q * GS + 16 * m + 8 * h) & 127u | 0xc300u) << 16)
-                      : -136.f;
-        const uint64_t s2 = ptx::f2_pack(s, s), z2 = ptx::f2_pack(z, z);
+        const uint64_t s2 = ptx::f2_pack(s, s);
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
           const uint64_t d = ptx::f2_pack(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
           float(&t)[4] = tot[m][n];
-          ptx::f2_unpack(ptx::f2_fma(s2, ptx::f2_fma(z2, sx[n], d), ptx::f2_pack(t[2 * h], t[2 * h + 1])),
-                         t[2 * h], t[2 * h + 1]);
+          ptx::f2_unpack(ptx::f2_fma(s2, d, ptx::f2_pack(t[2 * h], t[2 * h + 1])), t[2 * h], t[2 * h + 1]);
         }
       }
   }
@@ -496,8 +483,7 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
   }
   if (W4 && warp <= C::HELPERS) {
     // the tokens' elements in pairs (i, i + 4) of each eight, as the codes unpack, the 16-byte
-    // pieces of odd tokens four places on (so that two tokens' pieces are in all banks), and
-    // their sums over each 32
+    // pieces of odd tokens four places on (so that two tokens' pieces are in all banks)
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     for (Place v = begin; ok; advance(v)) {
@@ -509,30 +495,21 @@ product_few_kernel(const __grid_constant__ Maps maps, const FewProduct p) {
                                                     abort_flag));
         if (!ok) break;
         uint8_t* st = stages + stage * C::STAGE;
-        // three tokens at a time: what bounds these warps is the shuffles' latency
+        // three tokens at a time: what bounds these warps is the loads' latency
         for (int tok0 = warp - 1; tok0 < ntok; tok0 += 3 * C::HELPERS) {
           uint4 q[3];
-          float s[3];
           uint8_t* r[3];
 #pragma unroll
           for (int i = 0; i < 3; ++i) {
             const int tok = min(tok0 + i * C::HELPERS, ntok - 1);
             r[i] = st + C::X_OFF + (lane >> 3) * (ntok * 128) + tok * 128;
             q[i] = *reinterpret_cast<const uint4*>(r[i] + (((lane & 7) ^ (tok & 7)) << 4));
-            s[i] = add_hi(add_lo(add_hi(add_lo(0.f, q[i].x), q[i].x), q[i].y), q[i].y) +
-                   add_hi(add_lo(add_hi(add_lo(0.f, q[i].z), q[i].z), q[i].w), q[i].w);
           }
-#pragma unroll
-          for (int o = 1; o < 4 * GC; o *= 2)
-#pragma unroll
-            for (int i = 0; i < 3; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 3; ++i) {
             const int tok = tok0 + i * C::HELPERS;
             if (tok >= ntok) break;
-            if (lane % (4 * GC) == 0)
-              *reinterpret_cast<float*>(st + C::SUM_OFF + (lane / (4 * GC) * kTok + tok) * 4) = s[i];
             *reinterpret_cast<uint4*>(r[i] + (token_place<GC>(tok, lane >> 3, lane & 7) << 4)) =
                 make_uint4(__byte_perm(q[i].x, q[i].z, 0x5410), __byte_perm(q[i].x, q[i].z, 0x7632),
                            __byte_perm(q[i].y, q[i].w, 0x5410), __byte_perm(q[i].y, q[i].w, 0x7632));
@@ -824,7 +801,7 @@ static_assert(kFewPart == kSlab * kTok, "parts as the kernel writes them");
 
 // Units of 16 tokens and 256 weight rows, weighed, that the kernel's 32-bit numbers hold.
 bool few_fits(int64_t rows, int G, int64_t N, int64_t K) {
-  return (rows / kTok + G + 1) * ((N + 127) / 128) * 7 < (1LL << 31) && K < (1LL << 24);
+  return (rows / kTok + G + 1) * ((N + 127) / 128) * Cfg<true>::W2 < (1LL << 31) && K < (1LL << 24);
 }
 
 // A pass of the stream has 16 tokens, a tile of the tensor cores' kernel up to 256. With more than
