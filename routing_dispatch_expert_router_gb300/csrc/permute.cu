@@ -92,12 +92,10 @@ permute_rank_kernel(const int32_t* __restrict__ idx, const int32_t* __restrict__
   const int t = c * kChunkTokens + tid;
 
   for (int i = tid; i < E * W; i += nt) (&bm[0][0])[i] = 0u;
-  if (n_chunk <= 1) ptx::grid_dependency_wait();
+  ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
   int e[kMaxK];
   const bool bad = t < T && token_experts(idx, t, k, E, e);
-  // (the histogram lets this kernel start behind its own wait, when idx is complete)
-  if (n_chunk > 1) ptx::grid_dependency_wait();
-  ptx::grid_launch_dependents();
   if (bad && n_chunk == 1 && blockIdx.x == 0) record_status(status, MOE_ERR_DEVICE_CHECK);
   if (tid < E && n_chunk > 1) {
     int a = 0, b = 0;
