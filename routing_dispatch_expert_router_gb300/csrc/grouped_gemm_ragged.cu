@@ -32,6 +32,7 @@
 #include <math.h>
 
 #include "gemm_common.cuh"
+#include "ragged_shares.h"
 
 namespace moe {
 namespace {
@@ -58,15 +59,6 @@ static_assert(kSmem <= 232448, "shared memory");
 struct Maps {
   CUtensorMap a, a2, b2, b[8];
 };
-
-// Pairs that share a tile's reduction of nk steps, `most` at most. A step takes some 600 clocks, a
-// part about 12 a column to join, one after the other: sqrt(nk tile / 50) steps make the least of
-// both. Joining at all costs the time of some 16 steps.
-__host__ __device__ inline int shares(int most, int nk, int tile) {
-  if (nk < 24) return 1;
-  const int least = (int)sqrtf(nk * tile * 0.02f), n = nk / (least < 2 ? 2 : least);
-  return n < 1 ? 1 : n < most ? n : most;
-}
 
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
