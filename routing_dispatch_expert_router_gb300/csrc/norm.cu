@@ -435,17 +435,26 @@ cudaError_t run_bwd(const RmsNormBwd& p, int* parts, cudaStream_t s) {
 
 cudaError_t launch_rmsnorm_fwd(const RmsNormFwd& p, cudaStream_t s) {
   constexpr int W = 32 * kRowWarps;
+  // A warp a row up to kWarpColumns. (us with residual and sum, a row a warp's and a CTA's: 8192 x 256
+  // 4.6 and 8.6, 8192 x 768 9.9 and 10.1, 65536 x 768 58 and 68, 65536 x 1024 78 and 77, 64 x 1024 2.6 and
+  // 1.8; backward, 8192 x 1024, 14.8 and 19.4, 64 x 1024 4.8 and 3.7.)
   if (p.H <= kWarpColumns) {
     const unsigned grid = (unsigned)((p.T + kRowWarps - 1) / kRowWarps);
     return launch_early(p.H <= 512 ? rmsnorm_fwd_kernel<2, true> : rmsnorm_fwd_kernel<4, true>, grid,
                         dim3(W, 1, 1), 0, s, p);
   }
-  // (with fewer rows than CTAs there is nothing to fetch ahead)
-  if (p.T > 2 * num_sms()) {
-    if (p.H <= 4096) return run_fwd_ring<1, 4, 512>(p, s);
+  // Long rows go through the ring where there are more than two an SM: with fewer there is nothing to
+  // fetch ahead, and shorter ones have CTAs enough in flight. (us with residual and sum, through the
+  // ring and a row a CTA's: 8192 x 4096 49.7 and 40.3, 8192 x 2048 24.8 and 21.2; 8192 x 7168 76.3 and 75.9,
+  // with MXFP8 codes 79.1 and 87.3, without residual 51.1 and 61.9; 8192 x 8192 90.7 and 83.6, 93.2 and
+  // 95.9, 55.8 and 67.5; 4096 x 16384 91.6 and 94.9, without residual 45.9 and 81.9. 304 rows of 7168 5.7
+  // and 4.6, 608 8.4 and 8.1, 1216 12.9 and 14.1.)
+  if (p.T > 2 * num_sms() && p.H > 4096) {
     if (p.H <= 8192) return run_fwd_ring<1, 3, 1024>(p, s);
     if (p.H <= 16384) return run_fwd_ring<2, 3, 1024>(p, s);
   }
+  // (the widest rows' four vectors a thread spill 24 bytes: 2048 x 16384 47 us, x 16392 62, x 32768 100,
+  // of 39, 39 and 79 that the bytes take; the backward's 48: 58, 72 and 116, of 30, 30 and 59)
   const int V = p.H <= 16384 ? 2 : 4;
   return launch_early(V == 2 ? rmsnorm_fwd_kernel<2, false> : rmsnorm_fwd_kernel<4, false>,
                       (unsigned)p.T, dim3(row_threads(p.H, V), 1, 1), 0, s, p);

@@ -1,6 +1,6 @@
-"""The norm's kernels that keep rows in flight, with more rows to every CTA than its ring has slots, so
-that each slot is filled and read again: every width that has a form of its own, the 8-bit output, in
-place, strided, and beside rows of NaN. Against the formulas in 64 bits, with the tolerances of the
+"""The norm's kernels of many rows. Those that keep rows in flight have more rows to every CTA than its
+ring has slots, so that each slot is filled and read again: every width that has a form of its own,
+the 8-bit output, in place, strided, and beside rows of NaN. Against the formulas in 64 bits, with the tolerances of the
 short cases (their sums are no deeper here; dgamma's grow with the rows).
 """
 import pytest
@@ -11,8 +11,8 @@ from test_gpu_rmsnorm import BF, EPS, U, check_fwd, codes_of, gamma_of, near, ro
 
 pytestmark = pytest.mark.gpu
 
-# rows, columns: at least eight rows a CTA with six CTAs an SM up to 2080 columns, three up to 4096, two
-# up to 8200, one above; on 152 SMs, and no whole number of rounds
+# rows, columns: eight rows a CTA or more where CTAs are persistent (three an SM at 4096 columns, two at
+# 7168 and 8200, one above; on 152 SMs), and no whole number of rounds
 WIDTHS = [(8301, 2056), (4201, 4096), (2501, 7168), (2501, 8200), (1301, 16384)]
 
 
