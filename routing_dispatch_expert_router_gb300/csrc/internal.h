@@ -353,7 +353,7 @@ struct FewProduct {
   uint32_t* arrived;          // [kFewCtas], zero before and after every launch
   int32_t* status;
   // set by the launcher
-  int F, slabs, steps, groups_per_step, group_log2;
+  int F, slabs, steps, groups_per_step;
   bool has_zeros, x_whole;
 };
 constexpr int kFewCtas = 256;

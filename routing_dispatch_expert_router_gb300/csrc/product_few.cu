@@ -852,7 +852,6 @@ cudaError_t launch_product_few(FewProduct p, const void* x, int64_t ldx, const v
   p.steps = (p.K + (w4 ? 255 : 63)) / (w4 ? 256 : 64);
   p.has_zeros = zeros != nullptr;
   p.groups_per_step = w4 ? 256 / p.group : 0;
-  p.group_log2 = p.group == 128 ? 7 : p.group == 64 ? 6 : 5;
   p.x_whole = w4 && p.K % 64 == 0;
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const uint64_t N = p.N, K = p.K, ld = ldx;
