@@ -26,9 +26,10 @@
 //     of the last block in both operands (zero times a NaN is one) before it hands the stage to
 //     the pair's MMAs.
 //
-// 32768 rows of 64 experts, 4096 x 2040 (0.55 PFLOP): data gradient 420 us, 1.31 PFLOP/s; weight
-// gradient 525, whose operands pass from L2 to the SMs at 10.6 TB/s (without MMAs and stores 424
-// are left, without stores 452). 8192^3 in one group: 1.65 to 1.70 PFLOP/s in each of the three.
+// 32768 rows of 64 experts, 4096 x 2040 (0.55 PFLOP), call after call: data gradient 470 us, 1.16
+// PFLOP/s; weight gradient 552, 0.99. In runs too short for the power limit 408 and 499. The weight
+// gradient's 4.9 GB from L2 to the SMs bound it (its loads alone take 424, all but its stores 452).
+// 8192^3 in one group: 1.65 to 1.70 PFLOP/s in each of the three.
 #include <math.h>
 
 #include "gemm_common.cuh"
@@ -661,7 +662,10 @@ cudaError_t run_ragged(const Maps& m, const RaggedProduct& p, cudaStream_t s) {
 // Columns of a tile, from what it takes in clocks: steps of 450 + 1.75 a column, an epilogue of 1280
 // + 20 a column beside the next tile's steps; in rounds over the pairs of SMs, or shared among them.
 // `others`: tiles in the other dimension; `groups`: each cuts `columns` once more (half a tile on
-// average), or 0; nk: steps.
+// average), or 0; nk: steps. (Against the best of 64, 128, 192 and 256 columns, 24 shapes from 333 rows of
+// 4096 x 4096 to 8192 of 8192 x 8192 in the three modes: the same or within 5 % for 21. 1000 rows of 8
+// experts, 2048 x 1024: 13.2 and 11.6 us, as a data gradient, whose joins it takes too low, 22.1 and 15.0;
+// 2801 rows of 4, 200 x 7776, as a data gradient 23.6 and 20.2.)
 int tile_columns(int64_t columns, int64_t others, int64_t groups, int nk, int least) {
   const int pairs = num_sms() / 2 < kRaggedPairs ? num_sms() / 2 : kRaggedPairs;
   int best = 256;
