@@ -12,7 +12,7 @@
 // 8192 rows of 7168 with residual, sum, bf16 output and MXFP8 codes: 80 us, 6.6 TB/s (a row a CTA with
 // loads that wait for nothing but themselves: 101, with instructions in 73 % of the issue slots and
 // HBM 63 % busy; the ring and packed arithmetic brought it here). 8192 rows of 4096 backward with
-// dsum and dgamma: 45 us, 5.9 TB/s (67 before). One row of 7168: 4.3 us, a launch.
+// dsum and dgamma: 45 us, 5.9 TB/s (67 before). One row of 4096 or 7168: 4.3 us, a launch.
 #include "common.cuh"
 #include "fp8_layout.cuh"
 #include "internal.h"
@@ -179,7 +179,7 @@ rmsnorm_fwd_kernel(const RmsNormFwd p) {
   finish_row<V>(p, row, h, g, ss, first, step, lane);
 }
 
-// Many rows: a persistent CTA keeps the loads of S rows in flight. Each thread copies its own
+// Many long rows: a persistent CTA keeps the loads of S rows in flight. Each thread copies its own
 // columns into its own places of shared memory (cp.async) and reads them back alone, so the
 // ring needs no barrier, and the rows in flight take no registers.
 template <int V, int S, int THREADS>

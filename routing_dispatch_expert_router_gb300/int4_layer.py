@@ -26,8 +26,8 @@ from .fp4_layer import ROOT, _time_graph
 
 # Rows an expert expects up to which the products read the codes once for every 16 rows. Beyond it
 # the experts become bf16 first, which costs 4.5 bytes of traffic a weight, eight readings of codes.
-# (A step of eight experts 28672 x 4096, 2 of them a token, us, streamed and not: 128 tokens 473 and
-# 1104, 256: 816 and 1102, 384: 1154 and about 1150, 512: 1472 and 1195.)
+# (A step of eight experts 28672 x 4096, 2 of them a token, us, streamed and not: 128 tokens 464 and
+# 1099, 256: 808 and 1103, 384: 1132 and 1103, 512: 1443 and 1193.)
 STREAM_ROWS = 96
 
 
